@@ -196,9 +196,9 @@ def prepare(c, seed):
         s["weights"] = weights
         return s
     s["x"] = _activations(g, T, c["K"]).to(DTYPE[c["dtype"]])
-    NW = c["N"] * (2 if c["gated"] else 1)
-    codes, scales, s["tiles"] = _weight(g, c["E"], NW, c["K"], c["fmt"])
-    s["codes"], s["scales"] = codes.view(c["E"], NW, -1), scales.view(c["E"], NW, -1)
+    for part in ("", "up_") if c["gated"] else ("",):
+        codes, scales, s[part + "tiles"] = _weight(g, c["E"], c["N"], c["K"], c["fmt"])
+        s[part + "codes"], s[part + "scales"] = codes.view(c["E"], c["N"], -1), scales.view(c["E"], c["N"], -1)
     # for the plain form: the rows of each expert, padded to the longest with row R (a zero row)
     off = s["offsets"].long()
     count = off[1:] - off[:-1]
@@ -293,11 +293,11 @@ def _plain(s):
         x = torch.cat((x, torch.zeros_like(x[:1])))
         token = torch.cat((torch.where(s["order"] >= 0, s["order"].long() // k, x.shape[0] - 1),
                            torch.full((1,), x.shape[0] - 1, device=x.device)))
-        w = _values(_unpacked(s["codes"]), s["scales"], s["fmt"])
-        y = torch.bmm(x[token[s["slots"]]], w.transpose(1, 2))
+        x = x[token[s["slots"]]]
+        y = torch.bmm(x, _values(_unpacked(s["codes"]), s["scales"], s["fmt"]).transpose(1, 2))
         if s["gated"]:
-            gate, up = y[..., : s["N"]], y[..., s["N"]:]
-            y = gate / (1.0 + torch.exp(-gate)) * up
+            up = torch.bmm(x, _values(_unpacked(s["up_codes"]), s["up_scales"], s["fmt"]).transpose(1, 2))
+            y = y / (1.0 + torch.exp(-y)) * up
         out = torch.zeros(R + 1, s["N"], dtype=torch.float32, device=x.device)
         out[s["slots"].reshape(-1)] = y.reshape(-1, s["N"])
         return {"y": out[:R].to(torch.bfloat16)}
@@ -326,7 +326,8 @@ def _framework(s):
         return {"y": uq.gemm_mx(s["x"], (s["codes"], s["tiles"]), s["fmt"])}
     if s["op"] == "experts":
         q = uq.quantize_mx(s["x"], s["fmt"], offsets=s["offsets"], pos=s["pos"])
-        return {"y": uq.gemm_mx_grouped(q, (s["codes"], s["tiles"]), s["offsets"], s["fmt"], gated=s["gated"])}
+        up = (s["up_codes"], s["up_tiles"]) if s["gated"] else None
+        return {"y": uq.gemm_mx_grouped(q, (s["codes"], s["tiles"]), s["offsets"], s["fmt"], up=up)}
     if s["op"] == "route":
         order, pos, offsets = uq.moe_sort(s["ids"], s["E"])
         xs = uq.moe_gather(s["x"], pos, offsets)
@@ -399,9 +400,10 @@ def exact(c, seed):
         for e in range(c["E"]):
             if off[e] == off[e + 1]:
                 continue
-            y = x[s["order"][off[e]:off[e + 1]].long() // k] @ _exact_weight(s["codes"][e], s["scales"][e], c["fmt"]).t()
+            rows = x[s["order"][off[e]:off[e + 1]].long() // k]
+            y = rows @ _exact_weight(s["codes"][e], s["scales"][e], c["fmt"]).t()
             if c["gated"]:
-                y = y[:, :c["N"]] * torch.sigmoid(y[:, :c["N"]]) * y[:, c["N"]:]
+                y = y * torch.sigmoid(y) * (rows @ _exact_weight(s["up_codes"][e], s["up_scales"][e], c["fmt"]).t())
             out[off[e]:off[e + 1]] = y
         return {"y": out}
     if c["op"] == "route":
