@@ -20,6 +20,7 @@ BITS = {"INT4_SYM": 4, "INT4_ASYM": 4, "INT8_SYM": 8, "INT2_ASYM": 2, "NF4": 4, 
 
 # every entry point declared in include/uq.h: name -> (restype, argtypes)
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
+_L, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "uq_status_string": (ctypes.c_char_p, [_I]),
     "uq_last_error": (ctypes.c_char_p, []),
@@ -45,6 +46,17 @@ SIGNATURES = {
     "uq_gemm_w4a8_kernel_count": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_I)]),
     "uq_rope_table": (_I, [_P, _I, _I, ctypes.c_double, _P]),
     "uq_rmsnorm_rope": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P]),
+    "uq_mx_scales_size": (_I, [_I, _I, _I, _I, _SZ]),
+    "uq_pack_mx_scales": (_I, [_P, _P, _I, _I, _I, _I, _P]),
+    "uq_quantize_mx": (_I, [_P, _I, _L, _P, _P, _I, _I, _I, _F, _P, _I, _P, _I, _P]),
+    "uq_dequant_mx": (_I, [_P, _P, _P, _I, _I, _I, _I, _F, _P, _I, _P]),
+    "uq_gemm_mx": (_I, [_P, _I, _L, _P, _F, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
+    "uq_gemm_mx_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "uq_moe_sort": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
+    "uq_moe_gather": (_I, [_P, _I, _P, _P, _I, _P, _I, _I, _I, _P]),
+    "uq_moe_gather_grad": (_I, [_P, _I, _P, _P, _I, _I, _I, _P]),
+    "uq_moe_combine": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "uq_moe_combine_grad": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P]),
 }
 
 _lib = None
@@ -322,3 +334,182 @@ def device_fault() -> int:
     v = ctypes.c_uint(0)
     _check(lib().uq_device_fault(ctypes.byref(v)), "uq_device_fault")
     return v.value
+
+
+# ---- microscaled 4-bit operands: a pair (codes uint8 [..., rows, K/2], scales uint8 tiles) -------------------------
+
+MX_FORMATS = {"MXFP4": 0, "NVFP4": 1}
+MX_BLOCK = {"MXFP4": 32, "NVFP4": 16}
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def mx_scales_size(rows: int, K: int, fmt: str, segments: int = 0) -> int:
+    """uq_mx_scales_size: bytes of an operand's scale tiles (host only)."""
+    v = ctypes.c_size_t()
+    _check(lib().uq_mx_scales_size(rows, K, MX_FORMATS[fmt], segments, ctypes.byref(v)), "uq_mx_scales_size")
+    return v.value
+
+
+def pack_mx_scales(scales: torch.Tensor, fmt: str, stream=None) -> torch.Tensor:
+    """uq_pack_mx_scales: scale bytes [rows][K/block] or [experts][rows][K/block] -> tiles (of each expert)."""
+    experts = scales.shape[0] if scales.dim() == 3 else 1
+    rows, K = scales.shape[-2], scales.shape[-1] * MX_BLOCK[fmt]
+    assert scales.dtype == torch.uint8
+    tiles = torch.empty((experts, mx_scales_size(rows, K, fmt)), dtype=torch.uint8, device=scales.device)
+    _check(lib().uq_pack_mx_scales(_ptr(scales), _ptr(tiles), experts, rows, K, MX_FORMATS[fmt], _stream(stream)),
+           "uq_pack_mx_scales")
+    return tiles if scales.dim() == 3 else tiles[0]
+
+
+def _rows(x: torch.Tensor):
+    """Pointer and row stride of a [rows][K] tensor whose rows are dense."""
+    assert x.is_cuda and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1), "x must be a CUDA matrix of dense rows"
+    ld = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return ctypes.c_void_p(x.data_ptr()), ld
+
+
+def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | None = None,
+                pos: torch.Tensor | None = None, stream=None):
+    """uq_quantize_mx: rows [T][K] (bf16, fp16 or fp32; rows may be strided) -> (codes, scales).
+
+    ``offsets`` (int32 [experts + 1]): the rows are sorted by expert; with ``pos`` (int32 [T][k]) they are gathered by
+    expert on the way, as moe_gather would, and the operand has T*k rows."""
+    T, K = x.shape
+    segments = 0 if offsets is None else offsets.numel() - 1
+    topk = 0 if pos is None else pos.shape[1]
+    assert offsets is None or offsets.dtype == torch.int32
+    assert pos is None or (pos.dtype == torch.int32 and pos.shape[0] == T)
+    rows = T if pos is None else T * topk
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(mx_scales_size(rows, K, fmt, segments), dtype=torch.uint8, device=x.device)
+    ptr, ld = _rows(x)
+    _check(lib().uq_quantize_mx(ptr, DTYPES[x.dtype], ld, _ptr(codes), _ptr(scales), T, K, MX_FORMATS[fmt], tscale,
+                                _ptr(offsets), segments, _ptr(pos), topk, _stream(stream)), "uq_quantize_mx")
+    return codes, scales
+
+
+def dequant_mx(q: tuple, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """uq_dequant_mx: the values (codes, scales) stand for, [rows][K] of ``dtype``."""
+    codes, scales = q
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    segments = 0 if offsets is None else offsets.numel() - 1
+    assert offsets is None or offsets.dtype == torch.int32
+    assert scales.numel() >= mx_scales_size(rows, K, fmt, segments)
+    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
+    _check(lib().uq_dequant_mx(_ptr(codes), _ptr(scales), _ptr(out), DTYPES[dtype], rows, K, MX_FORMATS[fmt], tscale,
+                               _ptr(offsets), segments, _stream(stream)), "uq_dequant_mx")
+    return out
+
+
+def gemm_mx(x, w: tuple, fmt: str, tscale: float = 1.0, alpha: float = 1.0, dtype: torch.dtype | None = None,
+            y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """uq_gemm_mx: y = alpha * x^ . w^T (``[M][N]``), both operands microscaled.
+
+    ``x``: a matrix (bf16, fp16 or fp32), quantized in the call with ``tscale``, or a pair (codes, scales) of
+    quantize_mx.  ``w``: (codes [N][K/2], scales).  The result has ``dtype`` (default: x's, bf16 for a pair)."""
+    wcodes, wscales = w
+    N, K = wcodes.shape[0], wcodes.shape[1] * 2
+    assert wcodes.dtype == torch.uint8 and wscales.dtype == torch.uint8
+    assert wscales.numel() >= mx_scales_size(N, K, fmt)
+    if isinstance(x, torch.Tensor):
+        assert x.shape[1] == K, "x and w have different K"
+        M, xtype, xscales = x.shape[0], DTYPES[x.dtype], None
+        xptr, ld = _rows(x)
+        out = x.dtype
+    else:
+        xcodes, xscales = x
+        assert xcodes.shape[1] * 2 == K, "x and w have different K"
+        M, xtype, xptr, ld, out = xcodes.shape[0], 0, _ptr(xcodes), 0, torch.bfloat16
+        assert xscales.numel() >= mx_scales_size(M, K, fmt)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype or out, device=wcodes.device)
+    assert y.shape == (M, N)
+    _check(lib().uq_gemm_mx(xptr, xtype, ld, _ptr(xscales), tscale, _ptr(wcodes), _ptr(wscales), _ptr(y),
+                            DTYPES[y.dtype], M, N, K, MX_FORMATS[fmt], alpha, _stream(stream)), "uq_gemm_mx")
+    return y
+
+
+def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tuple | None = None,
+                    alpha: torch.Tensor | None = None, alpha_up: torch.Tensor | None = None,
+                    dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """uq_gemm_mx_grouped: rows sorted by expert times each expert's weight, ``[rows][N]``.
+
+    ``x``: (codes, scales) of quantize_mx with these ``offsets``; ``w`` (and ``up``: silu(x w^T) * (x up^T)): codes
+    [experts][N][K/2] and the experts' scale tiles; ``alpha``, ``alpha_up``: fp32 [experts]."""
+    (xcodes, xscales), (wcodes, wscales) = x, w
+    ucodes, uscales = up if up is not None else (None, None)
+    E, N, K = wcodes.shape[0], wcodes.shape[1], wcodes.shape[2] * 2
+    R = xcodes.shape[0]
+    assert xcodes.shape[1] * 2 == K, "x and w have different K"
+    assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
+    assert xscales.numel() >= mx_scales_size(R, K, fmt, E) and wscales.numel() >= E * mx_scales_size(N, K, fmt)
+    assert up is None or (ucodes.shape == wcodes.shape and uscales.numel() >= E * mx_scales_size(N, K, fmt))
+    assert all(v is None or (v.dtype == torch.float32 and v.numel() == E) for v in (alpha, alpha_up))
+    if y is None:
+        y = torch.empty((R, N), dtype=dtype, device=xcodes.device)
+    assert y.shape == (R, N)
+    _check(lib().uq_gemm_mx_grouped(_ptr(xcodes), _ptr(xscales), _ptr(wcodes), _ptr(wscales), _ptr(ucodes),
+                                    _ptr(uscales), _ptr(offsets), _ptr(alpha), _ptr(alpha_up), _ptr(y),
+                                    DTYPES[y.dtype], R, E, N, K, MX_FORMATS[fmt], _stream(stream)),
+           "uq_gemm_mx_grouped")
+    return y
+
+
+# ---- expert routing ------------------------------------------------------------------------------------------------
+
+def moe_sort(ids: torch.Tensor, experts: int, stream=None):
+    """uq_moe_sort: int32 expert ids [T][k] -> (order int32 [T*k], pos int32 [T][k], offsets int32 [experts + 1])."""
+    T, k = ids.shape
+    assert ids.dtype == torch.int32
+    order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
+    pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    _check(lib().uq_moe_sort(_ptr(ids), T, k, experts, _ptr(order), _ptr(pos), _ptr(offsets), _stream(stream)),
+           "uq_moe_sort")
+    return order, pos, offsets
+
+
+def moe_gather(x: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
+    """uq_moe_gather: xs[pos[t][j]] = x[t], [T*k][H]; rows past offsets[-1] are zero."""
+    (T, H), k = x.shape, pos.shape[1]
+    assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and pos.shape[0] == T
+    xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    _check(lib().uq_moe_gather(_ptr(x), DTYPES[x.dtype], _ptr(pos), _ptr(offsets), offsets.numel() - 1, _ptr(xs), T, k,
+                               H, _stream(stream)), "uq_moe_gather")
+    return xs
+
+
+def moe_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, stream=None) -> torch.Tensor:
+    """uq_moe_gather_grad: dx[t] = sum_j dxs[pos[t][j]], [T][H]."""
+    (T, k), H = pos.shape, dxs.shape[1]
+    assert pos.dtype == torch.int32 and dxs.shape[0] == T * k
+    dx = torch.empty((T, H), dtype=dxs.dtype, device=dxs.device)
+    _check(lib().uq_moe_gather_grad(_ptr(dxs), DTYPES[dxs.dtype], _ptr(pos), _ptr(dx), T, k, H, _stream(stream)),
+           "uq_moe_gather_grad")
+    return dx
+
+
+def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stream=None) -> torch.Tensor:
+    """uq_moe_combine: y[t] = sum_j weights[t][j] * ys[pos[t][j]], [T][H]; weights fp32 [T][k]."""
+    (T, k), H = pos.shape, ys.shape[1]
+    assert pos.dtype == torch.int32 and weights.dtype == torch.float32
+    assert ys.shape[0] == T * k and weights.shape == pos.shape
+    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+    _check(lib().uq_moe_combine(_ptr(ys), DTYPES[ys.dtype], _ptr(pos), _ptr(weights), _ptr(y), T, k, H,
+                                _stream(stream)), "uq_moe_combine")
+    return y
+
+
+def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                     offsets: torch.Tensor, stream=None):
+    """uq_moe_combine_grad: (dys [T*k][H], dweights fp32 [T][k]) of moe_combine for the output gradient dy [T][H]."""
+    (T, k), H = pos.shape, ys.shape[1]
+    assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and weights.dtype == torch.float32
+    assert dy.dtype == ys.dtype and dy.shape == (T, H) and ys.shape[0] == T * k and weights.shape == pos.shape
+    dys = torch.empty_like(ys)
+    dw = torch.empty((T, k), dtype=torch.float32, device=ys.device)
+    _check(lib().uq_moe_combine_grad(_ptr(dy), _ptr(ys), DTYPES[ys.dtype], _ptr(pos), _ptr(weights), _ptr(offsets),
+                                     offsets.numel() - 1, _ptr(dys), _ptr(dw), T, k, H, _stream(stream)),
+           "uq_moe_combine_grad")
+    return dys, dw

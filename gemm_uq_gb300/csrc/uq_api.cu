@@ -13,7 +13,7 @@
 #include <utility>
 #include <vector>
 
-#include "uq_kernels.h"
+#include "uq_mx.cuh"
 
 namespace {
 
@@ -847,6 +847,287 @@ uq_status uq_gemm_kernel_count(int M, int N, int K, int group, uq_fmt fmt, int* 
     }
     *count = n;
     return UQ_OK;
+}
+
+// ---- microscaled 4-bit operands ---------------------------------------------------------------
+namespace {
+bool valid_dtype(int t) { return t >= UQ_BF16 && t <= UQ_FP32; }
+int dtype_size(int t) { return t == UQ_FP32 ? 4 : 2; }
+uq_status check_mx(int rows, int K, int fmt, int segments) {
+    if (fmt != UQ_MXFP4 && fmt != UQ_NVFP4) return fail(UQ_ERR_INVALID, "unknown microscaled format %d", fmt);
+    if (rows < 0 || K < 0 || segments < 0) return fail(UQ_ERR_INVALID, "negative size rows=%d K=%d segments=%d", rows, K, segments);
+    if (K % 32) return fail(UQ_ERR_INVALID, "K=%d is not a multiple of 32", K);
+    return UQ_OK;
+}
+uq_status check_tscale(int fmt, float t) {
+    if (!(t > 0.f) || t > 3.0e38f) return fail(UQ_ERR_INVALID, "tensor scale must be positive and finite");
+    if (fmt == UQ_MXFP4 && t != 1.f) return fail(UQ_ERR_INVALID, "UQ_MXFP4 has no tensor scale");
+    return UQ_OK;
+}
+size_t mx_scales_bytes(int rows, int K, int fmt, int segments) {
+    return (size_t)uq::mx_row_tiles(rows, segments) * uq::mx_ktiles(K, fmt) * 512;
+}
+uq_status check_quant_x(const void* x, int xtype, long long ldx, int K) {
+    if (!valid_dtype(xtype)) return fail(UQ_ERR_INVALID, "unknown element type %d", xtype);
+    if (!x) return fail(UQ_ERR_INVALID, "x is NULL");
+    if (ldx < K) return fail(UQ_ERR_INVALID, "row stride %lld is less than K=%d", ldx, K);
+    if (!aligned16(x) || ldx * dtype_size(xtype) % 16)
+        return fail(UQ_ERR_ALIGN, "x and its rows must be 16-byte aligned");
+    return UQ_OK;
+}
+}  // namespace
+
+uq_status uq_mx_scales_size(int rows, int K, uq_mx_fmt fmt, int segments, size_t* bytes) {
+    uq_status s = check_mx(rows, K, fmt, segments);
+    if (s != UQ_OK) return s;
+    if (!bytes) return fail(UQ_ERR_INVALID, "null pointer");
+    *bytes = mx_scales_bytes(rows, K, fmt, segments);
+    return UQ_OK;
+}
+
+uq_status uq_pack_mx_scales(const uint8_t* natural, uint8_t* tiles, int experts, int rows, int K, uq_mx_fmt fmt,
+                            void* stream) {
+    uq_status s = check_mx(rows, K, fmt, experts);
+    if (s != UQ_OK) return s;
+    if (experts == 0 || rows == 0 || K == 0) return UQ_OK;
+    if (!natural || !tiles) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(natural) || !aligned16(tiles)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    cudaError_t e = uq::launch_pack_mx_scales(fmt, natural, tiles, experts, rows, K, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "scale pack launch");
+}
+
+uq_status uq_quantize_mx(const void* x, uq_dtype xtype, long long ldx, uint8_t* codes, uint8_t* scales, int rows, int K,
+                         uq_mx_fmt fmt, float tscale, const int32_t* offsets, int segments, const int32_t* pos, int topk,
+                         void* stream) {
+    uq_status s = check_mx(rows, K, fmt, segments);
+    if (s != UQ_OK) return s;
+    if ((s = check_tscale(fmt, tscale)) != UQ_OK) return s;
+    if ((offsets != nullptr) != (segments > 0)) return fail(UQ_ERR_INVALID, "offsets must be given exactly with segments");
+    if (pos && (!offsets || topk < 0)) return fail(UQ_ERR_INVALID, "pos needs offsets and topk >= 0");
+    if (pos && (long long)rows * topk > 0x7FFFFFFFll) return fail(UQ_ERR_INVALID, "%d x %d routes are too many", rows, topk);
+    if (rows == 0 || K == 0 || (pos && topk == 0)) return UQ_OK;
+    if ((s = check_quant_x(x, xtype, ldx, K)) != UQ_OK) return s;
+    if (!codes || !scales) return fail(UQ_ERR_INVALID, "codes or scales is NULL");
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(offsets) || !aligned16(pos))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, scales, rows, K, tscale, offsets, segments, pos,
+                                           topk, ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled quantization launch");
+}
+
+uq_status uq_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* out, uq_dtype type, int rows, int K,
+                        uq_mx_fmt fmt, float tscale, const int32_t* offsets, int segments, void* stream) {
+    uq_status s = check_mx(rows, K, fmt, segments);
+    if (s != UQ_OK) return s;
+    if ((s = check_tscale(fmt, tscale)) != UQ_OK) return s;
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    if ((offsets != nullptr) != (segments > 0)) return fail(UQ_ERR_INVALID, "offsets must be given exactly with segments");
+    if (rows == 0 || K == 0) return UQ_OK;
+    if (!codes || !scales || !out) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out) || !aligned16(offsets))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_dequant_mx(fmt, codes, scales, out, type, rows, K, tscale, offsets, segments, ds->sms,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled dequantization launch");
+}
+
+uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t* xscales, float tscale_x,
+                     const uint8_t* wcodes, const uint8_t* wscales, void* y, uq_dtype ytype, int M, int N, int K,
+                     uq_mx_fmt fmt, float alpha, void* stream) {
+    uq_status s = check_mx(M, K, fmt, 0);
+    if (s != UQ_OK) return s;
+    if (N < 0) return fail(UQ_ERR_INVALID, "negative N");
+    if ((s = check_tscale(fmt, tscale_x)) != UQ_OK) return s;
+    if (!valid_dtype(ytype)) return fail(UQ_ERR_INVALID, "unknown element type %d", ytype);
+    if (M == 0 || N == 0) return UQ_OK;
+    if (!y) return fail(UQ_ERR_INVALID, "y is NULL");
+    if (!aligned16(y)) return fail(UQ_ERR_ALIGN, "y must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (K == 0) {
+        e = cudaMemsetAsync(y, 0, (size_t)M * N * dtype_size(ytype), st);
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!wcodes || !wscales) return fail(UQ_ERR_INVALID, "wcodes or wscales is NULL");
+    if (!aligned16(wcodes) || !aligned16(wscales) || !aligned16(xscales))
+        return fail(UQ_ERR_ALIGN, "codes and scales must be 16-byte aligned");
+    if (xscales) {
+        if (!x) return fail(UQ_ERR_INVALID, "x is NULL");
+        if (!aligned16(x)) return fail(UQ_ERR_ALIGN, "codes and scales must be 16-byte aligned");
+    } else if ((s = check_quant_x(x, xtype, ldx, K)) != UQ_OK) {
+        return s;
+    }
+    DeviceState* ds = nullptr;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    uq::MxGemmArgs a = {};
+    const uint8_t* xcodes = static_cast<const uint8_t*>(x);
+    a.xscales = xscales;
+    a.alpha = alpha;
+    if (!xscales) {
+        const size_t code_bytes = ((size_t)M * (K / 2) + 255) / 256 * 256;
+        Workspace* ws = nullptr;
+        if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
+        uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
+        uint8_t* scales = codes + code_bytes;
+        e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, scales, M, K, tscale_x, nullptr, 0, nullptr, 0, ds->sms, st);
+        if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
+        xcodes = codes;
+        a.xscales = scales;
+        a.alpha = alpha * tscale_x;
+        a.wait = 1;
+    }
+    a.wscales = wscales;
+    a.y = y;
+    a.fault = ds->words;
+    a.ytype = ytype;
+    a.rows = M;
+    a.experts = 1;
+    a.N = N;
+    a.K = K;
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, ds->sms, st);
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled product launch");
+}
+
+uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, const uint8_t* wcodes,
+                             const uint8_t* wscales, const uint8_t* wcodes_up, const uint8_t* wscales_up,
+                             const int32_t* offsets, const float* alpha, const float* alpha_up, void* y, uq_dtype ytype,
+                             int rows, int experts, int N, int K, uq_mx_fmt fmt, void* stream) {
+    uq_status s = check_mx(rows, K, fmt, experts);
+    if (s != UQ_OK) return s;
+    if (N < 0) return fail(UQ_ERR_INVALID, "negative N");
+    if (experts < 1) return fail(UQ_ERR_INVALID, "experts must be at least 1");
+    if (!valid_dtype(ytype)) return fail(UQ_ERR_INVALID, "unknown element type %d", ytype);
+    if ((wcodes_up != nullptr) != (wscales_up != nullptr))
+        return fail(UQ_ERR_INVALID, "wcodes_up and wscales_up must be given together");
+    if (alpha_up && !wcodes_up) return fail(UQ_ERR_INVALID, "alpha_up needs wcodes_up");
+    if ((long long)experts * N > 0x7FFFFFFFll) return fail(UQ_ERR_UNSUPPORTED, "experts * N must be below 2^31");
+    if (rows == 0 || N == 0) return UQ_OK;
+    if (!y) return fail(UQ_ERR_INVALID, "y is NULL");
+    if (!aligned16(y)) return fail(UQ_ERR_ALIGN, "y must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (K == 0) {
+        e = cudaMemsetAsync(y, 0, (size_t)rows * N * dtype_size(ytype), st);
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!xcodes || !xscales || !wcodes || !wscales || !offsets) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(xcodes) || !aligned16(xscales) || !aligned16(wcodes) || !aligned16(wscales) || !aligned16(wcodes_up) ||
+        !aligned16(wscales_up) || !aligned16(offsets) || !aligned16(alpha) || !aligned16(alpha_up))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    uq::MxGemmArgs a = {};
+    a.xscales = xscales;
+    a.wscales = wscales;
+    a.wscales_up = wscales_up;
+    a.offsets = offsets;
+    a.alpha = 1.f;
+    a.alpha_e = alpha;
+    a.alpha_up = alpha_up;
+    a.y = y;
+    a.fault = ds->words;
+    a.ytype = ytype;
+    a.rows = rows;
+    a.experts = experts;
+    a.N = N;
+    a.K = K;
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, ds->sms, st);
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "grouped microscaled product launch");
+}
+
+// ---- expert routing ---------------------------------------------------------------------------
+namespace {
+uq_status check_routes(int T, int topk, int H, int experts) {
+    if (T < 0 || topk < 0 || H < 0) return fail(UQ_ERR_INVALID, "negative size T=%d topk=%d H=%d", T, topk, H);
+    if (experts < 1) return fail(UQ_ERR_INVALID, "experts must be at least 1");
+    if ((long long)T * topk > 0x7FFFFFFFll) return fail(UQ_ERR_INVALID, "%d x %d routes are too many", T, topk);
+    return UQ_OK;
+}
+}  // namespace
+
+uq_status uq_moe_sort(const int32_t* ids, int T, int topk, int experts, int32_t* order, int32_t* pos, int32_t* offsets,
+                      void* stream) {
+    uq_status s = check_routes(T, topk, 0, experts);
+    if (s != UQ_OK) return s;
+    if (experts > 1024) return fail(UQ_ERR_UNSUPPORTED, "at most 1024 experts (got %d)", experts);
+    const long long n = (long long)T * topk;
+    if (!offsets || (n && (!ids || !order || !pos))) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(ids) || !aligned16(order) || !aligned16(pos) || !aligned16(offsets))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    cudaError_t e = uq::launch_moe_sort(ids, n, experts, order, pos, offsets, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "route sort launch");
+}
+
+uq_status uq_moe_gather(const void* x, uq_dtype type, const int32_t* pos, const int32_t* offsets, int experts, void* xs,
+                        int T, int topk, int H, void* stream) {
+    uq_status s = check_routes(T, topk, H, experts);
+    if (s != UQ_OK) return s;
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    if (T == 0 || topk == 0 || H == 0) return UQ_OK;
+    if (!x || !pos || !offsets || !xs) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(x) || !aligned16(pos) || !aligned16(offsets) || !aligned16(xs))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_moe_gather(x, type, pos, offsets, experts, xs, T, topk, H, ds->sms,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "route gather launch");
+}
+
+static uq_status moe_combine(const void* ys, int type, const int32_t* pos, const float* weights, bool weighted, void* y,
+                             int T, int topk, int H, void* stream) {
+    uq_status s = check_routes(T, topk, H, 1);
+    if (s != UQ_OK) return s;
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    if (T == 0 || H == 0) return UQ_OK;
+    if (!y) return fail(UQ_ERR_INVALID, "null pointer");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (topk == 0) {
+        e = cudaMemsetAsync(y, 0, (size_t)T * H * dtype_size(type), st);
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!ys || !pos || (weighted && !weights)) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(ys) || !aligned16(pos) || !aligned16(weights) || !aligned16(y))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    e = uq::launch_moe_combine(ys, type, pos, weights, y, T, topk, H, ds->sms, st);
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "route combine launch");
+}
+
+uq_status uq_moe_gather_grad(const void* dxs, uq_dtype type, const int32_t* pos, void* dx, int T, int topk, int H,
+                             void* stream) {
+    return moe_combine(dxs, type, pos, nullptr, false, dx, T, topk, H, stream);
+}
+
+uq_status uq_moe_combine(const void* ys, uq_dtype type, const int32_t* pos, const float* weights, void* y, int T,
+                         int topk, int H, void* stream) {
+    return moe_combine(ys, type, pos, weights, true, y, T, topk, H, stream);
+}
+
+uq_status uq_moe_combine_grad(const void* dy, const void* ys, uq_dtype type, const int32_t* pos, const float* weights,
+                              const int32_t* offsets, int experts, void* dys, float* dweights, int T, int topk, int H,
+                              void* stream) {
+    uq_status s = check_routes(T, topk, H, experts);
+    if (s != UQ_OK) return s;
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    if (T == 0 || topk == 0) return UQ_OK;
+    if (!dweights || !pos || !weights || !offsets) return fail(UQ_ERR_INVALID, "null pointer");
+    if (H && (!dy || !ys || !dys)) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(dy) || !aligned16(ys) || !aligned16(pos) || !aligned16(weights) || !aligned16(offsets) ||
+        !aligned16(dys) || !aligned16(dweights))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_moe_combine_grad(dy, ys, type, pos, weights, offsets, experts, dys, dweights, T, topk, H,
+                                                ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "route combine gradient launch");
 }
 
 uq_status uq_device_fault(unsigned int* flag) {

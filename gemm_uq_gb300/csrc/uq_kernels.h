@@ -165,4 +165,48 @@ int tc_plan(int fmt, int mpad, int group, size_t* smem);   // dynamic shared mem
 cudaError_t launch_colsum32(const uint16_t* x, float* sx, int M, int mpad, int K, int ldx, cudaStream_t st);
 cudaError_t launch_tc(int fmt, const uint16_t* x, const TcArgs& a, size_t smem, int grid, cudaStream_t st);
 
+// microscaled 4-bit quantization (uq_mx_quant.cu)
+cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
+                               int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
+                               int topk, int sms, cudaStream_t st);
+cudaError_t launch_dequant_mx(int fmt, const uint8_t* codes, const uint8_t* scales, void* out, int type, int rows, int K,
+                              float tscale, const int32_t* offsets, int segments, int sms, cudaStream_t st);
+cudaError_t launch_pack_mx_scales(int fmt, const uint8_t* natural, uint8_t* tiles, int experts, int rows, int K,
+                                  cudaStream_t st);
+
+// product of microscaled 4-bit operands (uq_mx_gemm.cu)
+struct MxGemmArgs {
+    const uint8_t* xscales;   // scale tiles of x
+    const uint8_t* wscales;   // of the weight(s)
+    const uint8_t* wscales_up;
+    const int32_t* offsets;   // segments of x [experts + 1], NULL: one weight for all rows
+    const float* alpha_e;     // per expert, NULL = 1
+    const float* alpha_up;
+    void* y;                  // [rows][N]
+    unsigned int* fault;
+    float alpha;
+    int ytype, rows, experts, N, K;
+    int wait;                 // launched with programmatic serialization behind the kernel that writes x
+    // set by launch_mx_gemm:
+    int gated;                // silu(product) * (product with the up weight)
+    int steps;                // k steps
+    int ktiles;               // scale tiles along K
+    long long wscale_stride;  // bytes of one expert's scale tiles
+    int TN, NT, S, stages;    // tokens per tile, weight tiles, CTAs sharing K, ring stages
+    int tmem_cols;
+};
+cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up, MxGemmArgs a,
+                           int sms, cudaStream_t st);
+
+// expert routing (uq_moe.cu)
+cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* order, int32_t* pos, int32_t* offsets,
+                            cudaStream_t st);
+cudaError_t launch_moe_gather(const void* x, int type, const int32_t* pos, const int32_t* offsets, int E, void* xs, int T,
+                              int topk, int H, int sms, cudaStream_t st);
+cudaError_t launch_moe_combine(const void* ys, int type, const int32_t* pos, const float* weights, void* y, int T,
+                               int topk, int H, int sms, cudaStream_t st);   // weights NULL: plain sum
+cudaError_t launch_moe_combine_grad(const void* dy, const void* ys, int type, const int32_t* pos, const float* weights,
+                                    const int32_t* offsets, int E, void* dys, float* dw, int T, int topk, int H, int sms,
+                                    cudaStream_t st);
+
 }  // namespace uq

@@ -1,0 +1,334 @@
+// uq_moe.cu -- expert routing: the stable sort of routes by expert, the rows carried there and back with the router's
+// weights applied, and the gradients of both.
+//
+// All but the sort are memory-bound row copies: a token's row is read once and written to its topk places (or its
+// topk rows are read and one row is written), 16 bytes per lane where rows are 16-byte multiples, else element by
+// element.
+#include "uq_mx.cuh"
+
+namespace uq {
+
+namespace {
+
+// ---- sort --------------------------------------------------------------------------------------
+// One cluster of CTAs, each CTA a contiguous range of the routes, each warp a contiguous range of its CTA's, walked
+// in strips of 32.  Counting sort: (1) every warp counts its routes per expert (match.any groups equal ids; the
+// group's first lane adds the group's size); (2) per expert the warps' counts become exclusive prefixes, the CTAs'
+// totals are read through distributed shared memory, and a scan over the experts gives the offsets; (3) the warps
+// walk their strips again, and a route's row is its warp's running count plus its rank within its group.  The order
+// of the additions decides nothing: the result is the stable order.
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+    int v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.b32 %0, [a];\n\t}"
+                 : "=r"(v) : "r"(smem_u32(p)), "r"(rank) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const int32_t* __restrict__ ids, long long n, int E,
+                                                                int32_t* __restrict__ order, int32_t* __restrict__ pos,
+                                                                int32_t* __restrict__ offsets) {
+    extern __shared__ int sm[];
+    int* hist = sm;                             // [SORT_WARPS][E]
+    int* total = sm + SORT_WARPS * E;           // [E] this CTA's routes per expert
+    int* base = total + E;                      // [E + 1] first row of each expert, then of this CTA's routes of it
+    __shared__ int scan[SORT_WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const long long strips = (n + 31) / 32, workers = (long long)ctas * SORT_WARPS;
+    const long long w = (long long)rank * SORT_WARPS + warp;
+    const long long s0 = strips * w / workers, s1 = strips * (w + 1) / workers;
+    int* mine = hist + warp * E;
+
+    for (int i = tid; i < SORT_WARPS * E; i += SORT_THREADS) hist[i] = 0;
+    __syncthreads();
+    for (long long s = s0; s < s1; ++s) {
+        const long long i = s * 32 + lane;
+        int e = i < n ? __ldg(ids + i) : -1;
+        if (e < 0 || e >= E) e = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += SORT_THREADS) {
+        int sum = 0;
+        for (int v = 0; v < SORT_WARPS; ++v) {
+            const int c = hist[v * E + e];
+            hist[v * E + e] = sum;
+            sum += c;
+        }
+        total[e] = sum;
+    }
+    cluster_sync();
+    // E <= SORT_THREADS: thread e owns expert e
+    int all = 0, before = 0;
+    if (tid < E)
+        for (uint32_t r = 0; r < ctas; ++r) {
+            const int c = ld_cluster(total + tid, r);
+            if (r < rank) before += c;
+            all += c;
+        }
+    int incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        int v = scan[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        scan[lane] = v;
+    }
+    __syncthreads();
+    const int excl = incl - all + (warp ? scan[warp - 1] : 0);
+    const int kept = scan[SORT_WARPS - 1];
+    if (tid < E) {
+        base[tid] = excl + before;
+        if (rank == 0) offsets[tid] = excl;
+    }
+    if (rank == 0 && tid == 0) offsets[E] = kept;
+    __syncthreads();
+    for (long long s = s0; s < s1; ++s) {
+        const long long i = s * 32 + lane;
+        int e = i < n ? __ldg(ids + i) : -1;
+        if (e < 0 || e >= E) e = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e >= 0) row = base[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (i < n) pos[i] = row;
+        if (row >= 0) order[row] = (int)i;
+    }
+    for (long long r = kept + (long long)rank * SORT_THREADS + tid; r < n; r += (long long)ctas * SORT_THREADS) order[r] = -1;
+    cluster_sync();                             // no CTA leaves while another may read its totals
+}
+
+// ---- rows --------------------------------------------------------------------------------------
+// A unit is 32 lanes x U vectors of V elements of one row.
+template <class T, int V> struct Rows {
+    static constexpr int U = 2;
+    static constexpr int SPAN = 32 * V * U;     // elements of a row per warp unit
+};
+
+template <class T, int V>
+__global__ void __launch_bounds__(256) moe_gather_kernel(const T* __restrict__ x, const int32_t* __restrict__ pos,
+                                                         const int32_t* __restrict__ offsets, int E, T* __restrict__ xs,
+                                                         int T_, int topk, int H) {
+    using R = Rows<T, V>;
+    using VT = Vec<T, V>;
+    const int lane = threadIdx.x & 31;
+    const int chunks = (H + R::SPAN - 1) / R::SPAN;
+    const int rows = T_ * topk;
+    const int kept = min(max(__ldg(offsets + E), 0), rows);
+    const long long front = (long long)T_ * chunks, units = front + (long long)(rows - kept) * chunks;
+    for (long long u = blockIdx.x * 8LL + (threadIdx.x >> 5); u < units; u += gridDim.x * 8LL) {
+        const bool tail = u >= front;
+        const long long v = tail ? u - front : u;
+        const int row = (int)(v / chunks), h = (int)(v % chunks) * R::SPAN + lane * V;
+        VT a[R::U] = {};
+        if (!tail) {
+#pragma unroll
+            for (int i = 0; i < R::U; ++i)
+                if (h + i * 32 * V < H) a[i] = *reinterpret_cast<const VT*>(x + (long long)row * H + h + i * 32 * V);
+        }
+        for (int j = 0; j < (tail ? 1 : topk); ++j) {
+            const int dst = tail ? kept + row : __ldg(pos + (long long)row * topk + j);
+            if (dst < 0 || dst >= rows) continue;
+#pragma unroll
+            for (int i = 0; i < R::U; ++i)
+                if (h + i * 32 * V < H) *reinterpret_cast<VT*>(xs + (long long)dst * H + h + i * 32 * V) = a[i];
+        }
+    }
+}
+
+// y[t] = sum_j w_j * rows[pos[t][j]] (WEIGHTED) or sum_j rows[pos[t][j]]
+template <class T, int V, bool WEIGHTED>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const T* __restrict__ ys, const int32_t* __restrict__ pos,
+                                                          const float* __restrict__ weights, T* __restrict__ y, int T_,
+                                                          int topk, int H) {
+    using R = Rows<T, V>;
+    using VT = Vec<T, V>;
+    const int lane = threadIdx.x & 31;
+    const int chunks = (H + R::SPAN - 1) / R::SPAN;
+    const int rows = T_ * topk;
+    const long long units = (long long)T_ * chunks;
+    for (long long u = blockIdx.x * 8LL + (threadIdx.x >> 5); u < units; u += gridDim.x * 8LL) {
+        const int t = (int)(u / chunks), h = (int)(u % chunks) * R::SPAN + lane * V;
+        float acc[R::U][V] = {};
+        for (int j = 0; j < topk; ++j) {
+            const int src = __ldg(pos + (long long)t * topk + j);
+            if (src < 0 || src >= rows) continue;
+            const float w = WEIGHTED ? __ldg(weights + (long long)t * topk + j) : 1.f;
+#pragma unroll
+            for (int i = 0; i < R::U; ++i)
+                if (h + i * 32 * V < H) {
+                    const VT a = *reinterpret_cast<const VT*>(ys + (long long)src * H + h + i * 32 * V);
+#pragma unroll
+                    for (int c = 0; c < V; ++c) acc[i][c] = fmaf(w, to_f32(a.v[c]), acc[i][c]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < R::U; ++i)
+            if (h + i * 32 * V < H) {
+                VT a;
+#pragma unroll
+                for (int c = 0; c < V; ++c) a.v[c] = from_f32<T>(acc[i][c]);
+                *reinterpret_cast<VT*>(y + (long long)t * H + h + i * 32 * V) = a;
+            }
+    }
+}
+
+// One CTA per token (grid-stride): its row of dy against the topk rows of ys; then the rows nobody owns are zeroed.
+template <class T, int V>
+__global__ void __launch_bounds__(256) moe_combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ ys,
+                                                               const int32_t* __restrict__ pos,
+                                                               const float* __restrict__ weights,
+                                                               const int32_t* __restrict__ offsets, int E,
+                                                               T* __restrict__ dys, float* __restrict__ dw, int T_,
+                                                               int topk, int H) {
+    using VT = Vec<T, V>;
+    __shared__ float red[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = T_ * topk;
+    for (int t = blockIdx.x; t < T_; t += gridDim.x)
+        for (int j = 0; j < topk; ++j) {
+            const long long f = (long long)t * topk + j;
+            const int r = __ldg(pos + f);
+            const bool on = r >= 0 && r < rows;
+            float sum = 0.f;
+            if (on) {
+                const float w = __ldg(weights + f);
+                for (int h = threadIdx.x * V; h < H; h += 256 * V) {
+                    const VT g = *reinterpret_cast<const VT*>(dy + (long long)t * H + h);
+                    const VT a = *reinterpret_cast<const VT*>(ys + (long long)r * H + h);
+                    VT o;
+#pragma unroll
+                    for (int c = 0; c < V; ++c) {
+                        const float gf = to_f32(g.v[c]);
+                        sum = fmaf(gf, to_f32(a.v[c]), sum);
+                        o.v[c] = from_f32<T>(w * gf);
+                    }
+                    *reinterpret_cast<VT*>(dys + (long long)r * H + h) = o;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) red[warp] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float s = 0.f;
+                for (int v = 0; v < 8; ++v) s += red[v];
+                dw[f] = on ? s : 0.f;
+            }
+            __syncthreads();
+        }
+    const int kept = min(max(__ldg(offsets + E), 0), rows);
+    const VT zero = {};
+    for (int r = kept + blockIdx.x; r < rows; r += gridDim.x)
+        for (int h = threadIdx.x * V; h < H; h += 256 * V) *reinterpret_cast<VT*>(dys + (long long)r * H + h) = zero;
+}
+
+int row_grid(long long rows, int H, int span, int sms) {
+    const long long b = (rows * ((H + span - 1) / span) + 7) / 8, most = 64LL * sms;
+    return (int)(b < most ? (b < 1 ? 1 : b) : most);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* order, int32_t* pos, int32_t* offsets,
+                            cudaStream_t st) {
+    const size_t smem = ((size_t)SORT_WARPS * E + 2 * E + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+    int ctas = 1;                               // CTAs of the cluster: about four strips a warp before another is added
+    while (ctas < 8 && n > (long long)ctas * SORT_THREADS * 4) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(SORT_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_sort_kernel, ids, n, E, order, pos, offsets);
+}
+
+cudaError_t launch_moe_gather(const void* x, int type, const int32_t* pos, const int32_t* offsets, int E, void* xs, int T,
+                              int topk, int H, int sms, cudaStream_t st) {
+    return with_dtype(type, [&](auto t) {
+        using E_ = decltype(t);
+        constexpr int V = 16 / sizeof(E_);
+        const long long rows = T + (long long)T * topk / 8;
+        if (H % V == 0)
+            moe_gather_kernel<E_, V><<<row_grid(rows, H, Rows<E_, V>::SPAN, sms), 256, 0, st>>>(
+                static_cast<const E_*>(x), pos, offsets, E, static_cast<E_*>(xs), T, topk, H);
+        else
+            moe_gather_kernel<E_, 1><<<row_grid(rows, H, Rows<E_, 1>::SPAN, sms), 256, 0, st>>>(
+                static_cast<const E_*>(x), pos, offsets, E, static_cast<E_*>(xs), T, topk, H);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_moe_combine(const void* ys, int type, const int32_t* pos, const float* weights, void* y, int T,
+                               int topk, int H, int sms, cudaStream_t st) {
+    return with_dtype(type, [&](auto t) {
+        using E_ = decltype(t);
+        constexpr int V = 16 / sizeof(E_);
+        auto go = [&](auto kernel, int span) {
+            kernel<<<row_grid(T, H, span, sms), 256, 0, st>>>(static_cast<const E_*>(ys), pos, weights,
+                                                             static_cast<E_*>(y), T, topk, H);
+            return cudaGetLastError();
+        };
+        if (H % V == 0)
+            return weights ? go(moe_combine_kernel<E_, V, true>, Rows<E_, V>::SPAN)
+                           : go(moe_combine_kernel<E_, V, false>, Rows<E_, V>::SPAN);
+        return weights ? go(moe_combine_kernel<E_, 1, true>, Rows<E_, 1>::SPAN)
+                       : go(moe_combine_kernel<E_, 1, false>, Rows<E_, 1>::SPAN);
+    });
+}
+
+cudaError_t launch_moe_combine_grad(const void* dy, const void* ys, int type, const int32_t* pos, const float* weights,
+                                    const int32_t* offsets, int E, void* dys, float* dw, int T, int topk, int H, int sms,
+                                    cudaStream_t st) {
+    return with_dtype(type, [&](auto t) {
+        using E_ = decltype(t);
+        constexpr int V = 16 / sizeof(E_);
+        const int grid = T < 32 * sms ? T : 32 * sms;
+        auto go = [&](auto kernel) {
+            kernel<<<grid, 256, 0, st>>>(static_cast<const E_*>(dy), static_cast<const E_*>(ys), pos, weights, offsets, E,
+                                         static_cast<E_*>(dys), dw, T, topk, H);
+            return cudaGetLastError();
+        };
+        return H % V == 0 ? go(moe_combine_grad_kernel<E_, V>) : go(moe_combine_grad_kernel<E_, 1>);
+    });
+}
+
+}  // namespace uq

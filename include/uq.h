@@ -69,6 +69,20 @@ typedef enum uq_gguf_type {
     UQ_GGUF_Q8_0 = 1    /* 32 weights in 34 bytes: fp16 d, 32 signed bytes q; w = d * q */
 } uq_gguf_type;
 
+/* Element types of the calls that take more than one. */
+typedef enum uq_dtype {
+    UQ_BF16 = 0,
+    UQ_FP16 = 1,
+    UQ_FP32 = 2
+} uq_dtype;
+
+/* Microscaled 4-bit floating point: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit 3 the
+ * sign) and one scale byte per block of consecutive k. */
+typedef enum uq_mx_fmt {
+    UQ_MXFP4 = 0,       /* blocks of 32, scale 2^(byte - 127), byte 255 = NaN */
+    UQ_NVFP4 = 1        /* blocks of 16, scale an e4m3 value, times a caller's tensor scale */
+} uq_mx_fmt;
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* uq_status_string(uq_status s);
 
@@ -322,7 +336,8 @@ uq_status uq_gemm_kernel_count(int M, int N, int K, int group, uq_fmt fmt, int* 
  * one of uq_gemm and the one of uq_gemm_noalloc, OR-ed together (bit 0 / bit 1: a GEMV /
  * tensor-core kernel's bounded wait ran out and the kernel returned early instead of hanging;
  * its output is then unspecified; bit 2: a GEMV launch was given a work split larger than the
- * kernel holds and computed nothing; bit 3: uq_rmsnorm_rope met a position outside its table).  Synchronizes the device; allocates nothing.
+ * kernel holds and computed nothing; bit 3: uq_rmsnorm_rope met a position outside its table; bit 4: a
+ * microscaled product's bounded wait ran out).  Synchronizes the device; allocates nothing.
  * *flag = 0 when no fault.
  */
 uq_status uq_device_fault(unsigned int* flag);
@@ -365,6 +380,119 @@ uq_status uq_gemm_noalloc(const uint16_t* x, const void* wq, const void* scales,
  */
 uq_status uq_gemm_noalloc_scratch(int M, int N, int K, int group, uq_fmt fmt, size_t* ticket_bytes,
                                   size_t* partial_bytes);
+
+/*
+ * Microscaled 4-bit operands.  An operand of `rows` x K (K a multiple of 32) is
+ *   codes  uint8 [rows][K/2], two e2m1 codes per byte, low nibble = even k;
+ *   scales uint8, 512-byte tiles of 128 rows x 4 blocks, byte (r % 32) * 16 + (r / 32) * 4 + block, tiles
+ *          along k first (ceil(K / (4 * block)) of them), then along the rows.
+ * Rows sorted by expert are one operand in `segments` segments, given by int32 offsets[segments + 1] (device,
+ * non-decreasing, offsets[0] = 0; rows from offsets[segments] on belong to nobody): segment e starts at row
+ * tile offsets[e] / 128 + e.  uq_mx_scales_size gives the bytes.  Scale bytes of blocks past K inside the last
+ * tile along k must not be NaN codes (uq_quantize_mx and uq_pack_mx_scales write 0).
+ */
+
+/* uq_mx_scales_size -- bytes of the scales of an operand (segments = 0: no segments).  Host-only. */
+uq_status uq_mx_scales_size(int rows, int K, uq_mx_fmt fmt, int segments, size_t* bytes);
+
+/*
+ * uq_pack_mx_scales -- scale bytes as a checkpoint stores them, [experts][rows][K/block] (device) -> the tiles of
+ * each expert, one after the other (device, experts * uq_mx_scales_size(rows, K, fmt, 0) bytes, padding 0).
+ * Asynchronous.
+ */
+uq_status uq_pack_mx_scales(const uint8_t* natural, uint8_t* tiles, int experts, int rows, int K, uq_mx_fmt fmt,
+                            void* stream);
+
+/*
+ * uq_quantize_mx -- rows -> microscaled 4-bit operand.  Per block with absmax a:
+ *   UQ_MXFP4: e = clamp(floor(log2 a) - 2, -127, 127), byte e + 127 (0 for a = 0), code = e2m1(x * 2^-e);
+ *   UQ_NVFP4: s = e4m3(a / (6 * tscale)) (at most 448), code = e2m1(x / (s * tscale)), 0 where s is 0;
+ * e2m1() to the nearest value, ties to the even code, magnitudes over 6 to 6.  s * tscale and the quotients are
+ * fp32 operations.  A block that holds a NaN or an infinity gets the NaN scale: all of it reads back as NaN.
+ *   x (device) [rows][K] of xtype, rows ldx elements apart (ldx * size a multiple of 16 bytes)
+ *   codes, scales (device) written; tscale > 0 (1 for UQ_MXFP4)
+ *   offsets (device or NULL) int32 [segments + 1]: the operand is in segments
+ *   pos (device or NULL) int32 [rows][topk]: x is quantized once and its row t written to rows pos[t][j] of an
+ *   operand of rows * topk rows (entries outside it are skipped), i.e. gathered by expert; needs offsets.
+ * Rows that nothing points to are left unwritten.  Asynchronous.
+ */
+uq_status uq_quantize_mx(const void* x, uq_dtype xtype, long long ldx, uint8_t* codes, uint8_t* scales, int rows,
+                         int K, uq_mx_fmt fmt, float tscale, const int32_t* offsets, int segments,
+                         const int32_t* pos, int topk, void* stream);
+
+/*
+ * uq_dequant_mx -- the values a microscaled operand stands for, code * scale (* tscale), rounded once to `type`:
+ * out (device) [rows][K], written.  Rows from offsets[segments] on are written as zeros.  Asynchronous.
+ */
+uq_status uq_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* out, uq_dtype type, int rows, int K,
+                        uq_mx_fmt fmt, float tscale, const int32_t* offsets, int segments, void* stream);
+
+/*
+ * uq_gemm_mx -- y[m][n] = alpha * sum_k x^[m][k] * w^[n][k] with both operands microscaled, fp32 accumulation on
+ * the block-scaled tensor instructions, rounded once to ytype.
+ *   x: either of xtype, [M][K] with rows ldx apart, quantized in the call as uq_quantize_mx does with tscale_x
+ *      (xscales NULL; the operand lives in the per-stream workspace); or an operand's codes with xscales its scales
+ *      (xtype and ldx ignored)
+ *   wcodes, wscales (device): the weight as an operand of N rows; y (device) [M][N], written.
+ *   alpha: multiplied with the fp32 sum; it holds the operands' tensor scales that the caller wants applied (an x
+ *   quantized in the call has tscale_x applied besides).
+ * M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Every sum has a fixed order: equal calls give equal bits.
+ * Workspace and stream capture as uq_gemm.
+ */
+uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t* xscales, float tscale_x,
+                     const uint8_t* wcodes, const uint8_t* wscales, void* y, uq_dtype ytype, int M, int N, int K,
+                     uq_mx_fmt fmt, float alpha, void* stream);
+
+/*
+ * uq_gemm_mx_grouped -- the same product for rows sorted by expert: row r of segment e is multiplied with expert e's
+ * weight,  y[r][n] = alpha[e] * sum_k x^[r][k] * w^[e][n][k]; rows that belong to nobody are written as zeros.
+ * With wcodes_up: y[r][n] = silu(g) * u, g = alpha[e] * (the product with wcodes) and u = alpha_up[e] * (the product
+ * with wcodes_up), all in fp32, rounded once.
+ *   xcodes, xscales (device): an operand of `rows` rows in `experts` segments (offsets as there)
+ *   wcodes (device) [experts][N][K/2], wscales (device) the experts' scale tiles one after the other; wcodes_up and
+ *   wscales_up (device, or both NULL) likewise
+ *   alpha, alpha_up (device or NULL = 1) fp32 [experts]; y (device) [rows][N], written.
+ * No host synchronisation: the counts are read on the device.  Asynchronous.
+ */
+uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, const uint8_t* wcodes,
+                             const uint8_t* wscales, const uint8_t* wcodes_up, const uint8_t* wscales_up,
+                             const int32_t* offsets, const float* alpha, const float* alpha_up, void* y,
+                             uq_dtype ytype, int rows, int experts, int N, int K, uq_mx_fmt fmt, void* stream);
+
+/*
+ * Expert routing.  Token t takes topk routes (t, j), flat index t * topk + j, to experts ids[t][j]; a route whose
+ * id lies outside [0, experts) is dropped.  R = T * topk.
+ *
+ * uq_moe_sort -- a stable sort of the routes by expert (equal experts in order of their flat index):
+ *   offsets (device, int32 [experts + 1]): rows offsets[e] .. offsets[e + 1] are expert e's
+ *   pos (device, int32 [T][topk]): the row of each route, -1 if dropped
+ *   order (device, int32 [R]): the flat index of each row, -1 from row offsets[experts] on.
+ * 1 <= experts <= 1024, R < 2^31.  One launch, no atomics whose order could matter.  Asynchronous.
+ */
+uq_status uq_moe_sort(const int32_t* ids, int T, int topk, int experts, int32_t* order, int32_t* pos,
+                      int32_t* offsets, void* stream);
+
+/* uq_moe_gather -- xs[pos[t][j]] = x[t] for every route kept; rows from offsets[experts] on are zero.
+ * x (device) [T][H], xs (device) [R][H], both of `type`, written.  Asynchronous. */
+uq_status uq_moe_gather(const void* x, uq_dtype type, const int32_t* pos, const int32_t* offsets, int experts,
+                        void* xs, int T, int topk, int H, void* stream);
+
+/* uq_moe_gather_grad -- the gradient of uq_moe_gather: dx[t] = sum_j dxs[pos[t][j]], fp32 sums in order of j, rounded
+ * once; a token without a kept route gets zeros.  Asynchronous. */
+uq_status uq_moe_gather_grad(const void* dxs, uq_dtype type, const int32_t* pos, void* dx, int T, int topk, int H,
+                             void* stream);
+
+/* uq_moe_combine -- y[t] = sum_j weights[t][j] * ys[pos[t][j]] over the routes kept (fp32 weights and sums, in order of
+ * j, rounded once).  ys (device) [R][H], y (device) [T][H] of `type`.  Asynchronous. */
+uq_status uq_moe_combine(const void* ys, uq_dtype type, const int32_t* pos, const float* weights, void* y, int T,
+                         int topk, int H, void* stream);
+
+/* uq_moe_combine_grad -- the gradients of uq_moe_combine: dys[pos[t][j]] = weights[t][j] * dy[t] (rows that belong to
+ * nobody: zero) and dweights[t][j] = sum_h dy[t][h] * ys[pos[t][j]][h] in fp32 (0 for a dropped route).
+ * Asynchronous. */
+uq_status uq_moe_combine_grad(const void* dy, const void* ys, uq_dtype type, const int32_t* pos,
+                              const float* weights, const int32_t* offsets, int experts, void* dys, float* dweights,
+                              int T, int topk, int H, void* stream);
 
 #ifdef __cplusplus
 }
