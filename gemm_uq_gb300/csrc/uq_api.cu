@@ -867,6 +867,17 @@ uq_status check_tscale(int fmt, float t) {
 size_t mx_scales_bytes(int rows, int K, int fmt, int segments) {
     return (size_t)uq::mx_row_tiles(rows, segments) * uq::mx_ktiles(K, fmt) * 512;
 }
+// plans a product and points it at the stream's workspace
+uq_status mx_workspace(uq::MxGemmArgs& a, int fmt, bool gated, const DeviceState& ds, int dev, cudaStream_t st, size_t aux,
+                       Workspace** ws) {
+    size_t partials = 0, tickets = 0;
+    uq::mx_gemm_plan(fmt, gated, a, ds.sms, &partials, &tickets);
+    uq_status s = workspace(dev, st, partials, tickets, ws, aux);
+    if (s != UQ_OK) return s;
+    a.partials = (*ws)->partials;
+    a.tickets = (*ws)->tickets;
+    return UQ_OK;
+}
 uq_status check_quant_x(const void* x, int xtype, long long ldx, int K) {
     if (!valid_dtype(xtype)) return fail(UQ_ERR_INVALID, "unknown element type %d", xtype);
     if (!x) return fail(UQ_ERR_INVALID, "x is NULL");
@@ -967,21 +978,8 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     uq::MxGemmArgs a = {};
     const uint8_t* xcodes = static_cast<const uint8_t*>(x);
     a.xscales = xscales;
-    a.alpha = alpha;
-    if (!xscales) {
-        const size_t code_bytes = ((size_t)M * (K / 2) + 255) / 256 * 256;
-        Workspace* ws = nullptr;
-        if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
-        uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
-        uint8_t* scales = codes + code_bytes;
-        e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, scales, M, K, tscale_x, nullptr, 0, nullptr, 0, ds->sms, st);
-        if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
-        xcodes = codes;
-        a.xscales = scales;
-        a.alpha = alpha * tscale_x;
-        a.wait = 1;
-    }
     a.wscales = wscales;
+    a.alpha = alpha;
     a.y = y;
     a.fault = ds->words;
     a.ytype = ytype;
@@ -989,7 +987,22 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     a.experts = 1;
     a.N = N;
     a.K = K;
-    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, ds->sms, st);
+    // scratch of an x quantized here: codes | scale tiles
+    const size_t code_bytes = xscales ? 0 : ((size_t)M * (K / 2) + 255) / 256 * 256;
+    Workspace* ws = nullptr;
+    if ((s = mx_workspace(a, fmt, false, *ds, dev, st, code_bytes + (xscales ? 0 : mx_scales_bytes(M, K, fmt, 0)), &ws)) != UQ_OK)
+        return s;
+    if (!xscales) {
+        uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
+        e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, codes + code_bytes, M, K, tscale_x, nullptr, 0, nullptr, 0,
+                                   ds->sms, st);
+        if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
+        xcodes = codes;
+        a.xscales = codes + code_bytes;
+        a.alpha = alpha * tscale_x;
+        a.wait = 1;
+    }
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled product launch");
 }
 
@@ -1005,6 +1018,7 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     if ((wcodes_up != nullptr) != (wscales_up != nullptr))
         return fail(UQ_ERR_INVALID, "wcodes_up and wscales_up must be given together");
     if (alpha_up && !wcodes_up) return fail(UQ_ERR_INVALID, "alpha_up needs wcodes_up");
+    if (experts > 1024) return fail(UQ_ERR_UNSUPPORTED, "at most 1024 experts (got %d)", experts);
     if ((long long)experts * N > 0x7FFFFFFFll) return fail(UQ_ERR_UNSUPPORTED, "experts * N must be below 2^31");
     if (rows == 0 || N == 0) return UQ_OK;
     if (!y) return fail(UQ_ERR_INVALID, "y is NULL");
@@ -1020,7 +1034,8 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
         !aligned16(wscales_up) || !aligned16(offsets) || !aligned16(alpha) || !aligned16(alpha_up))
         return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
     DeviceState* ds = nullptr;
-    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
     uq::MxGemmArgs a = {};
     a.xscales = xscales;
     a.wscales = wscales;
@@ -1036,7 +1051,9 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     a.experts = experts;
     a.N = N;
     a.K = K;
-    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, ds->sms, st);
+    Workspace* ws = nullptr;
+    if ((s = mx_workspace(a, fmt, wcodes_up != nullptr, *ds, dev, st, 0, &ws)) != UQ_OK) return s;
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "grouped microscaled product launch");
 }
 
