@@ -867,15 +867,9 @@ uq_status check_tscale(int fmt, float t) {
 size_t mx_scales_bytes(int rows, int K, int fmt, int segments) {
     return (size_t)uq::mx_row_tiles(rows, segments) * uq::mx_ktiles(K, fmt) * 512;
 }
-// plans a product and points it at the stream's workspace
-uq_status mx_workspace(uq::MxGemmArgs& a, int fmt, bool gated, const DeviceState& ds, int dev, cudaStream_t st, size_t aux,
-                       Workspace** ws) {
-    size_t partials = 0, tickets = 0;
-    uq::mx_gemm_plan(fmt, gated, a, ds.sms, &partials, &tickets);
-    uq_status s = workspace(dev, st, partials, tickets, ws, aux);
-    if (s != UQ_OK) return s;
-    a.partials = (*ws)->partials;
-    a.tickets = (*ws)->tickets;
+uq_status check_tiles(int rows, int experts, int N) {
+    if (((long long)rows / 64 + experts) * ((N + 127) / 128) > 0x3FFFFFFF)
+        return fail(UQ_ERR_UNSUPPORTED, "%d x %d outputs are too many tiles", rows, N);
     return UQ_OK;
 }
 uq_status check_quant_x(const void* x, int xtype, long long ldx, int K) {
@@ -987,12 +981,12 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     a.experts = 1;
     a.N = N;
     a.K = K;
-    // scratch of an x quantized here: codes | scale tiles
-    const size_t code_bytes = xscales ? 0 : ((size_t)M * (K / 2) + 255) / 256 * 256;
-    Workspace* ws = nullptr;
-    if ((s = mx_workspace(a, fmt, false, *ds, dev, st, code_bytes + (xscales ? 0 : mx_scales_bytes(M, K, fmt, 0)), &ws)) != UQ_OK)
-        return s;
+    // an x quantized here lives in the workspace: codes | scale tiles
+    if ((s = check_tiles(M, 1, N)) != UQ_OK) return s;
     if (!xscales) {
+        const size_t code_bytes = ((size_t)M * (K / 2) + 255) / 256 * 256;
+        Workspace* ws = nullptr;
+        if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
         uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
         e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, codes + code_bytes, M, K, tscale_x, nullptr, 0, nullptr, 0,
                                    ds->sms, st);
@@ -1002,7 +996,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
         a.alpha = alpha * tscale_x;
         a.wait = 1;
     }
-    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, st);
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, ds->sms, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled product launch");
 }
 
@@ -1034,8 +1028,7 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
         !aligned16(wscales_up) || !aligned16(offsets) || !aligned16(alpha) || !aligned16(alpha_up))
         return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
     DeviceState* ds = nullptr;
-    int dev = 0;
-    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
     uq::MxGemmArgs a = {};
     a.xscales = xscales;
     a.wscales = wscales;
@@ -1051,9 +1044,8 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     a.experts = experts;
     a.N = N;
     a.K = K;
-    Workspace* ws = nullptr;
-    if ((s = mx_workspace(a, fmt, wcodes_up != nullptr, *ds, dev, st, 0, &ws)) != UQ_OK) return s;
-    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, st);
+    if ((s = check_tiles(rows, experts, N)) != UQ_OK) return s;
+    e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, ds->sms, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "grouped microscaled product launch");
 }
 

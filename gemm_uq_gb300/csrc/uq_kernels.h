@@ -187,18 +187,16 @@ struct MxGemmArgs {
     float alpha;
     int ytype, rows, experts, N, K;
     int wait;                 // launched with programmatic serialization behind the kernel that writes x
-    float* partials;          // [2 * ctas] fp32 sums of tiles cut between CTAs
-    unsigned int* tickets;    // per tile, zero between calls
-    // set by mx_gemm_plan:
+    // set by launch_mx_gemm:
     int steps;                // k steps
     int ktiles;               // scale tiles along K
-    long long wscale_stride;  // bytes of one expert's scale tiles
-    int TN, NT, accs, stages; // tokens per tile, weight tiles, accumulators, ring stages
+    int folded;               // codes come in boxes of two 128-byte columns
+    int TN, NT, S;            // tokens per tile, weight tiles, CTAs sharing a tile's steps
+    int accs, stages;         // accumulators, ring stages
     int tmem_cols, smem, ctas;
 };
-void mx_gemm_plan(int fmt, bool gated, MxGemmArgs& a, int sms, size_t* partial_bytes, size_t* ticket_bytes);
-cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up,
-                           const MxGemmArgs& a, cudaStream_t st);
+cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up, MxGemmArgs a,
+                           int sms, cudaStream_t st);
 
 // expert routing (uq_moe.cu)
 cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* order, int32_t* pos, int32_t* offsets,

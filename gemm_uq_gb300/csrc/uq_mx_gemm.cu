@@ -3,20 +3,22 @@
 //
 // The 128 lanes of the accumulator are rows of the weight, its columns are rows of x ("tokens"): a tile of few
 // tokens then costs few columns, whatever the count, and a batch of one streams the weight at full tile height.
-// Both operands come by TMA in the 128-byte-swizzled K-major layout, 256 k (128 bytes) of a row per step; the scale
-// tiles come by plain bulk copies and go from shared to tensor memory by tcgen05.cp, in order before the MMAs.
+// Both operands come by TMA in the 128-byte-swizzled K-major layout, 512 k of a row per step (two 128-byte columns in
+// one box where K allows); the scale tiles come by TMA too and go from shared to tensor memory by tcgen05.cp, in order
+// before the MMAs.
 // Nothing is unpacked: the instruction multiplies e2m1 codes and applies both scales.
 //
-// One persistent CTA per SM, 192 threads: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2..5 epilogue.
+// One persistent CTA per SM, 224 threads: warp 0 loads the weights, warp 6 the tokens, warp 1 allocates tensor memory and
+// issues the MMAs, warps 2..5 are the epilogue.
 // The work is a list of tiles (a weight tile of 128 rows, or the gate and the up tile of the same 128 outputs, x a
-// token tile of TN) of `steps` k steps each.  The ring of stages runs on across tiles, and two accumulators let the
-// epilogue of one tile run under the next one's MMAs.  Many tiles: CTA c takes whole tiles c, c + P, ...  Few tiles
-// (decode: the weights are streamed once and the time is the memory's): all steps in a row are cut into P equal
-// ranges, so every SM streams the same bytes; a tile cut between CTAs leaves fp32 partial sums, and the last of its
-// contributors adds them in CTA order, so that nobody waits and equal calls give equal bits.
+// token tile of TN) of `steps` k steps each; CTA c takes tiles c, c + P, ...  The ring of stages runs on across tiles,
+// and two accumulators let the epilogue of one tile run under the next one's MMAs.  Where tiles would fill at most half
+// of the SMs, a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through distributed shared memory
+// in rank order, so equal calls give equal bits.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is
 // freed, and the fault word tells.
 #include <cuda.h>
+#include <algorithm>
 
 #include "uq_mx.cuh"
 
@@ -24,49 +26,105 @@ namespace uq {
 
 namespace {
 
-constexpr int THREADS = 192;
-constexpr int STEP_K = 256;                     // k per stage: 128 bytes of a row, four MMAs of 64
+constexpr int THREADS = 224;
+constexpr int STEP_K = 512;                     // k per stage: two 128-byte columns of a row, eight MMAs of 64
+// The tensor maps of a launch.
+struct MxGemmMaps {
+    CUtensorMap w, x, w_scales, x_scales, up, up_scales;
+};
+
 constexpr int MAX_STAGES = 12;
 constexpr int HEAD = 1024;                      // barriers and flags before the stages
 
 // ---- PTX wrappers ------------------------------------------------------------------------------
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
+// The producer and the MMA warp run their loops as whole warps, so that every operand is a warp-uniform value, and the
+// elected lane issues (one lane in a divergent branch issued a tcgen05 instruction every ~120 cycles).
+#define UQ_ELECT "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e "
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
-// K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    return ((uint64_t)(addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
-// scale tile: 32 rows of 16 bytes, unswizzled, 8-row groups 128 bytes apart
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-    return ((uint64_t)(addr & 0x3FFFFu) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile(UQ_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes) : "memory");
 }
-// one 512-byte scale tile -> 4 tensor-memory columns, repeated in the four lane quarters
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
-}
+// Low words of the shared-memory descriptors (address in 16-byte units, bit 16 set); the high words are constants:
+// an operand is K-major with the 128-byte swizzle, 8-row groups 1024 bytes apart; a scale tile is 32 rows of 16 bytes,
+// unswizzled, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+#define UQ_OPERAND_HI "0x40004040"
+#define UQ_SCALES_HI "0x00004008"
+
+// The instructions that share a scale tile, issued by the elected lane of the converged warp: tcgen05.cp of the tile
+// of each operand (512 bytes -> 4 tensor-memory columns, repeated in the four lane quarters), then the MMAs.  MXFP4: a
+// tile's four blocks are 128 k, two MMAs (bytes 0-1 of the scale columns, then 2-3; the second one only if `two`);
+// NVFP4: 64 k, one MMA.  The operand descriptors advance by 32 bytes (2) per MMA.
+//   d accumulator, a / b low descriptor words, sa / sb the scale tiles', ca / cb the scale columns written, cu the scale
+//   column of B that is used, on: add to the accumulator (the first MMA's; the second always does).
 template <int FMT>
-__device__ __forceinline__ void mma_block_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                                 uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void issue_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t sa, uint32_t sb, uint32_t ca,
+                                           uint32_t cb, uint32_t cu, uint32_t idesc, uint32_t on, uint32_t two) {
     if constexpr (FMT == UQ_MXFP4)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+        asm volatile("{\n\t.reg .pred p, e, f, t;\n\t.reg .b64 da, db, sa, sb;\n\t.reg .b32 i2;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "mov.b64 sa, {%3, " UQ_SCALES_HI "};\n\tmov.b64 sb, {%4, " UQ_SCALES_HI "};\n\t"
+                     "or.b32 i2, %8, 0x40000020;\n\tsetp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, %8, %8;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 f, %10, 0, e;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], sa;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%6], sb;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %8, [%5], [%7], p;\n\t"
+                     "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+                     "@f tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%5], [%7], t;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(sa), "r"(sb), "r"(ca), "r"(cb), "r"(cu), "r"(idesc), "r"(on), "r"(two)
+                     : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db, sa, sb;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "mov.b64 sa, {%3, " UQ_SCALES_HI "};\n\tmov.b64 sb, {%4, " UQ_SCALES_HI "};\n\t"
+                     "setp.ne.b32 p, %9, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], sa;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%6], sb;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %8, [%5], [%7], p;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(sa), "r"(sb), "r"(ca), "r"(cb), "r"(cu), "r"(idesc), "r"(on)
+                     : "memory");
+}
+// the same for a second weight tile against the same tokens, whose scales are in place
+template <int FMT>
+__device__ __forceinline__ void issue_more(uint32_t d, uint32_t a, uint32_t b, uint32_t sa, uint32_t ca, uint32_t cu,
+                                           uint32_t idesc, uint32_t on, uint32_t two) {
+    if constexpr (FMT == UQ_MXFP4)
+        asm volatile("{\n\t.reg .pred p, e, f, t;\n\t.reg .b64 da, db, sa;\n\t.reg .b32 i2;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "mov.b64 sa, {%3, " UQ_SCALES_HI "};\n\t"
+                     "or.b32 i2, %6, 0x40000020;\n\tsetp.ne.b32 p, %7, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 f, %8, 0, e;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], sa;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %6, [%4], [%5], p;\n\t"
+                     "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+                     "@f tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%4], [%5], t;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(sa), "r"(ca), "r"(cu), "r"(idesc), "r"(on), "r"(two) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db, sa;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "mov.b64 sa, {%3, " UQ_SCALES_HI "};\n\t"
+                     "setp.ne.b32 p, %7, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], sa;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %6, [%4], [%5], p;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(sa), "r"(ca), "r"(cu), "r"(idesc), "r"(on) : "memory");
 }
 // Instruction descriptor: A and B e2m1, both K-major, M = 128, N = n, scales ue8m0 (MXFP4) or ue4m3; the scale
 // factor ids (which bytes of a scale column) are OR-ed in per instruction.
 template <int FMT> __device__ __forceinline__ uint32_t block_idesc(int n) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (FMT == UQ_MXFP4 ? 1u << 23 : 0u) | (1u << 27);
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(UQ_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -78,6 +136,27 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
+// A whole warp's wait: false for all lanes once any lane's wait ran out or the CTA was told to stop.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned int* fault, volatile int* abort_flag) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)),
+                                                                     parity, fault, FAULT_MX_WAIT));
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Tiles are numbered in groups of GROUP weight tiles, token tiles within a group, weight tiles fastest, so that CTAs
 // running at the same time share both operands' tiles in L2.
 constexpr int GROUP = 16;
@@ -113,48 +192,26 @@ __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before
     return t;
 }
 
-// The k steps [k0, k1) of a tile that a CTA takes next.
-struct Segment {
-    int tile, k0, k1;
-};
+// The tiles of a CTA and its k steps of them.
 struct Schedule {
-    long long u, u1, units;                     // split: this CTA's range of all steps
-    int tile, tiles, steps, ctas;
-    bool split;
+    int tile, tiles, stride, k0, k1;
     __device__ __forceinline__ Schedule(const MxGemmArgs& a, int tt_all) {
-        steps = a.steps;
         tiles = tt_all * a.NT;
-        ctas = gridDim.x;
-        const int waves = (tiles + ctas - 1) / ctas;
-        // whole tiles unless they would leave over 12 % of the SMs' time idle
-        split = (long long)tiles * 100 < (long long)waves * ctas * 88;
-        units = (long long)tiles * steps;
-        if (split && units < 2LL * ctas) ctas = units < 2 ? 1 : (int)(units / 2);
-        tile = blockIdx.x;
-        u = u1 = 0;
-        if (split && (int)blockIdx.x < ctas) {
-            u = begin(blockIdx.x);
-            u1 = begin(blockIdx.x + 1);
+        if (a.S > 1) {                          // one tile per cluster
+            const int rank = blockIdx.x % a.S;
+            tile = blockIdx.x / a.S;
+            stride = tiles;
+            k0 = a.steps * rank / a.S;
+            k1 = a.steps * (rank + 1) / a.S;
+        } else {
+            tile = blockIdx.x;
+            stride = gridDim.x;
+            k0 = 0;
+            k1 = a.steps;
         }
     }
-    __device__ __forceinline__ long long begin(int c) const { return units * c / ctas; }
-    __device__ __forceinline__ int owner(long long v) const { return (int)(((v + 1) * ctas - 1) / units); }
-    __device__ __forceinline__ bool next(Segment& s) {
-        if (!split) {
-            if (tile >= tiles) return false;
-            s.tile = tile;
-            s.k0 = 0;
-            s.k1 = steps;
-            tile += ctas;
-            return true;
-        }
-        if (u >= u1) return false;
-        s.tile = (int)(u / steps);
-        s.k0 = (int)(u - (long long)s.tile * steps);
-        s.k1 = (int)min((long long)steps, s.k0 + (u1 - u));
-        u += s.k1 - s.k0;
-        return true;
-    }
+    __device__ __forceinline__ bool more() const { return tile < tiles; }
+    __device__ __forceinline__ void advance() { tile += stride; }
 };
 
 __device__ __forceinline__ void store_one(const MxGemmArgs& a, long long at, float v) {
@@ -165,10 +222,9 @@ __device__ __forceinline__ void store_one(const MxGemmArgs& a, long long at, flo
 
 template <int FMT, int NA>
 __global__ void __launch_bounds__(THREADS, 1)
-mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap_up,
-               const __grid_constant__ CUtensorMap xmap, const MxGemmArgs a) {
+mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     constexpr int TPS = STEP_K / mx_tile_k(FMT);                   // scale tiles per step and 128 rows
-    constexpr int A_BYTES = 128 * 128, SF_BYTES = TPS * 512;
+    constexpr int A_BYTES = 128 * (STEP_K / 2), SF_BYTES = TPS * 512;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(head);            // [stages] operands and scales landed
@@ -178,38 +234,44 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     uint64_t* drain = acc_empty + 2;                               // after a timeout: the MMAs issued so far
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
-    int* last_flag = reinterpret_cast<int*>(tmem_ptr + 2);
     uint8_t* ring = head + HEAD;
     const int TN = a.TN, AB = a.accs;
-    const int b_bytes = TN * 128, stage_bytes = NA * A_BYTES + b_bytes + (NA + 1) * SF_BYTES;
+    const int b_bytes = TN * (STEP_K / 2), stage_bytes = NA * A_BYTES + b_bytes + (NA + 1) * SF_BYTES;
     int* before = reinterpret_cast<int*>(ring + (size_t)a.stages * stage_bytes);   // [experts + 1]
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-    // One stage = step kt of a tile: both operands' codes and scale tiles, counted in bytes on full[s].
+    // One stage = step kt of a tile: both operands' codes and scale tiles, counted in bytes on full[s].  Columns and
+    // scale tiles past K are filled with zeros.
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    auto load_codes = [&](uint32_t dst, const CUtensorMap* map, int row, int rows, int kt, uint32_t bar) {
+        if (a.folded) {
+            tma_3d(dst, map, 0, row, kt * 2, bar);
+        } else {
+            tma_2d(dst, map, kt * 256, row, bar);
+            tma_2d(dst + rows * 128, map, kt * 256 + 128, row, bar);
+        }
+    };
     auto load_weights = [&](const Tile& t, int kt, int s) {
-        uint8_t* st = ring + (size_t)s * stage_bytes;
-        const int tiles = min(TPS, a.ktiles - kt * TPS), n = t.nt * 128;
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(NA * A_BYTES + b_bytes + (NA + 1) * tiles * 512));
+        const uint32_t st = ring0 + s * stage_bytes, bar = full0 + s * 8;
+        expect_bytes(bar, NA * (A_BYTES + SF_BYTES));
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
-            tma_2d(st + i * A_BYTES, i ? &wmap_up : &wmap, kt * 128, t.expert * a.N + n, &full[s]);
-            bulk_g2s(st + NA * A_BYTES + b_bytes + i * SF_BYTES,
-                     (i ? a.wscales_up : a.wscales) + t.expert * a.wscale_stride + ((long long)t.nt * a.ktiles + kt * TPS) * 512,
-                     tiles * 512, &full[s]);
+            load_codes(st + i * A_BYTES, i ? &maps.up : &maps.w, t.expert * a.N + t.nt * 128, 128, kt, bar);
+            tma_3d(st + NA * A_BYTES + b_bytes + i * SF_BYTES, i ? &maps.up_scales : &maps.w_scales, 0, kt * TPS,
+                   t.expert * a.NT + t.nt, bar);
         }
     };
     auto load_tokens = [&](const Tile& t, int kt, int s) {
-        uint8_t* st = ring + (size_t)s * stage_bytes;
-        const int tiles = min(TPS, a.ktiles - kt * TPS);
-        const long long xtile = (a.offsets ? (long long)((t.row0 - t.first) >> 7) + t.expert : 0) + (t.first >> 7);
-        tma_2d(st + NA * A_BYTES, &xmap, kt * 128, t.row0, &full[s]);
-        bulk_g2s(st + NA * A_BYTES + b_bytes + NA * SF_BYTES, a.xscales + (xtile * a.ktiles + kt * TPS) * 512, tiles * 512,
-                 &full[s]);
+        const uint32_t st = ring0 + s * stage_bytes, bar = full0 + s * 8;
+        expect_bytes(bar, b_bytes + SF_BYTES);
+        load_codes(st + NA * A_BYTES, &maps.x, t.row0, TN, kt, bar);
+        tma_3d(st + NA * A_BYTES + b_bytes + NA * SF_BYTES, &maps.x_scales, 0, kt * TPS,
+               (a.offsets ? ((t.row0 - t.first) >> 7) + t.expert : 0) + (t.first >> 7), bar);
     };
 
-    int pre = 0;                                                   // stages whose weights are requested already
     if (warp == 0) {
+        if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
         if (a.offsets) {
             int run = 0;
             for (int e0 = 0; e0 < a.experts; e0 += 32) {
@@ -229,7 +291,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         }
         if (lane == 0) {
             for (int s = 0; s < a.stages; ++s) {
-                mbar_init(&full[s], 1);
+                mbar_init(&full[s], 2);
                 mbar_init(&empty[s], 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -240,112 +302,103 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             *abort_flag = 0;
             fence_barrier_init();
             fence_proxy_async_smem();
-            // The first stages' weights do not depend on the kernel before: requested ahead of everything else.
-            const int tt_all = a.offsets ? before[a.experts] : (a.rows + TN - 1) / TN;
-            Schedule sch(a, tt_all);
-            Segment g;
-            while (pre < a.stages && sch.next(g)) {
-                const Tile t = find_tile(a, before, tt_all, g.tile);
-                for (int kt = g.k0; kt < g.k1 && pre < a.stages; ++kt) load_weights(t, kt, pre++);
-            }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_u32(tmem_ptr)), "r"((uint32_t)a.tmem_cols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    fence_before();
     __syncthreads();
-    fence_after();
-    const uint32_t tmem = *tmem_ptr;
-    const uint32_t sf_col = tmem + AB * NA * TN;                   // scale columns, per stage
-    constexpr uint32_t SF_COLS = (NA + 1) * TPS * 4;
     const int tt_all = a.offsets ? before[a.experts] : (a.rows + TN - 1) / TN;
     Schedule sch(a, tt_all);
-    Segment g;
+    constexpr uint32_t SF_COLS = (NA + 1) * TPS * 4;               // scale columns of a stage
+    constexpr int TMEM_WARPS = 1 + 4;                              // warps that use tensor memory
+    uint32_t tmem = 0;
+    if (warp >= 1 && warp <= 5) {
+        if (warp == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         :: "r"(smem_u32(tmem_ptr)), "r"((uint32_t)a.tmem_cols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        fence_before();
+        asm volatile("bar.sync 1, %0;" :: "n"(TMEM_WARPS * 32) : "memory");
+        fence_after();
+        tmem = (uint32_t)uniform((int)*tmem_ptr);
+    }
 
-    if (warp == 0 && lane == 0) {
-        // ------------------------------------------------------------ producer
-        if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0 || warp == 6) {
+        // ------------------------------------------------------------ producers
+        // The weights do not depend on the kernel before, the tokens may.
+        const bool tokens = warp == 6;
+        if (tokens && a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
         int issued = 0, s = 0;
         uint32_t ph = 1;                                           // empty[] of the first round counts as free
         bool ok = true;
-        while (ok && sch.next(g)) {
-            const Tile t = find_tile(a, before, tt_all, g.tile);
-            for (int kt = g.k0; kt < g.k1; ++kt) {
-                if (issued >= pre) {
-                    if (*abort_flag || !mbar_wait_bounded(&empty[s], ph, a.fault, FAULT_MX_WAIT)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    load_weights(t, kt, s);
+        for (; ok && sch.more(); sch.advance()) {
+            Tile t = find_tile(a, before, tt_all, sch.tile);
+            t.row0 = uniform(t.row0);
+            t.expert = uniform(t.expert);
+            for (int kt = sch.k0; kt < sch.k1; ++kt) {
+                if (issued >= a.stages && !warp_wait(empty0 + s * 8, ph, a.fault, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                load_tokens(t, kt, s);
+                if (tokens) load_tokens(t, kt, s);
+                else load_weights(t, kt, s);
                 ++issued;
                 if (++s == a.stages) { s = 0; ph ^= 1; }
             }
         }
-        // let the last copies land before the CTA can leave
+        if (!ok) *abort_flag = 1;
+        // let the last copies land before the CTA can leave (bounded; after a timeout a stage may lack its other half)
         for (int j = issued - 1; j >= 0 && j >= issued - a.stages; --j)
             mbar_wait_bounded(&full[j % a.stages], (uint32_t)((j / a.stages) & 1), a.fault, FAULT_MX_WAIT);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
-        const uint32_t ring0 = smem_u32(ring);
+        constexpr int PER = FMT == UQ_MXFP4 ? 2 : 1;               // MMAs per scale tile
+        const uint32_t sf0 = tmem + AB * NA * TN;
         int s = 0, n = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (; ok && sch.next(g); ++n) {
-            const Tile t = find_tile(a, before, tt_all, g.tile);
-            const uint32_t idesc = block_idesc<FMT>((t.rows + 15) / 16 * 16);
-            const uint32_t xshift = (uint32_t)(t.first & 127) >> 5;   // first scale column of the tile inside its 128 rows
+        for (; ok && sch.more(); sch.advance(), ++n) {
+            const Tile t = find_tile(a, before, tt_all, sch.tile);
+            const uint32_t idesc = block_idesc<FMT>((uniform(t.rows) + 15) / 16 * 16);
+            const uint32_t xshift = (uint32_t)(uniform(t.first) & 127) >> 5;   // first scale column of the tile in its 128 rows
             const int buf = AB == 2 ? n & 1 : 0;
             const uint32_t acc = tmem + buf * NA * TN;
             // the epilogue has read this accumulator's tile before (its first use counts as read)
             const uint32_t aph = (uint32_t)((AB == 2 ? n >> 1 : n) & 1) ^ 1u;
-            if (!mbar_wait_bounded(&acc_empty[buf], aph, a.fault, FAULT_MX_WAIT)) ok = false;
+            if (!warp_wait(smem_u32(&acc_empty[buf]), aph, a.fault, abort_flag)) ok = false;
             fence_after();
             uint32_t on = 0;
-            for (int kt = g.k0; ok && kt < g.k1; ++kt) {
-                if (*abort_flag || !mbar_wait_bounded(&full[s], ph, a.fault, FAULT_MX_WAIT)) {
+            for (int kt = sch.k0; ok && kt < sch.k1; ++kt) {
+                if (!warp_wait(full0 + s * 8, ph, a.fault, abort_flag)) {
                     ok = false;
                     break;
                 }
                 fence_after();
-                const uint32_t st = ring0 + s * stage_bytes, sc = st + NA * A_BYTES + b_bytes;
-                const uint32_t col = sf_col + s * SF_COLS;
-                const int tiles = min(TPS, a.ktiles - kt * TPS);
+                const uint32_t st = ring0 + s * stage_bytes;
+                const uint32_t al = desc_lo(st), bl = al + NA * (A_BYTES >> 4), sl = bl + (b_bytes >> 4);
+                const uint32_t col = sf0 + s * SF_COLS, cb = col + NA * TPS * 4, cu = cb + xshift;
+                const int mmas = min(STEP_K / 64, (a.K - kt * STEP_K + 63) >> 6);
 #pragma unroll
                 for (int j = 0; j < TPS; ++j) {
-                    if (j >= tiles) break;
-#pragma unroll
-                    for (int i = 0; i <= NA; ++i)
-                        cp_scales(col + (i * TPS + j) * 4, scale_desc(sc + i * SF_BYTES + j * 512));
-                }
-                const int mmas = min(4, (a.K - kt * STEP_K + 63) >> 6);
-                const uint64_t bd = operand_desc(st + NA * A_BYTES);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q >= mmas) break;
-                    // MXFP4: two instructions share a scale tile (bytes 0-1, then 2-3); NVFP4: one tile each
-                    const int j = FMT == UQ_MXFP4 ? q >> 1 : q;
-                    const uint32_t id = FMT == UQ_MXFP4 ? (uint32_t)(q & 1) * 2 : 0u;
-                    const uint32_t desc = idesc | (id << 4) | (id << 29);
-#pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        mma_block_scaled<FMT>(acc + i * TN, operand_desc(st + i * A_BYTES) + 2 * q, bd + 2 * q, desc,
-                                              col + (i * TPS + j) * 4, col + (NA * TPS + j) * 4 + xshift, on);
+                    if (j * PER >= mmas) break;
+                    const int q = j * PER;                         // first MMA of the tile: column q / 4, 32-byte part q % 4
+                    const uint32_t ao = (q >> 2) * (16384 >> 4) + 2 * (q & 3), bo = bl + (q >> 2) * (TN * 8) + 2 * (q & 3);
+                    const uint32_t two = q + 1 < mmas;
+                    issue_tile<FMT>(acc, al + ao, bo, sl + j * 32, sl + NA * (SF_BYTES >> 4) + j * 32, col + j * 4, cb + j * 4,
+                                    cu + j * 4, idesc, on, two);
+                    if constexpr (NA == 2)
+                        issue_more<FMT>(acc + TN, al + (A_BYTES >> 4) + ao, bo, sl + (SF_BYTES >> 4) + j * 32,
+                                        col + (TPS + j) * 4, cu + j * 4, idesc, on, two);
                     on = 1;
                 }
-                commit(&empty[s]);
+                commit(empty0 + s * 8);
                 if (++s == a.stages) { s = 0; ph ^= 1; }
             }
-            commit(&acc_full[buf]);
+            commit(smem_u32(&acc_full[buf]));
         }
         if (!ok) {
             *abort_flag = 1;
-            commit(drain);
+            __syncwarp();
+            commit(smem_u32(drain));
             mbar_wait_bounded(drain, 0, a.fault, FAULT_MX_WAIT);
         }
     } else if (warp >= 2) {
@@ -362,32 +415,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             for (long long i = c0 + at * 16; i < c1; i += all * 16) *reinterpret_cast<uint4*>(y + i) = make_uint4(0, 0, 0, 0);
             for (long long i = c1 + at * 2; i < b1; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
         }
-        for (int n = 0; sch.next(g); ++n) {
-            const Tile t = find_tile(a, before, tt_all, g.tile);
+        for (int n = 0; sch.more(); sch.advance(), ++n) {
+            const Tile t = find_tile(a, before, tt_all, sch.tile);
             const int buf = AB == 2 ? n & 1 : 0;
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * NA * TN;
-            // after a timeout the segments are walked without waiting (the warps stay together at the barriers below)
+            // after a timeout the tiles are walked without waiting
             if (!*abort_flag &&
                 !mbar_wait_bounded(&acc_full[buf], (uint32_t)((AB == 2 ? n >> 1 : n) & 1), a.fault, FAULT_MX_WAIT))
                 *abort_flag = 1;
             __syncwarp();
             fence_after();
-            const bool whole = g.k0 == 0 && g.k1 == a.steps;
             const int nn = t.nt * 128 + row;
             const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
             const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
-            auto put = [&](int c, const float* v) {                // column c .. c + 15 of this lane's row, NA sums each
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float r = v[j] * al;
-                    if constexpr (NA == 2) r = silu_mul(r, v[16 + j] * au);
-                    if (nn < a.N && c + j < t.rows) store_one(a, (long long)(t.row0 + c + j) * a.N + nn, r);
-                }
-            };
-            const long long slot_floats = (long long)NA * TN * 128;
-            // the slot of a contributor's sums of this tile: its first tile, or its last
-            auto slot = [&](int c) { return a.partials + (2LL * c + (sch.begin(c) / sch.steps == g.tile ? 0 : 1)) * slot_floats; };
-            float* mine = whole ? nullptr : slot(blockIdx.x);
             for (int c = 0; c < t.rows; c += 16) {
                 uint32_t r[NA * 16];
 #pragma unroll
@@ -398,47 +438,55 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_empty[buf]);
                 }
-                float v[NA * 16];
+                if (a.S > 1) {
+                    // the MMAs are done with the ring: the sums are left there, [token][weight tile][row]
+                    float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-                for (int j = 0; j < NA * 16; ++j) v[j] = __uint_as_float(r[j]);
-                if (whole) {
-                    put(c, v);
-                } else {
+                    for (int j = 0; j < NA * 16; ++j)
+                        if (c + (j & 15) < t.rows) sums[((c + (j & 15)) * NA + (j >> 4)) * 128 + row] = __uint_as_float(r[j]);
+                } else if (nn < a.N) {
 #pragma unroll
-                    for (int j = 0; j < NA * 16; ++j) __stcg(mine + ((j >> 4) * TN + c + (j & 15)) * 128 + row, v[j]);
+                    for (int j = 0; j < 16; ++j) {
+                        float v = __uint_as_float(r[j]) * al;
+                        if constexpr (NA == 2) v = silu_mul(v, __uint_as_float(r[16 + j]) * au);
+                        if (c + j < t.rows) store_one(a, (long long)(t.row0 + c + j) * a.N + nn, v);
+                    }
                 }
-            }
-            if (whole) continue;
-            // the last contributor to arrive adds all contributors' sums, in CTA order
-            const long long v0 = (long long)g.tile * sch.steps;
-            const int c0 = sch.owner(v0), c1 = sch.owner(v0 + sch.steps - 1);
-            __threadfence();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (et == 0) {
-                const unsigned int before_me = atomicAdd(a.tickets + g.tile, 1u);
-                *last_flag = before_me == (unsigned)(c1 - c0);
-                if (*last_flag) a.tickets[g.tile] = 0;             // ready for the next call
-                __threadfence();
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (!*last_flag) continue;
-            for (int c = 0; c < t.rows; c += 16) {
-                float v[NA * 16] = {};
-                for (int k = c0; k <= c1; ++k) {
-                    const float* p = slot(k);
-#pragma unroll
-                    for (int j = 0; j < NA * 16; ++j) v[j] += __ldcg(p + ((j >> 4) * TN + c + (j & 15)) * 128 + row);
-                }
-                put(c, v);
             }
         }
     }
     __syncwarp();
+    // Tensor memory is given back before the cluster waits for its CTAs: one that holds it waits for nobody, so CTAs
+    // whose allocation waits for it always get it.
     fence_before();
     __syncthreads();
     fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"((uint32_t)a.tmem_cols) : "memory");
+    if (a.S > 1) {
+        cluster_sync();
+        const Schedule mine(a, tt_all);
+        if (mine.more()) {
+            const Tile t = find_tile(a, before, tt_all, mine.tile);
+            const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
+            const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
+            const uint32_t sums = ring0;
+            for (int it = (blockIdx.x % a.S) * THREADS + threadIdx.x; it < t.rows * 128; it += a.S * THREADS) {
+                const int c = it >> 7, r = it & 127, nn = t.nt * 128 + r;
+                if (nn >= a.N) continue;
+                float v = 0.f, u = 0.f;
+#pragma unroll 8
+                for (int k = 0; k < a.S; ++k) {
+                    v += ld_cluster(sums + (c * NA * 128 + r) * 4, k);
+                    if constexpr (NA == 2) u += ld_cluster(sums + ((c * NA + 1) * 128 + r) * 4, k);
+                }
+                v *= al;
+                if constexpr (NA == 2) v = silu_mul(v, u * au);
+                store_one(a, (long long)(t.row0 + c) * a.N + nn, v);
+            }
+        }
+        cluster_sync();                                            // no CTA leaves while another reads its sums
+    }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -456,19 +504,30 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// codes [rows][K/2] as bytes, boxes of 128 bytes x `box` rows, 128-byte swizzle
-bool codes_map(CUtensorMap* m, const uint8_t* codes, long long rows, int K, int box) {
-    cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)K / 2};
-    cuuint32_t b[2] = {128, (cuuint32_t)box};
-    cuuint32_t es[2] = {1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, b, es,
+// codes [rows][K/2] as bytes, 128-byte columns x `box` rows, 128-byte swizzle; folded (K a multiple of 256): the columns
+// are the third dimension and a box takes two of them
+bool codes_map(CUtensorMap* m, const uint8_t* codes, long long rows, int K, int box, bool folded) {
+    cuuint64_t dims[3] = {folded ? 128ull : (cuuint64_t)K / 2, (cuuint64_t)rows, (cuuint64_t)K / 256};
+    cuuint64_t strides[2] = {(cuuint64_t)K / 2, 128};
+    cuuint32_t b[3] = {128, (cuuint32_t)box, 2};
+    cuuint32_t es[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, folded ? 3 : 2, const_cast<uint8_t*>(codes), dims, strides, b, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// scale tiles [row tiles][ktiles][512 bytes], boxes of one row tile x one step's tiles
+bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int ktiles, int tps) {
+    cuuint64_t dims[3] = {64, (cuuint64_t)ktiles, (cuuint64_t)row_tiles};
+    cuuint64_t strides[2] = {512, (cuuint64_t)ktiles * 512};
+    cuuint32_t b[3] = {64, (cuuint32_t)tps, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 3, const_cast<uint8_t*>(scales), dims, strides, b, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT, int NA>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& up, const CUtensorMap& x, const MxGemmArgs& a, cudaStream_t st) {
+cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st) {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -484,53 +543,75 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& up, const CUtensorMa
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = a.smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (a.S > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = a.S;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (a.wait) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = a.wait ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NA>, w, up, x, a);
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NA>, maps, a);
 }
 
-}  // namespace
-
-// Tiles, ring and grid of one product, and the workspace it needs.
-void mx_gemm_plan(int fmt, bool gated, MxGemmArgs& a, int sms, size_t* partial_bytes, size_t* ticket_bytes) {
+// Tiles, ring and grid of one product.
+void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const int tps = STEP_K / mx_tile_k(fmt), NA = gated ? 2 : 1;
     a.steps = (a.K + STEP_K - 1) / STEP_K;
     a.ktiles = mx_ktiles(a.K, fmt);
-    a.wscale_stride = mx_row_tiles(a.N, 0) * a.ktiles * 512;
     // token tile: the rows an expert gets on average (all of them when there is one).  Under 64 only where no second
     // tile can follow: a tile's scale columns then always start at an even column.
     const int mean = a.offsets ? (a.rows + a.experts - 1) / a.experts : a.rows;
     a.TN = a.rows <= 16 ? 16 : (a.rows <= 32 ? 32 : (mean <= 64 ? 64 : 128));
     a.NT = (a.N + 127) / 128;
-    const int stage_bytes = NA * 16384 + a.TN * 128 + (NA + 1) * tps * 512;
+    // token tiles: exact, or the most that any counts give
+    const long long tt = a.offsets ? std::min((long long)a.rows, a.rows / a.TN + (long long)a.experts)
+                                   : (a.rows + a.TN - 1) / a.TN;
+    const long long tiles = tt * a.NT;
+    // CTAs per tile: the fewest that give each the fewest steps
+    a.S = 1;
+    const int most = tiles * 2 <= sms ? std::min(8, std::min((int)(sms / tiles), a.steps)) : 1;
+    for (int s = 2; s <= most; ++s)
+        if ((a.steps + s - 1) / s < (a.steps + a.S - 1) / a.S) a.S = s;
+    a.ctas = a.S > 1 ? (int)tiles * a.S : (int)std::min(tiles, (long long)sms);
+    a.folded = a.K % 256 == 0;
+    const int stage_bytes = NA * 128 * (STEP_K / 2) + a.TN * (STEP_K / 2) + (NA + 1) * tps * 512;
     const int table = a.offsets ? (a.experts + 1) * 4 : 0;
     // tensor memory: two accumulators where 512 columns hold them beside three stages of scales
     const int sf = (NA + 1) * tps * 4;
     a.accs = 2 * NA * a.TN + 3 * sf <= 512 ? 2 : 1;
-    a.stages = min(min((222 * 1024 - HEAD - table) / stage_bytes, MAX_STAGES), (512 - a.accs * NA * a.TN) / sf);
+    a.stages = std::min(std::min((222 * 1024 - HEAD - table) / stage_bytes, MAX_STAGES), (512 - a.accs * NA * a.TN) / sf);
     const int cols = a.accs * NA * a.TN + a.stages * sf;
     a.tmem_cols = cols <= 64 ? 64 : (cols <= 128 ? 128 : (cols <= 256 ? 256 : 512));
     a.smem = 1024 + HEAD + a.stages * stage_bytes + table;
-    a.ctas = sms;
-    *partial_bytes = (size_t)2 * sms * NA * a.TN * 128 * sizeof(float);
-    // tiles are split only below 88 % of some number of waves, so below 9 waves of them
-    *ticket_bytes = (size_t)9 * sms * sizeof(unsigned int);
 }
 
+}  // namespace
+
 cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up,
-                           const MxGemmArgs& a, cudaStream_t st) {
+                           MxGemmArgs a, int sms, cudaStream_t st) {
     if (!encode_fn()) return cudaErrorNotSupported;
-    CUtensorMap w, up, x;
-    if (!codes_map(&w, wcodes, (long long)a.experts * a.N, a.K, 128)) return cudaErrorInvalidValue;
-    up = w;
-    if (wcodes_up && !codes_map(&up, wcodes_up, (long long)a.experts * a.N, a.K, 128)) return cudaErrorInvalidValue;
-    if (!codes_map(&x, xcodes, a.rows, a.K, a.TN)) return cudaErrorInvalidValue;
-    if (fmt == UQ_MXFP4)
-        return wcodes_up ? launch<UQ_MXFP4, 2>(w, up, x, a, st) : launch<UQ_MXFP4, 1>(w, up, x, a, st);
-    return wcodes_up ? launch<UQ_NVFP4, 2>(w, up, x, a, st) : launch<UQ_NVFP4, 1>(w, up, x, a, st);
+    plan(fmt, wcodes_up != nullptr, a, sms);
+    MxGemmMaps m;
+    const int tps = STEP_K / mx_tile_k(fmt);
+    const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.NT;
+    bool ok = codes_map(&m.w, wcodes, wrows, a.K, 128, a.folded) && scales_map(&m.w_scales, a.wscales, wtiles, a.ktiles, tps) &&
+              codes_map(&m.x, xcodes, a.rows, a.K, a.TN, a.folded) &&
+              scales_map(&m.x_scales, a.xscales, mx_row_tiles(a.rows, a.offsets ? a.experts : 0), a.ktiles, tps);
+    m.up = m.w;
+    m.up_scales = m.w_scales;
+    if (wcodes_up)
+        ok = ok && codes_map(&m.up, wcodes_up, wrows, a.K, 128, a.folded) &&
+             scales_map(&m.up_scales, a.wscales_up, wtiles, a.ktiles, tps);
+    if (!ok) return cudaErrorInvalidValue;
+    if (fmt == UQ_MXFP4) return wcodes_up ? launch<UQ_MXFP4, 2>(m, a, st) : launch<UQ_MXFP4, 1>(m, a, st);
+    return wcodes_up ? launch<UQ_NVFP4, 2>(m, a, st) : launch<UQ_NVFP4, 1>(m, a, st);
 }
 
 }  // namespace uq

@@ -1,9 +1,12 @@
 // uq_mx_quant.cu -- microscaled 4-bit quantization of rows (optionally gathered by expert), its inverse, and the
 // packing of a checkpoint's scales into tiles.
 //
-// A lane holds 8 consecutive k (one 16-byte load of a 16-bit type), so a block is 4 lanes (MXFP4) or 2 (NVFP4) and a
-// warp step covers 256 k of one row: absmax by one or two shuffles, one 4-byte store of codes per lane, one 4-byte
-// store of scales per 4 blocks.  Memory-bound: each value is read once, whatever the number of rows it is written to.
+// A warp takes 1024 k of one row in four steps of 256, a lane 8 consecutive k of each (one 16-byte load of a 16-bit
+// type, all four requested before the first is used).  A block is then 4 lanes (MXFP4) or 2 (NVFP4): its absmax takes
+// one or two shuffles, the codes one 4-byte store per lane, the scales of 4 blocks one 4-byte store.  Memory-bound: each
+// value is read once, whatever the number of rows it is written to.
+#include <type_traits>
+
 #include "uq_mx.cuh"
 
 namespace uq {
@@ -11,111 +14,174 @@ namespace uq {
 namespace {
 
 constexpr int STEP_K = 256;                     // k of a row per warp step
+constexpr int STEPS = 4;
+constexpr int UNIT_K = STEP_K * STEPS;          // k of a row per warp
 
-// 8 values of a row at element offset k (16-byte aligned)
-template <class T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+// 8 values of a row, as loaded
+template <class T> struct Raw {
+    Vec<T, 16 / sizeof(T)> part[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) part[i] = reinterpret_cast<const Vec<T, 16 / sizeof(T)>*>(p)[i];
+    }
+    __device__ __forceinline__ float at(int i) const {
+        constexpr int V = 16 / sizeof(T);
+        return to_f32(part[i / V].v[i % V]);
+    }
+};
+
+// absmax of the 8 values as a bit pattern of fp32: infinities and NaN compare above all numbers
+template <class T> __device__ __forceinline__ uint32_t absmax8(const Raw<T>& x) {
     if constexpr (sizeof(T) == 2) {
-        const Vec<T, 8> a = *reinterpret_cast<const Vec<T, 8>*>(p);
+        // in packed 16-bit patterns: without the sign, their order as integers is the values' order
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+        uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(a.v[i]);
+        for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        const uint16_t h = (uint16_t)max(m & 0xFFFFu, m >> 16);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return (uint32_t)h << 16;
+        else return __float_as_uint(half_bits_f32(h));
     } else {
-        const Vec<T, 4> a = *reinterpret_cast<const Vec<T, 4>*>(p), b = *reinterpret_cast<const Vec<T, 4>*>(p + 4);
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a.v[i];
-            v[4 + i] = b.v[i];
-        }
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.at(i)) & 0x7FFFFFFFu);
+        return m;
     }
 }
 
 // codes of a lane's 8 values and the scale byte of its block (the block's lanes agree on it)
-template <int FMT> __device__ __forceinline__ uint32_t quantize8(float (&v)[8], float six_t, float tscale, uint32_t& byte) {
-    uint32_t am = 0;                            // absmax as a bit pattern: infinities and NaN compare above all numbers
-#pragma unroll
-    for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+template <int FMT, class T>
+__device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, float tscale, uint32_t& byte) {
+    uint32_t am = absmax8(x);
     am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    float v[8];
     if constexpr (FMT == UQ_MXFP4) {
         am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
         const int e = (int)(am >> 23);          // exponent field: floor(log2 a) + 127, 0 for zero and subnormals
         byte = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
         const float inv = __uint_as_float(e == 255 ? 0u : (254u - byte) << 23);    // 2^(127 - byte), a normal number
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= inv;                                   // exact: a power of two
+        for (int i = 0; i < 8; ++i) v[i] = x.at(i) * inv;                          // exact: a power of two
     } else {
         const bool bad = am >= 0x7F800000u;
         byte = bad ? 0x7Fu : e4m3_of(__fdiv_rn(__uint_as_float(am), six_t));
         const float d = e4m3_value(byte) * tscale;
         const bool zero = bad || !(d > 0.f);
-        // A real quotient, not a product with a reciprocal: x / d of a tie is exact, so ties are ties.
+        if constexpr (sizeof(T) == 2) {
+            // x / d as x * (1 / d) with one step of residual correction: a representable quotient comes out exact, so
+            // a tie is a tie; and an x of at most 11 bits over a d of 4 (times a power of two) is no closer to a tie
+            // than 2^-16, far more than the error left.
+            const float r = zero ? 0.f : __frcp_rn(d), nd = zero ? 0.f : -d;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = zero ? v[i] * 0.f : __fdiv_rn(v[i], d);
+            for (int i = 0; i < 8; ++i) {
+                const float q = x.at(i) * r;
+                v[i] = fmaf(fmaf(q, nd, x.at(i)), r, q);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = zero ? x.at(i) * 0.f : __fdiv_rn(x.at(i), d);
+        }
     }
     return e2m1_pack8(v);
 }
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(256) quantize_mx_kernel(const T* __restrict__ x, long long ldx, uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ x, long long ldx, uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales, int rows, int K, float tscale,
                                                           const int32_t* __restrict__ offsets, int segments,
                                                           const int32_t* __restrict__ pos, int topk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int LPB = FMT == UQ_MXFP4 ? 4 : 2;                 // lanes per block
+    constexpr int TPS = STEP_K / mx_tile_k(FMT);                 // scale tiles per step
     const int lane = threadIdx.x & 31;
-    const int chunks = (K + STEP_K - 1) / STEP_K, ktiles = mx_ktiles(K, FMT);
-    const long long units = (long long)rows * chunks;
+    const unsigned units_k = (unsigned)(K + UNIT_K - 1) / UNIT_K;
+    const int ktiles = mx_ktiles(K, FMT);
     const float six_t = 6.0f * tscale;
     const int total = offsets ? min(__ldg(offsets + segments), pos ? rows * topk : rows) : rows;
-    for (long long u = blockIdx.x * 8LL + (threadIdx.x >> 5); u < units; u += gridDim.x * 8LL) {
-        const int row = (int)(u / chunks), k = (int)(u % chunks) * STEP_K + lane * 8;
-        float v[8] = {};
-        if (k < K) load8(x + row * ldx + k, v);
-        uint32_t byte;
-        const uint32_t q = quantize8<FMT>(v, six_t, tscale, byte);
-        if (k >= K) byte = 0;
-        // the 4 scale bytes of this lane's scale tile, from the 4 blocks' first lanes
-        const int first = lane & ~(4 * LPB - 1);
-        uint32_t word = 0;
+    const unsigned long long units = (unsigned long long)rows * units_k;
+    for (unsigned long long u0 = blockIdx.x * 4ull + (threadIdx.x >> 5); u0 < units; u0 += gridDim.x * 4ull) {
+        const int row = units <= 0xFFFFFFFFull ? (int)((unsigned)u0 / units_k) : (int)(u0 / units_k);
+        const int k0 = (int)(u0 - (unsigned long long)row * units_k) * UNIT_K + lane * 8;
+        Raw<T> v[STEPS] = {};
+        const T* xr = x + row * ldx;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) word |= __shfl_sync(0xffffffffu, byte, first + b * LPB) << (8 * b);
-        const int kt = k / mx_tile_k(FMT);
-        const bool puts = lane == first && kt < ktiles;
+        for (int i = 0; i < STEPS; ++i)
+            if (k0 + i * STEP_K < K) v[i].load(xr + k0 + i * STEP_K);
+        uint32_t q[STEPS], word[STEPS];
+        const int first = lane & ~(4 * LPB - 1);                 // first lane of this lane's scale tile
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            uint32_t byte;
+            q[i] = quantize8<FMT>(v[i], six_t, tscale, byte);
+            if (k0 + i * STEP_K >= K) byte = 0;
+            word[i] = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) word[i] |= __shfl_sync(0xffffffffu, byte, first + b * LPB) << (8 * b);
+        }
+        const int kt0 = k0 / mx_tile_k(FMT);
         const int routes = pos ? topk : 1;
-        for (int j = 0; j < routes; ++j) {
-            const int dst = pos ? __ldg(pos + (long long)row * topk + j) : row;
-            if (dst < 0 || dst >= total) continue;
-            const long long srow = offsets ? mx_srow(offsets, segments, dst) : dst;
-            if (k < K) *reinterpret_cast<uint32_t*>(codes + (long long)dst * (K >> 1) + (k >> 1)) = q;
-            if (puts) *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(srow, kt * 4, ktiles)) = word;
+        for (int j0 = 0; j0 < routes; j0 += 32) {
+            // lane j finds the row of route j0 + j
+            int dst = -1;
+            long long srow = 0;
+            if (j0 + lane < routes) {
+                dst = pos ? __ldg(pos + (long long)row * topk + j0 + lane) : row;
+                if (dst >= total) dst = -1;
+                if (dst >= 0) srow = offsets ? mx_srow(offsets, segments, dst) : dst;
+            }
+            for (int j = 0; j < min(32, routes - j0); ++j) {
+                const int d = __shfl_sync(0xffffffffu, dst, j);
+                const long long sr = __shfl_sync(0xffffffffu, srow, j);
+                if (d < 0) continue;
+                uint8_t* c = codes + (long long)d * (K >> 1) + (k0 >> 1);
+                uint8_t* sc = scales + mx_scale_offset(sr, kt0 * 4, ktiles);
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    if (k0 + i * STEP_K < K) *reinterpret_cast<uint32_t*>(c + i * (STEP_K / 2)) = q[i];
+                    if (lane == first && kt0 + i * TPS < ktiles) *reinterpret_cast<uint32_t*>(sc + i * TPS * 512) = word[i];
+                }
+            }
         }
     }
 }
 
 template <class T, int FMT>
-__global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+__global__ void __launch_bounds__(128) dequant_mx_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                          T* __restrict__ out, int rows, int K, float tscale,
                                                          const int32_t* __restrict__ offsets, int segments) {
-    const int kw = K >> 3, ktiles = mx_ktiles(K, FMT);
-    const long long units = (long long)rows * kw;
+    const int lane = threadIdx.x & 31;
+    const unsigned units_k = (unsigned)(K + UNIT_K - 1) / UNIT_K;
+    const int ktiles = mx_ktiles(K, FMT);
     const int total = offsets ? min(__ldg(offsets + segments), rows) : rows;
-    for (long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x; u < units; u += gridDim.x * (long long)blockDim.x) {
-        const int row = (int)(u / kw), k = (int)(u % kw) * 8;
-        float v[8] = {};
+    const unsigned long long units = (unsigned long long)rows * units_k;
+    for (unsigned long long u0 = blockIdx.x * 4ull + (threadIdx.x >> 5); u0 < units; u0 += gridDim.x * 4ull) {
+        const int row = units <= 0xFFFFFFFFull ? (int)((unsigned)u0 / units_k) : (int)(u0 / units_k);
+        const int k0 = (int)(u0 - (unsigned long long)row * units_k) * UNIT_K + lane * 8;
+        uint32_t q[STEPS] = {}, b[STEPS] = {};
         if (row < total) {
             const long long srow = offsets ? mx_srow(offsets, segments, row) : row;
-            e2m1_unpack8(__ldg(reinterpret_cast<const uint32_t*>(codes) + u), v);
-            const uint32_t b = __ldg(scales + mx_scale_offset(srow, k / mx_block(FMT), ktiles));
-            const float s = FMT == UQ_MXFP4 ? e8m0_value(b) : e4m3_value(b) * tscale;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= s;
+            for (int i = 0; i < STEPS; ++i)
+                if (k0 + i * STEP_K < K) {
+                    q[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (long long)row * (K >> 1) + ((k0 + i * STEP_K) >> 1)));
+                    b[i] = __ldg(scales + mx_scale_offset(srow, (k0 + i * STEP_K) / mx_block(FMT), ktiles));
+                }
         }
-        constexpr int V = 16 / sizeof(T);
-        Vec<T, V>* o = reinterpret_cast<Vec<T, V>*>(out + (long long)row * K + k);
 #pragma unroll
-        for (int h = 0; h < 8 / V; ++h) {
-            Vec<T, V> t;
+        for (int i = 0; i < STEPS; ++i) {
+            if (k0 + i * STEP_K >= K) break;
+            float v[8];
+            e2m1_unpack8(q[i], v);
+            const float s = FMT == UQ_MXFP4 ? e8m0_value(b[i]) : e4m3_value(b[i]) * tscale;
+            constexpr int V = 16 / sizeof(T);
+            Vec<T, V>* o = reinterpret_cast<Vec<T, V>*>(out + (long long)row * K + k0 + i * STEP_K);
 #pragma unroll
-            for (int i = 0; i < V; ++i) t.v[i] = from_f32<T>(v[h * V + i]);
-            o[h] = t;
+            for (int h = 0; h < 8 / V; ++h) {
+                Vec<T, V> t;
+#pragma unroll
+                for (int c = 0; c < V; ++c) t.v[c] = from_f32<T>(v[h * V + c] * s);
+                o[h] = t;
+            }
         }
     }
 }
@@ -145,14 +211,14 @@ int grid_for(long long units, int per_block, int sms, int waves) {
 cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
                                int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
                                int topk, int sms, cudaStream_t st) {
-    const int grid = grid_for((long long)rows * ((K + STEP_K - 1) / STEP_K), 8, sms, 64);
+    const int grid = grid_for((long long)rows * ((K + UNIT_K - 1) / UNIT_K), 4, sms, 64);
     return with_dtype(xtype, [&](auto t) {
         using T = decltype(t);
         if (fmt == UQ_MXFP4)
-            quantize_mx_kernel<T, UQ_MXFP4><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
+            quantize_mx_kernel<T, UQ_MXFP4><<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
                                                                   tscale, offsets, segments, pos, topk);
         else
-            quantize_mx_kernel<T, UQ_NVFP4><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
+            quantize_mx_kernel<T, UQ_NVFP4><<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
                                                                   tscale, offsets, segments, pos, topk);
         return cudaGetLastError();
     });
@@ -160,14 +226,14 @@ cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx,
 
 cudaError_t launch_dequant_mx(int fmt, const uint8_t* codes, const uint8_t* scales, void* out, int type, int rows, int K,
                               float tscale, const int32_t* offsets, int segments, int sms, cudaStream_t st) {
-    const int grid = grid_for((long long)rows * (K >> 3), 256, sms, 64);
+    const int grid = grid_for((long long)rows * ((K + UNIT_K - 1) / UNIT_K), 4, sms, 64);
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
         if (fmt == UQ_MXFP4)
-            dequant_mx_kernel<T, UQ_MXFP4><<<grid, 256, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
+            dequant_mx_kernel<T, UQ_MXFP4><<<grid, 128, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
                                                                  offsets, segments);
         else
-            dequant_mx_kernel<T, UQ_NVFP4><<<grid, 256, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
+            dequant_mx_kernel<T, UQ_NVFP4><<<grid, 128, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
                                                                  offsets, segments);
         return cudaGetLastError();
     });

@@ -452,7 +452,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
  *   wcodes (device) [experts][N][K/2], wscales (device) the experts' scale tiles one after the other; wcodes_up and
  *   wscales_up (device, or both NULL) likewise
  *   alpha, alpha_up (device or NULL = 1) fp32 [experts]; y (device) [rows][N], written.
- * 1 <= experts <= 1024.  No host synchronisation: the counts are read on the device.  Workspace as uq_gemm.
+ * 1 <= experts <= 1024.  No host synchronisation: the counts are read on the device.  Asynchronous.
  */
 uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, const uint8_t* wcodes,
                              const uint8_t* wscales, const uint8_t* wcodes_up, const uint8_t* wscales_up,
