@@ -337,10 +337,28 @@ def device_fault() -> int:
 
 
 # ---- microscaled 4-bit operands: a pair (codes uint8 [..., rows, K/2], scales uint8 tiles) -------------------------
+# These calls are issued once or more per layer and token, so their marshalling is kept short: plain integers for
+# pointers and handles.
 
 MX_FORMATS = {"MXFP4": 0, "NVFP4": 1}
 MX_BLOCK = {"MXFP4": 32, "NVFP4": 16}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _at(t: torch.Tensor) -> int:
+    assert t.is_cuda and t.is_contiguous(), "tensors passed to uq must be contiguous CUDA tensors"
+    return t.data_ptr()
+
+
+def _at_opt(t):
+    return None if t is None else _at(t)
+
+
+def _handle(stream) -> int:
+    """The current stream's handle, without building a Stream object."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def mx_scales_size(rows: int, K: int, fmt: str, segments: int = 0) -> int:
@@ -350,22 +368,27 @@ def mx_scales_size(rows: int, K: int, fmt: str, segments: int = 0) -> int:
     return v.value
 
 
+def _scale_bytes(rows: int, K: int, fmt: str, segments: int = 0) -> int:
+    row_tiles = rows // 128 + segments if segments else (rows + 127) // 128
+    return row_tiles * (-(-K // (4 * MX_BLOCK[fmt]))) * 512
+
+
 def pack_mx_scales(scales: torch.Tensor, fmt: str, stream=None) -> torch.Tensor:
     """uq_pack_mx_scales: scale bytes [rows][K/block] or [experts][rows][K/block] -> tiles (of each expert)."""
     experts = scales.shape[0] if scales.dim() == 3 else 1
     rows, K = scales.shape[-2], scales.shape[-1] * MX_BLOCK[fmt]
     assert scales.dtype == torch.uint8
     tiles = torch.empty((experts, mx_scales_size(rows, K, fmt)), dtype=torch.uint8, device=scales.device)
-    _check(lib().uq_pack_mx_scales(_ptr(scales), _ptr(tiles), experts, rows, K, MX_FORMATS[fmt], _stream(stream)),
+    _check(lib().uq_pack_mx_scales(_at(scales), _at(tiles), experts, rows, K, MX_FORMATS[fmt], _handle(stream)),
            "uq_pack_mx_scales")
     return tiles if scales.dim() == 3 else tiles[0]
 
 
-def _rows(x: torch.Tensor):
-    """Pointer and row stride of a [rows][K] tensor whose rows are dense."""
-    assert x.is_cuda and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1), "x must be a CUDA matrix of dense rows"
-    ld = x.stride(0) if x.shape[0] > 1 else x.shape[1]
-    return ctypes.c_void_p(x.data_ptr()), ld
+def _row_stride(x: torch.Tensor, T: int, K: int) -> int:
+    """Row stride of a [T][K] tensor whose rows are dense."""
+    ld, one = x.stride()
+    assert x.is_cuda and (one == 1 or K <= 1), "x must be a CUDA matrix of dense rows"
+    return ld if T > 1 else K
 
 
 def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | None = None,
@@ -375,16 +398,20 @@ def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.T
     ``offsets`` (int32 [experts + 1]): the rows are sorted by expert; with ``pos`` (int32 [T][k]) they are gathered by
     expert on the way, as moe_gather would, and the operand has T*k rows."""
     T, K = x.shape
-    segments = 0 if offsets is None else offsets.numel() - 1
-    topk = 0 if pos is None else pos.shape[1]
-    assert offsets is None or offsets.dtype == torch.int32
-    assert pos is None or (pos.dtype == torch.int32 and pos.shape[0] == T)
-    rows = T if pos is None else T * topk
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(mx_scales_size(rows, K, fmt, segments), dtype=torch.uint8, device=x.device)
-    ptr, ld = _rows(x)
-    _check(lib().uq_quantize_mx(ptr, DTYPES[x.dtype], ld, _ptr(codes), _ptr(scales), T, K, MX_FORMATS[fmt], tscale,
-                                _ptr(offsets), segments, _ptr(pos), topk, _stream(stream)), "uq_quantize_mx")
+    rows, topk, segments, off, at = T, 0, 0, None, None
+    if offsets is not None:
+        assert offsets.dtype == torch.int32
+        segments, off = offsets.numel() - 1, _at(offsets)
+    if pos is not None:
+        assert pos.dtype == torch.int32 and pos.shape[0] == T
+        topk, at = pos.shape[1], _at(pos)
+        rows = T * topk
+    dev = x.device
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty(_scale_bytes(rows, K, fmt, segments), dtype=torch.uint8, device=dev)
+    _check(lib().uq_quantize_mx(x.data_ptr(), DTYPES[x.dtype], _row_stride(x, T, K), codes.data_ptr(), scales.data_ptr(),
+                                T, K, MX_FORMATS[fmt], tscale, off, segments, at, topk, _handle(stream)),
+           "uq_quantize_mx")
     return codes, scales
 
 
@@ -392,13 +419,15 @@ def dequant_mx(q: tuple, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | 
                dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """uq_dequant_mx: the values (codes, scales) stand for, [rows][K] of ``dtype``."""
     codes, scales = q
-    rows, K = codes.shape[0], codes.shape[1] * 2
-    segments = 0 if offsets is None else offsets.numel() - 1
-    assert offsets is None or offsets.dtype == torch.int32
-    assert scales.numel() >= mx_scales_size(rows, K, fmt, segments)
-    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
-    _check(lib().uq_dequant_mx(_ptr(codes), _ptr(scales), _ptr(out), DTYPES[dtype], rows, K, MX_FORMATS[fmt], tscale,
-                               _ptr(offsets), segments, _stream(stream)), "uq_dequant_mx")
+    rows, half = codes.shape
+    segments, off = 0, None
+    if offsets is not None:
+        assert offsets.dtype == torch.int32
+        segments, off = offsets.numel() - 1, _at(offsets)
+    assert scales.numel() >= _scale_bytes(rows, half * 2, fmt, segments)
+    out = torch.empty((rows, half * 2), dtype=dtype, device=codes.device)
+    _check(lib().uq_dequant_mx(_at(codes), _at(scales), out.data_ptr(), DTYPES[dtype], rows, half * 2, MX_FORMATS[fmt],
+                               tscale, off, segments, _handle(stream)), "uq_dequant_mx")
     return out
 
 
@@ -409,24 +438,25 @@ def gemm_mx(x, w: tuple, fmt: str, tscale: float = 1.0, alpha: float = 1.0, dtyp
     ``x``: a matrix (bf16, fp16 or fp32), quantized in the call with ``tscale``, or a pair (codes, scales) of
     quantize_mx.  ``w``: (codes [N][K/2], scales).  The result has ``dtype`` (default: x's, bf16 for a pair)."""
     wcodes, wscales = w
-    N, K = wcodes.shape[0], wcodes.shape[1] * 2
-    assert wcodes.dtype == torch.uint8 and wscales.dtype == torch.uint8
-    assert wscales.numel() >= mx_scales_size(N, K, fmt)
+    N, half = wcodes.shape
+    K = half * 2
+    assert wcodes.dtype == torch.uint8 and wscales.dtype == torch.uint8 and wscales.numel() >= _scale_bytes(N, K, fmt)
     if isinstance(x, torch.Tensor):
-        assert x.shape[1] == K, "x and w have different K"
-        M, xtype, xscales = x.shape[0], DTYPES[x.dtype], None
-        xptr, ld = _rows(x)
-        out = x.dtype
+        M, xk = x.shape
+        xtype, xptr, xsc, ld = DTYPES[x.dtype], x.data_ptr(), None, _row_stride(x, M, K)
+        if dtype is None:
+            dtype = x.dtype
     else:
         xcodes, xscales = x
-        assert xcodes.shape[1] * 2 == K, "x and w have different K"
-        M, xtype, xptr, ld, out = xcodes.shape[0], 0, _ptr(xcodes), 0, torch.bfloat16
-        assert xscales.numel() >= mx_scales_size(M, K, fmt)
+        M, xk = xcodes.shape[0], xcodes.shape[1] * 2
+        assert xscales.numel() >= _scale_bytes(M, K, fmt)
+        xtype, xptr, xsc, ld = 0, _at(xcodes), _at(xscales), 0
+    assert xk == K, "x and w have different K"
     if y is None:
-        y = torch.empty((M, N), dtype=dtype or out, device=wcodes.device)
+        y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=wcodes.device)
     assert y.shape == (M, N)
-    _check(lib().uq_gemm_mx(xptr, xtype, ld, _ptr(xscales), tscale, _ptr(wcodes), _ptr(wscales), _ptr(y),
-                            DTYPES[y.dtype], M, N, K, MX_FORMATS[fmt], alpha, _stream(stream)), "uq_gemm_mx")
+    _check(lib().uq_gemm_mx(xptr, xtype, ld, xsc, tscale, _at(wcodes), _at(wscales), _at(y), DTYPES[y.dtype], M, N, K,
+                            MX_FORMATS[fmt], alpha, _handle(stream)), "uq_gemm_mx")
     return y
 
 
@@ -438,21 +468,25 @@ def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tup
     ``x``: (codes, scales) of quantize_mx with these ``offsets``; ``w`` (and ``up``: silu(x w^T) * (x up^T)): codes
     [experts][N][K/2] and the experts' scale tiles; ``alpha``, ``alpha_up``: fp32 [experts]."""
     (xcodes, xscales), (wcodes, wscales) = x, w
-    ucodes, uscales = up if up is not None else (None, None)
-    E, N, K = wcodes.shape[0], wcodes.shape[1], wcodes.shape[2] * 2
-    R = xcodes.shape[0]
-    assert xcodes.shape[1] * 2 == K, "x and w have different K"
+    E, N, half = wcodes.shape
+    K, R = half * 2, xcodes.shape[0]
+    assert xcodes.shape[1] == half, "x and w have different K"
     assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
-    assert xscales.numel() >= mx_scales_size(R, K, fmt, E) and wscales.numel() >= E * mx_scales_size(N, K, fmt)
-    assert up is None or (ucodes.shape == wcodes.shape and uscales.numel() >= E * mx_scales_size(N, K, fmt))
-    assert all(v is None or (v.dtype == torch.float32 and v.numel() == E) for v in (alpha, alpha_up))
+    wbytes = E * _scale_bytes(N, K, fmt)
+    assert xscales.numel() >= _scale_bytes(R, K, fmt, E) and wscales.numel() >= wbytes
+    uc = us = None
+    if up is not None:
+        ucodes, uscales = up
+        assert ucodes.shape == wcodes.shape and uscales.numel() >= wbytes
+        uc, us = _at(ucodes), _at(uscales)
+    for v in (alpha, alpha_up):
+        assert v is None or (v.dtype == torch.float32 and v.numel() == E)
     if y is None:
         y = torch.empty((R, N), dtype=dtype, device=xcodes.device)
     assert y.shape == (R, N)
-    _check(lib().uq_gemm_mx_grouped(_ptr(xcodes), _ptr(xscales), _ptr(wcodes), _ptr(wscales), _ptr(ucodes),
-                                    _ptr(uscales), _ptr(offsets), _ptr(alpha), _ptr(alpha_up), _ptr(y),
-                                    DTYPES[y.dtype], R, E, N, K, MX_FORMATS[fmt], _stream(stream)),
-           "uq_gemm_mx_grouped")
+    _check(lib().uq_gemm_mx_grouped(_at(xcodes), _at(xscales), _at(wcodes), _at(wscales), uc, us, _at(offsets),
+                                    _at_opt(alpha), _at_opt(alpha_up), _at(y), DTYPES[y.dtype], R, E, N, K,
+                                    MX_FORMATS[fmt], _handle(stream)), "uq_gemm_mx_grouped")
     return y
 
 
@@ -462,54 +496,55 @@ def moe_sort(ids: torch.Tensor, experts: int, stream=None):
     """uq_moe_sort: int32 expert ids [T][k] -> (order int32 [T*k], pos int32 [T][k], offsets int32 [experts + 1])."""
     T, k = ids.shape
     assert ids.dtype == torch.int32
-    order = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-    _check(lib().uq_moe_sort(_ptr(ids), T, k, experts, _ptr(order), _ptr(pos), _ptr(offsets), _stream(stream)),
-           "uq_moe_sort")
+    dev = ids.device
+    order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=dev)
+    _check(lib().uq_moe_sort(_at(ids), T, k, experts, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
+                             _handle(stream)), "uq_moe_sort")
     return order, pos, offsets
 
 
 def moe_gather(x: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
     """uq_moe_gather: xs[pos[t][j]] = x[t], [T*k][H]; rows past offsets[-1] are zero."""
-    (T, H), k = x.shape, pos.shape[1]
-    assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and pos.shape[0] == T
+    (T, H), (rows, k) = x.shape, pos.shape
+    assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and rows == T
     xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    _check(lib().uq_moe_gather(_ptr(x), DTYPES[x.dtype], _ptr(pos), _ptr(offsets), offsets.numel() - 1, _ptr(xs), T, k,
-                               H, _stream(stream)), "uq_moe_gather")
+    _check(lib().uq_moe_gather(_at(x), DTYPES[x.dtype], _at(pos), _at(offsets), offsets.numel() - 1, xs.data_ptr(), T, k,
+                               H, _handle(stream)), "uq_moe_gather")
     return xs
 
 
 def moe_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, stream=None) -> torch.Tensor:
     """uq_moe_gather_grad: dx[t] = sum_j dxs[pos[t][j]], [T][H]."""
-    (T, k), H = pos.shape, dxs.shape[1]
-    assert pos.dtype == torch.int32 and dxs.shape[0] == T * k
+    (T, k), (R, H) = pos.shape, dxs.shape
+    assert pos.dtype == torch.int32 and R == T * k
     dx = torch.empty((T, H), dtype=dxs.dtype, device=dxs.device)
-    _check(lib().uq_moe_gather_grad(_ptr(dxs), DTYPES[dxs.dtype], _ptr(pos), _ptr(dx), T, k, H, _stream(stream)),
+    _check(lib().uq_moe_gather_grad(_at(dxs), DTYPES[dxs.dtype], _at(pos), dx.data_ptr(), T, k, H, _handle(stream)),
            "uq_moe_gather_grad")
     return dx
 
 
 def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stream=None) -> torch.Tensor:
     """uq_moe_combine: y[t] = sum_j weights[t][j] * ys[pos[t][j]], [T][H]; weights fp32 [T][k]."""
-    (T, k), H = pos.shape, ys.shape[1]
+    (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and weights.dtype == torch.float32
-    assert ys.shape[0] == T * k and weights.shape == pos.shape
+    assert R == T * k and weights.shape == pos.shape
     y = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
-    _check(lib().uq_moe_combine(_ptr(ys), DTYPES[ys.dtype], _ptr(pos), _ptr(weights), _ptr(y), T, k, H,
-                                _stream(stream)), "uq_moe_combine")
+    _check(lib().uq_moe_combine(_at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), y.data_ptr(), T, k, H,
+                                _handle(stream)), "uq_moe_combine")
     return y
 
 
 def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
                      offsets: torch.Tensor, stream=None):
     """uq_moe_combine_grad: (dys [T*k][H], dweights fp32 [T][k]) of moe_combine for the output gradient dy [T][H]."""
-    (T, k), H = pos.shape, ys.shape[1]
+    (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and weights.dtype == torch.float32
-    assert dy.dtype == ys.dtype and dy.shape == (T, H) and ys.shape[0] == T * k and weights.shape == pos.shape
+    assert dy.dtype == ys.dtype and dy.shape == (T, H) and R == T * k and weights.shape == pos.shape
     dys = torch.empty_like(ys)
     dw = torch.empty((T, k), dtype=torch.float32, device=ys.device)
-    _check(lib().uq_moe_combine_grad(_ptr(dy), _ptr(ys), DTYPES[ys.dtype], _ptr(pos), _ptr(weights), _ptr(offsets),
-                                     offsets.numel() - 1, _ptr(dys), _ptr(dw), T, k, H, _stream(stream)),
+    _check(lib().uq_moe_combine_grad(_at(dy), _at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), _at(offsets),
+                                     offsets.numel() - 1, dys.data_ptr(), dw.data_ptr(), T, k, H, _handle(stream)),
            "uq_moe_combine_grad")
     return dys, dw
