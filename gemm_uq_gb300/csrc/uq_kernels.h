@@ -191,7 +191,10 @@ struct MxGemmArgs {
     int steps;                // k steps
     int ktiles;               // scale tiles along K
     int folded;               // codes come in boxes of two 128-byte columns
+    int pair;                 // pairs of CTAs (256 x 256 tiles)
     int TN, NT, S;            // tokens per tile, weight tiles, CTAs sharing a tile's steps
+    int group;                // weight tiles that are numbered together
+    int row_tiles;            // scale tiles of 128 rows of one expert's weight
     int accs, stages;         // accumulators, ring stages
     int tmem_cols, smem, ctas;
 };

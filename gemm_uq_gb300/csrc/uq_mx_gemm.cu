@@ -157,9 +157,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigne
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Tiles are numbered in groups of GROUP weight tiles, token tiles within a group, weight tiles fastest, so that CTAs
+// Tiles are numbered in groups of a.group weight tiles, token tiles within a group, weight tiles fastest, so that CTAs
 // running at the same time share both operands' tiles in L2.
-constexpr int GROUP = 16;
 
 struct Tile {
     int expert, nt;                             // weight tile nt of this expert
@@ -170,10 +169,10 @@ __device__ __forceinline__ int offset_of(const MxGemmArgs& a, int e) { return mi
 // `before`: token tiles before each expert (shared memory, experts + 1 entries), unused when there is one weight
 __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before, int tt_all, int tile) {
     Tile t;
-    const int per = GROUP * tt_all, g = tile / per, in = tile - g * per;
-    const int width = min(GROUP, a.NT - g * GROUP);
+    const int per = a.group * tt_all, g = tile / per, in = tile - g * per;
+    const int width = min(a.group, a.NT - g * a.group);
     const int tt = in / width;
-    t.nt = g * GROUP + in - tt * width;
+    t.nt = g * a.group + in - tt * width;
     int e = 0, r0 = 0, r1 = a.rows, lt = tt;
     if (a.offsets) {
         int hi = a.experts;
@@ -190,6 +189,37 @@ __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before
     t.row0 = r0 + t.first;
     t.rows = min(a.TN, r1 - t.row0);
     return t;
+}
+
+// Fills `before` (one warp).
+__device__ __forceinline__ void token_tiles(const MxGemmArgs& a, int* before) {
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < a.experts ? (max(offset_of(a, e + 1) - offset_of(a, e), 0) + a.TN - 1) / a.TN : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (e < a.experts) before[e] = run + incl - n;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) before[a.experts] = run;
+    __syncwarp();
+}
+
+// Rows that belong to nobody are zero; thread `at` of `all`.
+__device__ __forceinline__ void zero_tail(const MxGemmArgs& a, long long at, long long all) {
+    const int esize = a.ytype == UQ_FP32 ? 4 : 2;
+    uint8_t* y = static_cast<uint8_t*>(a.y);
+    const long long b0 = (long long)offset_of(a, a.experts) * a.N * esize, b1 = (long long)a.rows * a.N * esize;
+    const long long c0 = min((b0 + 15) & ~15ll, b1), c1 = max(b1 & ~15ll, c0);
+    for (long long i = b0 + at * 2; i < c0; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
+    for (long long i = c0 + at * 16; i < c1; i += all * 16) *reinterpret_cast<uint4*>(y + i) = make_uint4(0, 0, 0, 0);
+    for (long long i = c1 + at * 2; i < b1; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
 }
 
 // The tiles of a CTA and its k steps of them.
@@ -259,7 +289,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         for (int i = 0; i < NA; ++i) {
             load_codes(st + i * A_BYTES, i ? &maps.up : &maps.w, t.expert * a.N + t.nt * 128, 128, kt, bar);
             tma_3d(st + NA * A_BYTES + b_bytes + i * SF_BYTES, i ? &maps.up_scales : &maps.w_scales, 0, kt * TPS,
-                   t.expert * a.NT + t.nt, bar);
+                   t.expert * a.row_tiles + t.nt, bar);
         }
     };
     auto load_tokens = [&](const Tile& t, int kt, int s) {
@@ -272,23 +302,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
 
     if (warp == 0) {
         if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
-        if (a.offsets) {
-            int run = 0;
-            for (int e0 = 0; e0 < a.experts; e0 += 32) {
-                const int e = e0 + lane;
-                const int n = e < a.experts ? (max(offset_of(a, e + 1) - offset_of(a, e), 0) + TN - 1) / TN : 0;
-                int incl = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += v;
-                }
-                if (e < a.experts) before[e] = run + incl - n;
-                run += __shfl_sync(0xffffffffu, incl, 31);
-            }
-            if (lane == 0) before[a.experts] = run;
-            __syncwarp();
-        }
+        if (a.offsets) token_tiles(a, before);
         if (lane == 0) {
             for (int s = 0; s < a.stages; ++s) {
                 mbar_init(&full[s], 2);
@@ -404,17 +418,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue: lane = row of the weight tile
         const int q = warp & 3, row = q * 32 + lane, et = threadIdx.x - 64;
-        const int esize = a.ytype == UQ_FP32 ? 4 : 2;
-        if (a.offsets) {
-            // rows that belong to nobody
-            uint8_t* y = static_cast<uint8_t*>(a.y);
-            const long long b0 = (long long)offset_of(a, a.experts) * a.N * esize, b1 = (long long)a.rows * a.N * esize;
-            const long long c0 = min((b0 + 15) & ~15ll, b1), c1 = max(b1 & ~15ll, c0);
-            const long long at = blockIdx.x * 128LL + et, all = gridDim.x * 128LL;
-            for (long long i = b0 + at * 2; i < c0; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
-            for (long long i = c0 + at * 16; i < c1; i += all * 16) *reinterpret_cast<uint4*>(y + i) = make_uint4(0, 0, 0, 0);
-            for (long long i = c1 + at * 2; i < b1; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
-        }
+        if (a.offsets) zero_tail(a, blockIdx.x * 128LL + et, gridDim.x * 128LL);
         for (int n = 0; sch.more(); sch.advance(), ++n) {
             const Tile t = find_tile(a, before, tt_all, sch.tile);
             const int buf = AB == 2 ? n & 1 : 0;
@@ -489,6 +493,283 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Pairs of CTAs (cta_group::2) for many rows.  One MMA spans two SMs: 256 weight rows (128 in each SM's tensor memory) x
+// up to 256 tokens, each SM holding half of the token rows in shared memory.  With one SM alone a 128 x 128 x 64 MMA
+// reads 8 KB of shared memory in the 64 cycles it computes, all that shared memory delivers, beside the copies that
+// refill it; the pair's 256 x 256 MMA reads 8 KB per SM in 128 cycles, and every byte loaded is used twice as often.
+// The even CTA issues the scale copies and the MMAs for both; TMA loads of both count their bytes on its full[]
+// barriers; commits arrive in both.  A tile's accumulator is 256 columns (tokens; or 128 gate + 128 up); two of them
+// overlap in as many columns as the scales take (MXFP4 48, NVFP4 96, in two halves that alternate by step), and the
+// epilogue reads those columns first, so the next tile's MMAs wait for a fifth to a third of an epilogue only.
+constexpr int PAIR_STEP = 256;
+template <int FMT, int NA> struct Pair {
+    static constexpr int TN = 256 / NA;                            // tokens per tile
+    static constexpr int TPS = PAIR_STEP / mx_tile_k(FMT);         // scale tiles per step and 128 rows
+    static constexpr int XT = TN / 128;                            // row tiles of the tokens' scales
+    static constexpr int A = NA * 128 * 128, B = TN / 2 * 128, SA = NA * TPS * 512, SB = XT * TPS * 512;
+    static constexpr int STAGE = A + B + SA + SB;
+    static constexpr int STAGES = 218 * 1024 / STAGE;
+    static constexpr int SF = (NA + XT) * TPS * 4;                 // scale columns of a step
+    static constexpr int OVER = 2 * SF;                            // columns the two accumulators share
+    static_assert(STAGE % 1024 == 0 && STAGES <= MAX_STAGES, "stage layout");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+// three scale tiles -> three groups of four columns, in both CTAs from their own shared memory
+__device__ __forceinline__ void pair_cp3(uint32_t t0, uint32_t s0, uint32_t t1, uint32_t s1, uint32_t t2, uint32_t s2) {
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 a, b, c;\n\t"
+                 "mov.b64 a, {%1, " UQ_SCALES_HI "};\n\tmov.b64 b, {%3, " UQ_SCALES_HI "};\n\tmov.b64 c, {%5, " UQ_SCALES_HI "};\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%2], b;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], c;\n\t}"
+                 :: "r"(t0), "r"(s0), "r"(t1), "r"(s1), "r"(t2), "r"(s2) : "memory");
+}
+// the MMAs of one scale tile (MXFP4 two, the second if `two`; NVFP4 one), as issue_tile
+template <int FMT>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t ca, uint32_t cb, uint32_t idesc,
+                                         uint32_t on, uint32_t two) {
+    if constexpr (FMT == UQ_MXFP4)
+        asm volatile("{\n\t.reg .pred p, e, f, t;\n\t.reg .b64 da, db;\n\t.reg .b32 i2;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "or.b32 i2, %5, 0x40000020;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 f, %7, 0, e;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %5, [%3], [%4], p;\n\t"
+                     "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
+                     "@f tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%3], [%4], t;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(ca), "r"(cb), "r"(idesc), "r"(on), "r"(two) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %5, [%3], [%4], p;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b), "r"(ca), "r"(cb), "r"(idesc), "r"(on) : "memory");
+}
+// arrive on the barrier at this offset in both CTAs when the MMAs issued so far are complete
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+                 :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
+template <int FMT, int NA>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
+    using P = Pair<FMT, NA>;
+    constexpr int TN = P::TN, TPS = P::TPS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(head);            // [STAGES] both CTAs' loads landed (even CTA's)
+    uint64_t* empty = full + MAX_STAGES;                           // [STAGES] consumed by the MMAs
+    uint64_t* acc_full = empty + MAX_STAGES;                       // [2] accumulator complete
+    uint64_t* acc_free = acc_full + 2;                             // the shared columns have been read (even CTA's)
+    uint64_t* drain = acc_free + 1;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
+    uint8_t* ring = head + HEAD;
+    int* before = reinterpret_cast<int*>(ring + P::STAGES * P::STAGE);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full), empty0 = smem_u32(empty);
+
+    if (warp == 0) {
+        if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
+        if (a.offsets) token_tiles(a, before);
+        if (lane == 0) {
+            for (int s = 0; s < P::STAGES; ++s) {
+                mbar_init(&full[s], 2);
+                mbar_init(&empty[s], 1);
+            }
+            for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1);
+            mbar_init(acc_free, 8);
+            mbar_init(drain, 1);
+            *abort_flag = 0;
+            fence_barrier_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    cluster_sync();                                                // the other CTA's barriers are ready
+    const int tt_all = a.offsets ? before[a.experts] : (a.rows + TN - 1) / TN;
+    const int tiles = tt_all * a.NT, stride = gridDim.x >> 1;
+    uint32_t tmem = 0;
+    if (warp >= 1 && warp <= 5) {
+        if (warp == 1) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_ptr)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
+        fence_before();
+        asm volatile("bar.sync 1, 160;" ::: "memory");
+        fence_after();
+        tmem = (uint32_t)uniform((int)*tmem_ptr);
+    }
+    // the token columns a tile's MMAs use: a multiple of 16, half of the rows in each CTA
+    auto columns = [&](const Tile& t) { return (uniform(t.rows) + 15) / 16 * 16; };
+
+    if (warp == 0 || warp == 6) {
+        // ------------------------------------------------------------ producers
+        const bool tokens = warp == 6;
+        if (tokens && a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const uint32_t lead_full0 = cluster_addr(full0, 0);
+        int issued = 0, s = 0;
+        uint32_t ph = 1;                                           // empty[] of the first round counts as free
+        bool ok = true;
+        for (int tile = blockIdx.x >> 1; ok && tile < tiles; tile += stride) {
+            const Tile t = find_tile(a, before, tt_all, tile);
+            const int e = uniform(t.expert), n = t.nt * 256 + (int)rank * 128;
+            const int row = uniform(t.row0) + (int)rank * (columns(t) >> 1);
+            const int xtile = (a.offsets ? (uniform(t.row0 - t.first) >> 7) + e : 0) + (uniform(t.first) >> 7);
+            for (int kt = 0; kt < a.steps; ++kt) {
+                if (issued >= P::STAGES && !warp_wait(empty0 + s * 8, ph, a.fault, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = ring0 + s * P::STAGE, bar = lead_full0 + s * 8;
+                if (rank == 0) expect_bytes(full0 + s * 8, 2 * (tokens ? P::B + P::SB : P::A + P::SA));
+                if (tokens) {
+                    pair_tma_2d(st + P::A, &maps.x, kt * 128, row, bar);
+                    pair_tma_3d(st + P::A + P::B + P::SA, &maps.x_scales, 0, kt * TPS, xtile, bar);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NA; ++i) {
+                        pair_tma_2d(st + i * (128 * 128), i ? &maps.up : &maps.w, kt * 128, e * a.N + n, bar);
+                        pair_tma_3d(st + P::A + P::B + i * TPS * 512, i ? &maps.up_scales : &maps.w_scales, 0, kt * TPS,
+                                    e * a.row_tiles + (n >> 7), bar);
+                    }
+                }
+                ++issued;
+                if (++s == P::STAGES) { s = 0; ph ^= 1; }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+        // Let the last copies land before the CTA can leave: both CTAs' are counted on the even one's barriers, and the
+        // CTAs leave together.
+        if (rank == 0)
+            for (int j = issued - 1; j >= 0 && j >= issued - P::STAGES; --j)
+                mbar_wait_bounded(&full[j % P::STAGES], (uint32_t)((j / P::STAGES) & 1), a.fault, FAULT_MX_WAIT);
+    } else if (warp == 1 && rank == 0) {
+        // ------------------------------------------------------------ MMA issue
+        constexpr int PER = FMT == UQ_MXFP4 ? 2 : 1;               // MMAs per scale tile
+        int s = 0, n = 0;
+        uint32_t ph = 0, half = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x >> 1; ok && tile < tiles; tile += stride, ++n) {
+            const Tile t = find_tile(a, before, tt_all, tile);
+            const uint32_t idesc = block_idesc<FMT>(columns(t)) + (1u << 27);      // M = 256
+            const uint32_t acc = tmem + (n & 1) * (256 - P::OVER);
+            // the epilogue of the tile before has read the shared columns
+            if (n && !warp_wait(smem_u32(acc_free), (uint32_t)(n - 1) & 1, a.fault, abort_flag)) ok = false;
+            fence_after();
+            uint32_t on = 0;
+            for (int kt = 0; ok && kt < a.steps; ++kt) {
+                if (!warp_wait(full0 + s * 8, ph, a.fault, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t al = desc_lo(ring0 + s * P::STAGE), bl = al + (P::A >> 4), sl = bl + (P::B >> 4);
+                const uint32_t sx = sl + (P::SA >> 4), col = tmem + 512 - P::OVER + half * P::SF, cx = col + NA * TPS * 4;
+                const int mmas = min(PAIR_STEP / 64, (a.K - kt * PAIR_STEP + 63) >> 6);
+#pragma unroll
+                for (int j = 0; j < TPS; ++j) {
+                    const int q = j * PER;
+                    if (q >= mmas) break;
+                    const uint32_t two = q + 1 < mmas;
+                    // a row tile's columns of one scale tile lie together: the tokens' two row tiles are 8 columns
+                    if constexpr (NA == 1)
+                        pair_cp3(col + j * 4, sl + j * 32, cx + j * 8, sx + j * 32, cx + j * 8 + 4, sx + (TPS + j) * 32);
+                    else
+                        pair_cp3(col + j * 4, sl + j * 32, col + (TPS + j) * 4, sl + (TPS + j) * 32, cx + j * 4, sx + j * 32);
+#pragma unroll
+                    for (int i = 0; i < NA; ++i)
+                        pair_mma<FMT>(acc + i * TN, al + i * 1024 + 2 * q, bl + 2 * q, col + (i * TPS + j) * 4,
+                                      cx + j * 4 * P::XT, idesc, on, two);
+                    on = 1;
+                }
+                half ^= 1;
+                pair_commit(empty0 + s * 8);
+                if (++s == P::STAGES) { s = 0; ph ^= 1; }
+            }
+            pair_commit(smem_u32(&acc_full[n & 1]));
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            __syncwarp();
+            pair_commit(smem_u32(drain));
+            mbar_wait_bounded(drain, 0, a.fault, FAULT_MX_WAIT);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue: lane = weight row
+        const int q = warp & 3, row = q * 32 + lane;
+        if (a.offsets) zero_tail(a, blockIdx.x * 128LL + threadIdx.x - 64, gridDim.x * 128LL);
+        const uint32_t lead_free = cluster_addr(smem_u32(acc_free), 0);
+        int n = 0;
+        for (int tile = blockIdx.x >> 1; tile < tiles; tile += stride, ++n) {
+            const Tile t = find_tile(a, before, tt_all, tile);
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * (256 - P::OVER);
+            if (!*abort_flag && !mbar_wait_bounded(&acc_full[n & 1], (uint32_t)(n >> 1) & 1, a.fault, FAULT_MX_WAIT))
+                *abort_flag = 1;
+            __syncwarp();
+            fence_after();
+            const int nn = t.nt * 256 + (int)rank * 128 + row;
+            const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
+            const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
+            // the first accumulator shares its last columns, the second its first: those come first
+            const int c0 = n & 1 ? 0 : TN - P::OVER;
+            for (int i = 0; i < TN; i += 16) {
+                if (i == P::OVER) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(lead_free);
+                }
+                const int c = c0 + i < TN ? c0 + i : c0 + i - TN;
+                if (c >= t.rows) continue;
+                uint32_t r[NA * 16];
+#pragma unroll
+                for (int h = 0; h < NA; ++h) tmem_ld16(acc + h * TN + c, *reinterpret_cast<uint32_t(*)[16]>(r + 16 * h));
+                tmem_ld_wait();
+                if (nn < a.N)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float v = __uint_as_float(r[j]) * al;
+                        if constexpr (NA == 2) v = silu_mul(v, __uint_as_float(r[16 + j]) * au);
+                        if (c + j < t.rows) store_one(a, (long long)(t.row0 + c + j) * a.N + nn, v);
+                    }
+            }
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    cluster_sync();                                                // both CTAs are done with each other's memory
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -515,11 +796,11 @@ bool codes_map(CUtensorMap* m, const uint8_t* codes, long long rows, int K, int 
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// scale tiles [row tiles][ktiles][512 bytes], boxes of one row tile x one step's tiles
-bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int ktiles, int tps) {
+// scale tiles [row tiles][ktiles][512 bytes], boxes of box_rows row tiles x one step's tiles
+bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int ktiles, int tps, int box_rows) {
     cuuint64_t dims[3] = {64, (cuuint64_t)ktiles, (cuuint64_t)row_tiles};
     cuuint64_t strides[2] = {512, (cuuint64_t)ktiles * 512};
-    cuuint32_t b[3] = {64, (cuuint32_t)tps, 1};
+    cuuint32_t b[3] = {64, (cuuint32_t)tps, (cuuint32_t)box_rows};
     cuuint32_t es[3] = {1, 1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 3, const_cast<uint8_t*>(scales), dims, strides, b, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -535,6 +816,8 @@ cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
         e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(mx_gemm_pair_kernel<FMT, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
@@ -557,17 +840,45 @@ cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st)
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NA>, maps, a);
+    return a.pair ? cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<FMT, NA>, maps, a)
+                  : cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NA>, maps, a);
+}
+
+// Stage count and size of the pair kernel.
+template <int NA> void pair_ring(int fmt, MxGemmArgs& a) {
+    a.TN = 256 / NA;
+    a.smem = 1024 + HEAD + (fmt == UQ_MXFP4 ? Pair<UQ_MXFP4, NA>::STAGES * Pair<UQ_MXFP4, NA>::STAGE
+                                            : Pair<UQ_NVFP4, NA>::STAGES * Pair<UQ_NVFP4, NA>::STAGE);
 }
 
 // Tiles, ring and grid of one product.
 void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
-    const int tps = STEP_K / mx_tile_k(fmt), NA = gated ? 2 : 1;
-    a.steps = (a.K + STEP_K - 1) / STEP_K;
+    const int NA = gated ? 2 : 1;
     a.ktiles = mx_ktiles(a.K, fmt);
+    a.row_tiles = (a.N + 127) / 128;
+    const int table = a.offsets ? (a.experts + 1) * 4 : 0;
     // token tile: the rows an expert gets on average (all of them when there is one).  Under 64 only where no second
     // tile can follow: a tile's scale columns then always start at an even column.
     const int mean = a.offsets ? (a.rows + a.experts - 1) / a.experts : a.rows;
+    // pairs of CTAs where there are rows for their wide tiles and tiles for most of the pairs
+    const long long pairs = ((a.N + 255) / 256) * (a.rows / (256 / NA) + (a.offsets ? a.experts / 2 : 1));
+    a.pair = a.rows >= 256 && mean >= 128 && pairs * 2 >= sms;
+    if (a.pair) {
+        if (gated) pair_ring<2>(fmt, a);
+        else pair_ring<1>(fmt, a);
+        a.smem += table;
+        a.steps = (a.K + PAIR_STEP - 1) / PAIR_STEP;
+        a.NT = (a.N + 255) / 256;
+        a.group = 8;
+        a.S = 1;
+        const long long most = a.NT * (a.offsets ? std::min((long long)a.rows, a.rows / a.TN + (long long)a.experts)
+                                                 : (a.rows + a.TN - 1) / a.TN);
+        a.ctas = (int)std::min(2 * most, (long long)(sms & ~1));
+        return;
+    }
+    const int tps = STEP_K / mx_tile_k(fmt);
+    a.steps = (a.K + STEP_K - 1) / STEP_K;
+    a.group = 16;
     a.TN = a.rows <= 16 ? 16 : (a.rows <= 32 ? 32 : (mean <= 64 ? 64 : 128));
     a.NT = (a.N + 127) / 128;
     // token tiles: exact, or the most that any counts give
@@ -582,7 +893,6 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     a.ctas = a.S > 1 ? (int)tiles * a.S : (int)std::min(tiles, (long long)sms);
     a.folded = a.K % 256 == 0;
     const int stage_bytes = NA * 128 * (STEP_K / 2) + a.TN * (STEP_K / 2) + (NA + 1) * tps * 512;
-    const int table = a.offsets ? (a.experts + 1) * 4 : 0;
     // tensor memory: two accumulators where 512 columns hold them beside three stages of scales
     const int sf = (NA + 1) * tps * 4;
     a.accs = 2 * NA * a.TN + 3 * sf <= 512 ? 2 : 1;
@@ -599,16 +909,17 @@ cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes
     if (!encode_fn()) return cudaErrorNotSupported;
     plan(fmt, wcodes_up != nullptr, a, sms);
     MxGemmMaps m;
-    const int tps = STEP_K / mx_tile_k(fmt);
-    const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.NT;
-    bool ok = codes_map(&m.w, wcodes, wrows, a.K, 128, a.folded) && scales_map(&m.w_scales, a.wscales, wtiles, a.ktiles, tps) &&
-              codes_map(&m.x, xcodes, a.rows, a.K, a.TN, a.folded) &&
-              scales_map(&m.x_scales, a.xscales, mx_row_tiles(a.rows, a.offsets ? a.experts : 0), a.ktiles, tps);
+    const int tps = (a.pair ? PAIR_STEP : STEP_K) / mx_tile_k(fmt);
+    const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.row_tiles;
+    bool ok = codes_map(&m.w, wcodes, wrows, a.K, 128, a.folded) && scales_map(&m.w_scales, a.wscales, wtiles, a.ktiles, tps, 1) &&
+              codes_map(&m.x, xcodes, a.rows, a.K, a.pair ? a.TN / 2 : a.TN, a.folded) &&
+              scales_map(&m.x_scales, a.xscales, mx_row_tiles(a.rows, a.offsets ? a.experts : 0), a.ktiles, tps,
+                         a.pair ? a.TN / 128 : 1);
     m.up = m.w;
     m.up_scales = m.w_scales;
     if (wcodes_up)
         ok = ok && codes_map(&m.up, wcodes_up, wrows, a.K, 128, a.folded) &&
-             scales_map(&m.up_scales, a.wscales_up, wtiles, a.ktiles, tps);
+             scales_map(&m.up_scales, a.wscales_up, wtiles, a.ktiles, tps, 1);
     if (!ok) return cudaErrorInvalidValue;
     if (fmt == UQ_MXFP4) return wcodes_up ? launch<UQ_MXFP4, 2>(m, a, st) : launch<UQ_MXFP4, 1>(m, a, st);
     return wcodes_up ? launch<UQ_NVFP4, 2>(m, a, st) : launch<UQ_NVFP4, 1>(m, a, st);
