@@ -146,14 +146,26 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-// A whole warp's wait: false for all lanes once any lane's wait ran out or the CTA was told to stop.
+// A whole warp's wait: false for all lanes once WAIT_LIMIT_NS have passed (the fault word then tells) or the CTA was
+// told to stop.  Polls without a suspend hint: a warp put to sleep for up to a microsecond woke too late for a ring
+// whose steps take a quarter of that.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned int* fault, volatile int* abort_flag) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    if (__all_sync(0xffffffffu, ok)) return true;
-    return __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)),
-                                                                     parity, fault, FAULT_MX_WAIT));
+    unsigned long long t0 = 0;
+    for (unsigned int i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (i % 32 == 0) {
+            bool stop = *abort_flag != 0;
+            if (!t0) t0 = global_ns();
+            else if (global_ns() - t0 > WAIT_LIMIT_NS) {
+                atomicOr(fault, FAULT_MX_WAIT);
+                stop = true;
+            }
+            if (__any_sync(0xffffffffu, stop)) return false;
+        }
+    }
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -244,10 +256,59 @@ struct Schedule {
     __device__ __forceinline__ void advance() { tile += stride; }
 };
 
+// One output element; the split tiles' path.
 __device__ __forceinline__ void store_one(const MxGemmArgs& a, long long at, float v) {
     if (a.ytype == UQ_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
     else if (a.ytype == UQ_FP16) static_cast<__half*>(a.y)[at] = __float2half_rn(v);
     else static_cast<float*>(a.y)[at] = v;
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Writes 16 columns (tokens m0 .. m0 + count) of this lane's output nn; the warp's lanes hold 32 consecutive outputs.
+// 16-bit types with an even N: neighbouring lanes exchange every other value and store pairs of outputs, so a store
+// covers 64 bytes of each of two tokens, and conversions and stores are halved.
+template <class T> __device__ __forceinline__ void put16(const MxGemmArgs& a, int m0, int count, int nn, const float (&v)[16]) {
+    T* y = static_cast<T*>(a.y);
+    if constexpr (sizeof(T) == 2) {
+        if (!(a.N & 1)) {
+            const int odd = threadIdx.x & 1;
+            T* p = y + (long long)(m0 + odd) * a.N + (nn & ~1);
+            const long long step = 2ll * a.N;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2, p += step) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const uint32_t w = pack2(T(), odd ? got : v[j], odd ? v[j + 1] : got);
+                if (nn < a.N && j + odd < count) *reinterpret_cast<uint32_t*>(p) = w;
+            }
+            return;
+        }
+    }
+    T* p = y + (long long)m0 * a.N + nn;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, p += a.N)
+        if (nn < a.N && j < count) *p = from_f32<T>(v[j]);
+}
+// the sums r of 16 columns (gate and up: 2 x 16) -> output
+template <int NA>
+__device__ __forceinline__ void finish16(const MxGemmArgs& a, int m0, int count, int nn, const uint32_t* r, float al, float au) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        v[j] = __uint_as_float(r[j]) * al;
+        if constexpr (NA == 2) v[j] = silu_mul(v[j], __uint_as_float(r[16 + j]) * au);
+    }
+    if (a.ytype == UQ_BF16) put16<__nv_bfloat16>(a, m0, count, nn, v);
+    else if (a.ytype == UQ_FP16) put16<__half>(a, m0, count, nn, v);
+    else put16<float>(a, m0, count, nn, v);
 }
 
 template <int FMT, int NA>
@@ -367,6 +428,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         // ------------------------------------------------------------ MMA issue
         constexpr int PER = FMT == UQ_MXFP4 ? 2 : 1;               // MMAs per scale tile
         const uint32_t sf0 = tmem + AB * NA * TN;
+        const int full_steps = a.K / STEP_K;
         int s = 0, n = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -390,19 +452,23 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
                 const uint32_t st = ring0 + s * stage_bytes;
                 const uint32_t al = desc_lo(st), bl = al + NA * (A_BYTES >> 4), sl = bl + (b_bytes >> 4);
                 const uint32_t col = sf0 + s * SF_COLS, cb = col + NA * TPS * 4, cu = cb + xshift;
-                const int mmas = min(STEP_K / 64, (a.K - kt * STEP_K + 63) >> 6);
-#pragma unroll
-                for (int j = 0; j < TPS; ++j) {
-                    if (j * PER >= mmas) break;
-                    const int q = j * PER;                         // first MMA of the tile: column q / 4, 32-byte part q % 4
+                // scale tile j: its first MMA is 32-byte part q % 4 of the 128-byte column q / 4
+                auto issue = [&](int j, uint32_t two) {
+                    const int q = j * PER;
                     const uint32_t ao = (q >> 2) * (16384 >> 4) + 2 * (q & 3), bo = bl + (q >> 2) * (TN * 8) + 2 * (q & 3);
-                    const uint32_t two = q + 1 < mmas;
                     issue_tile<FMT>(acc, al + ao, bo, sl + j * 32, sl + NA * (SF_BYTES >> 4) + j * 32, col + j * 4, cb + j * 4,
                                     cu + j * 4, idesc, on, two);
                     if constexpr (NA == 2)
                         issue_more<FMT>(acc + TN, al + (A_BYTES >> 4) + ao, bo, sl + (SF_BYTES >> 4) + j * 32,
                                         col + (TPS + j) * 4, cu + j * 4, idesc, on, two);
                     on = 1;
+                };
+                if (kt < full_steps) {
+#pragma unroll
+                    for (int j = 0; j < TPS; ++j) issue(j, 1);
+                } else {
+                    const int mmas = (a.K - kt * STEP_K + 63) >> 6;                // K ends inside the step
+                    for (int j = 0; j * PER < mmas; ++j) issue(j, j * PER + 1 < mmas);
                 }
                 commit(empty0 + s * 8);
                 if (++s == a.stages) { s = 0; ph ^= 1; }
@@ -424,9 +490,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             const int buf = AB == 2 ? n & 1 : 0;
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * NA * TN;
             // after a timeout the tiles are walked without waiting
-            if (!*abort_flag &&
-                !mbar_wait_bounded(&acc_full[buf], (uint32_t)((AB == 2 ? n >> 1 : n) & 1), a.fault, FAULT_MX_WAIT))
-                *abort_flag = 1;
+            if (!warp_wait(smem_u32(&acc_full[buf]), (uint32_t)((AB == 2 ? n >> 1 : n) & 1), a.fault, abort_flag)) *abort_flag = 1;
             __syncwarp();
             fence_after();
             const int nn = t.nt * 128 + row;
@@ -448,13 +512,8 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
 #pragma unroll
                     for (int j = 0; j < NA * 16; ++j)
                         if (c + (j & 15) < t.rows) sums[((c + (j & 15)) * NA + (j >> 4)) * 128 + row] = __uint_as_float(r[j]);
-                } else if (nn < a.N) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float v = __uint_as_float(r[j]) * al;
-                        if constexpr (NA == 2) v = silu_mul(v, __uint_as_float(r[16 + j]) * au);
-                        if (c + j < t.rows) store_one(a, (long long)(t.row0 + c + j) * a.N + nn, v);
-                    }
+                } else {
+                    finish16<NA>(a, t.row0 + c, t.rows - c, nn, r, al, au);
                 }
             }
         }
@@ -535,35 +594,49 @@ __device__ __forceinline__ void pair_tma_3d(uint32_t dst, const CUtensorMap* map
                  " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
                  :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
-// three scale tiles -> three groups of four columns, in both CTAs from their own shared memory
-__device__ __forceinline__ void pair_cp3(uint32_t t0, uint32_t s0, uint32_t t1, uint32_t s1, uint32_t t2, uint32_t s2) {
-    asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 a, b, c;\n\t"
-                 "mov.b64 a, {%1, " UQ_SCALES_HI "};\n\tmov.b64 b, {%3, " UQ_SCALES_HI "};\n\tmov.b64 c, {%5, " UQ_SCALES_HI "};\n\t"
-                 "elect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t"
-                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%2], b;\n\t"
-                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], c;\n\t}"
-                 :: "r"(t0), "r"(s0), "r"(t1), "r"(s1), "r"(t2), "r"(s2) : "memory");
-}
-// the MMAs of one scale tile (MXFP4 two, the second if `two`; NVFP4 one), as issue_tile
-template <int FMT>
-__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t ca, uint32_t cb, uint32_t idesc,
-                                         uint32_t on, uint32_t two) {
-    if constexpr (FMT == UQ_MXFP4)
-        asm volatile("{\n\t.reg .pred p, e, f, t;\n\t.reg .b64 da, db;\n\t.reg .b32 i2;\n\t"
-                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
-                     "or.b32 i2, %5, 0x40000020;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
-                     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.b32 f, %7, 0, e;\n\t"
-                     "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %5, [%3], [%4], p;\n\t"
+// The instructions that share a scale tile of the pair's operands: the copies of its three scale tiles (NA = 1: weights,
+// tokens' first and second 128 rows; NA = 2: gate, up, tokens) to columns c0, c1, c2, in both CTAs from their own shared
+// memory, then the MMAs as issue_tile issues them.  ca / cb: the scale columns of weights and tokens.
+template <int FMT, int NA>
+__device__ __forceinline__ void pair_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t c0,
+                                          uint32_t c1, uint32_t c2, uint32_t cb, uint32_t idesc, uint32_t on, uint32_t two) {
+#define UQ_PAIR_HEAD \
+    "{\n\t.reg .pred p, e, f, t;\n\t.reg .b64 da, db, dc, x, y, z;\n\t.reg .b32 i2, d1;\n\t" \
+    "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t" \
+    "mov.b64 x, {%3, " UQ_SCALES_HI "};\n\tmov.b64 y, {%4, " UQ_SCALES_HI "};\n\tmov.b64 z, {%5, " UQ_SCALES_HI "};\n\t" \
+    "setp.ne.b32 p, %11, 0;\n\tsetp.eq.b32 t, %10, %10;\n\telect.sync _|e, 0xffffffff;\n\t" \
+    "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], x;\n\t" \
+    "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%7], y;\n\t" \
+    "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%8], z;\n\t"
+#define UQ_PAIR_ARGS \
+    :: "r"(d), "r"(a), "r"(b), "r"(s0), "r"(s1), "r"(s2), "r"(c0), "r"(c1), "r"(c2), "r"(cb), "r"(idesc), "r"(on), "r"(two) \
+    : "memory"
+    if constexpr (FMT == UQ_MXFP4 && NA == 1)
+        asm volatile(UQ_PAIR_HEAD "or.b32 i2, %10, 0x40000020;\n\tsetp.ne.and.b32 f, %12, 0, e;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %10, [%6], [%9], p;\n\t"
                      "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\t"
-                     "@f tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%3], [%4], t;\n\t}"
-                     :: "r"(d), "r"(a), "r"(b), "r"(ca), "r"(cb), "r"(idesc), "r"(on), "r"(two) : "memory");
+                     "@f tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%6], [%9], t;\n\t}"
+                     UQ_PAIR_ARGS);
+    else if constexpr (FMT == UQ_MXFP4)                            // the up tile: 128 rows (16 KB) and 128 columns on
+        asm volatile(UQ_PAIR_HEAD "or.b32 i2, %10, 0x40000020;\n\tsetp.ne.and.b32 f, %12, 0, e;\n\t"
+                     "add.s32 d1, %0, 128;\n\tadd.s64 dc, da, 1024;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %10, [%6], [%9], p;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [d1], dc, db, %10, [%7], [%9], p;\n\t"
+                     "add.s64 da, da, 2;\n\tadd.s64 db, db, 2;\n\tadd.s64 dc, dc, 2;\n\t"
+                     "@f tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, i2, [%6], [%9], t;\n\t"
+                     "@f tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [d1], dc, db, i2, [%7], [%9], t;\n\t}"
+                     UQ_PAIR_ARGS);
+    else if constexpr (NA == 1)
+        asm volatile(UQ_PAIR_HEAD
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %10, [%6], [%9], p;\n\t}"
+                     UQ_PAIR_ARGS);
     else
-        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-                     "mov.b64 da, {%1, " UQ_OPERAND_HI "};\n\tmov.b64 db, {%2, " UQ_OPERAND_HI "};\n\t"
-                     "setp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                     "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %5, [%3], [%4], p;\n\t}"
-                     :: "r"(d), "r"(a), "r"(b), "r"(ca), "r"(cb), "r"(idesc), "r"(on) : "memory");
+        asm volatile(UQ_PAIR_HEAD "add.s32 d1, %0, 128;\n\tadd.s64 dc, da, 1024;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %10, [%6], [%9], p;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [d1], dc, db, %10, [%7], [%9], p;\n\t}"
+                     UQ_PAIR_ARGS);
+#undef UQ_PAIR_HEAD
+#undef UQ_PAIR_ARGS
 }
 // arrive on the barrier at this offset in both CTAs when the MMAs issued so far are complete
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
@@ -674,6 +747,7 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issue
         constexpr int PER = FMT == UQ_MXFP4 ? 2 : 1;               // MMAs per scale tile
+        const int full_steps = a.K / PAIR_STEP;
         int s = 0, n = 0;
         uint32_t ph = 0, half = 0;
         bool ok = true;
@@ -693,22 +767,24 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
                 fence_after();
                 const uint32_t al = desc_lo(ring0 + s * P::STAGE), bl = al + (P::A >> 4), sl = bl + (P::B >> 4);
                 const uint32_t sx = sl + (P::SA >> 4), col = tmem + 512 - P::OVER + half * P::SF, cx = col + NA * TPS * 4;
-                const int mmas = min(PAIR_STEP / 64, (a.K - kt * PAIR_STEP + 63) >> 6);
-#pragma unroll
-                for (int j = 0; j < TPS; ++j) {
-                    const int q = j * PER;
-                    if (q >= mmas) break;
-                    const uint32_t two = q + 1 < mmas;
-                    // a row tile's columns of one scale tile lie together: the tokens' two row tiles are 8 columns
+                // scale tile j: its first MMA is 32-byte part j * PER of the column
+                auto issue = [&](int j, uint32_t two) {
+                    const uint32_t at = 2 * j * PER;
+                    // the tokens' two row tiles of one scale tile lie together: 8 columns
                     if constexpr (NA == 1)
-                        pair_cp3(col + j * 4, sl + j * 32, cx + j * 8, sx + j * 32, cx + j * 8 + 4, sx + (TPS + j) * 32);
+                        pair_tile<FMT, 1>(acc, al + at, bl + at, sl + j * 32, sx + j * 32, sx + (TPS + j) * 32, col + j * 4,
+                                          cx + j * 8, cx + j * 8 + 4, cx + j * 8, idesc, on, two);
                     else
-                        pair_cp3(col + j * 4, sl + j * 32, col + (TPS + j) * 4, sl + (TPS + j) * 32, cx + j * 4, sx + j * 32);
-#pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        pair_mma<FMT>(acc + i * TN, al + i * 1024 + 2 * q, bl + 2 * q, col + (i * TPS + j) * 4,
-                                      cx + j * 4 * P::XT, idesc, on, two);
+                        pair_tile<FMT, 2>(acc, al + at, bl + at, sl + j * 32, sl + (TPS + j) * 32, sx + j * 32, col + j * 4,
+                                          col + (TPS + j) * 4, cx + j * 4, cx + j * 4, idesc, on, two);
                     on = 1;
+                };
+                if (kt < full_steps) {
+#pragma unroll
+                    for (int j = 0; j < TPS; ++j) issue(j, 1);
+                } else {
+                    const int mmas = (a.K - kt * PAIR_STEP + 63) >> 6;             // K ends inside the step
+                    for (int j = 0; j * PER < mmas; ++j) issue(j, j * PER + 1 < mmas);
                 }
                 half ^= 1;
                 pair_commit(empty0 + s * 8);
@@ -731,34 +807,40 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
         for (int tile = blockIdx.x >> 1; tile < tiles; tile += stride, ++n) {
             const Tile t = find_tile(a, before, tt_all, tile);
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * (256 - P::OVER);
-            if (!*abort_flag && !mbar_wait_bounded(&acc_full[n & 1], (uint32_t)(n >> 1) & 1, a.fault, FAULT_MX_WAIT))
-                *abort_flag = 1;
+            // after a timeout the tiles are walked without waiting
+            if (!warp_wait(smem_u32(&acc_full[n & 1]), (uint32_t)(n >> 1) & 1, a.fault, abort_flag)) *abort_flag = 1;
             __syncwarp();
             fence_after();
             const int nn = t.nt * 256 + (int)rank * 128 + row;
             const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
             const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
-            // the first accumulator shares its last columns, the second its first: those come first
+            // The first accumulator shares its last columns, the second its first: those are read, and given free,
+            // before anything is written.
             const int c0 = n & 1 ? 0 : TN - P::OVER;
-            for (int i = 0; i < TN; i += 16) {
-                if (i == P::OVER) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(lead_free);
-                }
+            {
+                uint32_t r[P::OVER / 16][NA * 16];
+#pragma unroll
+                for (int i = 0; i < P::OVER / 16; ++i)
+#pragma unroll
+                    for (int h = 0; h < NA; ++h)
+                        tmem_ld16(acc + h * TN + c0 + i * 16, *reinterpret_cast<uint32_t(*)[16]>(r[i] + 16 * h));
+                tmem_ld_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(lead_free);
+#pragma unroll
+                for (int i = 0; i < P::OVER / 16; ++i)
+                    if (c0 + i * 16 < t.rows)
+                        finish16<NA>(a, t.row0 + c0 + i * 16, t.rows - c0 - i * 16, nn, r[i], al, au);
+            }
+            for (int i = P::OVER; i < TN; i += 16) {
                 const int c = c0 + i < TN ? c0 + i : c0 + i - TN;
                 if (c >= t.rows) continue;
                 uint32_t r[NA * 16];
 #pragma unroll
                 for (int h = 0; h < NA; ++h) tmem_ld16(acc + h * TN + c, *reinterpret_cast<uint32_t(*)[16]>(r + 16 * h));
                 tmem_ld_wait();
-                if (nn < a.N)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float v = __uint_as_float(r[j]) * al;
-                        if constexpr (NA == 2) v = silu_mul(v, __uint_as_float(r[16 + j]) * au);
-                        if (c + j < t.rows) store_one(a, (long long)(t.row0 + c + j) * a.N + nn, v);
-                    }
+                finish16<NA>(a, t.row0 + c, t.rows - c, nn, r, al, au);
             }
         }
     }
