@@ -1,8 +1,8 @@
 // uq_mx_quant.cu -- microscaled 4-bit quantization of rows (optionally gathered by expert), its inverse, and the
 // packing of a checkpoint's scales into tiles.
 //
-// A warp takes 1024 k of one row in four steps of 256, a lane 8 consecutive k of each (one 16-byte load of a 16-bit
-// type, all four requested before the first is used).  A block is then 4 lanes (MXFP4) or 2 (NVFP4): its absmax takes
+// A warp takes 2048 k of one row in eight steps of 256 (512 in two steps when there are too few rows to fill the SMs
+// otherwise), a lane 8 consecutive k of each (one 16-byte load of a 16-bit type, all requested before the first is used).  A block is then 4 lanes (MXFP4) or 2 (NVFP4): its absmax takes
 // one or two shuffles, the codes one 4-byte store per lane, the scales of 4 blocks one 4-byte store.  Memory-bound: each
 // value is read once, whatever the number of rows it is written to.
 #include <type_traits>
@@ -14,8 +14,6 @@ namespace uq {
 namespace {
 
 constexpr int STEP_K = 256;                     // k of a row per warp step
-constexpr int STEPS = 4;
-constexpr int UNIT_K = STEP_K * STEPS;          // k of a row per warp
 
 // 8 values of a row, as loaded
 template <class T> struct Raw {
@@ -49,6 +47,21 @@ template <class T> __device__ __forceinline__ uint32_t absmax8(const Raw<T>& x) 
     }
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // codes of a lane's 8 values and the scale byte of its block (the block's lanes agree on it)
 template <int FMT, class T>
 __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, float tscale, uint32_t& byte) {
@@ -61,23 +74,28 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, floa
         byte = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
         const float inv = __uint_as_float(e == 255 ? 0u : (254u - byte) << 23);    // 2^(127 - byte), a normal number
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.at(i) * inv;                          // exact: a power of two
+        for (int i = 0; i < 8; i += 2) {                                           // exact: a power of two
+            const float2 t = mul2(make_float2(x.at(i), x.at(i + 1)), make_float2(inv, inv));
+            v[i] = t.x;
+            v[i + 1] = t.y;
+        }
     } else {
         const bool bad = am >= 0x7F800000u;
         byte = bad ? 0x7Fu : e4m3_of(__fdiv_rn(__uint_as_float(am), six_t));
         const float d = e4m3_value(byte) * tscale;
-        const bool zero = bad || !(d > 0.f);
-        if constexpr (sizeof(T) == 2) {
-            // x / d as x * (1 / d) with one step of residual correction: a representable quotient comes out exact, so
-            // a tie is a tie; and an x of at most 11 bits over a d of 4 (times a power of two) is no closer to a tie
-            // than 2^-16, far more than the error left.
-            const float r = zero ? 0.f : __frcp_rn(d), nd = zero ? 0.f : -d;
+        if (!bad && d >= 0x1p-100f && d <= 0x1p100f) {
+            // x / d correctly rounded by Markstein's theorem (1990): with r = RN(1 / d) and q an approximation of the
+            // quotient, q + (x - q d) r, the residual by FMA.  A tie has residual 0, so a tie is a tie.
+            const float r = __frcp_rn(d);
+            const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = x.at(i) * r;
-                v[i] = fmaf(fmaf(q, nd, x.at(i)), r, q);
+            for (int i = 0; i < 8; i += 2) {
+                const float2 x2 = make_float2(x.at(i), x.at(i + 1)), q2 = mul2(x2, r2), t = fma2(fma2(q2, nd2, x2), r2, q2);
+                v[i] = t.x;
+                v[i + 1] = t.y;
             }
         } else {
+            const bool zero = bad || !(d > 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = zero ? x.at(i) * 0.f : __fdiv_rn(x.at(i), d);
         }
@@ -85,12 +103,13 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, floa
     return e2m1_pack8(v);
 }
 
-template <class T, int FMT>
+template <class T, int FMT, int STEPS>
 __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ x, long long ldx, uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales, int rows, int K, float tscale,
                                                           const int32_t* __restrict__ offsets, int segments,
                                                           const int32_t* __restrict__ pos, int topk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int UNIT_K = STEP_K * STEPS;                       // k of a row per warp
     constexpr int LPB = FMT == UQ_MXFP4 ? 4 : 2;                 // lanes per block
     constexpr int TPS = STEP_K / mx_tile_k(FMT);                 // scale tiles per step
     const int lane = threadIdx.x & 31;
@@ -114,9 +133,9 @@ __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ 
             uint32_t byte;
             q[i] = quantize8<FMT>(v[i], six_t, tscale, byte);
             if (k0 + i * STEP_K >= K) byte = 0;
-            word[i] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) word[i] |= __shfl_sync(0xffffffffu, byte, first + b * LPB) << (8 * b);
+            byte <<= 8 * ((lane / LPB) & 3);                     // its place in the word of the tile's four blocks
+            byte |= __shfl_xor_sync(0xffffffffu, byte, LPB);
+            word[i] = byte | __shfl_xor_sync(0xffffffffu, byte, 2 * LPB);
         }
         const int kt0 = k0 / mx_tile_k(FMT);
         const int routes = pos ? topk : 1;
@@ -145,10 +164,11 @@ __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ 
     }
 }
 
-template <class T, int FMT>
+template <class T, int FMT, int STEPS>
 __global__ void __launch_bounds__(128) dequant_mx_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                          T* __restrict__ out, int rows, int K, float tscale,
                                                          const int32_t* __restrict__ offsets, int segments) {
+    constexpr int UNIT_K = STEP_K * STEPS;
     const int lane = threadIdx.x & 31;
     const unsigned units_k = (unsigned)(K + UNIT_K - 1) / UNIT_K;
     const int ktiles = mx_ktiles(K, FMT);
@@ -208,34 +228,40 @@ int grid_for(long long units, int per_block, int sms, int waves) {
 
 }  // namespace
 
+namespace {
+// calls f(steps as a constant, grid): long units where they still give every SM its warps
+template <class F> cudaError_t with_steps(int rows, int K, int sms, F&& f) {
+    const auto units = [&](int steps) { return (long long)rows * ((K + STEP_K * steps - 1) / (STEP_K * steps)); };
+    if (units(8) >= 16LL * sms) return f(std::integral_constant<int, 8>(), grid_for(units(8), 4, sms, 64));
+    return f(std::integral_constant<int, 2>(), grid_for(units(2), 4, sms, 64));
+}
+}  // namespace
+
 cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
                                int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
                                int topk, int sms, cudaStream_t st) {
-    const int grid = grid_for((long long)rows * ((K + UNIT_K - 1) / UNIT_K), 4, sms, 64);
-    return with_dtype(xtype, [&](auto t) {
-        using T = decltype(t);
-        if (fmt == UQ_MXFP4)
-            quantize_mx_kernel<T, UQ_MXFP4><<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
-                                                                  tscale, offsets, segments, pos, topk);
-        else
-            quantize_mx_kernel<T, UQ_NVFP4><<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K,
-                                                                  tscale, offsets, segments, pos, topk);
-        return cudaGetLastError();
+    return with_steps(rows, K, sms, [&](auto steps, int grid) {
+        return with_dtype(xtype, [&](auto t) {
+            using T = decltype(t);
+            constexpr int S = decltype(steps)::value;
+            auto kernel = fmt == UQ_MXFP4 ? quantize_mx_kernel<T, UQ_MXFP4, S> : quantize_mx_kernel<T, UQ_NVFP4, S>;
+            kernel<<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K, tscale, offsets, segments,
+                                         pos, topk);
+            return cudaGetLastError();
+        });
     });
 }
 
 cudaError_t launch_dequant_mx(int fmt, const uint8_t* codes, const uint8_t* scales, void* out, int type, int rows, int K,
                               float tscale, const int32_t* offsets, int segments, int sms, cudaStream_t st) {
-    const int grid = grid_for((long long)rows * ((K + UNIT_K - 1) / UNIT_K), 4, sms, 64);
-    return with_dtype(type, [&](auto t) {
-        using T = decltype(t);
-        if (fmt == UQ_MXFP4)
-            dequant_mx_kernel<T, UQ_MXFP4><<<grid, 128, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
-                                                                 offsets, segments);
-        else
-            dequant_mx_kernel<T, UQ_NVFP4><<<grid, 128, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale,
-                                                                 offsets, segments);
-        return cudaGetLastError();
+    return with_steps(rows, K, sms, [&](auto steps, int grid) {
+        return with_dtype(type, [&](auto t) {
+            using T = decltype(t);
+            constexpr int S = decltype(steps)::value;
+            auto kernel = fmt == UQ_MXFP4 ? dequant_mx_kernel<T, UQ_MXFP4, S> : dequant_mx_kernel<T, UQ_NVFP4, S>;
+            kernel<<<grid, 128, 0, st>>>(codes, scales, static_cast<T*>(out), rows, K, tscale, offsets, segments);
+            return cudaGetLastError();
+        });
     });
 }
 

@@ -97,6 +97,28 @@ def test_quantize_limits_and_non_finite(fmt):
     assert np.isnan(got[3, :n]).all() and np.isfinite(got[3, n:]).all()             # the block only
 
 
+@pytest.mark.parametrize("tscale", [1.0, 0.0371, 2.0 ** -110])
+def test_quantize_nvfp4_quotients_at_and_next_to_ties(tscale):
+    """fp32 values on, one ulp below and one ulp above every midpoint of the element grid, for every scale mantissa: the
+    fp32 quotient decides, so the codes are the oracle's bit for bit (also where the scale is too small for a reciprocal)."""
+    t = np.float32(tscale)
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    rows = []
+    for b in range(0x20, 0x60):                                                     # e4m3 scales 2^-3 .. 2^4
+        d = np.float32(omx.E4M3[b]) * t
+        x = np.zeros(32, np.float32)
+        x[0] = x[16] = np.float32(6) * d
+        for i, m in enumerate(mids):
+            c = m * d
+            x[1 + i], x[8 + i] = c, np.nextafter(c, np.float32(0))
+            x[17 + i], x[24 + i] = np.nextafter(c, np.float32(np.inf)), -c
+        rows.append(x)
+    x = np.stack(rows)
+    codes, _ = uq.quantize_mx(torch.from_numpy(x).to(DEV), "NVFP4", tscale=tscale)
+    oc, _ = omx.quantize(x, "NVFP4", tscale)
+    assert np.array_equal(codes.cpu().numpy(), omx.pack_codes(oc))
+
+
 def test_quantize_strided_rows():
     big = _x(9, 20, 1024).to(DEV)
     part = big[3:17:2, 64:576]                                                      # row stride 2048, offset 64
