@@ -33,6 +33,7 @@ struct MxGemmMaps {
     CUtensorMap w, x, w_scales, x_scales, up, up_scales;
 };
 
+constexpr int MAX_SPLIT = 8;                    // CTAs of a cluster sharing a tile's steps
 constexpr int MAX_STAGES = 12;
 constexpr int HEAD = 1024;                      // barriers and flags before the stages
 
@@ -139,10 +140,10 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
 
@@ -256,11 +257,25 @@ struct Schedule {
     __device__ __forceinline__ void advance() { tile += stride; }
 };
 
-// One output element; the split tiles' path.
-__device__ __forceinline__ void store_one(const MxGemmArgs& a, long long at, float v) {
-    if (a.ytype == UQ_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
-    else if (a.ytype == UQ_FP16) static_cast<__half*>(a.y)[at] = __float2half_rn(v);
-    else static_cast<float*>(a.y)[at] = v;
+// Up to four neighbouring outputs (count of them) at element `at`; the split tiles' path.
+__device__ __forceinline__ void store4(const MxGemmArgs& a, long long at, int count, const float (&v)[4]) {
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        T* y = static_cast<T*>(a.y) + at;
+        if (count >= 4 && a.N % 4 == 0) {
+            Vec<T, 4> o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o.v[i] = from_f32<T>(v[i]);
+            *reinterpret_cast<Vec<T, 4>*>(y) = o;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) y[i] = from_f32<T>(v[i]);
+        }
+    };
+    if (a.ytype == UQ_BF16) go(__nv_bfloat16());
+    else if (a.ytype == UQ_FP16) go(__half());
+    else go(float());
 }
 __device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
     uint32_t d;
@@ -533,19 +548,32 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             const Tile t = find_tile(a, before, tt_all, mine.tile);
             const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
             const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
-            const uint32_t sums = ring0;
-            for (int it = (blockIdx.x % a.S) * THREADS + threadIdx.x; it < t.rows * 128; it += a.S * THREADS) {
-                const int c = it >> 7, r = it & 127, nn = t.nt * 128 + r;
+            // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
+            for (int it = (blockIdx.x % a.S) * THREADS + threadIdx.x; it < t.rows * 32; it += a.S * THREADS) {
+                const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
                 if (nn >= a.N) continue;
-                float v = 0.f, u = 0.f;
-#pragma unroll 8
-                for (int k = 0; k < a.S; ++k) {
-                    v += ld_cluster(sums + (c * NA * 128 + r) * 4, k);
-                    if constexpr (NA == 2) u += ld_cluster(sums + ((c * NA + 1) * 128 + r) * 4, k);
+                float4 p[MAX_SPLIT * NA];
+#pragma unroll
+                for (int k = 0; k < MAX_SPLIT; ++k)
+#pragma unroll
+                    for (int h = 0; h < NA; ++h)
+                        p[k * NA + h] = k < a.S ? ld_cluster4(ring0 + ((c * NA + h) * 128 + r) * 4, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float v[4] = {}, u[4] = {};
+#pragma unroll
+                for (int k = 0; k < MAX_SPLIT; ++k) {
+                    const float4 x = p[k * NA];
+                    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                    if constexpr (NA == 2) {
+                        const float4 y = p[k * NA + 1];
+                        u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+                    }
                 }
-                v *= al;
-                if constexpr (NA == 2) v = silu_mul(v, u * au);
-                store_one(a, (long long)(t.row0 + c) * a.N + nn, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] *= al;
+                    if constexpr (NA == 2) v[i] = silu_mul(v[i], u[i] * au);
+                }
+                store4(a, (long long)(t.row0 + c) * a.N + nn, a.N - nn, v);
             }
         }
         cluster_sync();                                            // no CTA leaves while another reads its sums
@@ -933,6 +961,26 @@ template <int NA> void pair_ring(int fmt, MxGemmArgs& a) {
                                             : Pair<UQ_NVFP4, NA>::STAGES * Pair<UQ_NVFP4, NA>::STAGE);
 }
 
+// Whether pairs of CTAs are the faster of the two kernels.
+//   One weight for all rows: by waves.  A wave of 128 x 128 tiles takes 625 cycles per 512 k (NVFP4 736), one of 256 x 256
+// pair tiles 1026 (less with fewer than 256 token columns; both measured alone), and the pairs' start and end cost about
+// 3000 cycles more.  Measured, us single / pairs, MXFP4: N = K = 8192: M = 256 13.4 / 16.5, 512 20.6 / 17.5, 2048 60.7 /
+// 49.7; N = K = 4096: M = 512 10.3 / 12.4, 2048 22.6 / 18.6; 14336 x 4096: M = 128 9.3 / 11.3, 256 14.4 / 13.4, 512 18.6 /
+// 19.5, 1024 30.8 / 25.0.
+//   Rows by expert: from 128 rows an expert on, where there are pair tiles for every pair.  Measured, 8 experts of 4096 x
+// 4096, mean rows 64 16.5 / 18.7, 128 20.7 / 20.2, 192 26.7 / 20.7, 512 45.3 / 35.8; gated 128 51.4 / 43.2; 32 experts of
+// 2048 x 2048: 64 20.4 / 22.7, 128 24.9 / 24.7, 256 35.1 / 36.9, 512 51.6 / 47.2.
+bool pays_in_pairs(int fmt, bool gated, const MxGemmArgs& a, int mean, int sms) {
+    const long long pair_n = (a.N + 255) / 256;
+    if (a.offsets) return mean >= 128 && 2 * pair_n * (a.rows / (gated ? 128 : 256) + a.experts / 2) >= sms;
+    if (a.rows <= 64) return false;
+    const long long steps = (a.K + 511) / 512, tiles = (long long)((a.N + 127) / 128) * ((a.rows + 127) / 128);
+    const long long waves = (tiles + sms - 1) / sms, pair_waves = (2 * pair_n * ((a.rows + 255) / 256) + sms - 1) / sms;
+    const int split = tiles * 2 <= sms ? (int)std::min((long long)MAX_SPLIT, sms / tiles) : 1;
+    const long long single = waves * steps * (fmt == UQ_MXFP4 ? 625 : 736) / split + (split > 1 ? 3000 : 0);
+    return pair_waves * steps * 1026 * std::min(a.rows, 256) / 256 + 3000 < single;
+}
+
 // Tiles, ring and grid of one product.
 void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const int NA = gated ? 2 : 1;
@@ -942,9 +990,7 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     // token tile: the rows an expert gets on average (all of them when there is one).  Under 64 only where no second
     // tile can follow: a tile's scale columns then always start at an even column.
     const int mean = a.offsets ? (a.rows + a.experts - 1) / a.experts : a.rows;
-    // pairs of CTAs where there are rows for their wide tiles and tiles for most of the pairs
-    const long long pairs = ((a.N + 255) / 256) * (a.rows / (256 / NA) + (a.offsets ? a.experts / 2 : 1));
-    a.pair = a.rows >= 256 && mean >= 128 && pairs * 2 >= sms;
+    a.pair = pays_in_pairs(fmt, gated, a, mean, sms);
     if (a.pair) {
         if (gated) pair_ring<2>(fmt, a);
         else pair_ring<1>(fmt, a);
@@ -969,16 +1015,16 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const long long tiles = tt * a.NT;
     // CTAs per tile: the fewest that give each the fewest steps
     a.S = 1;
-    const int most = tiles * 2 <= sms ? std::min(8, std::min((int)(sms / tiles), a.steps)) : 1;
+    const int most = tiles * 2 <= sms ? std::min(MAX_SPLIT, std::min((int)(sms / tiles), a.steps)) : 1;
     for (int s = 2; s <= most; ++s)
         if ((a.steps + s - 1) / s < (a.steps + a.S - 1) / a.S) a.S = s;
     a.ctas = a.S > 1 ? (int)tiles * a.S : (int)std::min(tiles, (long long)sms);
     a.folded = a.K % 256 == 0;
     const int stage_bytes = NA * 128 * (STEP_K / 2) + a.TN * (STEP_K / 2) + (NA + 1) * tps * 512;
-    // tensor memory: two accumulators where 512 columns hold them beside three stages of scales
-    const int sf = (NA + 1) * tps * 4;
-    a.accs = 2 * NA * a.TN + 3 * sf <= 512 ? 2 : 1;
-    a.stages = std::min(std::min((222 * 1024 - HEAD - table) / stage_bytes, MAX_STAGES), (512 - a.accs * NA * a.TN) / sf);
+    // tensor memory: two accumulators where 512 columns hold them beside the scales of the stages that fit (of three)
+    const int sf = (NA + 1) * tps * 4, fit = std::min((222 * 1024 - HEAD - table) / stage_bytes, MAX_STAGES);
+    a.accs = 2 * NA * a.TN + std::min(fit, 3) * sf <= 512 ? 2 : 1;
+    a.stages = std::min(fit, (512 - a.accs * NA * a.TN) / sf);
     const int cols = a.accs * NA * a.TN + a.stages * sf;
     a.tmem_cols = cols <= 64 ? 64 : (cols <= 128 ? 128 : (cols <= 256 ? 256 : 512));
     a.smem = 1024 + HEAD + a.stages * stage_bytes + table;

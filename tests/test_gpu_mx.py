@@ -164,7 +164,7 @@ def test_pack_mx_scales(fmt):
 # (M, N, K): one row to several token tiles, odd N, K of one block, K that ends inside a step, split k
 SHAPES = [(1, 128, 32), (1, 1, 256), (3, 200, 96), (17, 384, 1056), (32, 130, 320), (33, 257, 512), (64, 1024, 4096),
           (65, 512, 2080), (100, 136, 14336), (129, 640, 1024), (300, 1000, 544), (520, 2320, 256),
-          (1100, 4100, 544), (2049, 2304, 96)]
+          (1100, 4100, 544), (2049, 2304, 96), (1000, 8100, 4128)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
