@@ -981,9 +981,15 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     a.experts = 1;
     a.N = N;
     a.K = K;
-    // an x quantized here lives in the workspace: codes | scale tiles
     if ((s = check_tiles(M, 1, N)) != UQ_OK) return s;
-    if (!xscales) {
+    if (!xscales) a.alpha = alpha * tscale_x;
+    if (!xscales && uq::mx_gemm_quantizes(M)) {
+        a.xraw = x;
+        a.ldx = ldx;
+        a.xtype = xtype;
+        a.tscale = tscale_x;
+    } else if (!xscales) {
+        // the quantized x lives in the workspace: codes | scale tiles
         const size_t code_bytes = ((size_t)M * (K / 2) + 255) / 256 * 256;
         Workspace* ws = nullptr;
         if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
@@ -993,7 +999,6 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
         if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
         xcodes = codes;
         a.xscales = codes + code_bytes;
-        a.alpha = alpha * tscale_x;
         a.wait = 1;
     }
     e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, ds->sms, st);

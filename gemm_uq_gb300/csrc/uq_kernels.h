@@ -187,6 +187,10 @@ struct MxGemmArgs {
     float alpha;
     int ytype, rows, experts, N, K;
     int wait;                 // launched with programmatic serialization behind the kernel that writes x
+    const void* xraw;         // few tokens that the kernel quantizes itself (xcodes and xscales unused), or NULL
+    long long ldx;
+    int xtype;
+    float tscale;
     // set by launch_mx_gemm:
     int steps;                // k steps
     int ktiles;               // scale tiles along K
@@ -198,6 +202,7 @@ struct MxGemmArgs {
     int accs, stages;         // accumulators, ring stages
     int tmem_cols, smem, ctas;
 };
+bool mx_gemm_quantizes(int rows);   // whether a product of so many tokens quantizes them itself
 cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up, MxGemmArgs a,
                            int sms, cudaStream_t st);
 

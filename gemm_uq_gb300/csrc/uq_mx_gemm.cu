@@ -20,13 +20,16 @@
 #include <cuda.h>
 #include <algorithm>
 
-#include "uq_mx.cuh"
+#include "uq_mx_quant.cuh"
 
 namespace uq {
 
 namespace {
 
 constexpr int THREADS = 224;
+constexpr int QUANT_WARPS = 4;                  // of the kernel that quantizes the tokens itself, in place of warp 6
+constexpr int FUSED_THREADS = THREADS + (QUANT_WARPS - 1) * 32;
+constexpr int FUSED_ROWS = 2;                   // its most tokens (rule at mx_gemm_quantizes)
 constexpr int STEP_K = 512;                     // k per stage: two 128-byte columns of a row, eight MMAs of 64
 // The tensor maps of a launch.
 struct MxGemmMaps {
@@ -339,8 +342,78 @@ __device__ __forceinline__ void finish16(const MxGemmArgs& a, int m0, int count,
     else put16<float>(a, m0, count, nn, v);
 }
 
-template <int FMT, int NA>
-__global__ void __launch_bounds__(THREADS, 1)
+// Quantizes the tokens (at most FUSED_ROWS) of every step of this CTA straight into the ring, in the layouts TMA would
+// have left.  A unit is 256 k of one row; a step has 2 * rows units, and warp w of the quantizers takes every fourth,
+// eight lanes' values of four units requested ahead of the four being quantized.  Every CTA quantizes the same rows,
+// which for few rows costs less than a launch of its own before (rule at mx_gemm_quantizes).
+template <int FMT, class T>
+__device__ __forceinline__ void quantize_tokens(const MxGemmArgs& a, Schedule sch, int w, uint32_t tokens0, int stage_bytes,
+                                                uint32_t sf_off, uint32_t full0, uint32_t empty0, volatile int* abort_flag) {
+    constexpr int TPS = STEP_K / mx_tile_k(FMT), AHEAD = 4;
+    constexpr int LANES = mx_tile_k(FMT) / 8;                      // lanes of a scale tile
+    const int lane = threadIdx.x & 31, per = 2 * a.rows;           // units of a step
+    const T* x = static_cast<const T*>(a.xraw);
+    const float six_t = 6.f * a.tscale;
+    int tiles = 0;
+    for (; sch.more(); sch.advance()) ++tiles;
+    const int steps = sch.k1 - sch.k0, total = (tiles * steps * per - w + QUANT_WARPS - 1) / QUANT_WARPS;
+    int ls = w / per % steps, lu = w % per;                        // step and unit to be requested next
+    Raw<T> cur[AHEAD] = {}, nxt[AHEAD] = {};
+    auto request = [&](Raw<T> (&v)[AHEAD]) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = (sch.k0 + ls) * STEP_K + (lu & 1) * 256 + lane * 8;
+            v[i] = Raw<T>{};
+            if (k < a.K) v[i].load(x + (long long)(lu >> 1) * a.ldx + k);
+            lu += QUANT_WARPS;
+            while (lu >= per) {
+                lu -= per;
+                if (++ls == steps) ls = 0;
+            }
+        }
+    };
+    // the unit being quantized: its step's stage, how many steps have gone before, k step, unit of the step
+    int n = w / per, s = n % a.stages, kt = sch.k0 + n % steps, un = w % per;
+    uint32_t ph = 1u ^ (uint32_t)(n / a.stages & 1);
+    request(cur);
+    for (int u = 0; u < total; u += AHEAD) {
+        if (u + AHEAD < total) request(nxt);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (u + i >= total) break;
+            if (n >= a.stages && !warp_wait(empty0 + s * 8, ph, a.fault, abort_flag)) {
+                *abort_flag = 1;
+                return;
+            }
+            const int r = un >> 1, h = un & 1;
+            const uint32_t st = tokens0 + s * stage_bytes;
+            uint32_t byte;
+            const uint32_t q = quantize8<FMT>(cur[i], six_t, a.tscale, byte);
+            if (kt * STEP_K + h * 256 + lane * 8 >= a.K) byte = 0; // (q is 0 there)
+            const uint32_t word = scale_word<FMT>(byte, lane);
+            // 128-byte column h of the row, 16-byte parts swizzled by the row
+            asm volatile("st.shared.b32 [%0], %1;" :: "r"(st + h * (a.TN * 128) + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4), "r"(q) : "memory");
+            if (lane % LANES == 0)
+                asm volatile("st.shared.b32 [%0], %1;" :: "r"(st + sf_off + (h * (TPS / 2) + lane / LANES) * 512 + r * 16), "r"(word) : "memory");
+            fence_proxy_async_smem();                              // the MMAs read through the async proxy
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(full0 + s * 8) : "memory");
+            un += QUANT_WARPS;
+            while (un >= per) {
+                un -= per;
+                ++n;
+                if (++kt == sch.k1) kt = sch.k0;
+                if (++s == a.stages) { s = 0; ph ^= 1; }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) cur[i] = nxt[i];
+    }
+}
+
+// FUSED: the tokens are quantized in the kernel
+template <int FMT, int NA, bool FUSED>
+__global__ void __launch_bounds__(FUSED ? FUSED_THREADS : THREADS, 1)
 mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     constexpr int TPS = STEP_K / mx_tile_k(FMT);                   // scale tiles per step and 128 rows
     constexpr int A_BYTES = 128 * (STEP_K / 2), SF_BYTES = TPS * 512;
@@ -394,7 +467,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         if (a.offsets) token_tiles(a, before);
         if (lane == 0) {
             for (int s = 0; s < a.stages; ++s) {
-                mbar_init(&full[s], 2);
+                mbar_init(&full[s], FUSED ? 1 + 2 * a.rows : 2);
                 mbar_init(&empty[s], 1);
             }
             for (int i = 0; i < 2; ++i) {
@@ -425,7 +498,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         tmem = (uint32_t)uniform((int)*tmem_ptr);
     }
 
-    if (warp == 0 || warp == 6) {
+    if (warp == 0 || (!FUSED && warp == 6)) {
         // ------------------------------------------------------------ producers
         // The weights do not depend on the kernel before, the tokens may.
         const bool tokens = warp == 6;
@@ -509,6 +582,17 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             commit(smem_u32(drain));
             mbar_wait_bounded(drain, 0, a.fault, FAULT_MX_WAIT);
         }
+    } else if (FUSED && warp >= 6) {
+        // ------------------------------------------------------------ quantizers
+        if constexpr (FUSED) {
+            const uint32_t tokens0 = ring0 + NA * A_BYTES, sf_off = b_bytes + NA * SF_BYTES;
+            if (a.xtype == UQ_BF16)
+                quantize_tokens<FMT, __nv_bfloat16>(a, sch, warp - 6, tokens0, stage_bytes, sf_off, full0, empty0, abort_flag);
+            else if (a.xtype == UQ_FP16)
+                quantize_tokens<FMT, __half>(a, sch, warp - 6, tokens0, stage_bytes, sf_off, full0, empty0, abort_flag);
+            else
+                quantize_tokens<FMT, float>(a, sch, warp - 6, tokens0, stage_bytes, sf_off, full0, empty0, abort_flag);
+        }
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue: lane = row of the weight tile
         const int q = warp & 3, row = q * 32 + lane, et = threadIdx.x - 64;
@@ -562,7 +646,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
             const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
             // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
-            for (int it = (blockIdx.x % a.S) * THREADS + threadIdx.x; it < t.rows * 32; it += a.S * THREADS) {
+            for (int it = (blockIdx.x % a.S) * (int)blockDim.x + threadIdx.x; it < t.rows * 32; it += a.S * (int)blockDim.x) {
                 const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
                 if (nn >= a.N) continue;
                 float4 p[MAX_SPLIT * NA];
@@ -930,23 +1014,23 @@ bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int NA>
-cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st) {
-    static bool configured[64] = {};
+// Opts a kernel into its shared memory, once per device.
+template <class K> cudaError_t configure(K kernel, bool (&done)[64]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
-        e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(mx_gemm_pair_kernel<FMT, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e != cudaSuccess) return e;
-        configured[dev] = true;
-    }
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+template <int FMT, int NA>
+cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.ctas);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(a.xraw ? FUSED_THREADS : THREADS);
     cfg.dynamicSmemBytes = a.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -963,8 +1047,15 @@ cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st)
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return a.pair ? cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<FMT, NA>, maps, a)
-                  : cudaLaunchKernelEx(&cfg, mx_gemm_kernel<FMT, NA>, maps, a);
+    auto go = [&](auto kernel, bool (&done)[64]) {
+        const cudaError_t e = configure(kernel, done);
+        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, maps, a) : e;
+    };
+    static bool pair_done[64] = {}, one_done[64] = {}, fused_done[64] = {};
+    if (a.pair) return go(mx_gemm_pair_kernel<FMT, NA>, pair_done);
+    if constexpr (NA == 1)
+        if (a.xraw) return go(mx_gemm_kernel<FMT, 1, true>, fused_done);
+    return go(mx_gemm_kernel<FMT, NA, false>, one_done);
 }
 
 // Stage count and size of the pair kernel.
@@ -1045,6 +1136,12 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
 
 }  // namespace
 
+// One launch instead of two up to FUSED_ROWS tokens: a call then takes 7.4 us of host time instead of 10, and on the GPU
+// (graph replay, us one launch / two) MXFP4 14336 x 4096 M = 1 7.6 / 8.2, M = 2 8.9 / 8.6, M = 3 8.9 / 8.2, M = 4 10.8 / 8.9;
+// 4096 x 14336 9.6 / 10.3, 10.3 / 9.7, 10.3 / 9.8, 11.6 / 10.3; 1024 x 4096 6.4 / 6.9, 6.9 / 7.5, 6.9 / 7.5, 6.9 / 7.5.
+// From 3 tokens on the quantizing warps hold up long streams of weights.
+bool mx_gemm_quantizes(int rows) { return rows <= FUSED_ROWS; }
+
 cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up,
                            MxGemmArgs a, int sms, cudaStream_t st) {
     if (!encode_fn()) return cudaErrorNotSupported;
@@ -1052,10 +1149,15 @@ cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes
     MxGemmMaps m;
     const int tps = (a.pair ? PAIR_STEP : STEP_K) / mx_tile_k(fmt);
     const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.row_tiles;
-    bool ok = codes_map(&m.w, wcodes, wrows, a.K, 128, a.folded) && scales_map(&m.w_scales, a.wscales, wtiles, a.ktiles, tps, 1) &&
-              codes_map(&m.x, xcodes, a.rows, a.K, a.pair ? a.TN / 2 : a.TN, a.folded) &&
+    bool ok = codes_map(&m.w, wcodes, wrows, a.K, 128, a.folded) && scales_map(&m.w_scales, a.wscales, wtiles, a.ktiles, tps, 1);
+    if (a.xraw) {
+        m.x = m.w;
+        m.x_scales = m.w_scales;
+    } else {
+        ok = ok && codes_map(&m.x, xcodes, a.rows, a.K, a.pair ? a.TN / 2 : a.TN, a.folded) &&
               scales_map(&m.x_scales, a.xscales, mx_row_tiles(a.rows, a.offsets ? a.experts : 0), a.ktiles, tps,
-                         a.pair ? a.TN / 128 : 1);
+                        a.pair ? a.TN / 128 : 1);
+    }
     m.up = m.w;
     m.up_scales = m.w_scales;
     if (wcodes_up)

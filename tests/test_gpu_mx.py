@@ -185,6 +185,24 @@ def test_product_parity(fmt, M, N, K):
     assert uq.device_fault() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 20000, 544), (2, 20000, 1056), (2, 130, 14336), (1, 19, 32), (3, 20000, 544)])
+def test_product_of_few_tokens_quantizes_the_same_in_one_launch(fmt, dtype, M, N, K):
+    """One or two tokens are quantized inside the product's kernel: the same bits as quantized before, for every type,
+    strided rows, several tiles a CTA, K that ends inside a step, and a k split."""
+    rng = np.random.default_rng([M, N, K])
+    codes = torch.from_numpy(rng.integers(0, 256, (N, K // 2), dtype=np.uint8)).to(DEV)
+    byte = rng.integers(110, 130, (N, K // omx.BLOCK[fmt])).astype(np.uint8) if fmt == "MXFP4" else \
+        rng.integers(0x08, 0x60, (N, K // omx.BLOCK[fmt])).astype(np.uint8)
+    w = (codes, torch.from_numpy(omx.tile_scales(byte, fmt)).to(DEV))
+    x = _x(M + K, 2 * M, K + 64, dtype).to(DEV)[::2, 32:32 + K]
+    t = 1.0 if fmt == "MXFP4" else 0.5
+    y = uq.gemm_mx(x, w, fmt, tscale=t, dtype=torch.float32)
+    z = uq.gemm_mx(uq.quantize_mx(x, fmt, tscale=t), w, fmt, alpha=t, dtype=torch.float32)
+    assert torch.equal(y, z) and uq.device_fault() == 0
+
+
 def test_product_scales_strides_and_empty():
     N, K = 192, 512
     w = np.random.default_rng(2).normal(size=(N, K)).astype(np.float32)
