@@ -15,6 +15,9 @@
 // and two accumulators let the epilogue of one tile run under the next one's MMAs.  Where tiles would fill at most half
 // of the SMs, a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through distributed shared memory
 // in rank order, so equal calls give equal bits.
+// One GB300, graph replay: 1 x 14336 x 4096 MXFP4 7.6 us (4.1 TB/s), 37 x 4096 x 14336 NVFP4 11.6 us; large products on
+// pairs of CTAs (below) 8192^3 MXFP4 156 us (7.0 PFLOP/s).  What bounds them: few tokens start and end of a kernel (3 us)
+// and then memory; many the tensor cores.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is
 // freed, and the fault word tells.
 #include <cuda.h>
@@ -153,12 +156,19 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
 // A whole warp's wait: false for all lanes once WAIT_LIMIT_NS have passed (the fault word then tells) or the CTA was
 // told to stop.  Polls without a suspend hint: a warp put to sleep for up to a microsecond woke too late for a ring
 // whose steps take a quarter of that.
+// CLUSTER: arrivals of the pair's other CTA count on the barrier.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned int* fault, volatile int* abort_flag) {
     unsigned long long t0 = 0;
     for (unsigned int i = 0;; ++i) {
         uint32_t ok;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if constexpr (CLUSTER)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
         if (__all_sync(0xffffffffu, ok)) return true;
         if (i % 32 == 0) {
             bool stop = *abort_flag != 0;
@@ -842,7 +852,7 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
             const int row = uniform(t.row0) + (int)rank * (columns(t) >> 1);
             const int xtile = (a.offsets ? (uniform(t.row0 - t.first) >> 7) + e : 0) + (uniform(t.first) >> 7);
             for (int kt = 0; kt < a.steps; ++kt) {
-                if (issued >= P::STAGES && !warp_wait(empty0 + s * 8, ph, a.fault, abort_flag)) {
+                if (issued >= P::STAGES && !warp_wait<true>(empty0 + s * 8, ph, a.fault, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -881,11 +891,11 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
             const uint32_t idesc = block_idesc<FMT>(columns(t)) + (1u << 27);      // M = 256
             const uint32_t acc = tmem + (n & 1) * (256 - P::OVER);
             // the epilogue of the tile before has read the shared columns
-            if (n && !warp_wait(smem_u32(acc_free), (uint32_t)(n - 1) & 1, a.fault, abort_flag)) ok = false;
+            if (n && !warp_wait<true>(smem_u32(acc_free), (uint32_t)(n - 1) & 1, a.fault, abort_flag)) ok = false;
             fence_after();
             uint32_t on = 0;
             for (int kt = 0; ok && kt < a.steps; ++kt) {
-                if (!warp_wait(full0 + s * 8, ph, a.fault, abort_flag)) {
+                if (!warp_wait<true>(full0 + s * 8, ph, a.fault, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -933,7 +943,7 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
             const Tile t = find_tile(a, before, tt_all, tile);
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * (256 - P::OVER);
             // after a timeout the tiles are walked without waiting
-            if (!warp_wait(smem_u32(&acc_full[n & 1]), (uint32_t)(n >> 1) & 1, a.fault, abort_flag)) *abort_flag = 1;
+            if (!warp_wait<true>(smem_u32(&acc_full[n & 1]), (uint32_t)(n >> 1) & 1, a.fault, abort_flag)) *abort_flag = 1;
             __syncwarp();
             fence_after();
             const int nn = t.nt * 256 + (int)rank * 128 + row;
