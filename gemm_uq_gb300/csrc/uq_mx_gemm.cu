@@ -192,7 +192,10 @@ struct Tile {
 };
 __device__ __forceinline__ int offset_of(const MxGemmArgs& a, int e) { return min(max(__ldg(a.offsets + e), 0), a.rows); }
 
-// `before`: token tiles before each expert (shared memory, experts + 1 entries), unused when there is one weight
+// The table of the experts' token tiles (shared memory): tiles before each expert, then each expert's first row,
+// experts + 1 entries both.
+__host__ __device__ constexpr int table_bytes(int experts) { return 2 * (experts + 1) * 4; }
+
 __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before, int tt_all, int tile) {
     Tile t;
     const int per = a.group * tt_all, g = tile / per, in = tile - g * per;
@@ -206,8 +209,9 @@ __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before
             const int mid = (e + hi) >> 1;
             if (before[mid] <= tt) e = mid; else hi = mid;
         }
-        r0 = offset_of(a, e);
-        r1 = max(offset_of(a, e + 1), r0);
+        const int* start = before + a.experts + 1;
+        r0 = start[e];
+        r1 = max(start[e + 1], r0);
         lt = tt - before[e];
     }
     t.expert = e;
@@ -217,23 +221,43 @@ __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before
     return t;
 }
 
-// Fills `before` (one warp).
+// Fills the table (one warp).  128 experts at a time, all their offsets requested before the first is used.
 __device__ __forceinline__ void token_tiles(const MxGemmArgs& a, int* before) {
     const int lane = threadIdx.x & 31;
+    int* start = before + a.experts + 1;
     int run = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-        const int e = e0 + lane;
-        const int n = e < a.experts ? (max(offset_of(a, e + 1) - offset_of(a, e), 0) + a.TN - 1) / a.TN : 0;
-        int incl = n;
+    for (int e0 = 0; e0 < a.experts; e0 += 128) {
+        int o[5];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+        for (int j = 0; j < 5; ++j) o[j] = offset_of(a, min(e0 + lane * 4 + j, a.experts));
+        int n[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            n[j] = (max(o[j + 1] - o[j], 0) + a.TN - 1) / a.TN;    // 0 past the last expert
+            sum += n[j];
         }
-        if (e < a.experts) before[e] = run + incl - n;
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        int at = run + incl - sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = e0 + lane * 4 + j;
+            if (e < a.experts) {
+                before[e] = at;
+                start[e] = o[j];
+            }
+            at += n[j];
+        }
         run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) before[a.experts] = run;
+    if (lane == 0) {
+        before[a.experts] = run;
+        start[a.experts] = offset_of(a, a.experts);
+    }
     __syncwarp();
 }
 
@@ -363,7 +387,7 @@ __device__ __forceinline__ void quantize_tokens(const MxGemmArgs& a, Schedule sc
     constexpr int LANES = mx_tile_k(FMT) / 8;                      // lanes of a scale tile
     const int lane = threadIdx.x & 31, per = 2 * a.rows;           // units of a step
     const T* x = static_cast<const T*>(a.xraw);
-    const float six_t = 6.f * a.tscale;
+    const SixT six(a.tscale);
     int tiles = 0;
     for (; sch.more(); sch.advance()) ++tiles;
     const int steps = sch.k1 - sch.k0, total = (tiles * steps * per - w + QUANT_WARPS - 1) / QUANT_WARPS;
@@ -398,7 +422,7 @@ __device__ __forceinline__ void quantize_tokens(const MxGemmArgs& a, Schedule sc
             const int r = un >> 1, h = un & 1;
             const uint32_t st = tokens0 + s * stage_bytes;
             uint32_t byte;
-            const uint32_t q = quantize8<FMT>(cur[i], six_t, a.tscale, byte);
+            const uint32_t q = quantize8<FMT>(cur[i], six, a.tscale, byte);
             if (kt * STEP_K + h * 256 + lane * 8 >= a.K) byte = 0; // (q is 0 there)
             const uint32_t word = scale_word<FMT>(byte, lane);
             // 128-byte column h of the row, 16-byte parts swizzled by the row
@@ -439,7 +463,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     uint8_t* ring = head + HEAD;
     const int TN = a.TN, AB = a.accs;
     const int b_bytes = TN * (STEP_K / 2), stage_bytes = NA * A_BYTES + b_bytes + (NA + 1) * SF_BYTES;
-    int* before = reinterpret_cast<int*>(ring + (size_t)a.stages * stage_bytes);   // [experts + 1]
+    int* before = reinterpret_cast<int*>(ring + (size_t)a.stages * stage_bytes);   // the table, when rows are by expert
 
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -1100,7 +1124,7 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const int NA = gated ? 2 : 1;
     a.ktiles = mx_ktiles(a.K, fmt);
     a.row_tiles = (a.N + 127) / 128;
-    const int table = a.offsets ? (a.experts + 1) * 4 : 0;
+    const int table = a.offsets ? table_bytes(a.experts) : 0;
     // token tile: the rows an expert gets on average (all of them when there is one).  Under 64 only where no second
     // tile can follow: a tile's scale columns then always start at an even column.
     const int mean = a.offsets ? (a.rows + a.experts - 1) / a.experts : a.rows;

@@ -55,9 +55,23 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+// The divisor of the NVFP4 scales, 6 t, and its reciprocal.  divide() is a correctly rounded quotient by Markstein's
+// theorem (1990): with r = RN(1 / t) and q an approximation, q + (a - q t) r, the residual by FMA.  Far from 1 (fast
+// false) underflow could spoil the residual.
+struct SixT {
+    float t, r;
+    bool fast;
+    __device__ __forceinline__ explicit SixT(float tscale) : t(6.f * tscale), r(1.f / (6.f * tscale)),
+                                                               fast(t >= 0x1p-40f && t <= 0x1p40f) {}
+    __device__ __forceinline__ float divide(float a) const {
+        const float q = a * r;
+        return q > 1000.f ? q : fmaf(fmaf(-q, t, a), r, q);        // over 448 it saturates, whatever its last bits
+    }
+};
+
 // codes of a lane's 8 values and the scale byte of its block (the block's lanes agree on it)
 template <int FMT, class T>
-__device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, float tscale, uint32_t& byte) {
+__device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, const SixT& six, float tscale, uint32_t& byte) {
     uint32_t am = absmax8(x);
     am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
     float v[8];
@@ -74,12 +88,15 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, float six_t, floa
         }
     } else {
         const bool bad = am >= 0x7F800000u;
-        byte = bad ? 0x7Fu : e4m3_of(__fdiv_rn(__uint_as_float(am), six_t));
+        const float amax = __uint_as_float(am);
+        byte = bad ? 0x7Fu : e4m3_of(six.fast ? six.divide(amax) : __fdiv_rn(amax, six.t));
         const float d = e4m3_value(byte) * tscale;
         if (!bad && d >= 0x1p-100f && d <= 0x1p100f) {
-            // x / d correctly rounded by Markstein's theorem (1990): with r = RN(1 / d) and q an approximation of the
-            // quotient, q + (x - q d) r, the residual by FMA.  A tie has residual 0, so a tie is a tie.
-            const float r = __frcp_rn(d);
+            // x / d in the same way.  A tie comes out as a tie: its residual is exact.  For 16-bit types an approximate
+            // reciprocal will do: their quotients lie no closer to a tie than 2^-16, unless they are one.
+            float r;
+            if constexpr (sizeof(T) == 2) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+            else r = __frcp_rn(d);
             const float2 r2 = make_float2(r, r), nd2 = make_float2(-d, -d);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
