@@ -107,6 +107,22 @@ def test_gradients_agree_with_differences_of_the_forward_calls():
             assert abs((fn(arr + d) - fn(arr - d)) / 2 - float(grad.view(-1)[i])) < 1e-4
 
 
+def test_rows_past_32_bit_offsets():
+    """R * H = 2.4e9: each of the row calls at the far end."""
+    T, k, E, H = 18433, 8, 8, 16384
+    ids = torch.arange(T * k, device=DEV, dtype=torch.int32).view(T, k) % E
+    _, pos, off = uq.moe_sort(ids, E)
+    x = torch.randint(-4, 5, (T, H), device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    xs = uq.moe_gather(x, pos, off)
+    assert torch.equal(xs[pos[-1].long()], x[-1:].expand(k, -1)) and torch.equal(xs[-1], x[(pos == T * k - 1).nonzero()[0, 0]])
+    w = torch.full((T, k), 0.5, device=DEV)
+    assert torch.equal(uq.moe_combine(xs, pos, w), x * 4)
+    assert torch.equal(uq.moe_gather_grad(xs, pos), x * 8)
+    dys, dw = uq.moe_combine_grad(x, xs, pos, w, off)
+    assert torch.equal(dys, xs * 0.5)
+    assert torch.equal(dw[-3:], x[-3:].float().square().sum(1, keepdim=True).expand(-1, k))
+
+
 def test_refusals():
     ids = torch.zeros(3, 2, dtype=torch.int32, device=DEV)
     for E, status in ((0, 1), (1025, 2)):

@@ -308,6 +308,27 @@ def test_product_on_another_stream_and_in_a_graph():
     assert torch.equal(y, want)
 
 
+def test_operands_past_32_bit_offsets():
+    """2.3e9 elements (codes past 2^30 bytes, values past 2^32): the last rows equal those of a small call.  Small
+    integers, so every sum is exact whatever the kernel and its order."""
+    T, K, N, n = 70001, 32768, 128, 37
+    x = torch.randint(-1, 2, (T, K), device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    w = torch.randint(-1, 2, (N, K), device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    wq = uq.quantize_mx(w, "MXFP4")
+    q = uq.quantize_mx(x, "MXFP4")
+    tail = x[-n:].contiguous()
+    qt = uq.quantize_mx(tail, "MXFP4")
+    assert torch.equal(q[0][-n:], qt[0])
+    assert torch.equal(uq.dequant_mx(q, "MXFP4")[-n:], tail)
+    y = uq.gemm_mx(q, wq, "MXFP4", dtype=torch.float32)
+    assert torch.equal(y[-n:], tail.float() @ w.float().t())
+    off = torch.tensor([0, T - n, T], dtype=torch.int32, device=DEV)
+    qs = uq.quantize_mx(x, "MXFP4", offsets=off)
+    ys = uq.gemm_mx_grouped(qs, (wq[0].repeat(2, 1, 1), wq[1].repeat(2, 1)), off, "MXFP4", dtype=torch.float32)
+    assert torch.equal(ys, y)
+    assert uq.device_fault() == 0
+
+
 def test_refusals():
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
     w = (torch.zeros(8, 32, dtype=torch.uint8, device=DEV), torch.zeros(512, dtype=torch.uint8, device=DEV))
