@@ -22,6 +22,7 @@
 // freed, and the fault word tells.
 #include <cuda.h>
 #include <algorithm>
+#include <atomic>
 
 #include "uq_mx_quant.cuh"
 
@@ -1099,6 +1100,41 @@ template <int NA> void pair_ring(int fmt, MxGemmArgs& a) {
                                             : Pair<UQ_NVFP4, NA>::STAGES * Pair<UQ_NVFP4, NA>::STAGE);
 }
 
+// Clusters of s CTAs that run at the same time, one CTA per SM: fewer than SMs / s, since a cluster stays within a GPC
+// (16 clusters of 8 took two rounds, 15 us against 9 for clusters of 4).  Asked once per device.
+int clusters_at_once(int s) {
+    static std::atomic<int> known[64][MAX_SPLIT + 1] = {};
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][s].load(std::memory_order_relaxed);
+    if (n) return n - 1;
+    if (configure(mx_gemm_kernel<UQ_MXFP4, 1, false>, done) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = 220 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<UQ_MXFP4, 1, false>, &cfg) != cudaSuccess) return 0;
+    known[dev][s].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs per tile: the fewest that give each the fewest steps, among the clusters that all run at the same time.
+int split_of(long long tiles, int steps, int sms) {
+    int best = 1;
+    if (tiles * 2 > sms) return best;
+    for (int s = 2; s <= std::min(MAX_SPLIT, steps); ++s)
+        if ((steps + s - 1) / s < (steps + best - 1) / best && tiles <= clusters_at_once(s)) best = s;
+    return best;
+}
+
 // Whether pairs of CTAs are the faster of the two kernels.
 //   One weight for all rows: by waves.  A wave of 128 x 128 tiles takes 625 cycles per 512 k (NVFP4 736), one of 256 x 256
 // pair tiles 1026 (less with fewer than 256 token columns; both measured alone), and the pairs' start and end cost about
@@ -1114,7 +1150,7 @@ bool pays_in_pairs(int fmt, bool gated, const MxGemmArgs& a, int mean, int sms) 
     if (a.rows <= 64) return false;
     const long long steps = (a.K + 511) / 512, tiles = (long long)((a.N + 127) / 128) * ((a.rows + 127) / 128);
     const long long waves = (tiles + sms - 1) / sms, pair_waves = (2 * pair_n * ((a.rows + 255) / 256) + sms - 1) / sms;
-    const int split = tiles * 2 <= sms ? (int)std::min((long long)MAX_SPLIT, sms / tiles) : 1;
+    const int split = split_of(tiles, (int)steps, sms);
     const long long single = waves * steps * (fmt == UQ_MXFP4 ? 625 : 736) / split + (split > 1 ? 3000 : 0);
     return pair_waves * steps * 1026 * std::min(a.rows, 256) / 256 + 3000 < single;
 }
@@ -1151,11 +1187,7 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const long long tt = a.offsets ? std::min((long long)a.rows, a.rows / a.TN + (long long)a.experts)
                                    : (a.rows + a.TN - 1) / a.TN;
     const long long tiles = tt * a.NT;
-    // CTAs per tile: the fewest that give each the fewest steps
-    a.S = 1;
-    const int most = tiles * 2 <= sms ? std::min(MAX_SPLIT, std::min((int)(sms / tiles), a.steps)) : 1;
-    for (int s = 2; s <= most; ++s)
-        if ((a.steps + s - 1) / s < (a.steps + a.S - 1) / a.S) a.S = s;
+    a.S = split_of(tiles, a.steps, sms);
     a.ctas = a.S > 1 ? (int)tiles * a.S : (int)std::min(tiles, (long long)sms);
     a.folded = a.K % 256 == 0;
     const int stage_bytes = NA * 128 * (STEP_K / 2) + a.TN * (STEP_K / 2) + (NA + 1) * tps * 512;

@@ -230,7 +230,7 @@ def test_product_nan_block_stays_in_its_row():
 # T, k, E, N, K, empty experts
 GROUPS = [(1, 1, 1, 128, 64, ()), (3, 2, 8, 640, 1024, ()), (5, 4, 16, 200, 288, (3, 15)), (70, 2, 4, 257, 544, (0,)),
           (333, 4, 40, 136, 512, (7, 8, 9)), (400, 2, 3, 384, 1024, ()), (9, 2, 2, 128, 4096, (0, 1)),
-          (1500, 2, 5, 4100, 288, (2,)), (1100, 1, 3, 4352, 544, ())]
+          (1500, 2, 5, 4100, 288, (2,)), (1100, 1, 3, 4352, 544, ()), (1500, 1, 2, 4351, 288, ())]
 
 
 @pytest.mark.parametrize("gated", [False, True])
