@@ -197,6 +197,7 @@ struct MxGemmArgs {
     int folded;               // codes come in boxes of two 128-byte columns
     int pair;                 // pairs of CTAs (256 x 256 tiles)
     int TN, NT, S;            // tokens per tile, weight tiles, CTAs sharing a tile's steps
+    int share, extra;         // steps of a CTA of them: share, of the first `extra` one more
     int group;                // weight tiles that are numbered together
     int row_tiles;            // scale tiles of 128 rows of one expert's weight
     int accs, stages;         // accumulators, ring stages

@@ -199,10 +199,15 @@ __host__ __device__ constexpr int table_bytes(int experts) { return 2 * (experts
 
 __device__ __forceinline__ Tile find_tile(const MxGemmArgs& a, const int* before, int tt_all, int tile) {
     Tile t;
-    const int per = a.group * tt_all, g = tile / per, in = tile - g * per;
-    const int width = min(a.group, a.NT - g * a.group);
-    const int tt = in / width;
-    t.nt = g * a.group + in - tt * width;
+    // divisions only where they are needed: they are a part of a short call's start
+    int tt = 0;
+    t.nt = tile;
+    if (tt_all > 1) {
+        const unsigned per = a.group * tt_all, g = a.NT > a.group ? (unsigned)tile / per : 0, in = tile - g * per;
+        const unsigned width = min(a.group, a.NT - (int)g * a.group);
+        tt = in / width;
+        t.nt = g * a.group + in - tt * width;
+    }
     int e = 0, r0 = 0, r1 = a.rows, lt = tt;
     if (a.offsets) {
         int hi = a.experts;
@@ -274,16 +279,22 @@ __device__ __forceinline__ void zero_tail(const MxGemmArgs& a, long long at, lon
 }
 
 // The tiles of a CTA and its k steps of them.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
 struct Schedule {
     int tile, tiles, stride, k0, k1;
     __device__ __forceinline__ Schedule(const MxGemmArgs& a, int tt_all) {
         tiles = tt_all * a.NT;
         if (a.S > 1) {                          // one tile per cluster
-            const int rank = blockIdx.x % a.S;
-            tile = blockIdx.x / a.S;
+            const int rank = (int)cluster_rank();
+            asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(tile));
             stride = tiles;
-            k0 = a.steps * rank / a.S;
-            k1 = a.steps * (rank + 1) / a.S;
+            k0 = a.share * rank + min(rank, a.extra);
+            k1 = k0 + a.share + (rank < a.extra);
         } else {
             tile = blockIdx.x;
             stride = gridDim.x;
@@ -500,20 +511,18 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     if (warp == 0) {
         if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
         if (a.offsets) token_tiles(a, before);
-        if (lane == 0) {
-            for (int s = 0; s < a.stages; ++s) {
-                mbar_init(&full[s], FUSED ? 1 + 2 * a.rows : 2);
-                mbar_init(&empty[s], 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&acc_full[i], 1);
-                mbar_init(&acc_empty[i], 4);
-            }
+        if (lane < a.stages) {
+            mbar_init(&full[lane], FUSED ? 1 + 2 * a.rows : 2);
+            mbar_init(&empty[lane], 1);
+        } else if (lane >= 30) {
+            mbar_init(&acc_full[lane - 30], 1);
+            mbar_init(&acc_empty[lane - 30], 4);
+        } else if (lane == 29) {
             mbar_init(drain, 1);
             *abort_flag = 0;
-            fence_barrier_init();
-            fence_proxy_async_smem();
         }
+        fence_barrier_init();
+        fence_proxy_async_smem();
     }
     __syncthreads();
     const int tt_all = a.offsets ? before[a.experts] : (a.rows + TN - 1) / TN;
@@ -681,7 +690,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
             const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
             // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
-            for (int it = (blockIdx.x % a.S) * (int)blockDim.x + threadIdx.x; it < t.rows * 32; it += a.S * (int)blockDim.x) {
+            for (int it = (int)cluster_rank() * (int)blockDim.x + threadIdx.x; it < t.rows * 32; it += a.S * (int)blockDim.x) {
                 const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
                 if (nn >= a.N) continue;
                 float4 p[MAX_SPLIT * NA];
@@ -734,11 +743,6 @@ template <int FMT, int NA> struct Pair {
     static_assert(STAGE % 1024 == 0 && STAGES <= MAX_STAGES, "stage layout");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
@@ -1126,32 +1130,42 @@ int clusters_at_once(int s) {
     return n;
 }
 
-// CTAs per tile: the fewest that give each the fewest steps, among the clusters that all run at the same time.
-int split_of(long long tiles, int steps, int sms) {
+// CTAs per tile, by the time in steps: a CTA's own, longer where all together ask for more than memory delivers (CTAs
+// beyond `enough` share it: each takes about 100 GB/s), and for a split the cluster's start and end and the sums' way
+// through it, CTA by CTA a share of the token columns.  Ties go to the larger split.  Measured, weights read from DRAM, us
+// unsplit / best split, 4 rows, MXFP4: N = 1024, K = 2048 5.0 / 5.5, 4096 6.6 / 6.1, 8192 9.3 / 6.7; N = 4096, K = 4096 6.9 /
+// 7.3, 8192 9.6 / 8.5, 14336 13.7 / 10.6; N = 8192, K = 8192 10.8 / 11.2; 64 rows, N = 4096, K = 8192 10.8 / 10.0; gated,
+// 8 rows for 8 experts of 1024 x 4096 12.9 / 12.9, x 8192 20.9 / 18.5.
+int split_of(long long tiles, int steps, int tokens, bool gated, int sms) {
+    if (tiles * 2 > sms) return 1;
+    const double enough = gated ? 96 : 70, fixed = gated ? 2.25 : 5;
     int best = 1;
-    if (tiles * 2 > sms) return best;
-    for (int s = 2; s <= std::min(MAX_SPLIT, steps); ++s)
-        if ((steps + s - 1) / s < (steps + best - 1) / best && tiles <= clusters_at_once(s)) best = s;
+    double least = 0;
+    for (int s = 1; s <= std::min(MAX_SPLIT, steps); ++s) {
+        if (s > 1 && tiles > clusters_at_once(s)) continue;
+        const double t = (steps + s - 1) / s * std::max(1.0, tiles * s / enough) + (s > 1 ? fixed + tokens / (8.0 * s) : 0);
+        if (s == 1 || t <= least) best = s, least = t;
+    }
     return best;
 }
 
 // Whether pairs of CTAs are the faster of the two kernels.
-//   One weight for all rows: by waves.  A wave of 128 x 128 tiles takes 625 cycles per 512 k (NVFP4 736), one of 256 x 256
+//   One weight for all rows: by waves.  A wave of 128 x 128 tiles takes 715 cycles per 512 k (NVFP4 842), one of 256 x 256
 // pair tiles 1026 (less with fewer than 256 token columns; both measured alone), and the pairs' start and end cost about
-// 3000 cycles more.  Measured, us single / pairs, MXFP4: N = K = 8192: M = 256 13.4 / 16.5, 512 20.6 / 17.5, 2048 60.7 /
-// 49.7; N = K = 4096: M = 512 10.3 / 12.4, 2048 22.6 / 18.6; 14336 x 4096: M = 128 9.3 / 11.3, 256 14.4 / 13.4, 512 18.6 /
-// 19.5, 1024 30.8 / 25.0.
+// 3000 cycles more; where one wave of 128 x 64 tiles does it, pairs were slower at every size.  Measured, us single /
+// pairs, MXFP4: N = K = 8192: M = 256 12.1 / 15.8, 512 19.7 / 16.5, 2048 60.7 / 49.7; N = K = 4096: M = 256 7.4 / 11.3, 512
+// 8.8 / 11.3, 1024 12.8 / 11.9, 2048 22.6 / 18.6; 14336 x 4096: M = 128 9.3 / 11.3, 256 14.4 / 13.4, 512 18.6 / 19.5, 1024
+// 30.8 / 25.0.
 //   Rows by expert: from 128 rows an expert on, where there are pair tiles for every pair.  Measured, 8 experts of 4096 x
 // 4096, mean rows 64 16.5 / 18.7, 128 20.7 / 20.2, 192 26.7 / 20.7, 512 45.3 / 35.8; gated 128 51.4 / 43.2; 32 experts of
 // 2048 x 2048: 64 20.4 / 22.7, 128 24.9 / 24.7, 256 35.1 / 36.9, 512 51.6 / 47.2.
 bool pays_in_pairs(int fmt, bool gated, const MxGemmArgs& a, int mean, int sms) {
     const long long pair_n = (a.N + 255) / 256;
     if (a.offsets) return mean >= 128 && 2 * pair_n * (a.rows / (gated ? 128 : 256) + a.experts / 2) >= sms;
-    if (a.rows <= 64) return false;
+    if (a.rows <= 64 || (long long)((a.N + 127) / 128) * ((a.rows + 63) / 64) <= sms) return false;
     const long long steps = (a.K + 511) / 512, tiles = (long long)((a.N + 127) / 128) * ((a.rows + 127) / 128);
     const long long waves = (tiles + sms - 1) / sms, pair_waves = (2 * pair_n * ((a.rows + 255) / 256) + sms - 1) / sms;
-    const int split = split_of(tiles, (int)steps, sms);
-    const long long single = waves * steps * (fmt == UQ_MXFP4 ? 625 : 736) / split + (split > 1 ? 3000 : 0);
+    const long long single = waves * steps * (fmt == UQ_MXFP4 ? 715 : 842);
     return pair_waves * steps * 1026 * std::min(a.rows, 256) / 256 + 3000 < single;
 }
 
@@ -1181,13 +1195,18 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
     const int tps = STEP_K / mx_tile_k(fmt);
     a.steps = (a.K + STEP_K - 1) / STEP_K;
     a.group = 16;
-    a.TN = a.rows <= 16 ? 16 : (a.rows <= 32 ? 32 : (mean <= 64 ? 64 : 128));
     a.NT = (a.N + 127) / 128;
     // token tiles: exact, or the most that any counts give
-    const long long tt = a.offsets ? std::min((long long)a.rows, a.rows / a.TN + (long long)a.experts)
-                                   : (a.rows + a.TN - 1) / a.TN;
-    const long long tiles = tt * a.NT;
-    a.S = split_of(tiles, a.steps, sms);
+    const auto token_tiles = [&](int tn) {
+        return a.offsets ? std::min((long long)a.rows, a.rows / tn + (long long)a.experts) : (long long)((a.rows + tn - 1) / tn);
+    };
+    // 64 columns also for more rows where one wave takes all tiles: the epilogue, the longer part of such a call, halves
+    // (MXFP4 us, 128 / 64 columns: 512 x 2048 x 2048 6.8 / 6.0, 256 x 4096 x 8192 11.7 / 10.3, 96 x 8192 x 4096 7.8 / 7.4)
+    a.TN = a.rows <= 16 ? 16 : (a.rows <= 32 ? 32 : (mean <= 64 || token_tiles(64) * a.NT <= sms ? 64 : 128));
+    const long long tiles = token_tiles(a.TN) * a.NT;
+    a.S = split_of(tiles, a.steps, std::min(a.TN, mean), gated, sms);
+    a.share = a.steps / a.S;
+    a.extra = a.steps % a.S;
     a.ctas = a.S > 1 ? (int)tiles * a.S : (int)std::min(tiles, (long long)sms);
     a.folded = a.K % 256 == 0;
     const int stage_bytes = NA * 128 * (STEP_K / 2) + a.TN * (STEP_K / 2) + (NA + 1) * tps * 512;

@@ -164,7 +164,8 @@ def test_pack_mx_scales(fmt):
 # (M, N, K): one row to several token tiles, odd N, K of one block, K that ends inside a step, split k
 SHAPES = [(1, 128, 32), (1, 1, 256), (3, 200, 96), (17, 384, 1056), (32, 130, 320), (33, 257, 512), (64, 1024, 4096),
           (65, 512, 2080), (100, 136, 14336), (129, 640, 1024), (300, 1000, 544), (520, 2320, 256),
-          (1100, 4100, 544), (2049, 2304, 96), (1000, 8100, 4128)]
+          (1100, 4100, 544), (2049, 2304, 96), (1000, 8100, 4128),
+          (16, 1024, 8224), (200, 900, 9248), (500, 4000, 800), (256, 2304, 1056)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -230,7 +231,8 @@ def test_product_nan_block_stays_in_its_row():
 # T, k, E, N, K, empty experts
 GROUPS = [(1, 1, 1, 128, 64, ()), (3, 2, 8, 640, 1024, ()), (5, 4, 16, 200, 288, (3, 15)), (70, 2, 4, 257, 544, (0,)),
           (333, 4, 40, 136, 512, (7, 8, 9)), (400, 2, 3, 384, 1024, ()), (9, 2, 2, 128, 4096, (0, 1)),
-          (1500, 2, 5, 4100, 288, (2,)), (1100, 1, 3, 4352, 544, ()), (1500, 1, 2, 4351, 288, ())]
+          (1500, 2, 5, 4100, 288, (2,)), (1100, 1, 3, 4352, 544, ()), (1500, 1, 2, 4351, 288, ()),
+          (7, 2, 4, 200, 8224, (1,)), (150, 1, 2, 130, 6176, ()), (800, 1, 8, 300, 544, ())]
 
 
 @pytest.mark.parametrize("gated", [False, True])
