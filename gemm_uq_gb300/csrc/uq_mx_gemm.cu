@@ -15,7 +15,7 @@
 // and two accumulators let the epilogue of one tile run under the next one's MMAs.  Where tiles would fill at most half
 // of the SMs, a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through distributed shared memory
 // in rank order, so equal calls give equal bits.
-// One GB300, graph replay: 1 x 14336 x 4096 MXFP4 7.6 us (4.1 TB/s), 37 x 4096 x 14336 NVFP4 11.6 us; large products on
+// One GB300, graph replay, weights from DRAM: 1 x 14336 x 4096 MXFP4 9.0 us (3.5 TB/s), 37 x 4096 x 14336 NVFP4 11.8 us; large products on
 // pairs of CTAs (below) 8192^3 MXFP4 156 us (7.0 PFLOP/s).  What bounds them: few tokens start and end of a kernel (3 us)
 // and then memory; many the tensor cores.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is
@@ -33,7 +33,7 @@ namespace {
 constexpr int THREADS = 224;
 constexpr int QUANT_WARPS = 4;                  // of the kernel that quantizes the tokens itself, in place of warp 6
 constexpr int FUSED_THREADS = THREADS + (QUANT_WARPS - 1) * 32;
-constexpr int FUSED_ROWS = 2;                   // its most tokens (rule at mx_gemm_quantizes)
+constexpr int FUSED_ROWS = 3;                   // its most tokens (rule at mx_gemm_quantizes)
 constexpr int STEP_K = 512;                     // k per stage: two 128-byte columns of a row, eight MMAs of 64
 // The tensor maps of a launch.
 struct MxGemmMaps {
@@ -1138,7 +1138,7 @@ int clusters_at_once(int s) {
 // 8 rows for 8 experts of 1024 x 4096 12.9 / 12.9, x 8192 20.9 / 18.5.
 int split_of(long long tiles, int steps, int tokens, bool gated, int sms) {
     if (tiles * 2 > sms) return 1;
-    const double enough = gated ? 96 : 70, fixed = gated ? 2.25 : 5;
+    const double enough = gated ? 96 : 70, fixed = gated ? 2.75 : 5;
     int best = 1;
     double least = 0;
     for (int s = 1; s <= std::min(MAX_SPLIT, steps); ++s) {
@@ -1222,9 +1222,9 @@ void plan(int fmt, bool gated, MxGemmArgs& a, int sms) {
 }  // namespace
 
 // One launch instead of two up to FUSED_ROWS tokens: a call then takes 7.4 us of host time instead of 10, and on the GPU
-// (graph replay, us one launch / two) MXFP4 14336 x 4096 M = 1 7.6 / 8.2, M = 2 8.9 / 8.6, M = 3 8.9 / 8.2, M = 4 10.8 / 8.9;
-// 4096 x 14336 9.6 / 10.3, 10.3 / 9.7, 10.3 / 9.8, 11.6 / 10.3; 1024 x 4096 6.4 / 6.9, 6.9 / 7.5, 6.9 / 7.5, 6.9 / 7.5.
-// From 3 tokens on the quantizing warps hold up long streams of weights.
+// (graph replay, weights from DRAM, us one launch / two) MXFP4 14336 x 4096 M = 1 9.0 / 9.5, 2 8.8 / 10.2, 3 9.5 / 10.1, 4
+// 10.8 / 10.1; 4096 x 14336 10.3 / 11.4, 10.5 / 11.4, 11.1 / 11.5, 12.4 / 11.6; 4096 x 4096 6.9 / 8.0, 7.2 / 8.0, 7.8 / 8.1,
+// 9.0 / 8.0; 1024 x 4096 5.6 / 6.7 to 5.8 / 6.9.  From 4 tokens on the quantizing warps hold up long streams of weights.
 bool mx_gemm_quantizes(int rows) { return rows <= FUSED_ROWS; }
 
 cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes, const uint8_t* wcodes_up,

@@ -431,7 +431,7 @@ uq_status uq_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* out, 
  * uq_gemm_mx -- y[m][n] = alpha * sum_k x^[m][k] * w^[n][k] with both operands microscaled, fp32 accumulation on
  * the block-scaled tensor instructions, rounded once to ytype.
  *   x: either of xtype, [M][K] with rows ldx apart, quantized in the call as uq_quantize_mx does with tscale_x
- *      (xscales NULL; one or two rows inside the product's kernel, more into the per-stream workspace); or an operand's
+ *      (xscales NULL; up to three rows inside the product's kernel, more into the per-stream workspace); or an operand's
  *      codes with xscales its scales (xtype and ldx ignored)
  *   wcodes, wscales (device): the weight as an operand of N rows; y (device) [M][N], written.
  *   alpha: multiplied with the fp32 sum; it holds the operands' tensor scales that the caller wants applied (an x

@@ -190,7 +190,7 @@ def test_product_parity(fmt, M, N, K):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(1, 20000, 544), (2, 20000, 1056), (2, 130, 14336), (1, 19, 32), (3, 20000, 544)])
 def test_product_of_few_tokens_quantizes_the_same_in_one_launch(fmt, dtype, M, N, K):
-    """One or two tokens are quantized inside the product's kernel: the same bits as quantized before, for every type,
+    """Up to three tokens are quantized inside the product's kernel: the same bits as quantized before, for every type,
     strided rows, several tiles a CTA, K that ends inside a step, and a k split."""
     rng = np.random.default_rng([M, N, K])
     codes = torch.from_numpy(rng.integers(0, 256, (N, K // 2), dtype=np.uint8)).to(DEV)
