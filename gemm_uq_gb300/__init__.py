@@ -310,7 +310,7 @@ def quantize_k4(w: torch.Tensor, stream=None):
 
 
 def set_launch_overlap(enable: bool) -> None:
-    """uq_set_launch_overlap: let GEMV launches prefetch their (constant) weights early."""
+    """uq_set_launch_overlap: let GEMV, GEMM and microscaled launches prefetch their (constant) weights early."""
     _check(lib().uq_set_launch_overlap(1 if enable else 0), "uq_set_launch_overlap")
 
 

@@ -7,7 +7,7 @@ namespace uq {
 
 // records the message uq_last_error() returns on the calling thread (uq_api.cu)
 void set_last_error(const char* msg);
-// whether GEMV kernels are launched with programmatic dependent launch (uq_set_launch_overlap)
+// whether GEMV, GEMM and microscaled kernels are launched with programmatic dependent launch (uq_set_launch_overlap)
 bool launch_overlap();
 
 // reads and clears the fault word of uq_gemm_noalloc launches on the current device (uq_noalloc.cu)
@@ -186,7 +186,7 @@ struct MxGemmArgs {
     unsigned int* fault;
     float alpha;
     int ytype, rows, experts, N, K;
-    int wait;                 // launched with programmatic serialization behind the kernel that writes x
+    int wait;                 // launched with programmatic serialization: the kernel before may still run
     const void* xraw;         // few tokens that the kernel quantizes itself (xcodes and xscales unused), or NULL
     long long ldx;
     int xtype;

@@ -278,6 +278,15 @@ __device__ __forceinline__ void zero_tail(const MxGemmArgs& a, long long at, lon
     for (long long i = c1 + at * 2; i < b1; i += all * 2) *reinterpret_cast<uint16_t*>(y + i) = 0;
 }
 
+// With launch overlap (or behind the call's own quantizer) a kernel starts while the one before it on the stream still
+// runs; this one's tokens and offsets may be its output, and y may be read by it.  The weights are requested before.
+__device__ __forceinline__ void after_prior_work(const MxGemmArgs& a) {
+    if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next kernel's CTAs start as these leave their SMs.  Not before this CTA has its tensor memory: one that
+// started before and took it would hold it until this kernel is done.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The tiles of a CTA and its k steps of them.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -421,6 +430,7 @@ __device__ __forceinline__ void quantize_tokens(const MxGemmArgs& a, Schedule sc
     // the unit being quantized: its step's stage, how many steps have gone before, k step, unit of the step
     int n = w / per, s = n % a.stages, kt = sch.k0 + n % steps, un = w % per;
     uint32_t ph = 1u ^ (uint32_t)(n / a.stages & 1);
+    after_prior_work(a);
     request(cur);
     for (int u = 0; u < total; u += AHEAD) {
         if (u + AHEAD < total) request(nxt);
@@ -510,7 +520,10 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
 
     if (warp == 0) {
         if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
-        if (a.offsets) token_tiles(a, before);
+        if (a.offsets) {
+            after_prior_work(a);
+            token_tiles(a, before);
+        }
         if (lane < a.stages) {
             mbar_init(&full[lane], FUSED ? 1 + 2 * a.rows : 2);
             mbar_init(&empty[lane], 1);
@@ -535,6 +548,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                          :: "r"(smem_u32(tmem_ptr)), "r"((uint32_t)a.tmem_cols) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+            launch_dependents();
         }
         fence_before();
         asm volatile("bar.sync 1, %0;" :: "n"(TMEM_WARPS * 32) : "memory");
@@ -546,7 +560,7 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         // ------------------------------------------------------------ producers
         // The weights do not depend on the kernel before, the tokens may.
         const bool tokens = warp == 6;
-        if (tokens && a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (tokens) after_prior_work(a);
         int issued = 0, s = 0;
         uint32_t ph = 1;                                           // empty[] of the first round counts as free
         bool ok = true;
@@ -640,7 +654,10 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue: lane = row of the weight tile
         const int q = warp & 3, row = q * 32 + lane, et = threadIdx.x - 64;
-        if (a.offsets) zero_tail(a, blockIdx.x * 128LL + et, gridDim.x * 128LL);
+        if (a.offsets) {
+            after_prior_work(a);
+            zero_tail(a, blockIdx.x * 128LL + et, gridDim.x * 128LL);
+        }
         for (int n = 0; sch.more(); sch.advance(), ++n) {
             const Tile t = find_tile(a, before, tt_all, sch.tile);
             const int buf = AB == 2 ? n & 1 : 0;
@@ -834,7 +851,10 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
 
     if (warp == 0) {
         if (lane < 6) asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.w + lane) : "memory");
-        if (a.offsets) token_tiles(a, before);
+        if (a.offsets) {
+            after_prior_work(a);
+            token_tiles(a, before);
+        }
         if (lane == 0) {
             for (int s = 0; s < P::STAGES; ++s) {
                 mbar_init(&full[s], 2);
@@ -858,6 +878,7 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
         if (warp == 1) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_ptr)) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+            launch_dependents();
         }
         fence_before();
         asm volatile("bar.sync 1, 160;" ::: "memory");
@@ -870,7 +891,7 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
     if (warp == 0 || warp == 6) {
         // ------------------------------------------------------------ producers
         const bool tokens = warp == 6;
-        if (tokens && a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (tokens) after_prior_work(a);
         const uint32_t lead_full0 = cluster_addr(full0, 0);
         int issued = 0, s = 0;
         uint32_t ph = 1;                                           // empty[] of the first round counts as free
@@ -965,7 +986,10 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue: lane = weight row
         const int q = warp & 3, row = q * 32 + lane;
-        if (a.offsets) zero_tail(a, blockIdx.x * 128LL + threadIdx.x - 64, gridDim.x * 128LL);
+        if (a.offsets) {
+            after_prior_work(a);
+            zero_tail(a, blockIdx.x * 128LL + threadIdx.x - 64, gridDim.x * 128LL);
+        }
         const uint32_t lead_free = cluster_addr(smem_u32(acc_free), 0);
         int n = 0;
         for (int tile = blockIdx.x >> 1; tile < tiles; tile += stride, ++n) {
@@ -1231,6 +1255,7 @@ cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes
                            MxGemmArgs a, int sms, cudaStream_t st) {
     if (!encode_fn()) return cudaErrorNotSupported;
     plan(fmt, wcodes_up != nullptr, a, sms);
+    if (launch_overlap()) a.wait = 1;
     MxGemmMaps m;
     const int tps = (a.pair ? PAIR_STEP : STEP_K) / mx_tile_k(fmt);
     const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.row_tiles;

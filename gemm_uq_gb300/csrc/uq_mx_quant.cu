@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ 
                                                           const int32_t* __restrict__ offsets, int segments,
                                                           const int32_t* __restrict__ pos, int topk) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");           // with launch overlap: x follows earlier work
     constexpr int UNIT_K = STEP_K * STEPS;                       // k of a row per warp
     constexpr int LPB = FMT == UQ_MXFP4 ? 4 : 2;                 // lanes per block
     constexpr int TPS = STEP_K / mx_tile_k(FMT);                 // scale tiles per step
@@ -156,9 +157,17 @@ cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx,
             using T = decltype(t);
             constexpr int S = decltype(steps)::value;
             auto kernel = fmt == UQ_MXFP4 ? quantize_mx_kernel<T, UQ_MXFP4, S> : quantize_mx_kernel<T, UQ_NVFP4, S>;
-            kernel<<<grid, 128, 0, st>>>(static_cast<const T*>(x), ldx, codes, scales, rows, K, tscale, offsets, segments,
-                                         pos, topk);
-            return cudaGetLastError();
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(grid);
+            cfg.blockDim = dim3(128);
+            cfg.stream = st;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = launch_overlap() ? 1 : 0;
+            return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), ldx, codes, scales, rows, K, tscale, offsets,
+                                      segments, pos, topk);
         });
     });
 }

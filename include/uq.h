@@ -312,11 +312,13 @@ uq_status uq_set_gemm_path(int path);
 
 /*
  * uq_set_launch_overlap -- process-wide switch (default 0 = off) for how uq_gemm launches its
- * GEMV and tensor-core kernels.  When on, each launch uses programmatic dependent launch: the kernel may
+ * GEMV and tensor-core kernels, and uq_quantize_mx, uq_gemm_mx and uq_gemm_mx_grouped theirs.
+ * When on, each launch uses programmatic dependent launch: the kernel may
  * begin while the previous kernel on the same stream is still finishing, and streams its packed
  * weights, scales and zero points from HBM during that time; it waits for the previous kernel to
- * complete before it reads x, touches the split-K workspace or writes y.  Turn it on only when
- * wq / scales / zeros_or_codebook are not written by the work that immediately precedes the
+ * complete before it reads x (or the offsets of rows by expert, on which its weight requests
+ * depend), touches a workspace or writes its output.  Turn it on only when
+ * wq / scales / zeros_or_codebook (wcodes / wscales) are not written by the work that immediately precedes the
  * call on the stream (true for a decode loop over fixed weights).  Host-only; always UQ_OK.
  */
 uq_status uq_set_launch_overlap(int enable);
