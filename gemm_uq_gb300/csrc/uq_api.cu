@@ -918,7 +918,7 @@ uq_status uq_quantize_mx(const void* x, uq_dtype xtype, long long ldx, uint8_t* 
     DeviceState* ds = nullptr;
     if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
     cudaError_t e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, scales, rows, K, tscale, offsets, segments, pos,
-                                           topk, ds->sms, static_cast<cudaStream_t>(stream));
+                                           topk, ds->sms, false, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled quantization launch");
 }
 
@@ -995,7 +995,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
         if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
         uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
         e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, codes + code_bytes, M, K, tscale_x, nullptr, 0, nullptr, 0,
-                                   ds->sms, st);
+                                   ds->sms, true, st);
         if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
         xcodes = codes;
         a.xscales = codes + code_bytes;

@@ -20,8 +20,10 @@ template <class T, int FMT, int STEPS>
 __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ x, long long ldx, uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales, int rows, int K, float tscale,
                                                           const int32_t* __restrict__ offsets, int segments,
-                                                          const int32_t* __restrict__ pos, int topk) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                                                          const int32_t* __restrict__ pos, int topk, bool early) {
+    // Only a product's own quantizer lets the next kernel start early: what this one writes may be the weights that a
+    // later kernel requests before it waits for its predecessor.
+    if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");           // with launch overlap: x follows earlier work
     constexpr int UNIT_K = STEP_K * STEPS;                       // k of a row per warp
     constexpr int LPB = FMT == UQ_MXFP4 ? 4 : 2;                 // lanes per block
@@ -151,7 +153,7 @@ template <class F> cudaError_t with_steps(int rows, int K, int sms, F&& f) {
 
 cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
                                int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
-                               int topk, int sms, cudaStream_t st) {
+                               int topk, int sms, bool early, cudaStream_t st) {
     return with_steps(rows, K, sms, [&](auto steps, int grid) {
         return with_dtype(xtype, [&](auto t) {
             using T = decltype(t);
@@ -167,7 +169,7 @@ cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx,
             cfg.attrs = attr;
             cfg.numAttrs = launch_overlap() ? 1 : 0;
             return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), ldx, codes, scales, rows, K, tscale, offsets,
-                                      segments, pos, topk);
+                                      segments, pos, topk, early);
         });
     });
 }

@@ -137,3 +137,26 @@ def test_overlap_expert_layer_matches_plain(T):
     finally:
         uq.set_launch_overlap(False)
     assert uq.device_fault() == 0
+
+
+@pytest.mark.parametrize("M", [1, 5, 130])
+def test_overlap_weights_quantized_in_the_same_stream(M):
+    """Weights that quantize_mx writes one or two calls before the product that reads them."""
+    N, K = 2304, 2048
+    ws = [device_x(activations(970 + i, N, K), DEV) for i in range(4)]
+    x = device_x(activations(971, M, K), DEV)
+    other = uq.quantize_mx(ws[0], "MXFP4")
+    try:
+        uq.set_launch_overlap(False)
+        ref = [uq.gemm_mx(x, uq.quantize_mx(w, "MXFP4"), "MXFP4") for w in ws]
+        torch.cuda.synchronize()
+        uq.set_launch_overlap(True)
+        for rep in range(8):
+            for w, r in zip(ws, ref):
+                fresh = uq.quantize_mx(w, "MXFP4")
+                if rep % 2:
+                    uq.gemm_mx(x, other, "MXFP4")
+                assert torch.equal(r.view(torch.int16), uq.gemm_mx(x, fresh, "MXFP4").view(torch.int16))
+    finally:
+        uq.set_launch_overlap(False)
+    assert uq.device_fault() == 0
