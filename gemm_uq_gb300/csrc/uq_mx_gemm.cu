@@ -13,8 +13,8 @@
 // The work is a list of tiles (a weight tile of 128 rows, or the gate and the up tile of the same 128 outputs, x a
 // token tile of TN) of `steps` k steps each; CTA c takes tiles c, c + P, ...  The ring of stages runs on across tiles,
 // and two accumulators let the epilogue of one tile run under the next one's MMAs.  Where tiles would fill at most half
-// of the SMs and it saves time (split_of), a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through distributed shared memory
-// in rank order, so equal calls give equal bits.
+// of the SMs and it saves time (split_of), a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through
+// distributed shared memory in rank order, so equal calls give equal bits.
 // One GB300, graph replay: weights from DRAM 1 x 14336 x 4096 MXFP4 9.0 us (3.5 TB/s; 7.6 where L2 keeps a part), 37 x
 // 4096 x 14336 NVFP4 11.8 us; 512 x 2048 x 2048 MXFP4 6.9 us; large products on pairs of CTAs (below) 8192^3 MXFP4 156 us
 // (7.0 PFLOP/s).  What bounds them: few tokens start and end of a kernel (3 us) and then memory; many the tensor cores.
