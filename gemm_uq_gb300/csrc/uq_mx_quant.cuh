@@ -91,8 +91,9 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, const SixT& six, 
         const float amax = __uint_as_float(am);
         byte = bad ? 0x7Fu : e4m3_of(six.fast ? six.divide(amax) : __fdiv_rn(amax, six.t));
         const float d = e4m3_value(byte) * tscale;
-        if (!bad && d >= 0x1p-100f && d <= 0x1p100f) {
-            // x / d in the same way.  A tie comes out as a tie: its residual is exact.  For 16-bit types an approximate
+        if (!bad && d >= 0x1p-100f && d <= 0x1p100f && amax <= d * 0x1p100f) {
+            // x / d in the same way (with quotients far inside the range: where the block scale has saturated they can
+            // exceed it, and the residual of an infinite q is infinite with the other sign).  A tie comes out as a tie: its residual is exact.  For 16-bit types an approximate
             // reciprocal will do: their quotients lie no closer to a tie than 2^-16, unless they are one.
             float r;
             if constexpr (sizeof(T) == 2) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
