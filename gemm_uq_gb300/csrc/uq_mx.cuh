@@ -33,19 +33,38 @@ __host__ __device__ inline long long mx_scale_offset(long long srow, int blk, in
     return ((srow >> 7) * ktiles + (blk >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (blk & 3);
 }
 
+// Loads of what the kernel before on the stream may have written (rows, positions, offsets, factors), for kernels that
+// may be resident before it is done: plain loads, as the read-only path is for data that nobody writes while the kernel
+// runs, and volatile with a memory clobber, which keeps them behind the wait for that kernel.
+__device__ __forceinline__ int32_t ld_written(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_written(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_written(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // segment of row r: the last e with offsets[e] <= r (empty segments share their offset with the next one)
-__device__ __forceinline__ int mx_segment(const int32_t* __restrict__ offsets, int segments, int r) {
+__device__ __forceinline__ int mx_segment(const int32_t* offsets, int segments, int r) {
     int lo = 0, hi = segments;                  // offsets[0] <= r assumed; invariant offsets[lo] <= r
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(offsets + mid) <= r) lo = mid; else hi = mid;
+        if (ld_written(offsets + mid) <= r) lo = mid; else hi = mid;
     }
     return lo;
 }
 // row r of a segmented operand in tile coordinates
-__device__ __forceinline__ long long mx_srow(const int32_t* __restrict__ offsets, int segments, int r) {
+__device__ __forceinline__ long long mx_srow(const int32_t* offsets, int segments, int r) {
     const int e = mx_segment(offsets, segments, r);
-    const int o = min(max(__ldg(offsets + e), 0), r);
+    const int o = min(max(ld_written(offsets + e), 0), r);
     return ((long long)(o >> 7) + e) * 128 + (r - o);
 }
 

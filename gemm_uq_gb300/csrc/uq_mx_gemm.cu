@@ -191,7 +191,7 @@ struct Tile {
     int expert, nt;                             // weight tile nt of this expert
     int row0, rows, first;                      // token rows: first, count (<= TN), first - the expert's first
 };
-__device__ __forceinline__ int offset_of(const MxGemmArgs& a, int e) { return min(max(__ldg(a.offsets + e), 0), a.rows); }
+__device__ __forceinline__ int offset_of(const MxGemmArgs& a, int e) { return min(max(ld_written(a.offsets + e), 0), a.rows); }
 
 // The table of the experts' token tiles (shared memory): tiles before each expert, then each expert's first row,
 // experts + 1 entries both.
@@ -667,8 +667,8 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             __syncwarp();
             fence_after();
             const int nn = t.nt * 128 + row;
-            const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
-            const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
+            const float al = a.alpha * (a.alpha_e ? ld_written(a.alpha_e + t.expert) : 1.f);
+            const float au = a.alpha * (a.alpha_up ? ld_written(a.alpha_up + t.expert) : 1.f);
             for (int c = 0; c < t.rows; c += 16) {
                 uint32_t r[NA * 16];
 #pragma unroll
@@ -704,8 +704,8 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
         const Schedule mine(a, tt_all);
         if (mine.more()) {
             const Tile t = find_tile(a, before, tt_all, mine.tile);
-            const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
-            const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
+            const float al = a.alpha * (a.alpha_e ? ld_written(a.alpha_e + t.expert) : 1.f);
+            const float au = a.alpha * (a.alpha_up ? ld_written(a.alpha_up + t.expert) : 1.f);
             // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
             for (int it = (int)cluster_rank() * (int)blockDim.x + threadIdx.x; it < t.rows * 32; it += a.S * (int)blockDim.x) {
                 const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
@@ -1000,8 +1000,8 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
             __syncwarp();
             fence_after();
             const int nn = t.nt * 256 + (int)rank * 128 + row;
-            const float al = a.alpha * (a.alpha_e ? __ldg(a.alpha_e + t.expert) : 1.f);
-            const float au = a.alpha * (a.alpha_up ? __ldg(a.alpha_up + t.expert) : 1.f);
+            const float al = a.alpha * (a.alpha_e ? ld_written(a.alpha_e + t.expert) : 1.f);
+            const float au = a.alpha * (a.alpha_up ? ld_written(a.alpha_up + t.expert) : 1.f);
             // The first accumulator shares its last columns, the second its first: those are read, and given free,
             // before anything is written.
             const int c0 = n & 1 ? 0 : TN - P::OVER;

@@ -17,10 +17,9 @@ namespace {
 constexpr int STEP_K = 256;                     // k of a row per warp step
 
 template <class T, int FMT, int STEPS>
-__global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ x, long long ldx, uint8_t* __restrict__ codes,
-                                                          uint8_t* __restrict__ scales, int rows, int K, float tscale,
-                                                          const int32_t* __restrict__ offsets, int segments,
-                                                          const int32_t* __restrict__ pos, int topk, bool early) {
+__global__ void __launch_bounds__(128) quantize_mx_kernel(const T* x, long long ldx, uint8_t* codes, uint8_t* scales,
+                                                          int rows, int K, float tscale, const int32_t* offsets,
+                                                          int segments, const int32_t* pos, int topk, bool early) {
     // Only a product's own quantizer lets the next kernel start early: what this one writes may be the weights that a
     // later kernel requests before it waits for its predecessor.
     if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -32,7 +31,7 @@ __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ 
     const unsigned units_k = (unsigned)(K + UNIT_K - 1) / UNIT_K;
     const int ktiles = mx_ktiles(K, FMT);
     const SixT six(tscale);
-    const int total = offsets ? min(__ldg(offsets + segments), pos ? rows * topk : rows) : rows;
+    const int total = offsets ? min(ld_written(offsets + segments), pos ? rows * topk : rows) : rows;
     const unsigned long long units = (unsigned long long)rows * units_k;
     for (unsigned long long u0 = blockIdx.x * 4ull + (threadIdx.x >> 5); u0 < units; u0 += gridDim.x * 4ull) {
         const int row = units <= 0xFFFFFFFFull ? (int)((unsigned)u0 / units_k) : (int)(u0 / units_k);
@@ -58,7 +57,7 @@ __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* __restrict__ 
             int dst = -1;
             long long srow = 0;
             if (j0 + lane < routes) {
-                dst = pos ? __ldg(pos + (long long)row * topk + j0 + lane) : row;
+                dst = pos ? ld_written(pos + (long long)row * topk + j0 + lane) : row;
                 if (dst >= total) dst = -1;
                 if (dst >= 0) srow = offsets ? mx_srow(offsets, segments, dst) : dst;
             }

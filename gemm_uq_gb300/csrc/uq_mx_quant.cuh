@@ -2,6 +2,7 @@
 // lanes (MXFP4) or 2 (NVFP4) of the warp.
 #pragma once
 
+#include <cstring>
 #include <type_traits>
 
 #include "uq_mx.cuh"
@@ -13,7 +14,10 @@ template <class T> struct Raw {
     Vec<T, 16 / sizeof(T)> part[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) part[i] = reinterpret_cast<const Vec<T, 16 / sizeof(T)>*>(p)[i];
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 w = ld_written(reinterpret_cast<const uint4*>(p) + i);
+            memcpy(&part[i], &w, 16);
+        }
     }
     __device__ __forceinline__ float at(int i) const {
         constexpr int V = 16 / sizeof(T);
