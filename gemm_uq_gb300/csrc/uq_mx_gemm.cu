@@ -283,9 +283,13 @@ __device__ __forceinline__ void zero_tail(const MxGemmArgs& a, long long at, lon
 __device__ __forceinline__ void after_prior_work(const MxGemmArgs& a) {
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-// Lets the next kernel's CTAs start as these leave their SMs.  Not before this CTA has its tensor memory: one that
-// started before and took it would hold it until this kernel is done.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Lets the next kernel's CTAs start as these leave their SMs.  Not before this kernel's own wait, since the next one may
+// request weights that work before this kernel writes; and not before this CTA has its tensor memory: one that started
+// before and took it would hold it until this kernel is done.
+__device__ __forceinline__ void launch_dependents(const MxGemmArgs& a) {
+    after_prior_work(a);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // The tiles of a CTA and its k steps of them.
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -548,12 +552,12 @@ mx_gemm_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                          :: "r"(smem_u32(tmem_ptr)), "r"((uint32_t)a.tmem_cols) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-            launch_dependents();
         }
         fence_before();
         asm volatile("bar.sync 1, %0;" :: "n"(TMEM_WARPS * 32) : "memory");
         fence_after();
         tmem = (uint32_t)uniform((int)*tmem_ptr);
+        if (warp == 1) launch_dependents(a);
     }
 
     if (warp == 0 || (!FUSED && warp == 6)) {
@@ -878,12 +882,12 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
         if (warp == 1) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_ptr)) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-            launch_dependents();
         }
         fence_before();
         asm volatile("bar.sync 1, 160;" ::: "memory");
         fence_after();
         tmem = (uint32_t)uniform((int)*tmem_ptr);
+        if (warp == 1) launch_dependents(a);
     }
     // the token columns a tile's MMAs use: a multiple of 16, half of the rows in each CTA
     auto columns = [&](const Tile& t) { return (uniform(t.rows) + 15) / 16 * 16; };

@@ -20,8 +20,10 @@ template <class T, int FMT, int STEPS>
 __global__ void __launch_bounds__(128) quantize_mx_kernel(const T* x, long long ldx, uint8_t* codes, uint8_t* scales,
                                                           int rows, int K, float tscale, const int32_t* offsets,
                                                           int segments, const int32_t* pos, int topk, bool early) {
-    // Only a product's own quantizer lets the next kernel start early: what this one writes may be the weights that a
-    // later kernel requests before it waits for its predecessor.
+    // Only a product's own quantizer lets the next kernel, that product, start early: what this one writes may otherwise be
+    // the weights that a later kernel requests before it waits for its predecessor.  It may do so at once: the work before
+    // this call is what overlap's users promise does not write the weights, and the work before that was complete when
+    // this kernel could start.
     if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");           // with launch overlap: x follows earlier work
     constexpr int UNIT_K = STEP_K * STEPS;                       // k of a row per warp

@@ -319,7 +319,11 @@ uq_status uq_set_gemm_path(int path);
  * complete before it reads x (or the offsets of rows by expert, on which its weight requests
  * depend), touches a workspace or writes its output.  Turn it on only when
  * wq / scales / zeros_or_codebook (wcodes / wscales) are not written by the work that immediately precedes the
- * call on the stream (true for a decode loop over fixed weights).  Host-only; always UQ_OK.
+ * call on the stream (true for a decode loop over fixed weights).  The kernels of uq_gemm, uq_gemm_gated and
+ * uq_gemm_w4a8 let the next one start before they have waited for their own predecessor, so a run of such calls
+ * counts as one: the weights of the call after it must not be written by the work before it either.  The
+ * microscaled calls wait first: all that precedes one of them is complete when the next call requests weights.
+ * Host-only; always UQ_OK.
  */
 uq_status uq_set_launch_overlap(int enable);
 

@@ -47,3 +47,21 @@ def test_no_read_only_loads_of_what_a_predecessor_may_write(file, kernel):
         for k in _kernels(shared).values():
             parts = parts.replace(k, "")
         assert "__ldg(" not in parts and "__restrict__" not in parts, shared
+
+
+@pytest.mark.parametrize("kernel", [k for f, k in EARLY if f == "uq_mx_gemm.cu"])
+def test_products_let_dependents_go_after_their_own_wait(kernel):
+    """The next kernel requests its weights before it waits, so it may start only once all work before this product is
+    complete: the trigger follows the product's wait, in the same warp."""
+    text, trigger = _source("uq_mx_gemm.cu"), "griddepcontrol.launch_dependents"
+    assert text.count(trigger) == 1 and trigger not in _kernels("uq_mx_gemm.cu")[kernel]
+    helper = text[text.index("void launch_dependents("):]
+    helper = helper[:helper.index("}")]
+    assert 0 <= helper.find("after_prior_work(a);") < helper.index(trigger)
+    assert _kernels("uq_mx_gemm.cu")[kernel].count("launch_dependents(a)") == 1
+
+
+def test_only_a_products_own_quantizer_lets_dependents_go():
+    body = _kernels("uq_mx_quant.cu")["quantize_mx_kernel"]
+    assert body.count("griddepcontrol.launch_dependents") == 1
+    assert re.search(r"if \(early\) asm volatile\(\"griddepcontrol\.launch_dependents;", body)
