@@ -86,6 +86,7 @@ struct Workspace {
     size_t ticket_bytes = 0;
     float* gate32 = nullptr;           // gated projection: fp32 gate outputs [M][N]
     size_t gate32_bytes = 0;
+    bool fresh_operands = false;       // a microscaled operand was written since the last microscaled product
 };
 std::map<std::pair<int, void*>, Workspace> g_ws;
 
@@ -163,6 +164,21 @@ uq_status workspace(int dev, cudaStream_t st, size_t partial_bytes, size_t ticke
     if (s != UQ_OK) return s;
     *out = &w;
     return UQ_OK;
+}
+
+// Launch overlap of the microscaled calls.  A product requests its weights before it waits for the work before it, so one
+// that follows a call that writes operands (they may be its weights) starts without overlap.
+void operands_written(int dev, cudaStream_t st) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_ws[{dev, (void*)st}].fresh_operands = true;
+}
+// whether operands were written since the last product on the stream
+bool take_fresh_operands(int dev, cudaStream_t st) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    Workspace& w = g_ws[{dev, (void*)st}];
+    const bool fresh = w.fresh_operands;
+    w.fresh_operands = false;
+    return fresh;
 }
 
 // Output mode of a launch: plain bf16 y; or the gated projection's gate pass (fp32 into out32) or up
@@ -897,7 +913,11 @@ uq_status uq_pack_mx_scales(const uint8_t* natural, uint8_t* tiles, int experts,
     if (experts == 0 || rows == 0 || K == 0) return UQ_OK;
     if (!natural || !tiles) return fail(UQ_ERR_INVALID, "null pointer");
     if (!aligned16(natural) || !aligned16(tiles)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
-    cudaError_t e = uq::launch_pack_mx_scales(fmt, natural, tiles, experts, rows, K, static_cast<cudaStream_t>(stream));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    operands_written(dev, static_cast<cudaStream_t>(stream));
+    e = uq::launch_pack_mx_scales(fmt, natural, tiles, experts, rows, K, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "scale pack launch");
 }
 
@@ -916,9 +936,11 @@ uq_status uq_quantize_mx(const void* x, uq_dtype xtype, long long ldx, uint8_t* 
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(offsets) || !aligned16(pos))
         return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
     DeviceState* ds = nullptr;
-    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    operands_written(dev, static_cast<cudaStream_t>(stream));
     cudaError_t e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, scales, rows, K, tscale, offsets, segments, pos,
-                                           topk, ds->sms, false, static_cast<cudaStream_t>(stream));
+                                           topk, ds->sms, false, uq::launch_overlap(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled quantization launch");
 }
 
@@ -982,6 +1004,8 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     a.N = N;
     a.K = K;
     if ((s = check_tiles(M, 1, N)) != UQ_OK) return s;
+    const bool overlap = uq::launch_overlap() && !take_fresh_operands(dev, st);
+    a.wait = overlap;
     if (!xscales) a.alpha = alpha * tscale_x;
     if (!xscales && uq::mx_gemm_quantizes(M)) {
         a.xraw = x;
@@ -995,7 +1019,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
         if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + mx_scales_bytes(M, K, fmt, 0))) != UQ_OK) return s;
         uint8_t* codes = reinterpret_cast<uint8_t*>(ws->aux);
         e = uq::launch_quantize_mx(fmt, x, xtype, ldx, codes, codes + code_bytes, M, K, tscale_x, nullptr, 0, nullptr, 0,
-                                   ds->sms, true, st);
+                                   ds->sms, true, overlap, st);
         if (e != cudaSuccess) return cuda_fail(e, "microscaled quantization launch");
         xcodes = codes;
         a.xscales = codes + code_bytes;
@@ -1033,7 +1057,8 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
         !aligned16(wscales_up) || !aligned16(offsets) || !aligned16(alpha) || !aligned16(alpha_up))
         return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
     DeviceState* ds = nullptr;
-    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
     uq::MxGemmArgs a = {};
     a.xscales = xscales;
     a.wscales = wscales;
@@ -1050,6 +1075,11 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     a.N = N;
     a.K = K;
     if ((s = check_tiles(rows, experts, N)) != UQ_OK) return s;
+    // the offsets are needed before any weights are requested, so the wait comes first here, fresh operands or not
+    if (uq::launch_overlap()) {
+        take_fresh_operands(dev, st);
+        a.wait = 1;
+    }
     e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, ds->sms, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "grouped microscaled product launch");
 }

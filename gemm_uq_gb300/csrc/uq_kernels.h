@@ -166,10 +166,10 @@ cudaError_t launch_colsum32(const uint16_t* x, float* sx, int M, int mpad, int K
 cudaError_t launch_tc(int fmt, const uint16_t* x, const TcArgs& a, size_t smem, int grid, cudaStream_t st);
 
 // microscaled 4-bit quantization (uq_mx_quant.cu)
-// early: the next kernel may start before this one is done
+// early: the next kernel may start before this one is done; overlap: this one before the work before it is
 cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
                                int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
-                               int topk, int sms, bool early, cudaStream_t st);
+                               int topk, int sms, bool early, bool overlap, cudaStream_t st);
 cudaError_t launch_dequant_mx(int fmt, const uint8_t* codes, const uint8_t* scales, void* out, int type, int rows, int K,
                               float tscale, const int32_t* offsets, int segments, int sms, cudaStream_t st);
 cudaError_t launch_pack_mx_scales(int fmt, const uint8_t* natural, uint8_t* tiles, int experts, int rows, int K,

@@ -1259,7 +1259,6 @@ cudaError_t launch_mx_gemm(int fmt, const uint8_t* xcodes, const uint8_t* wcodes
                            MxGemmArgs a, int sms, cudaStream_t st) {
     if (!encode_fn()) return cudaErrorNotSupported;
     plan(fmt, wcodes_up != nullptr, a, sms);
-    if (launch_overlap()) a.wait = 1;
     MxGemmMaps m;
     const int tps = (a.pair ? PAIR_STEP : STEP_K) / mx_tile_k(fmt);
     const long long wrows = (long long)a.experts * a.N, wtiles = (long long)a.experts * a.row_tiles;

@@ -154,7 +154,7 @@ template <class F> cudaError_t with_steps(int rows, int K, int sms, F&& f) {
 
 cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx, uint8_t* codes, uint8_t* scales,
                                int rows, int K, float tscale, const int32_t* offsets, int segments, const int32_t* pos,
-                               int topk, int sms, bool early, cudaStream_t st) {
+                               int topk, int sms, bool early, bool overlap, cudaStream_t st) {
     return with_steps(rows, K, sms, [&](auto steps, int grid) {
         return with_dtype(xtype, [&](auto t) {
             using T = decltype(t);
@@ -168,7 +168,7 @@ cudaError_t launch_quantize_mx(int fmt, const void* x, int xtype, long long ldx,
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
             attr[0].val.programmaticStreamSerializationAllowed = 1;
             cfg.attrs = attr;
-            cfg.numAttrs = launch_overlap() ? 1 : 0;
+            cfg.numAttrs = overlap ? 1 : 0;
             return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), ldx, codes, scales, rows, K, tscale, offsets,
                                       segments, pos, topk, early);
         });

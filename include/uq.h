@@ -323,6 +323,8 @@ uq_status uq_set_gemm_path(int path);
  * uq_gemm_w4a8 let the next one start before they have waited for their own predecessor, so a run of such calls
  * counts as one: the weights of the call after it must not be written by the work before it either.  The
  * microscaled calls wait first: all that precedes one of them is complete when the next call requests weights.
+ * Operands that uq_quantize_mx or uq_pack_mx_scales writes may be the next product's weights on that stream: such a
+ * product is launched without overlap.
  * Host-only; always UQ_OK.
  */
 uq_status uq_set_launch_overlap(int enable);
