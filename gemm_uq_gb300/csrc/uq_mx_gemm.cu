@@ -374,8 +374,9 @@ template <class T> __device__ __forceinline__ void put16(const MxGemmArgs& a, in
     for (int j = 0; j < 16; ++j, p += a.N)
         if (nn < a.N && j < count) *p = from_f32<T>(v[j]);
 }
-// silu(g) * u = g * u / (1 + e^-g) to about 2^-21: e^-g = 2^t with t = -g log2(e) rounded, corrected to first order by
-// what the rounding left (t alone would lose |t| 2^-24), then an approximate reciprocal.  A gated tile's epilogue is
+// silu(g) * u = g * u / (1 + e^-g) to 2^-20: e^-g = 2^t with t = -g log2(e) rounded, corrected to first order by what
+// the rounding left (t alone would lose |t| 2^-24) wherever 2^t is finite and matters, |t| < 128, then an approximate
+// reciprocal.  Below g = -88.72 e^-g exceeds fp32 and the result is zero.  A gated tile's epilogue is
 // 128 of these per lane beside MMAs that may take only a few thousand cycles; with expf and a correctly rounded
 // division it took longer than they did (16384 rows, 64 experts of 1408 x 2048 gated: 150 us, without the gate 47).
 __device__ __forceinline__ float swiglu(float g, float u) {
@@ -383,7 +384,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
     const float left = fmaf(g, -1.4426950408889634f, -t) - g * 1.9259630e-8f;      // log2(e) = 1.44269502.. + 1.92596e-8
     float e, r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
-    if (fabsf(t) < 120.f) e = fmaf(e * 0.6931471805599453f, left, e);
+    if (fabsf(t) < 128.f) e = fmaf(e * 0.6931471805599453f, left, e);
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return g * r * u;
 }

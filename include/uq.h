@@ -455,7 +455,8 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
  * uq_gemm_mx_grouped -- the same product for rows sorted by expert: row r of segment e is multiplied with expert e's
  * weight,  y[r][n] = alpha[e] * sum_k x^[r][k] * w^[e][n][k]; rows that belong to nobody are written as zeros.
  * With wcodes_up: y[r][n] = silu(g) * u, g = alpha[e] * (the product with wcodes) and u = alpha_up[e] * (the product
- * with wcodes_up), all in fp32, rounded once.
+ * with wcodes_up), in fp32, rounded once.  silu(g) = g / (1 + e^-g) has a relative error below 2^-20, for fp32 outputs
+ * too; where e^-g exceeds fp32 (g < -88.72) it is zero, at minus infinity NaN.
  *   xcodes, xscales (device): an operand of `rows` rows in `experts` segments (offsets as there)
  *   wcodes (device) [experts][N][K/2], wscales (device) the experts' scale tiles one after the other; wcodes_up and
  *   wscales_up (device, or both NULL) likewise

@@ -1,4 +1,6 @@
-"""Microscaled operands at their limits, against the oracle: quotients past the fp32 range."""
+"""Microscaled operands at their limits, against the oracle: quotients past the fp32 range, and gate values out to where
+e^-g leaves it.
+"""
 import numpy as np
 import pytest
 import torch
@@ -45,3 +47,56 @@ def test_magnitudes_over_six_keep_their_sign(dtype, tscale):
         y = uq.gemm_mx(x[rows].to(DEV), w, "NVFP4", tscale=tscale, dtype=torch.float32)
         assert np.array_equal(y.cpu().numpy(), ref[rows])
     assert uq.device_fault() == 0
+
+
+def _sums(values, K):
+    """Weight rows fp32 [len(values)][K] of multiples of 0.5 up to 4 that add up to each value (multiples of 0.5)."""
+    w = np.zeros((len(values), K), np.float32)
+    for r, v in enumerate(values):
+        left, s = abs(v), np.sign(v)
+        for k in range(K):
+            step = min(4.0, left) if min(4.0, left) in omx.GRID else max(c for c in omx.GRID if c <= min(4.0, left))
+            w[r, k] = s * step
+            left -= step
+        assert left == 0
+    return w
+
+
+@pytest.mark.parametrize("R", [1, 20, 700])
+def test_gate_values_out_to_the_range_of_fp32(R):
+    """silu(g) for g to +-130.  Its relative error is that of ex2 (2^-22), 1 + e^-g (2^-24), the reciprocal (2^-23, and half
+    a subnormal step where it is subnormal) and two products (2^-24 each), under 2^-20 in all; past g = -88.72 e^-g
+    exceeds fp32 and the result is zero."""
+    K = 64
+    g = np.arange(-130, 130.5, 0.5)
+    # one block scale for all: the values are the e2m1 grid's, at scale 1
+    wc = omx.e2m1_encode(np.abs(_sums(g, K))) | (np.signbit(_sums(g, K)).astype(np.uint8) << 3)
+    byte = np.full((len(g), K // 32), 127, np.uint8)
+    w = (torch.from_numpy(omx.pack_codes(wc)).to(DEV)[None], torch.from_numpy(omx.tile_scales(byte, "MXFP4")).to(DEV)[None])
+    uc = np.zeros((len(g), K), np.uint8)
+    uc[:, 0] = 2                                                                     # up = 1
+    up = (torch.from_numpy(omx.pack_codes(uc)).to(DEV)[None], w[1])
+    off = torch.tensor([0, R], dtype=torch.int32, device=DEV)
+    q = uq.quantize_mx(torch.ones(R, K, dtype=torch.bfloat16, device=DEV), "MXFP4", offsets=off)
+    for scale in (1.0, 0.99, 0.9871):
+        alpha = torch.tensor([scale], dtype=torch.float32, device=DEV)
+        y = uq.gemm_mx_grouped(q, w, off, "MXFP4", up=up, alpha=alpha, dtype=torch.float32).cpu().numpy().astype(np.float64)
+        gs = (g.astype(np.float32) * np.float32(scale)).astype(np.float64)
+        ref = gs / (1 + np.exp(-gs))
+        inside = gs > -88.72
+        assert np.array_equal(y, np.broadcast_to(y[0], y.shape))
+        lim = 2.0 ** -20 * np.abs(ref) + np.abs(gs) * 2.0 ** -149
+        assert np.all(np.abs(y[0] - ref)[inside] <= lim[inside]), np.max((np.abs(y[0] - ref) / lim)[inside])
+        assert not y[0][~inside].any()
+
+
+def test_gate_of_infinities_and_nan():
+    """alpha carries the gate to +-inf and NaN: silu(inf) u = inf u, silu(-inf) and silu(NaN) are NaN as g / (1 + e^-g) is."""
+    x = torch.ones(3, 64, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device=DEV)
+    q = uq.quantize_mx(x, "MXFP4", offsets=off)
+    w1 = uq.quantize_mx(torch.ones(130, 64, dtype=torch.bfloat16, device=DEV), "MXFP4")
+    w = (w1[0].repeat(3, 1, 1), w1[1].repeat(3, 1))
+    alpha = torch.tensor([float("inf"), float("-inf"), float("nan")], device=DEV)
+    y = uq.gemm_mx_grouped(q, w, off, "MXFP4", up=w, alpha=alpha, dtype=torch.float32)
+    assert torch.isposinf(y[0]).all() and torch.isnan(y[1:]).all()
