@@ -2,7 +2,8 @@
 
 Every function here forwards torch tensors' device pointers, sizes and the current CUDA
 stream to the same-named ``extern "C"`` entry point of ``libuq.so`` and raises
-``UqError`` on a non-OK status.  No step of the computation runs in Python or in
+``UqError`` on a non-OK status.  With ``stream=`` a call runs on that stream, and its result comes
+from that stream's memory pool.  No step of the computation runs in Python or in
 PyTorch: if the library is missing, importing the ops raises instead of falling back.
 """
 from __future__ import annotations
@@ -102,6 +103,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A result's memory, from the pool of the stream that writes it: memory of the current stream's pool may still
+    be in use by work queued there, and may be given out again there while the given stream writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def packed_size(N: int, K: int, group: int, fmt: str):
     """(wq_bytes, scales_bytes, zeros_bytes) -- host only."""
     a, b, c = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
@@ -114,7 +124,7 @@ def pack_layout(codes: torch.Tensor, group: int, fmt: str, stream=None) -> torch
     """int8 codes [N][K] (device) -> packed uint8 plane (synchronizes the stream)."""
     N, K = codes.shape
     wq_bytes, _, _ = packed_size(N, K, group, fmt)
-    wq = torch.empty(max(wq_bytes, 16), dtype=torch.uint8, device=codes.device)
+    wq = _empty(max(wq_bytes, 16), torch.uint8, codes.device, stream)
     _check(lib().uq_pack_layout(_ptr(codes), _ptr(wq), N, K, group, FORMATS[fmt], _stream(stream)),
            "uq_pack_layout")
     return wq
@@ -127,8 +137,8 @@ def pack_gguf(blocks: torch.Tensor, qtype: str, N: int, K: int, stream=None):
     """uq_pack_gguf: GGUF Q4_0 / Q8_0 block bytes (device uint8) -> (wq, scales) of INT4_SYM / INT8_SYM, group 32."""
     t, fmt = GGUF_TYPES[qtype]
     wq_bytes, sc_bytes, _ = packed_size(N, K, 32, fmt)
-    wq = torch.empty(max(wq_bytes, 16), dtype=torch.uint8, device=blocks.device)
-    scales = torch.empty((N, K // 32), dtype=torch.int16, device=blocks.device)
+    wq = _empty(max(wq_bytes, 16), torch.uint8, blocks.device, stream)
+    scales = _empty((N, K // 32), torch.int16, blocks.device, stream)
     assert blocks.is_cuda and blocks.is_contiguous()
     _check(lib().uq_pack_gguf(ctypes.c_void_p(blocks.data_ptr()), t, _ptr(wq), _ptr(scales), N, K, _stream(stream)),
            "uq_pack_gguf")
@@ -138,7 +148,7 @@ def pack_gguf(blocks: torch.Tensor, qtype: str, N: int, K: int, stream=None):
 def pack_kmeta(d, dmin, sc, m, stream=None) -> torch.Tensor:
     """K4 fp16 d, dmin [N][S] (as int16/uint16/float16 tensors), uint8 sc, m [N][S][8] -> records [N][S][16]."""
     N, S = d.shape
-    meta = torch.empty((N, S, 16), dtype=torch.uint8, device=d.device)
+    meta = _empty((N, S, 16), torch.uint8, d.device, stream)
     _check(lib().uq_pack_kmeta(_ptr(d), _ptr(dmin), _ptr(sc), _ptr(m), _ptr(meta), N, S * 256, _stream(stream)),
            "uq_pack_kmeta")
     return meta
@@ -147,7 +157,7 @@ def pack_kmeta(d, dmin, sc, m, stream=None) -> torch.Tensor:
 def pack_zeros(z: torch.Tensor, stream=None) -> torch.Tensor:
     """INT4_ASYM zeros, one per byte [N][G] -> two per byte [N][ceil(G/2)]."""
     N, G = z.shape
-    out = torch.empty((N, (G + 1) // 2), dtype=torch.uint8, device=z.device)
+    out = _empty((N, (G + 1) // 2), torch.uint8, z.device, stream)
     _check(lib().uq_pack_zeros(_ptr(z), _ptr(out), N, G, _stream(stream)), "uq_pack_zeros")
     return out
 
@@ -158,7 +168,7 @@ def gemm(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, zc, N: int, gr
     M, K = x.shape
     assert x.dtype == torch.bfloat16
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     _check(lib().uq_gemm(_ptr(x), _ptr(wq), _ptr(scales), _ptr(zc), _ptr(y), M, N, K, group, FORMATS[fmt],
                          _stream(stream)), "uq_gemm")
     return y
@@ -170,7 +180,7 @@ def gemm_gated(x: torch.Tensor, gate: tuple, up: tuple, N: int, group: int, fmt:
     M, K = x.shape
     assert x.dtype == torch.bfloat16
     if h is None:
-        h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        h = _empty((M, N), torch.bfloat16, x.device, stream)
     (wg, sg, zg), (wu, su, zu) = gate, up
     _check(lib().uq_gemm_gated(_ptr(x), _ptr(wg), _ptr(sg), _ptr(zg), _ptr(wu), _ptr(su), _ptr(zu), _ptr(h),
                                M, N, K, group, FORMATS[fmt], _stream(stream)), "uq_gemm_gated")
@@ -195,7 +205,7 @@ def gemm_gated_kernel_count(M: int, N: int, K: int, group: int, fmt: str) -> int
 
 def rope_table(max_pos: int, head_dim: int, base: float, device=None, stream=None) -> torch.Tensor:
     """uq_rope_table: fp32 [max_pos][head_dim/2][2] (cos, sin) on the device."""
-    t = torch.empty((max_pos, head_dim // 2, 2), dtype=torch.float32, device=device or "cuda")
+    t = _empty((max_pos, head_dim // 2, 2), torch.float32, device or "cuda", stream)
     _check(lib().uq_rope_table(_ptr(t), max_pos, head_dim, float(base), _stream(stream)), "uq_rope_table")
     return t
 
@@ -206,7 +216,7 @@ def rmsnorm_rope(x: torch.Tensor, gamma: torch.Tensor, pos: torch.Tensor, table:
     M, D = x.shape
     assert x.dtype == torch.bfloat16 and gamma.dtype == torch.bfloat16 and pos.dtype == torch.int32
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _check(lib().uq_rmsnorm_rope(_ptr(x), _ptr(gamma), _ptr(pos), _ptr(table), _ptr(y), M, D, head_dim,
                                  table.shape[0], float(eps), _stream(stream)), "uq_rmsnorm_rope")
     return y
@@ -218,7 +228,7 @@ def gemm_w4a8(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, zc, N: in
     M, K = x.shape
     assert x.dtype == torch.bfloat16
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     _check(lib().uq_gemm_w4a8(_ptr(x), _ptr(wq), _ptr(scales), _ptr(zc), _ptr(y), M, N, K, group, FORMATS[fmt],
                               _stream(stream)), "uq_gemm_w4a8")
     return y
@@ -264,7 +274,7 @@ def gemm_ptrs(x_ptr: int, wq_ptr: int, scales_ptr: int, zc_ptr, y_ptr: int, M: i
 
 
 def unpack_codes(wq: torch.Tensor, N: int, K: int, group: int, fmt: str, stream=None) -> torch.Tensor:
-    codes = torch.empty((N, K), dtype=torch.int8, device=wq.device)
+    codes = _empty((N, K), torch.int8, wq.device, stream)
     _check(lib().uq_unpack_codes(_ptr(wq), _ptr(codes), N, K, group, FORMATS[fmt], _stream(stream)),
            "uq_unpack_codes")
     return codes
@@ -272,7 +282,7 @@ def unpack_codes(wq: torch.Tensor, N: int, K: int, group: int, fmt: str, stream=
 
 def dequant(wq: torch.Tensor, scales: torch.Tensor, zc, N: int, K: int, group: int, fmt: str,
             stream=None) -> torch.Tensor:
-    w = torch.empty((N, K), dtype=torch.float32, device=wq.device)
+    w = _empty((N, K), torch.float32, wq.device, stream)
     _check(lib().uq_dequant(_ptr(wq), _ptr(scales), _ptr(zc), _ptr(w), N, K, group, FORMATS[fmt],
                             _stream(stream)), "uq_dequant")
     return w
@@ -282,13 +292,13 @@ def quantize(w: torch.Tensor, group: int, fmt: str, codebook: torch.Tensor | Non
     """GPU quantizer for the flat formats: returns (codes int8 [N][K], scales fp16 bits [N][G], zeros)."""
     N, K = w.shape
     G = K // group if group else 0
-    codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
-    scales = torch.empty((N, G), dtype=torch.int16, device=w.device)
+    codes = _empty((N, K), torch.int8, w.device, stream)
+    scales = _empty((N, G), torch.int16, w.device, stream)
     zeros = None
     if fmt == "INT4_ASYM":
-        zeros = torch.empty((N, G), dtype=torch.uint8, device=w.device)
+        zeros = _empty((N, G), torch.uint8, w.device, stream)
     elif fmt == "INT2_ASYM":
-        zeros = torch.empty((N, G), dtype=torch.int16, device=w.device)
+        zeros = _empty((N, G), torch.int16, w.device, stream)
     _check(lib().uq_quantize(_ptr(w), _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(codebook), N, K, group,
                              FORMATS[fmt], _stream(stream)), "uq_quantize")
     return codes, scales, zeros
@@ -299,11 +309,11 @@ def quantize_k4(w: torch.Tensor, stream=None):
     N, K = w.shape
     S = K // 256
     dev = w.device
-    codes = torch.empty((N, K), dtype=torch.int8, device=dev)
-    d = torch.empty((N, S), dtype=torch.int16, device=dev)
-    dmin = torch.empty((N, S), dtype=torch.int16, device=dev)
-    sc = torch.empty((N, S, 8), dtype=torch.uint8, device=dev)
-    m = torch.empty((N, S, 8), dtype=torch.uint8, device=dev)
+    codes = _empty((N, K), torch.int8, dev, stream)
+    d = _empty((N, S), torch.int16, dev, stream)
+    dmin = _empty((N, S), torch.int16, dev, stream)
+    sc = _empty((N, S, 8), torch.uint8, dev, stream)
+    m = _empty((N, S, 8), torch.uint8, dev, stream)
     _check(lib().uq_quantize_k4(_ptr(w), _ptr(codes), _ptr(d), _ptr(dmin), _ptr(sc), _ptr(m), N, K,
                                 _stream(stream)), "uq_quantize_k4")
     return codes, d, dmin, sc, m
@@ -378,7 +388,7 @@ def pack_mx_scales(scales: torch.Tensor, fmt: str, stream=None) -> torch.Tensor:
     experts = scales.shape[0] if scales.dim() == 3 else 1
     rows, K = scales.shape[-2], scales.shape[-1] * MX_BLOCK[fmt]
     assert scales.dtype == torch.uint8
-    tiles = torch.empty((experts, mx_scales_size(rows, K, fmt)), dtype=torch.uint8, device=scales.device)
+    tiles = _empty((experts, mx_scales_size(rows, K, fmt)), torch.uint8, scales.device, stream)
     _check(lib().uq_pack_mx_scales(_at(scales), _at(tiles), experts, rows, K, MX_FORMATS[fmt], _handle(stream)),
            "uq_pack_mx_scales")
     return tiles if scales.dim() == 3 else tiles[0]
@@ -407,8 +417,8 @@ def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.T
         topk, at = pos.shape[1], _at(pos)
         rows = T * topk
     dev = x.device
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(_scale_bytes(rows, K, fmt, segments), dtype=torch.uint8, device=dev)
+    codes = _empty((rows, K // 2), torch.uint8, dev, stream)
+    scales = _empty(_scale_bytes(rows, K, fmt, segments), torch.uint8, dev, stream)
     _check(lib().uq_quantize_mx(x.data_ptr(), DTYPES[x.dtype], _row_stride(x, T, K), codes.data_ptr(), scales.data_ptr(),
                                 T, K, MX_FORMATS[fmt], tscale, off, segments, at, topk, _handle(stream)),
            "uq_quantize_mx")
@@ -425,7 +435,7 @@ def dequant_mx(q: tuple, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | 
         assert offsets.dtype == torch.int32
         segments, off = offsets.numel() - 1, _at(offsets)
     assert scales.numel() >= _scale_bytes(rows, half * 2, fmt, segments)
-    out = torch.empty((rows, half * 2), dtype=dtype, device=codes.device)
+    out = _empty((rows, half * 2), dtype, codes.device, stream)
     _check(lib().uq_dequant_mx(_at(codes), _at(scales), out.data_ptr(), DTYPES[dtype], rows, half * 2, MX_FORMATS[fmt],
                                tscale, off, segments, _handle(stream)), "uq_dequant_mx")
     return out
@@ -453,7 +463,7 @@ def gemm_mx(x, w: tuple, fmt: str, tscale: float = 1.0, alpha: float = 1.0, dtyp
         xtype, xptr, xsc, ld = 0, _at(xcodes), _at(xscales), 0
     assert xk == K, "x and w have different K"
     if y is None:
-        y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=wcodes.device)
+        y = _empty((M, N), dtype or torch.bfloat16, wcodes.device, stream)
     assert y.shape == (M, N)
     _check(lib().uq_gemm_mx(xptr, xtype, ld, xsc, tscale, _at(wcodes), _at(wscales), _at(y), DTYPES[y.dtype], M, N, K,
                             MX_FORMATS[fmt], alpha, _handle(stream)), "uq_gemm_mx")
@@ -482,7 +492,7 @@ def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tup
     for v in (alpha, alpha_up):
         assert v is None or (v.dtype == torch.float32 and v.numel() == E)
     if y is None:
-        y = torch.empty((R, N), dtype=dtype, device=xcodes.device)
+        y = _empty((R, N), dtype, xcodes.device, stream)
     assert y.shape == (R, N)
     _check(lib().uq_gemm_mx_grouped(_at(xcodes), _at(xscales), _at(wcodes), _at(wscales), uc, us, _at(offsets),
                                     _at_opt(alpha), _at_opt(alpha_up), _at(y), DTYPES[y.dtype], R, E, N, K,
@@ -497,9 +507,9 @@ def moe_sort(ids: torch.Tensor, experts: int, stream=None):
     T, k = ids.shape
     assert ids.dtype == torch.int32
     dev = ids.device
-    order = torch.empty(T * k, dtype=torch.int32, device=dev)
-    pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-    offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=dev)
+    order = _empty(T * k, torch.int32, dev, stream)
+    pos = _empty((T, k), torch.int32, dev, stream)
+    offsets = _empty(max(experts, 0) + 1, torch.int32, dev, stream)
     _check(lib().uq_moe_sort(_at(ids), T, k, experts, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
                              _handle(stream)), "uq_moe_sort")
     return order, pos, offsets
@@ -509,7 +519,7 @@ def moe_gather(x: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor, stream
     """uq_moe_gather: xs[pos[t][j]] = x[t], [T*k][H]; rows past offsets[-1] are zero."""
     (T, H), (rows, k) = x.shape, pos.shape
     assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and rows == T
-    xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    xs = _empty((T * k, H), x.dtype, x.device, stream)
     _check(lib().uq_moe_gather(_at(x), DTYPES[x.dtype], _at(pos), _at(offsets), offsets.numel() - 1, xs.data_ptr(), T, k,
                                H, _handle(stream)), "uq_moe_gather")
     return xs
@@ -519,7 +529,7 @@ def moe_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, stream=None) -> torch.
     """uq_moe_gather_grad: dx[t] = sum_j dxs[pos[t][j]], [T][H]."""
     (T, k), (R, H) = pos.shape, dxs.shape
     assert pos.dtype == torch.int32 and R == T * k
-    dx = torch.empty((T, H), dtype=dxs.dtype, device=dxs.device)
+    dx = _empty((T, H), dxs.dtype, dxs.device, stream)
     _check(lib().uq_moe_gather_grad(_at(dxs), DTYPES[dxs.dtype], _at(pos), dx.data_ptr(), T, k, H, _handle(stream)),
            "uq_moe_gather_grad")
     return dx
@@ -530,7 +540,7 @@ def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stre
     (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and weights.dtype == torch.float32
     assert R == T * k and weights.shape == pos.shape
-    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+    y = _empty((T, H), ys.dtype, ys.device, stream)
     _check(lib().uq_moe_combine(_at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), y.data_ptr(), T, k, H,
                                 _handle(stream)), "uq_moe_combine")
     return y
@@ -542,8 +552,8 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weig
     (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and weights.dtype == torch.float32
     assert dy.dtype == ys.dtype and dy.shape == (T, H) and R == T * k and weights.shape == pos.shape
-    dys = torch.empty_like(ys)
-    dw = torch.empty((T, k), dtype=torch.float32, device=ys.device)
+    dys = _empty(ys.shape, ys.dtype, ys.device, stream)
+    dw = _empty((T, k), torch.float32, ys.device, stream)
     _check(lib().uq_moe_combine_grad(_at(dy), _at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), _at(offsets),
                                      offsets.numel() - 1, dys.data_ptr(), dw.data_ptr(), T, k, H, _handle(stream)),
            "uq_moe_combine_grad")
