@@ -355,20 +355,29 @@ MX_BLOCK = {"MXFP4": 32, "NVFP4": 16}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _at(t: torch.Tensor) -> int:
-    assert t.is_cuda and t.is_contiguous(), "tensors passed to uq must be contiguous CUDA tensors"
+def _at(t: torch.Tensor, dev: int) -> int:
+    assert t.get_device() == dev and t.is_contiguous(), "tensors passed to uq must be contiguous and on one CUDA device"
     return t.data_ptr()
 
 
-def _at_opt(t):
-    return None if t is None else _at(t)
+def _at_opt(t, dev: int):
+    return None if t is None else _at(t, dev)
 
 
-def _handle(stream) -> int:
-    """The current stream's handle, without building a Stream object."""
+def _operand(q: tuple, dev: int, scale_bytes: int):
+    """Pointers of a microscaled operand's codes and scales."""
+    codes, scales = q
+    assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "codes and scales are uint8"
+    assert scales.numel() >= scale_bytes, "fewer scale tiles than the operand has"
+    return _at(codes, dev), _at(scales, dev)
+
+
+def _handle(stream, dev: int) -> int:
+    """The stream's handle (the current one's without building a Stream object); the tensors' device must be current."""
+    assert torch._C._cuda_getDevice() == dev, "tensors passed to uq must be on the current CUDA device"
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def mx_scales_size(rows: int, K: int, fmt: str, segments: int = 0) -> int:
@@ -388,8 +397,10 @@ def pack_mx_scales(scales: torch.Tensor, fmt: str, stream=None) -> torch.Tensor:
     experts = scales.shape[0] if scales.dim() == 3 else 1
     rows, K = scales.shape[-2], scales.shape[-1] * MX_BLOCK[fmt]
     assert scales.dtype == torch.uint8
+    dev = scales.get_device()
     tiles = _empty((experts, mx_scales_size(rows, K, fmt)), torch.uint8, scales.device, stream)
-    _check(lib().uq_pack_mx_scales(_at(scales), _at(tiles), experts, rows, K, MX_FORMATS[fmt], _handle(stream)),
+    _check(lib().uq_pack_mx_scales(_at(scales, dev), tiles.data_ptr(), experts, rows, K, MX_FORMATS[fmt],
+                                   _handle(stream, dev)),
            "uq_pack_mx_scales")
     return tiles if scales.dim() == 3 else tiles[0]
 
@@ -408,19 +419,18 @@ def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.T
     ``offsets`` (int32 [experts + 1]): the rows are sorted by expert; with ``pos`` (int32 [T][k]) they are gathered by
     expert on the way, as moe_gather would, and the operand has T*k rows."""
     T, K = x.shape
-    rows, topk, segments, off, at = T, 0, 0, None, None
+    rows, topk, segments, off, at, dev = T, 0, 0, None, None, x.get_device()
     if offsets is not None:
         assert offsets.dtype == torch.int32
-        segments, off = offsets.numel() - 1, _at(offsets)
+        segments, off = offsets.numel() - 1, _at(offsets, dev)
     if pos is not None:
         assert pos.dtype == torch.int32 and pos.shape[0] == T
-        topk, at = pos.shape[1], _at(pos)
+        topk, at = pos.shape[1], _at(pos, dev)
         rows = T * topk
-    dev = x.device
-    codes = _empty((rows, K // 2), torch.uint8, dev, stream)
-    scales = _empty(_scale_bytes(rows, K, fmt, segments), torch.uint8, dev, stream)
+    codes = _empty((rows, K // 2), torch.uint8, x.device, stream)
+    scales = _empty(_scale_bytes(rows, K, fmt, segments), torch.uint8, x.device, stream)
     _check(lib().uq_quantize_mx(x.data_ptr(), DTYPES[x.dtype], _row_stride(x, T, K), codes.data_ptr(), scales.data_ptr(),
-                                T, K, MX_FORMATS[fmt], tscale, off, segments, at, topk, _handle(stream)),
+                                T, K, MX_FORMATS[fmt], tscale, off, segments, at, topk, _handle(stream, dev)),
            "uq_quantize_mx")
     return codes, scales
 
@@ -428,16 +438,15 @@ def quantize_mx(x: torch.Tensor, fmt: str, tscale: float = 1.0, offsets: torch.T
 def dequant_mx(q: tuple, fmt: str, tscale: float = 1.0, offsets: torch.Tensor | None = None,
                dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """uq_dequant_mx: the values (codes, scales) stand for, [rows][K] of ``dtype``."""
-    codes, scales = q
-    rows, half = codes.shape
+    (rows, half), dev = q[0].shape, q[0].get_device()
     segments, off = 0, None
     if offsets is not None:
         assert offsets.dtype == torch.int32
-        segments, off = offsets.numel() - 1, _at(offsets)
-    assert scales.numel() >= _scale_bytes(rows, half * 2, fmt, segments)
-    out = _empty((rows, half * 2), dtype, codes.device, stream)
-    _check(lib().uq_dequant_mx(_at(codes), _at(scales), out.data_ptr(), DTYPES[dtype], rows, half * 2, MX_FORMATS[fmt],
-                               tscale, off, segments, _handle(stream)), "uq_dequant_mx")
+        segments, off = offsets.numel() - 1, _at(offsets, dev)
+    codes, scales = _operand(q, dev, _scale_bytes(rows, half * 2, fmt, segments))
+    out = _empty((rows, half * 2), dtype, q[0].device, stream)
+    _check(lib().uq_dequant_mx(codes, scales, out.data_ptr(), DTYPES[dtype], rows, half * 2, MX_FORMATS[fmt],
+                               tscale, off, segments, _handle(stream, dev)), "uq_dequant_mx")
     return out
 
 
@@ -447,26 +456,25 @@ def gemm_mx(x, w: tuple, fmt: str, tscale: float = 1.0, alpha: float = 1.0, dtyp
 
     ``x``: a matrix (bf16, fp16 or fp32), quantized in the call with ``tscale``, or a pair (codes, scales) of
     quantize_mx.  ``w``: (codes [N][K/2], scales).  The result has ``dtype`` (default: x's, bf16 for a pair)."""
-    wcodes, wscales = w
-    N, half = wcodes.shape
+    (N, half), dev = w[0].shape, w[0].get_device()
     K = half * 2
-    assert wcodes.dtype == torch.uint8 and wscales.dtype == torch.uint8 and wscales.numel() >= _scale_bytes(N, K, fmt)
+    wcodes, wscales = _operand(w, dev, _scale_bytes(N, K, fmt))
     if isinstance(x, torch.Tensor):
         M, xk = x.shape
+        assert x.get_device() == dev, "x and w are on different devices"
         xtype, xptr, xsc, ld = DTYPES[x.dtype], x.data_ptr(), None, _row_stride(x, M, K)
         if dtype is None:
             dtype = x.dtype
     else:
-        xcodes, xscales = x
-        M, xk = xcodes.shape[0], xcodes.shape[1] * 2
-        assert xscales.numel() >= _scale_bytes(M, K, fmt)
-        xtype, xptr, xsc, ld = 0, _at(xcodes), _at(xscales), 0
+        M, xk = x[0].shape[0], x[0].shape[1] * 2
+        xptr, xsc = _operand(x, dev, _scale_bytes(M, K, fmt))
+        xtype, ld = 0, 0
     assert xk == K, "x and w have different K"
     if y is None:
-        y = _empty((M, N), dtype or torch.bfloat16, wcodes.device, stream)
+        y = _empty((M, N), dtype or torch.bfloat16, w[0].device, stream)
     assert y.shape == (M, N)
-    _check(lib().uq_gemm_mx(xptr, xtype, ld, xsc, tscale, _at(wcodes), _at(wscales), _at(y), DTYPES[y.dtype], M, N, K,
-                            MX_FORMATS[fmt], alpha, _handle(stream)), "uq_gemm_mx")
+    _check(lib().uq_gemm_mx(xptr, xtype, ld, xsc, tscale, wcodes, wscales, _at(y, dev), DTYPES[y.dtype], M, N, K,
+                            MX_FORMATS[fmt], alpha, _handle(stream, dev)), "uq_gemm_mx")
     return y
 
 
@@ -477,26 +485,25 @@ def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tup
 
     ``x``: (codes, scales) of quantize_mx with these ``offsets``; ``w`` (and ``up``: silu(x w^T) * (x up^T)): codes
     [experts][N][K/2] and the experts' scale tiles; ``alpha``, ``alpha_up``: fp32 [experts]."""
-    (xcodes, xscales), (wcodes, wscales) = x, w
-    E, N, half = wcodes.shape
-    K, R = half * 2, xcodes.shape[0]
-    assert xcodes.shape[1] == half, "x and w have different K"
+    (E, N, half), dev = w[0].shape, w[0].get_device()
+    K, R = half * 2, x[0].shape[0]
+    assert x[0].shape[1] == half, "x and w have different K"
     assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
     wbytes = E * _scale_bytes(N, K, fmt)
-    assert xscales.numel() >= _scale_bytes(R, K, fmt, E) and wscales.numel() >= wbytes
+    xcodes, xscales = _operand(x, dev, _scale_bytes(R, K, fmt, E))
+    wcodes, wscales = _operand(w, dev, wbytes)
     uc = us = None
     if up is not None:
-        ucodes, uscales = up
-        assert ucodes.shape == wcodes.shape and uscales.numel() >= wbytes
-        uc, us = _at(ucodes), _at(uscales)
+        assert up[0].shape == w[0].shape
+        uc, us = _operand(up, dev, wbytes)
     for v in (alpha, alpha_up):
         assert v is None or (v.dtype == torch.float32 and v.numel() == E)
     if y is None:
-        y = _empty((R, N), dtype, xcodes.device, stream)
+        y = _empty((R, N), dtype, w[0].device, stream)
     assert y.shape == (R, N)
-    _check(lib().uq_gemm_mx_grouped(_at(xcodes), _at(xscales), _at(wcodes), _at(wscales), uc, us, _at(offsets),
-                                    _at_opt(alpha), _at_opt(alpha_up), _at(y), DTYPES[y.dtype], R, E, N, K,
-                                    MX_FORMATS[fmt], _handle(stream)), "uq_gemm_mx_grouped")
+    _check(lib().uq_gemm_mx_grouped(xcodes, xscales, wcodes, wscales, uc, us, _at(offsets, dev),
+                                    _at_opt(alpha, dev), _at_opt(alpha_up, dev), _at(y, dev), DTYPES[y.dtype], R, E, N,
+                                    K, MX_FORMATS[fmt], _handle(stream, dev)), "uq_gemm_mx_grouped")
     return y
 
 
@@ -506,12 +513,12 @@ def moe_sort(ids: torch.Tensor, experts: int, stream=None):
     """uq_moe_sort: int32 expert ids [T][k] -> (order int32 [T*k], pos int32 [T][k], offsets int32 [experts + 1])."""
     T, k = ids.shape
     assert ids.dtype == torch.int32
-    dev = ids.device
-    order = _empty(T * k, torch.int32, dev, stream)
-    pos = _empty((T, k), torch.int32, dev, stream)
-    offsets = _empty(max(experts, 0) + 1, torch.int32, dev, stream)
-    _check(lib().uq_moe_sort(_at(ids), T, k, experts, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
-                             _handle(stream)), "uq_moe_sort")
+    dev = ids.get_device()
+    order = _empty(T * k, torch.int32, ids.device, stream)
+    pos = _empty((T, k), torch.int32, ids.device, stream)
+    offsets = _empty(max(experts, 0) + 1, torch.int32, ids.device, stream)
+    _check(lib().uq_moe_sort(_at(ids, dev), T, k, experts, order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
+                             _handle(stream, dev)), "uq_moe_sort")
     return order, pos, offsets
 
 
@@ -519,9 +526,9 @@ def moe_gather(x: torch.Tensor, pos: torch.Tensor, offsets: torch.Tensor, stream
     """uq_moe_gather: xs[pos[t][j]] = x[t], [T*k][H]; rows past offsets[-1] are zero."""
     (T, H), (rows, k) = x.shape, pos.shape
     assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and rows == T
-    xs = _empty((T * k, H), x.dtype, x.device, stream)
-    _check(lib().uq_moe_gather(_at(x), DTYPES[x.dtype], _at(pos), _at(offsets), offsets.numel() - 1, xs.data_ptr(), T, k,
-                               H, _handle(stream)), "uq_moe_gather")
+    dev, xs = x.get_device(), _empty((T * k, H), x.dtype, x.device, stream)
+    _check(lib().uq_moe_gather(_at(x, dev), DTYPES[x.dtype], _at(pos, dev), _at(offsets, dev), offsets.numel() - 1,
+                               xs.data_ptr(), T, k, H, _handle(stream, dev)), "uq_moe_gather")
     return xs
 
 
@@ -529,9 +536,9 @@ def moe_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, stream=None) -> torch.
     """uq_moe_gather_grad: dx[t] = sum_j dxs[pos[t][j]], [T][H]."""
     (T, k), (R, H) = pos.shape, dxs.shape
     assert pos.dtype == torch.int32 and R == T * k
-    dx = _empty((T, H), dxs.dtype, dxs.device, stream)
-    _check(lib().uq_moe_gather_grad(_at(dxs), DTYPES[dxs.dtype], _at(pos), dx.data_ptr(), T, k, H, _handle(stream)),
-           "uq_moe_gather_grad")
+    dev, dx = dxs.get_device(), _empty((T, H), dxs.dtype, dxs.device, stream)
+    _check(lib().uq_moe_gather_grad(_at(dxs, dev), DTYPES[dxs.dtype], _at(pos, dev), dx.data_ptr(), T, k, H,
+                                    _handle(stream, dev)), "uq_moe_gather_grad")
     return dx
 
 
@@ -540,9 +547,9 @@ def moe_combine(ys: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, stre
     (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and weights.dtype == torch.float32
     assert R == T * k and weights.shape == pos.shape
-    y = _empty((T, H), ys.dtype, ys.device, stream)
-    _check(lib().uq_moe_combine(_at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), y.data_ptr(), T, k, H,
-                                _handle(stream)), "uq_moe_combine")
+    dev, y = ys.get_device(), _empty((T, H), ys.dtype, ys.device, stream)
+    _check(lib().uq_moe_combine(_at(ys, dev), DTYPES[ys.dtype], _at(pos, dev), _at(weights, dev), y.data_ptr(), T, k, H,
+                                _handle(stream, dev)), "uq_moe_combine")
     return y
 
 
@@ -552,9 +559,9 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, weig
     (T, k), (R, H) = pos.shape, ys.shape
     assert pos.dtype == torch.int32 and offsets.dtype == torch.int32 and weights.dtype == torch.float32
     assert dy.dtype == ys.dtype and dy.shape == (T, H) and R == T * k and weights.shape == pos.shape
-    dys = _empty(ys.shape, ys.dtype, ys.device, stream)
+    dev, dys = ys.get_device(), _empty(ys.shape, ys.dtype, ys.device, stream)
     dw = _empty((T, k), torch.float32, ys.device, stream)
-    _check(lib().uq_moe_combine_grad(_at(dy), _at(ys), DTYPES[ys.dtype], _at(pos), _at(weights), _at(offsets),
-                                     offsets.numel() - 1, dys.data_ptr(), dw.data_ptr(), T, k, H, _handle(stream)),
-           "uq_moe_combine_grad")
+    _check(lib().uq_moe_combine_grad(_at(dy, dev), _at(ys, dev), DTYPES[ys.dtype], _at(pos, dev), _at(weights, dev),
+                                     _at(offsets, dev), offsets.numel() - 1, dys.data_ptr(), dw.data_ptr(), T, k, H,
+                                     _handle(stream, dev)), "uq_moe_combine_grad")
     return dys, dw

@@ -1,4 +1,5 @@
-"""The binding's care for memory: results of a call on a given stream come from that stream's pool."""
+"""The binding's care for memory: results of a call on a given stream come from that stream's pool, and operands of a
+type that the kernels would misread are refused."""
 import pytest
 import torch
 
@@ -51,3 +52,33 @@ def test_results_come_from_the_pool_of_the_given_stream():
     for i, t in enumerate(results):
         assert _pool_stream(t) == s.cuda_stream, f"result {i}"
     assert _pool_stream(uq.gemm_mx(x, q, "MXFP4")) == torch.cuda.current_stream().cuda_stream
+
+
+def test_operands_of_another_type_are_refused():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    w = (torch.zeros(8, 32, dtype=torch.uint8, device=DEV), torch.zeros(512, dtype=torch.uint8, device=DEV))
+    off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    q, qs = uq.quantize_mx(x, "MXFP4"), uq.quantize_mx(x, "MXFP4", offsets=off)
+    wg = (w[0][None], w[1][None])
+
+    def wide(t):
+        return t.to(torch.int32)
+
+    def refused(f):
+        with pytest.raises(AssertionError):
+            f()
+
+    for i in range(2):
+        other = tuple(wide(t) if j == i else t for j, t in enumerate(q))
+        refused(lambda: uq.dequant_mx(other, "MXFP4"))
+        refused(lambda: uq.gemm_mx(other, w, "MXFP4"))
+        refused(lambda: uq.gemm_mx(x, tuple(wide(t) if j == i else t for j, t in enumerate(w)), "MXFP4"))
+        refused(lambda: uq.gemm_mx_grouped(tuple(wide(t) if j == i else t for j, t in enumerate(qs)), wg, off, "MXFP4"))
+        other_w = tuple(wide(t) if j == i else t for j, t in enumerate(wg))
+        refused(lambda: uq.gemm_mx_grouped(qs, other_w, off, "MXFP4"))
+        refused(lambda: uq.gemm_mx_grouped(qs, wg, off, "MXFP4", up=other_w))
+    refused(lambda: uq.dequant_mx(q, "MXFP4", offsets=off.long()))
+    refused(lambda: uq.quantize_mx(x.cpu(), "MXFP4"))
+    refused(lambda: uq.gemm_mx(x, (w[0].cpu(), w[1]), "MXFP4"))
+    refused(lambda: uq.gemm_mx(x, w, "MXFP4", y=torch.zeros(4, 8, dtype=torch.bfloat16)))
+    refused(lambda: uq.moe_sort(torch.zeros(4, 2, dtype=torch.int32), 4))
