@@ -3,6 +3,7 @@
 //
 // All but the sort are memory-bound row copies: a token's row is read once and written to its topk places (or its
 // topk rows are read and one row is written), in the widest vectors that rows are whole numbers of.
+#include <atomic>
 #include <type_traits>
 
 #include "uq_mx.cuh"
@@ -296,6 +297,8 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const T* __restri
         for (int h = threadIdx.x * V; h < H; h += blockDim.x * V) *reinterpret_cast<VT*>(dys + (long long)r * H + h) = zero;
 }
 
+constexpr size_t sort_smem(int E) { return ((size_t)SORT_WARPS * E + 2 * E + 1) * sizeof(int); }
+
 int row_grid(long long rows, int H, int span, int sms) {
     const long long b = (rows * ((H + span - 1) / span) + 7) / 8, most = 64LL * sms;
     return (int)(b < most ? (b < 1 ? 1 : b) : most);
@@ -303,9 +306,36 @@ int row_grid(long long rows, int H, int span, int sms) {
 
 }  // namespace
 
+namespace {
+// CTAs of the largest cluster that the sort can have on this device: up to 16 (more than 8 are not portable, so they are
+// asked for), once per device.  Any size is right.
+int sort_cluster(int dev) {
+    static std::atomic<int> known[64] = {};
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    for (n = 16; n > 1; n /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(SORT_THREADS);
+        cfg.dynamicSmemBytes = sort_smem(1024);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = n;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int placed = 0;
+        if (cudaOccupancyMaxActiveClusters(&placed, moe_sort_kernel, &cfg) == cudaSuccess && placed > 0) break;
+        cudaGetLastError();                     // a refusal is an answer
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+}  // namespace
+
 cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* order, int32_t* pos, int32_t* offsets,
                             cudaStream_t st) {
-    const size_t smem = ((size_t)SORT_WARPS * E + 2 * E + 1) * sizeof(int);
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -319,11 +349,12 @@ cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* ord
         configured[dev] = true;
     }
     int ctas = 1;                               // CTAs of the cluster: one strip a warp before another is added
-    while (ctas < 16 && n > (long long)ctas * SORT_THREADS) ctas *= 2;
+    const int most = sort_cluster(dev);
+    while (ctas < most && n > (long long)ctas * SORT_THREADS) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(SORT_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sort_smem(E);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

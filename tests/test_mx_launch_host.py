@@ -49,3 +49,13 @@ def test_no_overlap_unless_asked_for(cuda):
         launched = _product(cuda, M)
         # a product's own quantizer lets the product start under it in any case
         assert [x.overlap for x in launched] == ([0] if M == 1 else [0, 1])
+
+
+@pytest.mark.parametrize("largest", [16, 8, 4, 1])
+def test_route_sort_takes_the_cluster_that_can_be_placed(cuda, largest):
+    """A cluster of 16 CTAs is not portable: where none can be placed the sort takes a smaller one (any size is right)."""
+    f, a = cuda, cuda.at
+    f.lib.fake_set_largest_cluster(largest)
+    for n, ctas in ((1, 1), (1024, 1), (1025, 2), (8193, 16), (100000, 16)):
+        launched = f.launches(lambda: f.lib.uq_moe_sort(a, n, 1, 64, a, a, a, None))
+        assert [(x.grid, x.cluster) for x in launched] == [(min(ctas, largest),) * 2]
