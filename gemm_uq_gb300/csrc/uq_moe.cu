@@ -336,17 +336,17 @@ int sort_cluster(int dev) {
 
 cudaError_t launch_moe_sort(const int32_t* ids, long long n, int E, int32_t* order, int32_t* pos, int32_t* offsets,
                             cudaStream_t st) {
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64] = {};  // per device; a second thread that sets the attributes too does no harm
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
+    if (!configured[dev].load(std::memory_order_relaxed)) {
         e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        configured[dev] = true;
+        configured[dev].store(true, std::memory_order_relaxed);
     }
     int ctas = 1;                               // CTAs of the cluster: one strip a warp before another is added
     const int most = sort_cluster(dev);

@@ -1049,13 +1049,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
+    static std::atomic<EncodeTiledFn> known{nullptr};
+    EncodeTiledFn fn = known.load(std::memory_order_relaxed);
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess && q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
+            known.store(fn = reinterpret_cast<EncodeTiledFn>(p), std::memory_order_relaxed);
     }
     return fn;
 }
@@ -1082,15 +1083,16 @@ bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Opts a kernel into its shared memory, once per device.
-template <class K> cudaError_t configure(K kernel, bool (&done)[64]) {
+// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
+using Done = std::atomic<bool>[64];
+template <class K> cudaError_t configure(K kernel, Done& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev]) return cudaSuccess;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) done[dev] = true;
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
     return e;
 }
 
@@ -1115,11 +1117,11 @@ cudaError_t launch(const MxGemmMaps& maps, const MxGemmArgs& a, cudaStream_t st)
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    auto go = [&](auto kernel, bool (&done)[64]) {
+    auto go = [&](auto kernel, Done& done) {
         const cudaError_t e = configure(kernel, done);
         return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, maps, a) : e;
     };
-    static bool pair_done[64] = {}, one_done[64] = {}, fused_done[64] = {};
+    static Done pair_done = {}, one_done = {}, fused_done = {};
     if (a.pair) return go(mx_gemm_pair_kernel<FMT, NA>, pair_done);
     if constexpr (NA == 1)
         if (a.xraw) return go(mx_gemm_kernel<FMT, 1, true>, fused_done);
@@ -1137,7 +1139,7 @@ template <int NA> void pair_ring(int fmt, MxGemmArgs& a) {
 // (16 clusters of 8 took two rounds, 15 us against 9 for clusters of 4).  Asked once per device.
 int clusters_at_once(int s) {
     static std::atomic<int> known[64][MAX_SPLIT + 1] = {};
-    static bool done[64] = {};
+    static Done done = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int n = known[dev][s].load(std::memory_order_relaxed);
