@@ -97,8 +97,11 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<T>& x, const SixT& six, 
         const float d = e4m3_value(byte) * tscale;
         if (!bad && d >= 0x1p-100f && d <= 0x1p100f && amax <= d * 0x1p100f) {
             // x / d in the same way (with quotients far inside the range: where the block scale has saturated they can
-            // exceed it, and the residual of an infinite q is infinite with the other sign).  A tie comes out as a tie: its residual is exact.  For 16-bit types an approximate
-            // reciprocal will do: their quotients lie no closer to a tie than 2^-16, unless they are one.
+            // exceed it, and the residual of an infinite q is infinite with the other sign).  A tie comes out as a tie:
+            // its residual is exact.  For 16-bit types an approximate reciprocal (1 ulp) will do: before its rounding the
+            // corrected quotient is within 2^-44 of the true one, and the code changes only if a middle between a tie of
+            // the grid and an fp32 neighbour lies in between.  Over all 24-bit divisors and 16-bit values such middles are
+            // 2^-43 away, but for one pair (2^-48: 1 / 2 by 2 - 2^-23, times powers of two), which is tested.
             float r;
             if constexpr (sizeof(T) == 2) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
             else r = __frcp_rn(d);

@@ -1,5 +1,5 @@
-"""Microscaled operands at their limits, against the oracle: quotients past the fp32 range, and gate values out to where
-e^-g leaves it.
+"""Microscaled operands at their limits, against the oracle: quotients past the fp32 range, 16-bit values next to the
+element grid's midpoints under a tensor scale, and gate values out to where e^-g leaves the range.
 """
 import numpy as np
 import pytest
@@ -11,7 +11,7 @@ import gemm_uq_gb300 as uq  # noqa: E402
 from oracle import mx as omx  # noqa: E402
 
 DEV = torch.device("cuda:0")
-DTYPE = {"bf16": torch.bfloat16, "fp32": torch.float32}
+DTYPE = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
 
 def _quantized(x, fmt, tscale=1.0):
@@ -47,6 +47,53 @@ def test_magnitudes_over_six_keep_their_sign(dtype, tscale):
         y = uq.gemm_mx(x[rows].to(DEV), w, "NVFP4", tscale=tscale, dtype=torch.float32)
         assert np.array_equal(y.cpu().numpy(), ref[rows])
     assert uq.device_fault() == 0
+
+
+def _step(v, dtype, up):
+    """The neighbouring value of the 16-bit type, away from zero (up) or towards it; v > 0."""
+    bits = v.view(torch.int16) + (1 if up else -1)
+    return bits.to(torch.int16).view(DTYPE[dtype])
+
+
+@pytest.mark.parametrize("tscale", [1.0, 0.1, 1.0 / 3, 0.0371, 1.7])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_16_bit_quotients_next_to_ties(dtype, tscale):
+    """The 16-bit values on both sides of every midpoint of the element grid, for every scale mantissa: bit for bit the
+    fp32 quotient's codes."""
+    t = np.float32(tscale)
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    rows = []
+    for b in range(0x20, 0x60):                                                     # e4m3 scales 2^-3 .. 2^4
+        d = float(np.float32(omx.E4M3[b]) * t)
+        c = (mids * d).to(DTYPE[dtype])
+        x = torch.zeros(32, dtype=DTYPE[dtype])
+        x[0] = x[16] = 6 * d
+        x[1:8], x[8:15] = c, _step(c, dtype, False)
+        x[17:24], x[24:31] = _step(c, dtype, True), -c
+        rows.append(x)
+    x = torch.stack(rows)
+    want, _, _ = _quantized(x.float().numpy(), "NVFP4", tscale)
+    codes, _ = uq.quantize_mx(x.to(DEV), "NVFP4", tscale=tscale)
+    assert np.array_equal(codes.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("power", [-20, -3, 0, 2])
+def test_quotients_nearest_to_an_fp32_midpoint(dtype, power):
+    """x / d lies 2^-48 (relative) above the middle between 0.25, a tie of the element grid, and the fp32 value after it,
+    for x = 2^(power - 1) and d = (2 - 2^-23) 2^power.  Of all divisors and 16-bit values it is the nearest to such a
+    middle; the next are 2^-43 away (enumerated over all 2^23 divisor mantissas and the seven midpoints)."""
+    t = float(np.float32(2.0 - 2.0 ** -23) * np.float32(2.0 ** power))
+    x = torch.zeros(4, 32, dtype=torch.float32)
+    for r, s in enumerate((1.0, -1.0)):
+        x[r, 0] = x[r, 16] = 12.0 * 2.0 ** power                                    # block scale 1
+        x[r, 1:9] = s * 2.0 ** (power - 1)
+        x[r, 17:25] = s * 2.0 ** (power - 1) * torch.tensor([1.0, 3.0, 5.0, 7.0, 10.0, 14.0, 20.0, 0.5])
+    x = x.to(DTYPE[dtype])
+    want, _, byte = _quantized(x.float().numpy(), "NVFP4", t)
+    assert (byte[:2] == 0x38).all() and (want[0, 1] & 15) == 1
+    codes, _ = uq.quantize_mx(x.to(DEV), "NVFP4", tscale=t)
+    assert np.array_equal(codes.cpu().numpy(), want)
 
 
 def _sums(values, K):
