@@ -173,12 +173,14 @@ void operands_written(int dev, cudaStream_t st) {
     g_ws[{dev, (void*)st}].fresh_operands = true;
 }
 // whether operands were written since the last product on the stream
-bool take_fresh_operands(int dev, cudaStream_t st) {
+bool fresh_operands(int dev, cudaStream_t st) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace& w = g_ws[{dev, (void*)st}];
-    const bool fresh = w.fresh_operands;
-    w.fresh_operands = false;
-    return fresh;
+    return g_ws[{dev, (void*)st}].fresh_operands;
+}
+// a product has been launched: work after it finds them complete
+void operands_settled(int dev, cudaStream_t st) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_ws[{dev, (void*)st}].fresh_operands = false;
 }
 
 // Output mode of a launch: plain bf16 y; or the gated projection's gate pass (fp32 into out32) or up
@@ -1004,7 +1006,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     a.N = N;
     a.K = K;
     if ((s = check_tiles(M, 1, N)) != UQ_OK) return s;
-    const bool overlap = uq::launch_overlap() && !take_fresh_operands(dev, st);
+    const bool may = uq::launch_overlap(), overlap = may && !fresh_operands(dev, st);
     a.wait = overlap;
     if (!xscales) a.alpha = alpha * tscale_x;
     if (!xscales && uq::mx_gemm_quantizes(M)) {
@@ -1026,7 +1028,9 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
         a.wait = 1;
     }
     e = uq::launch_mx_gemm(fmt, xcodes, wcodes, nullptr, a, ds->sms, st);
-    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "microscaled product launch");
+    if (e != cudaSuccess) return cuda_fail(e, "microscaled product launch");
+    if (may) operands_settled(dev, st);
+    return UQ_OK;
 }
 
 uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, const uint8_t* wcodes,
@@ -1076,12 +1080,11 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     a.K = K;
     if ((s = check_tiles(rows, experts, N)) != UQ_OK) return s;
     // the offsets are needed before any weights are requested, so the wait comes first here, fresh operands or not
-    if (uq::launch_overlap()) {
-        take_fresh_operands(dev, st);
-        a.wait = 1;
-    }
+    a.wait = uq::launch_overlap();
     e = uq::launch_mx_gemm(fmt, xcodes, wcodes, wcodes_up, a, ds->sms, st);
-    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "grouped microscaled product launch");
+    if (e != cudaSuccess) return cuda_fail(e, "grouped microscaled product launch");
+    if (a.wait) operands_settled(dev, st);
+    return UQ_OK;
 }
 
 // ---- expert routing ---------------------------------------------------------------------------

@@ -21,7 +21,7 @@ struct Launch {
 std::mutex mu;
 std::map<const void*, std::string>& names() { static std::map<const void*, std::string> m; return m; }
 std::vector<Launch>& launches() { static std::vector<Launch> v; return v; }
-int largest_cluster = 16, sms = 152;
+int largest_cluster = 16, sms = 152, no_memory = 0;
 thread_local struct { dim3 grid, block; size_t smem; cudaStream_t st; } call;
 
 CUresult encode_tiled(CUtensorMap* m, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -46,6 +46,7 @@ void record(const void* f, dim3 grid, dim3 block, cudaStream_t st, const cudaLau
 extern "C" {
 // ---- for the tests
 void fake_set_largest_cluster(int n) { largest_cluster = n; }
+void fake_set_no_memory(int on) { no_memory = on; }
 int fake_launch_count() { return (int)launches().size(); }
 void fake_clear() { launches().clear(); }
 const char* fake_launch(int i, unsigned* grid, unsigned* block, unsigned* cluster, int* overlap) {
@@ -112,7 +113,7 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** p, unsigned, un
     return cudaSuccess;
 }
 cudaError_t cudaMalloc(void** p, size_t n) {
-    *p = aligned_alloc(256, (n + 255) / 256 * 256);
+    *p = no_memory ? nullptr : aligned_alloc(256, (n + 255) / 256 * 256);
     return *p ? cudaSuccess : cudaErrorMemoryAllocation;
 }
 cudaError_t cudaMemset(void* p, int v, size_t n) { memset(p, v, n); return cudaSuccess; }

@@ -43,6 +43,18 @@ def test_a_product_after_a_call_that_writes_operands_does_not_overlap_it(cuda, M
     assert [x.overlap for x in _product(f, M, None, pair)] == [1] * kernels
 
 
+def test_a_product_that_fails_does_not_settle_fresh_operands(cuda):
+    """Operands are written, a product that needs a workspace gets none, the next product may still have them as weights."""
+    f, a = cuda, cuda.at
+    f.lib.uq_set_launch_overlap(1)
+    _quantize(f)
+    f.lib.fake_set_no_memory(1)
+    assert f.lib.uq_gemm_mx(a, 0, 2048, None, 1.0, a, a, a, 0, 5, 1024, 2048, 0, 1.0, None) == 5     # UQ_ERR_NOMEM
+    f.lib.fake_set_no_memory(0)
+    assert [x.overlap for x in _product(f, 1)] == [0]
+    assert [x.overlap for x in _product(f, 1)] == [1]
+
+
 def test_no_overlap_unless_asked_for(cuda):
     _quantize(cuda)
     for M in (1, 5):
