@@ -869,13 +869,19 @@ uq_status uq_gemm_kernel_count(int M, int N, int K, int group, uq_fmt fmt, int* 
 
 // ---- microscaled 4-bit operands ---------------------------------------------------------------
 namespace {
+// Sizes are rounded up to tiles, steps and units of at most 4096 in 32 bits.
+constexpr int MOST = 0x7FFFEFFF;
+uq_status check_most(const char* name, int size) {
+    return size <= MOST ? UQ_OK : fail(UQ_ERR_UNSUPPORTED, "%s=%d is too large (at most %d)", name, size, MOST);
+}
 bool valid_dtype(int t) { return t >= UQ_BF16 && t <= UQ_FP32; }
 int dtype_size(int t) { return t == UQ_FP32 ? 4 : 2; }
 uq_status check_mx(int rows, int K, int fmt, int segments) {
     if (fmt != UQ_MXFP4 && fmt != UQ_NVFP4) return fail(UQ_ERR_INVALID, "unknown microscaled format %d", fmt);
     if (rows < 0 || K < 0 || segments < 0) return fail(UQ_ERR_INVALID, "negative size rows=%d K=%d segments=%d", rows, K, segments);
     if (K % 32) return fail(UQ_ERR_INVALID, "K=%d is not a multiple of 32", K);
-    return UQ_OK;
+    const uq_status s = check_most("rows", rows);
+    return s == UQ_OK ? check_most("K", K) : s;
 }
 uq_status check_tscale(int fmt, float t) {
     if (!(t > 0.f) || t > 3.0e38f) return fail(UQ_ERR_INVALID, "tensor scale must be positive and finite");
@@ -970,6 +976,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     uq_status s = check_mx(M, K, fmt, 0);
     if (s != UQ_OK) return s;
     if (N < 0) return fail(UQ_ERR_INVALID, "negative N");
+    if ((s = check_most("N", N)) != UQ_OK) return s;
     if ((s = check_tscale(fmt, tscale_x)) != UQ_OK) return s;
     if (!valid_dtype(ytype)) return fail(UQ_ERR_INVALID, "unknown element type %d", ytype);
     if (M == 0 || N == 0) return UQ_OK;
@@ -1040,13 +1047,14 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
     uq_status s = check_mx(rows, K, fmt, experts);
     if (s != UQ_OK) return s;
     if (N < 0) return fail(UQ_ERR_INVALID, "negative N");
+    if ((s = check_most("N", N)) != UQ_OK) return s;
     if (experts < 1) return fail(UQ_ERR_INVALID, "experts must be at least 1");
     if (!valid_dtype(ytype)) return fail(UQ_ERR_INVALID, "unknown element type %d", ytype);
     if ((wcodes_up != nullptr) != (wscales_up != nullptr))
         return fail(UQ_ERR_INVALID, "wcodes_up and wscales_up must be given together");
     if (alpha_up && !wcodes_up) return fail(UQ_ERR_INVALID, "alpha_up needs wcodes_up");
     if (experts > 1024) return fail(UQ_ERR_UNSUPPORTED, "at most 1024 experts (got %d)", experts);
-    if ((long long)experts * N > 0x7FFFFFFFll) return fail(UQ_ERR_UNSUPPORTED, "experts * N must be below 2^31");
+    if ((long long)experts * N > MOST) return fail(UQ_ERR_UNSUPPORTED, "experts * N must be at most %d", MOST);
     if (rows == 0 || N == 0) return UQ_OK;
     if (!y) return fail(UQ_ERR_INVALID, "y is NULL");
     if (!aligned16(y)) return fail(UQ_ERR_ALIGN, "y must be 16-byte aligned");
@@ -1093,7 +1101,7 @@ uq_status check_routes(int T, int topk, int H, int experts) {
     if (T < 0 || topk < 0 || H < 0) return fail(UQ_ERR_INVALID, "negative size T=%d topk=%d H=%d", T, topk, H);
     if (experts < 1) return fail(UQ_ERR_INVALID, "experts must be at least 1");
     if ((long long)T * topk > 0x7FFFFFFFll) return fail(UQ_ERR_INVALID, "%d x %d routes are too many", T, topk);
-    return UQ_OK;
+    return check_most("H", H);
 }
 }  // namespace
 

@@ -398,6 +398,7 @@ uq_status uq_gemm_noalloc_scratch(int M, int N, int K, int group, uq_fmt fmt, si
  * non-decreasing, offsets[0] = 0; rows from offsets[segments] on belong to nobody): segment e starts at row
  * tile offsets[e] / 128 + e.  uq_mx_scales_size gives the bytes.  Scale bytes of blocks past K inside the last
  * tile along k must not be NaN codes (uq_quantize_mx and uq_pack_mx_scales write 0).
+ * rows, N, K and experts * N are at most 2^31 - 4097 (UQ_ERR_UNSUPPORTED beyond).
  */
 
 /* uq_mx_scales_size -- bytes of the scales of an operand (segments = 0: no segments).  Host-only. */
@@ -470,7 +471,7 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
 
 /*
  * Expert routing.  Token t takes topk routes (t, j), flat index t * topk + j, to experts ids[t][j]; a route whose
- * id lies outside [0, experts) is dropped.  R = T * topk.
+ * id lies outside [0, experts) is dropped.  R = T * topk.  H is at most 2^31 - 4097 (UQ_ERR_UNSUPPORTED beyond).
  *
  * uq_moe_sort -- a stable sort of the routes by expert (equal experts in order of their flat index):
  *   offsets (device, int32 [experts + 1]): rows offsets[e] .. offsets[e + 1] are expert e's

@@ -81,3 +81,22 @@ def test_routing_refusals(L, al):
     assert L.uq_moe_gather_grad(al, 0, None, al, 1, 2, 8, None) == 1
     assert L.uq_moe_combine_grad(al, al, 0, al, al, al, 4, None, al, 1, 2, 8, None) == 1
     assert L.uq_moe_combine_grad(al, al, 0, al, al, al, 4, al, al, 0, 2, 8, None) == 0
+
+
+def test_sizes_next_to_2_31_are_refused(L, al):
+    """Within a tile of 2^31 the sizes rounded up to tiles and steps leave 32 bits."""
+    for big in (2 ** 31 - 1, 2 ** 31 - 32, 2 ** 31 - 256, 2 ** 31 - 4096):
+        assert L.uq_gemm_mx(al, 0, 64, al, 1.0, al, al, al, 0, big, 1, 64, 0, 1.0, None) == 2
+        assert L.uq_gemm_mx(al, 0, 64, al, 1.0, al, al, al, 0, 1, big, 64, 0, 1.0, None) == 2
+        assert L.uq_gemm_mx_grouped(al, al, al, al, None, None, al, None, None, al, 0, big, 1, 1, 64, 0, None) == 2
+        assert L.uq_gemm_mx_grouped(al, al, al, al, None, None, al, None, None, al, 0, 1, 1, big, 64, 0, None) == 2
+        assert L.uq_moe_gather(al, 0, al, al, 4, al, 1, 2, big, None) == 2
+        assert L.uq_moe_combine(al, 0, al, al, al, 1, 2, big, None) == 2
+        assert L.uq_moe_gather_grad(al, 0, al, al, 1, 2, big, None) == 2
+        assert L.uq_moe_combine_grad(al, al, 0, al, al, al, 4, al, al, 1, 2, big, None) == 2
+        assert L.uq_gemm_mx_grouped(al, al, al, al, None, None, al, None, None, al, 0, 1, 2, 2 ** 30 - 1, 64, 0, None) == 2
+        K = big // 32 * 32
+        assert L.uq_gemm_mx(al, 0, K, al, 1.0, al, al, al, 0, 1, 1, K, 0, 1.0, None) == 2
+        assert L.uq_quantize_mx(al, 0, K, al, al, 1, K, 0, 1.0, None, 0, None, 0, None) == 2
+        assert L.uq_dequant_mx(al, al, al, 0, 1, K, 0, 1.0, None, 0, None) == 2
+        assert L.uq_pack_mx_scales(al, al, 1, 1, K, 0, None) == 2
