@@ -508,6 +508,8 @@ def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tup
 
 
 # ---- expert routing ------------------------------------------------------------------------------------------------
+# Plain calls, unknown to autograd: the gradient of moe_gather is moe_gather_grad, that of moe_combine is
+# moe_combine_grad, and a caller that trains with them wraps them in a torch.autograd.Function.
 
 def moe_sort(ids: torch.Tensor, experts: int, stream=None):
     """uq_moe_sort: int32 expert ids [T][k] -> (order int32 [T*k], pos int32 [T][k], offsets int32 [experts + 1])."""

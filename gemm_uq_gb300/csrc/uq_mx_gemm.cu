@@ -15,9 +15,10 @@
 // and two accumulators let the epilogue of one tile run under the next one's MMAs.  Where tiles would fill at most half
 // of the SMs and it saves time (split_of), a cluster of S CTAs shares each tile's k steps and adds the fp32 sums through
 // distributed shared memory in rank order, so equal calls give equal bits.
-// One GB300, graph replay: weights from DRAM 1 x 14336 x 4096 MXFP4 9.0 us (3.5 TB/s; 7.6 where L2 keeps a part), 37 x
-// 4096 x 14336 NVFP4 11.8 us; 512 x 2048 x 2048 MXFP4 6.9 us; large products on pairs of CTAs (below) 8192^3 MXFP4 156 us
-// (7.0 PFLOP/s).  What bounds them: few tokens start and end of a kernel (3 us) and then memory; many the tensor cores.
+// One GB300, graph replay, weights from DRAM, us with x quantized in the call / before: 1 x 14336 x 4096 MXFP4 9.0 / 8.8
+// (6.9 / 6.4 where L2 keeps them), 37 x 4096 x 14336 NVFP4 13.7 / 11.9; 512 x 2048 x 2048 MXFP4 7.4 / 6.1; large products
+// on pairs of CTAs (below) 8192^3 MXFP4 185 / 156 (7.0 PFLOP/s), NVFP4 201 / 167.  What bounds them: few tokens start and
+// end of a kernel (3 us) and then memory; many the tensor cores (their pipe is active in 81 % of an 8192^3's cycles).
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is
 // freed, and the fault word tells.
 #include <cuda.h>
@@ -378,7 +379,8 @@ template <class T> __device__ __forceinline__ void put16(const MxGemmArgs& a, in
 // the rounding left (t alone would lose |t| 2^-24) wherever 2^t is finite and matters, |t| < 128, then an approximate
 // reciprocal.  Below g = -88.72 e^-g exceeds fp32 and the result is zero.  A gated tile's epilogue is
 // 128 of these per lane beside MMAs that may take only a few thousand cycles; with expf and a correctly rounded
-// division it took longer than they did (16384 rows, 64 experts of 1408 x 2048 gated: 150 us, without the gate 47).
+// division it took longer than they did (16384 rows, 64 experts of 1408 x 2048 gated: 150 us; now 82 to 90, and 47 without
+// the gate: the epilogue still outlasts the MMAs at such short k).
 __device__ __forceinline__ float swiglu(float g, float u) {
     const float t = g * -1.4426950408889634f;
     const float left = fmaf(g, -1.4426950408889634f, -t) - g * 1.9259630e-8f;      // log2(e) = 1.44269502.. + 1.92596e-8
@@ -1189,7 +1191,8 @@ int split_of(long long tiles, int steps, int tokens, bool gated, int sms) {
 // 30.8 / 25.0.
 //   Rows by expert: from 128 rows an expert on, where there are pair tiles for every pair.  Measured, 8 experts of 4096 x
 // 4096, mean rows 64 16.5 / 18.7, 128 20.7 / 20.2, 192 26.7 / 20.7, 512 45.3 / 35.8; gated 128 51.4 / 43.2; 32 experts of
-// 2048 x 2048: 64 20.4 / 22.7, 128 24.9 / 24.7, 256 35.1 / 36.9, 512 51.6 / 47.2.
+// 2048 x 2048: 64 20.4 / 22.7, 128 24.9 / 24.7, 256 35.1 / 36.9 (the one of these that the rule takes wrongly: it does not
+// weigh a short K, where a pair tile's fixed 1900 cycles are half of its steps), 512 51.6 / 47.2.
 bool pays_in_pairs(int fmt, bool gated, const MxGemmArgs& a, int mean, int sms) {
     const long long pair_n = (a.N + 255) / 256;
     if (a.offsets) return mean >= 128 && 2 * pair_n * (a.rows / (gated ? 128 : 256) + a.experts / 2) >= sms;

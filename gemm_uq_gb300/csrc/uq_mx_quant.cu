@@ -6,8 +6,8 @@
 // of a 16-bit type, all requested before the first is used.  A block is then 4 lanes (MXFP4) or 2 (NVFP4): its absmax
 // takes one or two shuffles, the codes one 4-byte store per lane, the scales of 4 blocks one 4-byte store.
 // Each value is read once, whatever the number of rows it is written to.  8192 x 8192 bf16 -> MXFP4 29.5 us (5.8 TB/s),
-// near the memory's bound; NVFP4 36.7 us (4.7 TB/s), bound by instructions issued (a quotient per value); fp32 -> MXFP4
-// 45.8 us (6.6 TB/s); read back as bf16 28.6 us (5.9 TB/s).
+// near the memory's bound; NVFP4 36.7 us (4.7 TB/s), 75 % of the issue slots and 66 % of the ALU pipe taken (a quotient per
+// value); fp32 -> MXFP4 45.8 us (6.6 TB/s); read back as bf16 28.6 us (5.9 TB/s).
 #include "uq_mx_quant.cuh"
 
 namespace uq {
