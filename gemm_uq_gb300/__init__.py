@@ -53,6 +53,13 @@ SIGNATURES = {
     "uq_dequant_mx": (_I, [_P, _P, _P, _I, _I, _I, _I, _F, _P, _I, _P]),
     "uq_gemm_mx": (_I, [_P, _I, _L, _P, _F, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
     "uq_gemm_mx_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "uq_quantize_q8": (_I, [_P, _I, _L, _P, _P, _I, _I, _P]),
+    "uq_dequant_q8": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "uq_rmsnorm_q8": (_I, [_P, _P, _P, _I, _L, _P, _P, _P, _P, _I, _I, _F, _P]),
+    "uq_rmsnorm_grad": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _F, _P]),
+    "uq_gemm_w8a8": (_I, [_P, _I, _L, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "uq_moe_route": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _I, _I, _I, _P]),
+    "uq_moe_route_grad": (_I, [_P, _I, _P, _P, _I, _I, _F, _P, _I, _I, _I, _P]),
     "uq_moe_sort": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
     "uq_moe_gather": (_I, [_P, _I, _P, _P, _I, _P, _I, _I, _I, _P]),
     "uq_moe_gather_grad": (_I, [_P, _I, _P, _P, _I, _I, _I, _P]),
@@ -507,9 +514,135 @@ def gemm_mx_grouped(x: tuple, w: tuple, offsets: torch.Tensor, fmt: str, up: tup
     return y
 
 
+# ---- rows in 8 bits: a pair (codes int8 [rows][K], scales fp32 [rows]) ----------------------------------------------
+
+def quantize_q8(x: torch.Tensor, stream=None):
+    """uq_quantize_q8: rows [T][K] (bf16, fp16 or fp32; rows may be strided) -> (codes, scales), a scale per row."""
+    T, K = x.shape
+    dev = x.get_device()
+    codes = _empty((T, K), torch.int8, x.device, stream)
+    scales = _empty(T, torch.float32, x.device, stream)
+    _check(lib().uq_quantize_q8(x.data_ptr(), DTYPES[x.dtype], _row_stride(x, T, K), codes.data_ptr(), scales.data_ptr(), T, K,
+                                _handle(stream, dev)), "uq_quantize_q8")
+    return codes, scales
+
+
+def _rows8(q: tuple, dev: int):
+    """Pointers of a row operand's codes and scales."""
+    codes, scales = q
+    assert codes.dtype == torch.int8 and scales.dtype == torch.float32, "codes are int8, scales fp32"
+    assert scales.shape == codes.shape[:1], "one scale for each row of codes"
+    return _at(codes, dev), _at(scales, dev)
+
+
+def dequant_q8(q: tuple, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """uq_dequant_q8: the values (codes, scales) stand for, [rows][K] of ``dtype``."""
+    (T, K), dev = q[0].shape, q[0].get_device()
+    codes, scales = _rows8(q, dev)
+    out = _empty((T, K), dtype, q[0].device, stream)
+    _check(lib().uq_dequant_q8(codes, scales, out.data_ptr(), DTYPES[dtype], T, K, _handle(stream, dev)), "uq_dequant_q8")
+    return out
+
+
+def rmsnorm_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+               normed: bool = False, quantized: bool = True, h: torch.Tensor | None = None, stream=None):
+    """uq_rmsnorm_q8: (h, y, (codes, scales)) of h = x + residual, y = h / sqrt(mean(h^2) + eps) * gamma.
+
+    ``normed``: y is wanted (else None); ``quantized``: codes and scales are (else None).  Without a residual h is x.
+    ``h``: where h is written (it may be x or residual)."""
+    T, D = x.shape
+    dev = x.get_device()
+    assert gamma.dtype == x.dtype and gamma.shape == (D,), "gamma is [D] of x's type"
+    hp = rp = None
+    if residual is not None:
+        assert residual.dtype == x.dtype and residual.shape == x.shape, "residual is of x's shape and type"
+        rp = _at(residual, dev)
+        if h is None:
+            h = _empty((T, D), x.dtype, x.device, stream)
+    if h is not None:
+        assert h.dtype == x.dtype and h.shape == x.shape
+        hp = _at(h, dev)
+    y = _empty((T, D), x.dtype, x.device, stream) if normed else None
+    codes = _empty((T, D), torch.int8, x.device, stream) if quantized else None
+    scales = _empty(T, torch.float32, x.device, stream) if quantized else None
+    _check(lib().uq_rmsnorm_q8(x.data_ptr(), rp, _at(gamma, dev), DTYPES[x.dtype], _row_stride(x, T, D), hp, _at_opt(y, dev),
+                               _at_opt(codes, dev), _at_opt(scales, dev), T, D, eps, _handle(stream, dev)), "uq_rmsnorm_q8")
+    return x if h is None else h, y, (codes, scales) if quantized else None
+
+
+def rmsnorm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, eps: float, dh: torch.Tensor | None = None, stream=None):
+    """uq_rmsnorm_grad: (dx [T][D], dgamma fp32 [D]) of y = h / sqrt(mean(h^2) + eps) * gamma for y's gradient dy, and h's
+    own gradient dh, which is added."""
+    (T, D), dev = h.shape, h.get_device()
+    assert dy.dtype == h.dtype and dy.shape == h.shape and gamma.dtype == h.dtype and gamma.shape == (D,)
+    assert dh is None or (dh.dtype == h.dtype and dh.shape == h.shape)
+    dx = _empty((T, D), h.dtype, h.device, stream)
+    dgamma = _empty(D, torch.float32, h.device, stream)
+    _check(lib().uq_rmsnorm_grad(_at(dy, dev), _at(h, dev), _at(gamma, dev), _at_opt(dh, dev), DTYPES[h.dtype], dx.data_ptr(),
+                                 dgamma.data_ptr(), T, D, eps, _handle(stream, dev)), "uq_rmsnorm_grad")
+    return dx, dgamma
+
+
+def gemm_w8a8(x, w: tuple, dtype: torch.dtype | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """uq_gemm_w8a8: y = x . w^T (``[M][N]``) of 8-bit operands, a scale per token and per output channel.
+
+    ``x``: a matrix (bf16, fp16 or fp32), quantized in the call, or a pair (codes, scales); ``w``: (codes [N][K], scales [N])
+    of quantize_q8.  The result has ``dtype`` (default: x's, bf16 for a pair)."""
+    (N, K), dev = w[0].shape, w[0].get_device()
+    wcodes, wscales = _rows8(w, dev)
+    if isinstance(x, torch.Tensor):
+        M, xk = x.shape
+        assert x.get_device() == dev, "x and w are on different devices"
+        xtype, xptr, xsc, ld = DTYPES[x.dtype], x.data_ptr(), None, _row_stride(x, M, K)
+        if dtype is None:
+            dtype = x.dtype
+    else:
+        M, xk = x[0].shape
+        xptr, xsc = _rows8(x, dev)
+        xtype, ld = 0, 0
+    assert xk == K, "x and w have different K"
+    if y is None:
+        y = _empty((M, N), dtype or torch.bfloat16, w[0].device, stream)
+    assert y.shape == (M, N)
+    _check(lib().uq_gemm_w8a8(xptr, xtype, ld, xsc, wcodes, wscales, _at(y, dev), DTYPES[y.dtype], M, N, K,
+                              _handle(stream, dev)), "uq_gemm_w8a8")
+    return y
+
+
 # ---- expert routing ------------------------------------------------------------------------------------------------
 # Plain calls, unknown to autograd: the gradient of moe_gather is moe_gather_grad, that of moe_combine is
 # moe_combine_grad, and a caller that trains with them wraps them in a torch.autograd.Function.
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
+              top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """uq_moe_route: (ids int32 [T][topk], weights fp32 [T][topk]) of the router's logits [T][experts] (bf16, fp16, fp32).
+
+    ``score``: "softmax" or "sigmoid"; ``bias`` fp32 [experts]: added to the scores for the choice alone; ``groups``,
+    ``top_groups``, ``group_top``: experts are chosen from the best groups only; ``renormalize``: weights sum to ``scale``."""
+    T, E = logits.shape
+    dev = logits.get_device()
+    assert bias is None or (bias.dtype == torch.float32 and bias.shape == (E,)), "bias is fp32 [experts]"
+    ids = _empty((T, max(topk, 0)), torch.int32, logits.device, stream)
+    weights = _empty((T, max(topk, 0)), torch.float32, logits.device, stream)
+    _check(lib().uq_moe_route(_at(logits, dev), DTYPES[logits.dtype], _at_opt(bias, dev), SCORES[score], groups, top_groups,
+                              group_top, renormalize, scale, ids.data_ptr(), weights.data_ptr(), T, E, topk, _handle(stream, dev)),
+           "uq_moe_route")
+    return ids, weights
+
+
+def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """uq_moe_route_grad: the gradient of the logits [T][experts] from that of moe_route's weights [T][topk]."""
+    (T, E), (rows, k), dev = logits.shape, ids.shape, logits.get_device()
+    assert ids.dtype == torch.int32 and dweights.dtype == torch.float32 and dweights.shape == ids.shape and rows == T
+    dx = _empty((T, E), logits.dtype, logits.device, stream)
+    _check(lib().uq_moe_route_grad(_at(logits, dev), DTYPES[logits.dtype], _at(ids, dev), _at(dweights, dev), SCORES[score],
+                                   renormalize, scale, dx.data_ptr(), T, E, k, _handle(stream, dev)), "uq_moe_route_grad")
+    return dx
+
 
 def moe_sort(ids: torch.Tensor, experts: int, stream=None):
     """uq_moe_sort: int32 expert ids [T][k] -> (order int32 [T*k], pos int32 [T][k], offsets int32 [experts + 1])."""

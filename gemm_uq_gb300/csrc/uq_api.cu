@@ -1185,6 +1185,202 @@ uq_status uq_moe_combine_grad(const void* dy, const void* ys, uq_dtype type, con
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "route combine gradient launch");
 }
 
+// ---- rows in 8 bits -----------------------------------------------------------------------------
+namespace {
+constexpr int MOST_K8 = 131056;                 // 128 * 128 * K stays below 2^31
+uq_status check_rows(int rows, int D, int type) {
+    if (rows < 0 || D < 0) return fail(UQ_ERR_INVALID, "negative size %d x %d", rows, D);
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    const uq_status s = check_most("rows", rows);
+    return s == UQ_OK ? check_most("D", D) : s;
+}
+uq_status check_x8(const void* x, long long ldx, int K) {
+    if (!x) return fail(UQ_ERR_INVALID, "x is NULL");
+    if (ldx < K) return fail(UQ_ERR_INVALID, "row stride %lld is less than the row's %d elements", ldx, K);
+    if (!aligned16(x)) return fail(UQ_ERR_ALIGN, "x must be 16-byte aligned");
+    return UQ_OK;
+}
+}  // namespace
+
+uq_status uq_quantize_q8(const void* x, uq_dtype xtype, long long ldx, int8_t* codes, float* scales, int rows, int K,
+                         void* stream) {
+    uq_status s = check_rows(rows, K, xtype);
+    if (s != UQ_OK) return s;
+    if (rows == 0 || K == 0) return UQ_OK;
+    if ((s = check_x8(x, ldx, K)) != UQ_OK) return s;
+    if (!codes || !scales) return fail(UQ_ERR_INVALID, "codes or scales is NULL");
+    if (!aligned16(codes) || !aligned16(scales)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_quantize_q8(x, xtype, ldx, codes, scales, rows, K, ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit quantization launch");
+}
+
+uq_status uq_dequant_q8(const int8_t* codes, const float* scales, void* out, uq_dtype type, int rows, int K, void* stream) {
+    uq_status s = check_rows(rows, K, type);
+    if (s != UQ_OK) return s;
+    if (rows == 0 || K == 0) return UQ_OK;
+    if (!codes || !scales || !out) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_dequant_q8(codes, scales, out, type, rows, K, ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit dequantization launch");
+}
+
+uq_status uq_rmsnorm_q8(const void* x, const void* residual, const void* gamma, uq_dtype type, long long ldx, void* h, void* y,
+                        int8_t* codes, float* scales, int rows, int D, float eps, void* stream) {
+    uq_status s = check_rows(rows, D, type);
+    if (s != UQ_OK) return s;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(UQ_ERR_INVALID, "eps must be finite and not negative");
+    if ((codes != nullptr) != (scales != nullptr)) return fail(UQ_ERR_INVALID, "codes and scales must be given together");
+    if (rows == 0 || D == 0) return UQ_OK;
+    if ((s = check_x8(x, ldx, D)) != UQ_OK) return s;
+    if (!gamma) return fail(UQ_ERR_INVALID, "gamma is NULL");
+    if (!h && !y && !codes) return fail(UQ_ERR_INVALID, "no output is wanted");
+    if (h && h == y) return fail(UQ_ERR_INVALID, "h and y are the same");
+    if ((h == x || y == x) && ldx != D) return fail(UQ_ERR_INVALID, "h or y over x needs ldx = D");
+    if (!aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(y) || !aligned16(codes) || !aligned16(scales))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_rmsnorm_q8(x, residual, gamma, type, ldx, h, y, codes, scales, rows, D, eps, ds->sms,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "norm launch");
+}
+
+uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, uq_dtype type, void* dx,
+                          float* dgamma, int rows, int D, float eps, void* stream) {
+    uq_status s = check_rows(rows, D, type);
+    if (s != UQ_OK) return s;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(UQ_ERR_INVALID, "eps must be finite and not negative");
+    if (D == 0) return UQ_OK;
+    if (!dgamma) return fail(UQ_ERR_INVALID, "dgamma is NULL");
+    if (!aligned16(dgamma)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (rows == 0) {
+        e = cudaMemsetAsync(dgamma, 0, (size_t)D * 4, st);
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!dy || !h || !gamma || !dx) return fail(UQ_ERR_INVALID, "null pointer");
+    if (dx == h) return fail(UQ_ERR_INVALID, "dx and h are the same");
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(gamma) || !aligned16(dh) || !aligned16(dx))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    Workspace* ws = nullptr;
+    if ((s = workspace(dev, st, 0, 0, &ws, (size_t)uq::norm_grad_partials(type, rows, D, ds->sms) * D * sizeof(float))) != UQ_OK)
+        return s;
+    e = uq::launch_rmsnorm_grad(dy, h, gamma, dh, type, dx, dgamma, ws->aux, rows, D, eps, ds->sms, st);
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "norm gradient launch");
+}
+
+uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float* xscales, const int8_t* w,
+                       const float* wscales, void* y, uq_dtype ytype, int M, int N, int K, void* stream) {
+    if (M < 0 || N < 0 || K < 0) return fail(UQ_ERR_INVALID, "negative size M=%d N=%d K=%d", M, N, K);
+    if (K % 16) return fail(UQ_ERR_INVALID, "K=%d is not a multiple of 16", K);
+    if (!valid_dtype(ytype)) return fail(UQ_ERR_INVALID, "unknown element type %d", ytype);
+    if (!xscales && !valid_dtype(xtype)) return fail(UQ_ERR_INVALID, "unknown element type %d", xtype);
+    uq_status s;
+    if ((s = check_most("M", M)) != UQ_OK || (s = check_most("N", N)) != UQ_OK) return s;
+    if (K > MOST_K8) return fail(UQ_ERR_UNSUPPORTED, "K=%d is too large (at most %d)", K, MOST_K8);
+    if (M == 0 || N == 0) return UQ_OK;
+    if ((s = check_tiles(M, 1, N)) != UQ_OK) return s;
+    if (!y) return fail(UQ_ERR_INVALID, "y is NULL");
+    if (!aligned16(y)) return fail(UQ_ERR_ALIGN, "y must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (K == 0) {
+        e = cudaMemsetAsync(y, 0, (size_t)M * N * dtype_size(ytype), st);
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!w || !wscales) return fail(UQ_ERR_INVALID, "w or wscales is NULL");
+    if ((s = check_x8(x, xscales ? K : ldx, K)) != UQ_OK) return s;
+    if (!aligned16(w) || !aligned16(wscales) || !aligned16(xscales)) return fail(UQ_ERR_ALIGN, "codes and scales must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    int dev = 0;
+    if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    uq::Q8GemmArgs a = {};
+    a.x = static_cast<const int8_t*>(x);
+    a.w = w;
+    a.sx = xscales;
+    a.sw = wscales;
+    a.y = y;
+    a.fault = ds->words;
+    a.ytype = ytype;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    if (!xscales) {
+        // the quantized x lives in the workspace: codes | scales
+        const size_t code_bytes = ((size_t)M * K + 255) / 256 * 256;
+        Workspace* ws = nullptr;
+        if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + (size_t)M * sizeof(float))) != UQ_OK) return s;
+        int8_t* codes = reinterpret_cast<int8_t*>(ws->aux);
+        float* scales = reinterpret_cast<float*>(codes + code_bytes);
+        e = uq::launch_quantize_q8(x, xtype, ldx, codes, scales, M, K, ds->sms, st);
+        if (e != cudaSuccess) return cuda_fail(e, "8-bit quantization launch");
+        a.x = codes;
+        a.sx = scales;
+    }
+    e = uq::launch_q8_gemm(a, ds->sms, st);
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit product launch");
+}
+
+// ---- the router -----------------------------------------------------------------------------------
+namespace {
+uq_status check_router(int type, int score, float scale, int T, int experts, int topk) {
+    if (T < 0 || topk < 0) return fail(UQ_ERR_INVALID, "negative size T=%d topk=%d", T, topk);
+    if (experts < 1) return fail(UQ_ERR_INVALID, "experts must be at least 1");
+    if (!valid_dtype(type)) return fail(UQ_ERR_INVALID, "unknown element type %d", type);
+    if (score != UQ_SOFTMAX && score != UQ_SIGMOID) return fail(UQ_ERR_INVALID, "unknown score %d", score);
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(UQ_ERR_INVALID, "scale must be finite");
+    if (experts > 1024) return fail(UQ_ERR_UNSUPPORTED, "at most 1024 experts (got %d)", experts);
+    if (topk > 32) return fail(UQ_ERR_UNSUPPORTED, "at most 32 routes a token (got %d)", topk);
+    if ((long long)T * topk > 0x7FFFFFFFll) return fail(UQ_ERR_INVALID, "%d x %d routes are too many", T, topk);
+    return UQ_OK;
+}
+}  // namespace
+
+uq_status uq_moe_route(const void* logits, uq_dtype type, const float* bias, uq_score score, int groups, int top_groups,
+                       int group_top, int renormalize, float scale, int32_t* ids, float* weights, int T, int experts, int topk,
+                       void* stream) {
+    uq_status s = check_router(type, score, scale, T, experts, topk);
+    if (s != UQ_OK) return s;
+    if (groups < 1 || experts % groups) return fail(UQ_ERR_INVALID, "%d experts do not form %d equal groups", experts, groups);
+    if (groups > 32) return fail(UQ_ERR_UNSUPPORTED, "at most 32 groups (got %d)", groups);
+    if (top_groups < 1 || top_groups > groups) return fail(UQ_ERR_INVALID, "top_groups must lie in 1 .. %d", groups);
+    if (group_top != 1 && group_top != 2) return fail(UQ_ERR_INVALID, "group_top must be 1 or 2");
+    if (topk > experts / groups * top_groups) return fail(UQ_ERR_INVALID, "topk=%d is more than the experts to choose from", topk);
+    if (T == 0 || topk == 0) return UQ_OK;
+    if (!logits || !ids || !weights) return fail(UQ_ERR_INVALID, "null pointer");
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_moe_route(logits, type, bias, ids, weights, T, experts, topk, score == UQ_SIGMOID, groups, top_groups,
+                                         group_top, renormalize != 0, scale, ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "router launch");
+}
+
+uq_status uq_moe_route_grad(const void* logits, uq_dtype type, const int32_t* ids, const float* dweights, uq_score score,
+                            int renormalize, float scale, void* dlogits, int T, int experts, int topk, void* stream) {
+    uq_status s = check_router(type, score, scale, T, experts, topk);
+    if (s != UQ_OK) return s;
+    if (T == 0) return UQ_OK;
+    if (!logits || !dlogits || (topk && (!ids || !dweights))) return fail(UQ_ERR_INVALID, "null pointer");
+    if (dlogits == logits) return fail(UQ_ERR_INVALID, "dlogits and logits are the same");
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(dweights) || !aligned16(dlogits))
+        return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    DeviceState* ds = nullptr;
+    if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
+    cudaError_t e = uq::launch_moe_route_grad(logits, type, ids, dweights, dlogits, T, experts, topk, score == UQ_SIGMOID,
+                                              renormalize != 0, scale, ds->sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? UQ_OK : cuda_fail(e, "router gradient launch");
+}
+
 uq_status uq_device_fault(unsigned int* flag) {
     if (!flag) return fail(UQ_ERR_INVALID, "null pointer");
     *flag = 0;

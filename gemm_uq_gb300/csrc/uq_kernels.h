@@ -219,4 +219,31 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* ys, int type, co
                                     const int32_t* offsets, int E, void* dys, float* dw, int T, int topk, int H, int sms,
                                     cudaStream_t st);
 
+// rows in 8 bits, the norm that ends in them and its gradient (uq_q8.cu)
+cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, float* scales, int rows, int K, int sms,
+                               cudaStream_t st);
+cudaError_t launch_dequant_q8(const int8_t* codes, const float* scales, void* out, int type, int rows, int K, int sms, cudaStream_t st);
+cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* gamma, int type, long long ldx, void* h, void* y,
+                              int8_t* codes, float* scales, int rows, int D, float eps, int sms, cudaStream_t st);
+int norm_grad_partials(int type, int rows, int D, int sms);        // rows of D floats of `partials`
+cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, int type, void* dx, float* dgamma,
+                                float* partials, int rows, int D, float eps, int sms, cudaStream_t st);
+
+// product of 8-bit operands with a scale per row of each (uq_q8_gemm.cu)
+struct Q8GemmArgs {
+    const int8_t *x, *w;      // [M][K], [N][K]
+    const float *sx, *sw;     // [M], [N]
+    void* y;                  // [M][N]
+    unsigned int* fault;
+    int ytype, M, N, K;
+};
+cudaError_t launch_q8_gemm(const Q8GemmArgs& a, int sms, cudaStream_t st);
+
+// the router (uq_route.cu)
+cudaError_t launch_moe_route(const void* logits, int type, const float* bias, int32_t* ids, float* weights, int T, int E, int topk,
+                             bool sigmoid, int groups, int top_groups, int group_top, bool renorm, float scale, int sms,
+                             cudaStream_t st);
+cudaError_t launch_moe_route_grad(const void* logits, int type, const int32_t* ids, const float* dweights, void* dlogits, int T,
+                                  int E, int topk, bool sigmoid, bool renorm, float scale, int sms, cudaStream_t st);
+
 }  // namespace uq

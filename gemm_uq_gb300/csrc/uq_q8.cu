@@ -1,0 +1,511 @@
+// uq_q8.cu -- rows in 8 bits with one scale each: the quantizer, the norm that ends in it, and the norm's gradient.
+//
+// RMSNorm with the residual's addition, per row of D values:
+//     h = x + residual, rounded to the rows' type (it is the residual stream that the next layer reads, so that the norm
+//         is the norm of what was stored),
+//     y = h * r * gamma,  r = 1 / sqrt(mean(h^2) + eps),
+//     s = max|y| / 127,  code = y / s to the nearest integer, ties to even.
+// With m = max|h gamma|: s = r m / 127 and code = rne(h gamma * 127 / m), so the sum of squares and the maximum are one
+// pass and one reduction.  The row stays in registers between that pass and the one that writes.
+// Its gradient, g = dy gamma and n = h r:  dx = r (g - n mean(g n)) + dh,  dgamma = sum over rows of dy n.
+//
+// All of it is bound by memory: a row is read once and written once, in the widest accesses that its address, stride and
+// length allow.
+#include <cstring>
+#include <type_traits>
+
+#include "uq_mx.cuh"
+
+namespace uq {
+
+namespace {
+
+constexpr int MAX_THREADS = 1024;               // of a row; of the gradient's, whose threads hold more
+constexpr int GRAD_THREADS = 512;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t INF_BITS = 0x7F800000u;
+
+// The low byte of the sum with 1.5 * 2^23 is the nearest integer's two's complement (|v| < 2^22, ties to even).
+constexpr float ROUND = 12582912.f;
+__device__ __forceinline__ uint32_t code_bits(float v) { return __float_as_uint(v + ROUND); }
+// code = t * inv rounded once, to the integer
+__device__ __forceinline__ uint32_t code_bits(float t, float inv) { return __float_as_uint(fmaf(t, inv, ROUND)); }
+
+// the low bytes of V words, stored together
+template <int V> __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t (&w)[V]) {
+    if constexpr (V == 1) {
+        *p = (int8_t)w[0];
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)__byte_perm(w[0], w[1], 0x0040);
+    } else {
+        uint32_t o[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            o[i] = __byte_perm(__byte_perm(w[4 * i], w[4 * i + 1], 0x0040), __byte_perm(w[4 * i + 2], w[4 * i + 3], 0x0040), 0x5410);
+        if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = o[0];
+        else *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+    }
+}
+
+// Quotients x / s as correctly rounded fp32 divisions by Markstein's theorem (1990): r = RN(1 / s), q = x r,
+// q + (x - q s) r with the residual by FMA.  Scales far from 1 are divided by the instruction sequence for all values.
+struct Divisor {
+    float s, r;
+    bool fast, zero;
+    __device__ __forceinline__ explicit Divisor(float scale) : s(scale) {
+        r = 1.f / scale;
+        fast = scale >= 0x1p-90f && scale <= 0x1p90f;
+        zero = !(scale > 0.f) || scale > 3.0e38f;
+    }
+    __device__ __forceinline__ uint32_t code(float x) const {
+        if (fast) {
+            const float q = x * r;
+            return code_bits(fmaf(fmaf(-q, s, x), r, q));
+        }
+        return zero ? 0u : code_bits(fminf(fmaxf(__fdiv_rn(x, s), -127.f), 127.f));
+    }
+};
+
+// An access's elements in fp32, and back with one rounding.
+template <class T, int V> __device__ __forceinline__ void unpack(const Vec<T, V>& w, float (&f)[V]) {
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = to_f32(w.v[j]);
+    } else {
+        uint32_t u[V / 2];
+        memcpy(u, &w, sizeof u);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[2 * j] = bf16lo_f32(u[j]);
+                f[2 * j + 1] = bf16hi_f32(u[j]);
+            } else {
+                f[2 * j] = half_bits_f32((uint16_t)u[j]);
+                f[2 * j + 1] = half_bits_f32((uint16_t)(u[j] >> 16));
+            }
+        }
+    }
+}
+template <class T, int V> __device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+    Vec<T, V> w;
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) w.v[j] = from_f32<T>(f[j]);
+    } else {
+        uint32_t u[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(f[2 * j + 1]), "f"(f[2 * j]));
+            else
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(f[2 * j + 1]), "f"(f[2 * j]));
+        }
+        memcpy(&w, u, sizeof u);
+    }
+    return w;
+}
+
+struct RowArgs {
+    const void *x, *residual, *gamma;
+    void *h, *y;
+    int8_t* codes;
+    float* scales;
+    long long ldx;
+    int rows, D;
+    float eps;
+    int group;                                  // threads per row
+};
+
+// NORM: the norm; else the plain quantizer (h, y, residual and gamma unused).
+// V elements per access, NV accesses of a thread kept in registers; what a longer row has beyond is read again.
+template <class T, int V, int NV, bool NORM>
+__global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
+    using W = Vec<T, V>;
+    __shared__ float sums[2][MAX_THREADS / 32];
+    __shared__ uint32_t maxima[2][MAX_THREADS / 32];
+    const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
+    const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
+    const int nvec = a.D / V;
+    const W* gamma = static_cast<const W*>(a.gamma);
+    W gam[NV];
+    if constexpr (NORM) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * a.group < nvec) gam[i] = gamma[tid + i * a.group];
+    }
+    int buf = 0;
+    for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += (long long)gridDim.x * per_cta, buf ^= 1) {
+        const long long row = base + mine;
+        const bool on = row < a.rows;
+        const W* x = reinterpret_cast<const W*>(static_cast<const T*>(a.x) + (on ? row : 0) * a.ldx);
+        const W* res = reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + (on ? row : 0) * a.D);
+        auto load = [&](int v) {
+            W w = x[v];
+            if constexpr (NORM)
+                if (a.residual) {
+                    float f[V], r[V];
+                    unpack(w, f);
+                    unpack(res[v], r);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[j] += r[j];
+                    w = pack<T, V>(f);
+                }
+            return w;
+        };
+        float sum = 0.f;
+        uint32_t most = 0;
+        auto look = [&](const W& w, const W& g) {
+            float f[V], c[V];
+            unpack(w, f);
+            if constexpr (NORM) unpack(g, c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if constexpr (NORM) sum = fmaf(f[j], f[j], sum);
+                most = max(most, magnitude(NORM ? f[j] * c[j] : f[j]));
+            }
+        };
+        W kept[NV];
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) kept[i] = load(tid + i * a.group);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) look(kept[i], gam[i]);
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) look(load(v), NORM ? gamma[v] : W());
+        }
+        if constexpr (NORM) sum = warp_sum(sum);
+        most = warp_max(most);
+        if (warps > 1) {
+            // two sets of slots: those of this row are written again only after the barrier of the next one
+            if (lane == 0) {
+                if constexpr (NORM) sums[buf][threadIdx.x >> 5] = sum;
+                maxima[buf][threadIdx.x >> 5] = most;
+            }
+            __syncthreads();
+            const int w = first_warp + lane;
+            if constexpr (NORM) sum = warp_sum(lane < warps ? sums[buf][w] : 0.f);
+            most = warp_max(lane < warps ? maxima[buf][w] : 0u);
+        }
+        if (!on) continue;
+        const bool bad = most >= INF_BITS;
+        const float m = __uint_as_float(most);
+        if constexpr (NORM) {
+            const float r = __frsqrt_rn(sum / (float)a.D + a.eps);
+            // 127 / m stays finite for the smallest m
+            const float up = m < 0x1p-64f ? 0x1p80f : 1.f;
+            const float inv = most == 0 || bad ? 0.f : 127.f / (m * up);
+            if (tid == 0 && a.scales) a.scales[row] = bad ? __uint_as_float(0x7FC00000u) : r * m / 127.f;
+            W* h = a.h ? reinterpret_cast<W*>(static_cast<T*>(a.h) + row * a.D) : nullptr;
+            W* y = a.y ? reinterpret_cast<W*>(static_cast<T*>(a.y) + row * a.D) : nullptr;
+            int8_t* codes = a.codes ? a.codes + row * a.D : nullptr;
+            auto write = [&](int v, const W& w, const W& g) {
+                float f[V], c[V];
+                if (h) h[v] = w;
+                unpack(w, f);
+                unpack(g, c);
+                if (y) {
+                    float o[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) o[j] = f[j] * r * c[j];
+                    y[v] = pack<T, V>(o);
+                }
+                if (codes) {
+                    uint32_t q[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) q[j] = bad ? 0u : code_bits(f[j] * c[j] * up, inv);
+                    store_codes<V>(codes + (long long)v * V, q);
+                }
+            };
+            // before anything is written, which may be over x or the residual
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), gamma[v]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gam[i]);
+        } else {
+            const float s = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(m, 127.f);
+            if (tid == 0) a.scales[row] = s;
+            const Divisor d(s);
+            int8_t* codes = a.codes + row * a.D;
+            auto write = [&](int v, const W& w) {
+                float f[V];
+                uint32_t c[V];
+                unpack(w, f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) c[j] = d.code(f[j]);
+                store_codes<V>(codes + (long long)v * V, c);
+            };
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i]);
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v));
+        }
+    }
+}
+
+// out = code * scale, rounded once; 16 codes a thread where the rows allow it
+template <class T, int V>
+__global__ void __launch_bounds__(256) dequant_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales,
+                                                      T* __restrict__ out, long long vecs, int per_row) {
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < vecs; i += gridDim.x * 256LL) {
+        const Vec<int8_t, V> c = reinterpret_cast<const Vec<int8_t, V>*>(codes)[i];
+        const float s = scales[i / per_row];
+        constexpr int O = V * sizeof(T) <= 16 ? V : 16 / sizeof(T);
+#pragma unroll
+        for (int b = 0; b < V; b += O) {
+            Vec<T, O> o;
+#pragma unroll
+            for (int j = 0; j < O; ++j) o.v[j] = from_f32<T>((float)c.v[b + j] * s);
+            *reinterpret_cast<Vec<T, O>*>(out + i * V + b) = o;
+        }
+    }
+}
+
+struct GradArgs {
+    const void *dy, *h, *gamma, *dh;
+    void* dx;
+    float* partials;                            // [row groups of the grid][D]
+    int rows, D;
+    float eps;
+    int group;
+};
+
+// A group of threads takes every P-th row; its share of dgamma stays in registers (of a longer row, in its own row of
+// `partials`) until its rows are done.
+template <class T, int V, int NV>
+__global__ void __launch_bounds__(GRAD_THREADS) norm_grad_kernel(const GradArgs a) {
+    using W = Vec<T, V>;
+    __shared__ float2 sums[2][GRAD_THREADS / 32];
+    const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
+    const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
+    const int nvec = a.D / V;
+    const W* gamma = static_cast<const W*>(a.gamma);
+    float* part = a.partials + ((long long)blockIdx.x * per_cta + mine) * a.D;
+    W gam[NV];
+    float dg[NV][V] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (tid + i * a.group < nvec) gam[i] = gamma[tid + i * a.group];
+    for (int v = tid + NV * a.group; v < nvec; v += a.group)
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[(long long)v * V + j] = 0.f;
+    int buf = 0;
+    for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += (long long)gridDim.x * per_cta, buf ^= 1) {
+        const long long row = base + mine;
+        const bool on = row < a.rows;
+        const long long at = (on ? row : 0) * (long long)nvec;
+        const W *dy = static_cast<const W*>(a.dy) + at, *h = static_cast<const W*>(a.h) + at;
+        const W* dh = a.dh ? static_cast<const W*>(a.dh) + at : nullptr;
+        W* dx = static_cast<W*>(a.dx) + at;
+        float s1 = 0.f, s2 = 0.f;
+        auto look = [&](const W& u, const W& w, const W& g) {
+            float t[V], f[V], c[V];
+            unpack(u, t);
+            unpack(w, f);
+            unpack(g, c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s1 = fmaf(f[j], f[j], s1);
+                s2 = fmaf(t[j] * c[j], f[j], s2);
+            }
+        };
+        W ku[NV], kw[NV], kd[NV];
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) {
+                    ku[i] = dy[tid + i * a.group];
+                    kw[i] = h[tid + i * a.group];
+                    if (dh) kd[i] = dh[tid + i * a.group];
+                }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) look(ku[i], kw[i], gam[i]);
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) look(dy[v], h[v], gamma[v]);
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (warps > 1) {
+            if (lane == 0) sums[buf][threadIdx.x >> 5] = make_float2(s1, s2);
+            __syncthreads();
+            const float2 p = lane < warps ? sums[buf][first_warp + lane] : make_float2(0.f, 0.f);
+            s1 = warp_sum(p.x);
+            s2 = warp_sum(p.y);
+        }
+        if (!on) continue;
+        const float r = __frsqrt_rn(s1 / (float)a.D + a.eps);
+        const float c = r * r * (s2 / (float)a.D);                 // n mean(g n) = h r (r s2 / D)
+        auto write = [&](int v, const W& u, const W& w, const W& g, const W& d, float (&out)[V]) {
+            float t[V], f[V], e[V];
+            unpack(u, t);
+            unpack(w, f);
+            unpack(g, e);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                out[j] = fmaf(t[j] * r, f[j], out[j]);
+                e[j] = r * fmaf(-f[j], c, t[j] * e[j]);
+            }
+            if (dh) {
+                unpack(d, t);
+#pragma unroll
+                for (int j = 0; j < V; ++j) e[j] += t[j];
+            }
+            dx[v] = pack<T, V>(e);
+        };
+        for (int v = tid + NV * a.group; v < nvec; v += a.group) {
+            float out[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = part[(long long)v * V + j];
+            write(v, dy[v], h[v], gamma[v], dh ? dh[v] : W(), out);
+#pragma unroll
+            for (int j = 0; j < V; ++j) part[(long long)v * V + j] = out[j];
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * a.group < nvec) write(tid + i * a.group, ku[i], kw[i], gam[i], kd[i], dg[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (tid + i * a.group < nvec)
+#pragma unroll
+            for (int j = 0; j < V; ++j) part[(long long)(tid + i * a.group) * V + j] = dg[i][j];
+}
+
+// dgamma = the sum of the P partial rows, in order: a CTA of 32 x 8 threads takes 32 columns, its warps every 8th row, and
+// adds the warps' sums in order.
+__global__ void __launch_bounds__(256) partials_sum_kernel(const float* __restrict__ partials, float* __restrict__ out, int P, int D) {
+    __shared__ float part[8][32];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    float s = 0.f;
+    if (col < D) {
+#pragma unroll 8
+        for (int p = w; p < P; p += 8) s += partials[(long long)p * D + col];
+    }
+    part[w][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (w == 0 && col < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+        out[col] = s;
+    }
+}
+
+// Elements per access: 16 bytes, or 4, or one element, whatever divides the row and its addresses' alignment (pointers are
+// 16-byte aligned).
+template <class T> int access(int D, long long ld) {
+    const long long both = (long long)D | ld;
+    if (both % (16 / (int)sizeof(T)) == 0) return 16 / sizeof(T);
+    return both % (4 / (int)sizeof(T)) == 0 ? 4 / sizeof(T) : 1;
+}
+
+// Threads per row and accesses per thread for rows of nvec accesses.
+struct Shape { int group, nv, block; };
+Shape shape_of(int nvec, int most_threads) {
+    Shape s = {32, 1, 0};
+    while (s.group < most_threads && s.group * 2 < nvec) s.group *= 2;
+    while (s.nv < 4 && s.group * s.nv < nvec) s.nv *= 2;
+    s.block = s.group < 128 ? 128 : s.group;
+    return s;
+}
+
+// f(integral constants V, NV)
+template <class T, class F> cudaError_t with_shape(int v, int nv, F&& f) {
+    auto by_nv = [&](auto V) {
+        if (nv == 1) return f(V, std::integral_constant<int, 1>());
+        if (nv == 2) return f(V, std::integral_constant<int, 2>());
+        return f(V, std::integral_constant<int, 4>());
+    };
+    constexpr int WIDE = 16 / sizeof(T), FOUR = 4 / sizeof(T);
+    if (v == WIDE) return by_nv(std::integral_constant<int, WIDE>());
+    if (FOUR > 1 && v == FOUR) return by_nv(std::integral_constant<int, FOUR>());
+    return by_nv(std::integral_constant<int, 1>());
+}
+
+template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sms, cudaStream_t st) {
+    return with_dtype(type, [&](auto t) {
+        using T = decltype(t);
+        RowArgs a = a0;
+        const int v = access<T>(a.D, a.ldx);
+        const Shape s = shape_of(a.D / v, MAX_THREADS);
+        a.group = s.group;
+        const long long tiles = ((long long)a.rows + s.block / s.group - 1) / (s.block / s.group), most = (long long)sms * (2048 / s.block);
+        return with_shape<T>(v, s.nv, [&](auto V, auto NV) {
+            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM><<<(unsigned)(tiles < most ? tiles : most), s.block, 0, st>>>(a);
+            return cudaGetLastError();
+        });
+    });
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, float* scales, int rows, int K, int sms,
+                               cudaStream_t st) {
+    RowArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.codes = codes;
+    a.scales = scales;
+    a.rows = rows;
+    a.D = K;
+    return launch_rows<false>(a, type, sms, st);
+}
+
+cudaError_t launch_dequant_q8(const int8_t* codes, const float* scales, void* out, int type, int rows, int K, int sms, cudaStream_t st) {
+    return with_dtype(type, [&](auto t) {
+        using T = decltype(t);
+        auto go = [&](auto V) {
+            constexpr int N = decltype(V)::value;
+            const long long vecs = (long long)rows * (K / N), ctas = (vecs + 255) / 256;
+            dequant_kernel<T, N><<<(unsigned)(ctas < 16LL * sms ? ctas : 16LL * sms), 256, 0, st>>>(codes, scales, static_cast<T*>(out), vecs, K / N);
+            return cudaGetLastError();
+        };
+        if (K % 16 == 0) return go(std::integral_constant<int, 16>());
+        if (K % 4 == 0) return go(std::integral_constant<int, 4>());
+        return go(std::integral_constant<int, 1>());
+    });
+}
+
+cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* gamma, int type, long long ldx, void* h, void* y,
+                              int8_t* codes, float* scales, int rows, int D, float eps, int sms, cudaStream_t st) {
+    const RowArgs a = {x, residual, gamma, h, y, codes, scales, ldx, rows, D, eps, 0};
+    return launch_rows<true>(a, type, sms, st);
+}
+
+// Row groups of the gradient's grid, each with a partial row of dgamma.
+static Shape grad_shape(int type, int D) {
+    const int v = type == UQ_FP32 ? access<float>(D, D) : access<__half>(D, D);
+    return shape_of(D / v, GRAD_THREADS);
+}
+int norm_grad_partials(int type, int rows, int D, int sms) {
+    const Shape s = grad_shape(type, D);
+    const int per = s.block / s.group;
+    const long long tiles = ((long long)rows + per - 1) / per, most = (long long)sms * (1024 / s.block);
+    return (int)(tiles < most ? tiles : most) * per;
+}
+
+cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, int type, void* dx, float* dgamma,
+                                float* partials, int rows, int D, float eps, int sms, cudaStream_t st) {
+    const Shape s = grad_shape(type, D);
+    const int P = norm_grad_partials(type, rows, D, sms);
+    const GradArgs a = {dy, h, gamma, dh, dx, partials, rows, D, eps, s.group};
+    cudaError_t e = with_dtype(type, [&](auto t) {
+        using T = decltype(t);
+        return with_shape<T>(access<T>(D, D), s.nv, [&](auto V, auto NV) {
+            norm_grad_kernel<T, decltype(V)::value, decltype(NV)::value><<<P / (s.block / s.group), s.block, 0, st>>>(a);
+            return cudaGetLastError();
+        });
+    });
+    if (e != cudaSuccess) return e;
+    partials_sum_kernel<<<(D + 31) / 32, 256, 0, st>>>(partials, dgamma, P, D);
+    return cudaGetLastError();
+}
+
+}  // namespace uq

@@ -1,0 +1,340 @@
+// uq_route.cu -- the router of a mixture of experts: expert ids and weights of each token's logits, and the gradient.
+//
+// Scores s = softmax(x) or 1 / (1 + e^-x); choice values c = s + bias (the bias balances the experts' load and does not
+// enter the weights).  Optionally the experts form groups of equal size: a group counts the sum of its group_top highest c,
+// and only the top_groups best groups stay.  The topk highest c are chosen, in that order, equal values by lower index.
+// Weights: s of the chosen, divided by their sum where asked, times a factor.
+//
+// The choice is the one that 64-bit scores give.  Where the order of c is that of x itself (no bias, groups by their best
+// member) it needs no scores.  Else c is computed in fp32 with a bound on its error, and where two neighbours in the order,
+// or the last group that stays and the first that does not, are nearer than their bounds allow to tell, the token is done
+// again in 64 bits (one expert's fp64 exponential costs a warp some thousand cycles: this part has few fp64 units).
+//
+// One warp per token; its choice values lie in shared memory.
+#include "uq_mx.cuh"
+
+namespace uq {
+
+namespace {
+
+constexpr int WARPS = 4;                        // tokens of a CTA
+constexpr uint32_t ALL = 0xffffffffu;
+__device__ __forceinline__ float low_value() { return __uint_as_float(0xFF800000u); }
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int T, E, topk, sigmoid, groups, top_groups, group_top, renorm;
+    float scale;
+};
+
+__device__ __forceinline__ float warp_max_f(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
+    return v;
+}
+template <class S> __device__ __forceinline__ S warp_add(S v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
+    return v;
+}
+
+// 1 / (1 + e^-x) times e^-low for low <= 0 (low = 0: itself): sigmoids far below one keep their ratios
+__device__ __forceinline__ float sigmoid_over(float x, float low) {
+    return x >= 0.f ? 1.f / (1.f + expf(-x)) : expf(x - low) / (1.f + expf(x));
+}
+
+// A choice value of NaN (a NaN logit or bias) ranks below all numbers and above what cannot be chosen, which is marked by
+// minus infinity; NaN itself must not be compared.
+template <class S> __device__ __forceinline__ S ranked(S c, bool can) {
+    const S least = sizeof(S) == 8 ? (S)-1.7e308 : (S)-3.4e38f;
+    if (!can) return (S)low_value();
+    return c != c ? least : (c < least ? least : c);
+}
+
+// The largest of the lanes' values and, among equal ones, the smallest index; index E where all are minus infinity.
+__device__ __forceinline__ void best_of(float& c, int& e, int E) {
+    uint32_t k = __float_as_uint(c);
+    k = k & 0x80000000u ? ~k : k | 0x80000000u;                    // the order of the values
+    const uint32_t top = __reduce_max_sync(ALL, k);
+    e = (int)__reduce_min_sync(ALL, k == top ? (unsigned)e : (unsigned)E);
+    c = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+    if (c == low_value()) e = E;
+}
+__device__ __forceinline__ void best_of(double& c, int& e, int E) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const double oc = __shfl_xor_sync(ALL, c, o);
+        const int oe = __shfl_xor_sync(ALL, e, o);
+        if (oc > c || (oc == c && oe < e)) c = oc, e = oe;
+    }
+    if (c == (double)low_value()) e = E;
+}
+
+// Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it).  Lane j returns choice j, -1 for
+// none.  `exact`: c is the logits themselves; `sure`: every decision had more distance than the error of the values.
+template <class S, class T>
+__device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool exact, bool& sure) {
+    const int lane = threadIdx.x & 31, E = a.E;
+    const S none = (S)low_value();
+    sure = true;
+    // Error of a choice value: the score's, some roundings of it (softmax: and of its exponent, |x - max| 2^-24 relative,
+    // at most e^-1 2^-24 of the largest score), and the addition's.
+    auto apart = [&](S hi, S lo, S terms) {
+        const S m = fmax(fabs(hi), fabs(lo));
+        return hi - lo > (S)2 * terms * (m * (S)0x1p-24f + (S)0x1p-21f);
+    };
+    if (a.groups > 1) {
+        // 2^k lanes per group, each every 2^k-th member; the group's best two by shuffles
+        int per = 32;
+        while (per * a.groups > 32) per >>= 1;
+        const int g = lane / per, size = E / a.groups;
+        S b1 = none, b2 = none;
+        if (g < a.groups)
+            for (int i = lane % per; i < size; i += per) {
+                const S v = c[g * size + i];
+                if (v > b1) b2 = b1, b1 = v;
+                else if (v > b2) b2 = v;
+            }
+        for (int o = 1; o < per; o <<= 1) {
+            const S o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
+            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+            b1 = fmax(b1, o1);
+        }
+        S total = b1;
+        if (a.group_top == 2 && b2 > none) total += b2;
+        if (g >= a.groups) total = none;
+        int ahead = 0;                          // groups before this one
+        for (int o = 0; o < a.groups; ++o) {
+            const S t = __shfl_sync(ALL, total, o * per);
+            ahead += t > total || (t == total && o < g);
+        }
+        const bool stays = total > none && ahead < a.top_groups;
+        if constexpr (sizeof(S) == 4) {
+            if (!exact) {
+                // distance between the groups that stay and the others (one with the same members' values may tie)
+                const S worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
+                if (next > none && !apart(worst, next, (S)(2 * a.group_top))) sure = false;
+            }
+        }
+        const uint32_t open_ = __ballot_sync(ALL, stays && lane % per == 0);
+        // without a bias the order within the groups is that of x
+        if (!a.bias) exact = true;
+        for (int e = lane; e < E; e += 32) {
+            if (!(open_ >> (e / size * per) & 1u)) c[e] = none;
+            else if (!a.bias) c[e] = ranked<S>((S)to_f32(x[e]) + (S)0, to_f32(x[e]) != low_value());
+        }
+        __syncwarp();
+    }
+    S mine = none;                              // the lane's best remaining expert: of e = lane, lane + 32, ...
+    int at = lane;
+    auto rescan = [&] {
+        mine = none;
+        at = lane;
+        for (int e = lane; e < E; e += 32) {
+            const S v = c[e];
+            if (v > mine) mine = v, at = e;
+        }
+    };
+    rescan();
+    int id = -1, last = -1;
+    S before = none;
+    const int rounds = sizeof(S) == 4 && !exact ? a.topk + 1 : a.topk;     // the first that is not chosen, too
+    for (int j = 0; j < rounds; ++j) {
+        S v = mine;
+        int e = at;
+        best_of(v, e, E);
+        if (e == E) break;
+        if constexpr (sizeof(S) == 4) {
+            if (!exact && j && !apart(before, v, (S)1)) {
+                // the same logit and bias give the same value: the lower index is right
+                if (!(before == v && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) sure = false;
+            }
+            before = v;
+            last = e;
+        }
+        if (j < a.topk && lane == j) id = e;
+        if (at == e && mine > none) {
+            c[e] = none;
+            rescan();
+        }
+    }
+    return id;
+}
+
+// Choice values of a token in S, into c[] (by_logit: the logits themselves).
+template <class S, class T>
+__device__ __forceinline__ void values(const RouteArgs& a, S* c, const T* x, bool by_logit) {
+    const int lane = threadIdx.x & 31;
+    float m = low_value();
+    S sum = 0;
+    if (!a.sigmoid && !by_logit) {
+        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+        m = warp_max_f(m);
+        for (int e = lane; e < a.E; e += 32) {
+            const float v = to_f32(x[e]);
+            if (v > low_value()) sum += sizeof(S) == 8 ? (S)exp((double)v - (double)m) : (S)expf(v - m);
+        }
+        sum = warp_add(sum);
+    }
+    for (int e = lane; e < a.E; e += 32) {
+        const float v = to_f32(x[e]), b = a.bias ? a.bias[e] : 0.f;
+        S s;
+        if (by_logit) s = (S)v;
+        else if (sizeof(S) == 8) s = (S)(a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / (double)sum);
+        else s = (S)(a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - m) / (float)sum);
+        if (v != v) s = (S)v;
+        c[e] = ranked<S>(s + (S)b, v != low_value() && b != low_value());
+    }
+    __syncwarp();
+}
+
+template <class T>
+__global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+    uint8_t* mine = smem + (size_t)warp * a.E * (by_logit ? 4 : 8);
+    for (long long t = (long long)blockIdx.x * WARPS + warp; t < a.T; t += (long long)gridDim.x * WARPS) {
+        const T* x = static_cast<const T*>(a.logits) + t * a.E;
+        bool sure;
+        __syncwarp();
+        values<float>(a, reinterpret_cast<float*>(mine), x, by_logit);
+        int id = choose<float>(a, reinterpret_cast<float*>(mine), x, by_logit, sure);
+        if (!sure) {
+            __syncwarp();
+            values<double>(a, reinterpret_cast<double*>(mine), x, false);
+            id = choose<double>(a, reinterpret_cast<double*>(mine), x, false, sure);
+        }
+        // weights: lane j's
+        const float v = id >= 0 ? to_f32(x[id]) : low_value();
+        float w;
+        if (a.renorm) {
+            // among the chosen alone, from the largest logit of them: their ratios survive where the scores underflow
+            bool bad = id >= 0 && v != v;
+            const float m = warp_max_f(v);
+            if (a.sigmoid) {
+                w = id >= 0 ? sigmoid_over(v, fminf(m, 0.f)) : 0.f;
+            } else {
+                // a NaN among the logits makes all of softmax NaN
+                for (int e = lane; e < a.E; e += 32) bad |= to_f32(x[e]) != to_f32(x[e]);
+                w = id >= 0 ? expf(v - m) : 0.f;
+            }
+            const float all = warp_add(w);
+            w = __any_sync(ALL, bad) ? __uint_as_float(0x7FC00000u) : (all > 0.f || all != all ? w / all : 0.f);
+        } else if (a.sigmoid) {
+            w = 1.f / (1.f + expf(-v));
+        } else {
+            float m = low_value(), sum = 0.f;
+            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+            m = warp_max_f(m);
+            for (int e = lane; e < a.E; e += 32) {
+                const float u = to_f32(x[e]);
+                if (u != low_value()) sum += expf(u - m);
+            }
+            sum = warp_add(sum);
+            w = expf(v - m) / sum;
+        }
+        if (lane < a.topk) {
+            a.ids[t * a.topk + lane] = id;
+            a.weights[t * a.topk + lane] = id >= 0 ? w * a.scale : 0.f;
+        }
+    }
+}
+
+struct RouteGradArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* dweights;
+    void* dlogits;
+    int T, E, topk, sigmoid, renorm;
+    float scale;
+};
+
+// Gradient of a token's logits.  With dw the weights' gradient times the factor, over the routes that have an expert:
+//   renormalised, w_j = s_j / sum s: q_j = w_j (dw_j - sum_i w_i dw_i), dx of the chosen q_j (softmax), q_j (1 - s_j) (sigmoid)
+//   softmax: ds_e = sum of dw over the routes to e, dx_e = s_e (ds_e - sum s ds);  sigmoid: dx_e = s_e (1 - s_e) ds_e
+// Lane j holds route j; an expert's routes are found by all lanes' ids in turn, in order, so one expert may be named twice.
+template <class T>
+__global__ void __launch_bounds__(WARPS * 32) route_grad_kernel(const RouteGradArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (long long t = (long long)blockIdx.x * WARPS + warp; t < a.T; t += (long long)gridDim.x * WARPS) {
+        const T* x = static_cast<const T*>(a.logits) + t * a.E;
+        T* dx = static_cast<T*>(a.dlogits) + t * a.E;
+        int id = lane < a.topk ? a.ids[t * a.topk + lane] : -1;
+        if (id < 0 || id >= a.E) id = -1;
+        const float dw = id >= 0 ? a.dweights[t * a.topk + lane] * a.scale : 0.f;
+        const float v = id >= 0 ? to_f32(x[id]) : low_value();
+        float q = dw;                           // what route j adds to its expert
+        float m = low_value(), sum = 0.f, dot = 0.f;
+        if (a.renorm) {
+            const float top = warp_max_f(v);
+            float w = 0.f;
+            if (id >= 0) w = a.sigmoid ? sigmoid_over(v, fminf(top, 0.f)) : expf(v - top);
+            const float all = warp_add(w);
+            w = all > 0.f || all != all ? w / all : 0.f;
+            q = w * (dw - warp_add(w * dw));
+            if (a.sigmoid) q *= v >= 0.f ? expf(-v) / (1.f + expf(-v)) : 1.f / (1.f + expf(v));        // 1 - s
+            if (id < 0) q = 0.f;
+        } else if (!a.sigmoid) {
+            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+            m = warp_max_f(m);
+            for (int e = lane; e < a.E; e += 32) {
+                const float u = to_f32(x[e]);
+                if (u != low_value()) sum += expf(u - m);
+            }
+            sum = warp_add(sum);
+            dot = warp_add(id >= 0 ? expf(v - m) / sum * dw : 0.f);
+        }
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            float ds = 0.f;
+            for (int j = 0; j < a.topk; ++j) {
+                const int at = __shfl_sync(ALL, id, j);
+                const float add = __shfl_sync(ALL, q, j);
+                if (at == e) ds += add;
+            }
+            if (e >= a.E) continue;
+            const float u = to_f32(x[e]);
+            float d = ds;
+            if (!a.renorm) {
+                if (a.sigmoid) {
+                    const float n = expf(-fabsf(u));               // s (1 - s) = n / (1 + n)^2
+                    d = ds * (n / ((1.f + n) * (1.f + n)));
+                } else {
+                    d = u == low_value() ? 0.f : expf(u - m) / sum * (ds - dot);
+                }
+            }
+            dx[e] = from_f32<T>(d);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const void* logits, int type, const float* bias, int32_t* ids, float* weights, int T, int E, int topk,
+                             bool sigmoid, int groups, int top_groups, int group_top, bool renorm, float scale, int sms,
+                             cudaStream_t st) {
+    const RouteArgs a = {logits, bias, ids, weights, T, E, topk, sigmoid, groups, top_groups, group_top, renorm, scale};
+    const bool by_logit = !bias && (groups == 1 || group_top == 1);
+    const size_t smem = (size_t)WARPS * E * (by_logit ? 4 : 8);    // at most 32 KB
+    const long long ctas = ((long long)T + WARPS - 1) / WARPS, most = 16LL * sms;
+    return with_dtype(type, [&](auto t) {
+        route_kernel<decltype(t)><<<(unsigned)(ctas < most ? ctas : most), WARPS * 32, smem, st>>>(a);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_moe_route_grad(const void* logits, int type, const int32_t* ids, const float* dweights, void* dlogits, int T,
+                                  int E, int topk, bool sigmoid, bool renorm, float scale, int sms, cudaStream_t st) {
+    const RouteGradArgs a = {logits, ids, dweights, dlogits, T, E, topk, sigmoid, renorm, scale};
+    const long long ctas = ((long long)T + WARPS - 1) / WARPS, most = 16LL * sms;
+    return with_dtype(type, [&](auto t) {
+        route_grad_kernel<decltype(t)><<<(unsigned)(ctas < most ? ctas : most), WARPS * 32, 0, st>>>(a);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace uq

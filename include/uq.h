@@ -76,6 +76,12 @@ typedef enum uq_dtype {
     UQ_FP32 = 2
 } uq_dtype;
 
+/* Scores of a router's logits (uq_moe_route). */
+typedef enum uq_score {
+    UQ_SOFTMAX = 0,
+    UQ_SIGMOID = 1
+} uq_score;
+
 /* Microscaled 4-bit floating point: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit 3 the
  * sign) and one scale byte per block of consecutive k. */
 typedef enum uq_mx_fmt {
@@ -468,6 +474,88 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
                              const uint8_t* wscales, const uint8_t* wcodes_up, const uint8_t* wscales_up,
                              const int32_t* offsets, const float* alpha, const float* alpha_up, void* y,
                              uq_dtype ytype, int rows, int experts, int N, int K, uq_mx_fmt fmt, void* stream);
+
+/*
+ * Rows in 8 bits: int8 codes [rows][K] and one fp32 scale per row, the value code * scale.  Activations have a scale per
+ * token, a weight [N][K] one per output channel.  Sizes are at most 2^31 - 4097 (UQ_ERR_UNSUPPORTED beyond).
+ *
+ * uq_quantize_q8 -- rows -> codes and scales: s = max|x| / 127, code = RNE(x / s), both fp32 divisions; a row of zeros has
+ * s = 0, and a row that holds a NaN or an infinity s = NaN and codes 0, so that all of it reads back as NaN.
+ *   x (device) [rows][K] of xtype, rows ldx elements apart (any stride; every row element-aligned); codes (device) int8
+ *   [rows][K], scales (device) fp32 [rows], written.  K of any size.  Asynchronous.
+ */
+uq_status uq_quantize_q8(const void* x, uq_dtype xtype, long long ldx, int8_t* codes, float* scales, int rows, int K,
+                         void* stream);
+
+/* uq_dequant_q8 -- the values that codes and scales stand for, rounded once to `type`: out (device) [rows][K], written.
+ * Asynchronous. */
+uq_status uq_dequant_q8(const int8_t* codes, const float* scales, void* out, uq_dtype type, int rows, int K, void* stream);
+
+/*
+ * uq_rmsnorm_q8 -- the residual's addition, RMSNorm, and its result in 8 bits, in one pass over the row:
+ *     h = x + residual (fp32, rounded to `type`: the residual stream, of which the norm is taken),
+ *     y[j] = h[j] / sqrt(mean(h^2) + eps) * gamma[j]  (fp32),  s = max|y| / 127,  code = y / s to the nearest integer
+ *     (ties to even; y and s in fp32 before they are rounded: a quotient within 2^-20 of a tie may go either way).
+ *   x (device) [rows][D] of `type`, rows ldx elements apart; residual (device, or NULL: h = x) [rows][D]; gamma (device) [D].
+ *   h, y (device, or NULL: not wanted) [rows][D] of `type`; codes (device) int8 [rows][D] and scales (device) fp32 [rows],
+ *   both or neither; written.  h may be x (with ldx = D) or residual, and so may y.
+ * The mean of the squares has to lie within fp32.  A row with a NaN or an infinity gets a NaN scale and codes 0.  The
+ * gradient, with the codes taken for the values they stand for, is uq_rmsnorm_grad.  Asynchronous.
+ */
+uq_status uq_rmsnorm_q8(const void* x, const void* residual, const void* gamma, uq_dtype type, long long ldx, void* h, void* y,
+                        int8_t* codes, float* scales, int rows, int D, float eps, void* stream);
+
+/*
+ * uq_rmsnorm_grad -- gradients of y = h / sqrt(mean(h^2) + eps) * gamma:  with r = 1 / sqrt(mean(h^2) + eps), n = h r and
+ * g = dy * gamma,   dx = r * (g - n * mean(g * n)) + dh,   dgamma[j] = sum over rows of dy[j] * n[j].
+ *   dy, h (device) [rows][D] of `type`; gamma (device) [D]; dh (device, or NULL) [rows][D], the gradient that reaches h
+ *   besides; dx (device) [rows][D] of `type`: the gradient of h, and so of x and of the residual; it may be dy or dh.
+ *   dgamma (device) fp32 [D], written.  Sums in fp32 in a fixed order: equal calls give equal bits.
+ * Workspace and stream capture as uq_gemm.
+ */
+uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, uq_dtype type, void* dx,
+                          float* dgamma, int rows, int D, float eps, void* stream);
+
+/*
+ * uq_gemm_w8a8 -- y[m][n] = xscales[m] * wscales[n] * sum_k x[m][k] * w[n][k] of 8-bit operands, rounded once to ytype.
+ * The integer sums are exact over every 1024 k, and are added up in fp32 or exactly.
+ *   x: int8 codes [M][K] with xscales fp32 [M] (both device; xtype and ldx ignored); or, with xscales NULL, rows of xtype,
+ *      ldx apart, quantized in the call as uq_quantize_q8 does (into the per-stream workspace)
+ *   w (device) int8 [N][K], wscales (device) fp32 [N]; y (device) [M][N], written.
+ * K a multiple of 16, at most 131056 (UQ_ERR_UNSUPPORTED beyond).  M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Equal calls give equal bits.
+ * Workspace and stream capture as uq_gemm.
+ */
+uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float* xscales, const int8_t* w,
+                       const float* wscales, void* y, uq_dtype ytype, int M, int N, int K, void* stream);
+
+/*
+ * uq_moe_route -- the router: expert ids and weights of the logits, as uq_moe_sort and uq_moe_combine take them.
+ *   scores   s = softmax of the token's logits (over all experts), or 1 / (1 + e^-logit)
+ *   choice   c = s + bias; the topk experts of the highest c, in that order, equal c by lower index.  Decided as in 64-bit
+ *            arithmetic, without a bias by the logits themselves.  An expert whose logit (or bias) is minus infinity is
+ *            never chosen; one whose logit is NaN is chosen last.  Where fewer than topk can be chosen, the remaining ids are -1
+ *            and their weights 0.
+ *   groups   > 1: the experts form `groups` equal groups of neighbours; only experts of the top_groups best ones may be
+ *            chosen.  A group counts the sum of its group_top (1 or 2) highest c of experts that may be chosen; equal groups by
+ *            lower index.
+ *   weights  s of the chosen; renormalize: divided by their sum (0 / 0 = 0); times scale.  fp32.
+ * logits (device) [T][experts] of `type`; bias (device or NULL) fp32 [experts]; ids (device) int32 [T][topk], weights
+ * (device) fp32 [T][topk], written.  1 <= experts <= 1024, 1 <= groups <= 32, topk <= 32 and at most the experts of
+ * top_groups groups.  Asynchronous.
+ */
+uq_status uq_moe_route(const void* logits, uq_dtype type, const float* bias, uq_score score, int groups, int top_groups,
+                       int group_top, int renormalize, float scale, int32_t* ids, float* weights, int T, int experts, int topk,
+                       void* stream);
+
+/*
+ * uq_moe_route_grad -- the gradient of uq_moe_route's weights with respect to the logits (the ids, and with them the bias
+ * and the groups, have none):  dlogits (device) [T][experts] of `type`, written whole.
+ *   logits as given to uq_moe_route, ids (device) int32 [T][topk] its ids (or any: an entry outside [0, experts) is no route,
+ *   and an expert named twice gets both routes' gradients), dweights (device) fp32 [T][topk].
+ * Limits as uq_moe_route.  Asynchronous.
+ */
+uq_status uq_moe_route_grad(const void* logits, uq_dtype type, const int32_t* ids, const float* dweights, uq_score score,
+                            int renormalize, float scale, void* dlogits, int T, int experts, int topk, void* stream);
 
 /*
  * Expert routing.  Token t takes topk routes (t, j), flat index t * topk + j, to experts ids[t][j]; a route whose
