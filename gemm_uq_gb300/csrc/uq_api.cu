@@ -1212,7 +1212,8 @@ uq_status uq_quantize_q8(const void* x, uq_dtype xtype, long long ldx, int8_t* c
     if (!aligned16(codes) || !aligned16(scales)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
     DeviceState* ds = nullptr;
     if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
-    cudaError_t e = uq::launch_quantize_q8(x, xtype, ldx, codes, scales, rows, K, ds->sms, static_cast<cudaStream_t>(stream));
+    cudaError_t e = uq::launch_quantize_q8(x, xtype, ldx, codes, nullptr, scales, rows, K, false, ds->sms,
+                                           static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit quantization launch");
 }
 
@@ -1313,19 +1314,26 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
     a.M = M;
     a.N = N;
     a.K = K;
-    if (!xscales) {
-        // the quantized x lives in the workspace: codes | scales
-        const size_t code_bytes = ((size_t)M * K + 255) / 256 * 256;
+    const bool wide = uq::q8_gemm_wide(M);
+    void* x16 = nullptr;
+    if (wide || !xscales) {
+        // codes for the product (as fp16 for many tokens) | scales, in the workspace
+        const size_t code_bytes = ((size_t)M * K * (wide ? 2 : 1) + 255) / 256 * 256;
         Workspace* ws = nullptr;
         if ((s = workspace(dev, st, 0, 0, &ws, code_bytes + (size_t)M * sizeof(float))) != UQ_OK) return s;
         int8_t* codes = reinterpret_cast<int8_t*>(ws->aux);
         float* scales = reinterpret_cast<float*>(codes + code_bytes);
-        e = uq::launch_quantize_q8(x, xtype, ldx, codes, scales, M, K, ds->sms, st);
+        if (wide) x16 = codes;
+        if (xscales) {
+            e = uq::launch_q8_widen(a.x, x16, M, K, ds->sms, st);
+        } else {
+            e = uq::launch_quantize_q8(x, xtype, ldx, codes, x16, scales, M, K, wide, ds->sms, st);
+            a.x = codes;
+            a.sx = scales;
+        }
         if (e != cudaSuccess) return cuda_fail(e, "8-bit quantization launch");
-        a.x = codes;
-        a.sx = scales;
     }
-    e = uq::launch_q8_gemm(a, ds->sms, st);
+    e = wide ? uq::launch_q8_gemm_wide(a, x16, ds->sms, st) : uq::launch_q8_gemm(a, ds->sms, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit product launch");
 }
 

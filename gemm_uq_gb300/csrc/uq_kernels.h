@@ -220,8 +220,9 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* ys, int type, co
                                     cudaStream_t st);
 
 // rows in 8 bits, the norm that ends in them and its gradient (uq_q8.cu)
-cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, float* scales, int rows, int K, int sms,
-                               cudaStream_t st);
+// wide: the codes as fp16 there instead; early: the next kernel may start before this one is done
+cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, void* wide, float* scales, int rows, int K,
+                               bool early, int sms, cudaStream_t st);
 cudaError_t launch_dequant_q8(const int8_t* codes, const float* scales, void* out, int type, int rows, int K, int sms, cudaStream_t st);
 cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* gamma, int type, long long ldx, void* h, void* y,
                               int8_t* codes, float* scales, int rows, int D, float eps, int sms, cudaStream_t st);
@@ -237,6 +238,9 @@ struct Q8GemmArgs {
     unsigned int* fault;
     int ytype, M, N, K;
 };
+bool q8_gemm_wide(int M);           // whether a product of so many tokens takes their codes as fp16 (launch_q8_gemm_wide)
+cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st);
+cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& a, const void* x16, int sms, cudaStream_t st);
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, int sms, cudaStream_t st);
 
 // the router (uq_route.cu)

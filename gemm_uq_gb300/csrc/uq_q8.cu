@@ -122,6 +122,8 @@ struct RowArgs {
     int rows, D;
     float eps;
     int group;                                  // threads per row
+    __half* wide;                               // the quantizer's codes as fp16 instead
+    int early;                                  // the next kernel may start before this one is done
 };
 
 // NORM: the norm; else the plain quantizer (h, y, residual and gamma unused).
@@ -134,6 +136,8 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
     const int nvec = a.D / V;
+    if constexpr (!NORM)
+        if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const W* gamma = static_cast<const W*>(a.gamma);
     W gam[NV];
     if constexpr (NORM) {
@@ -234,14 +238,19 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
             const float s = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(m, 127.f);
             if (tid == 0) a.scales[row] = s;
             const Divisor d(s);
-            int8_t* codes = a.codes + row * a.D;
             auto write = [&](int v, const W& w) {
                 float f[V];
                 uint32_t c[V];
                 unpack(w, f);
 #pragma unroll
                 for (int j = 0; j < V; ++j) c[j] = d.code(f[j]);
-                store_codes<V>(codes + (long long)v * V, c);
+                if (a.wide) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[j] = (float)(int8_t)c[j];
+                    reinterpret_cast<Vec<__half, V>*>(a.wide + row * a.D)[v] = pack<__half, V>(f);
+                } else {
+                    store_codes<V>(a.codes + row * a.D + (long long)v * V, c);
+                }
             };
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -446,13 +455,15 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
 
 }  // namespace
 
-cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, float* scales, int rows, int K, int sms,
-                               cudaStream_t st) {
+cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* codes, void* wide, float* scales, int rows, int K,
+                               bool early, int sms, cudaStream_t st) {
     RowArgs a = {};
     a.x = x;
     a.ldx = ldx;
     a.codes = codes;
     a.scales = scales;
+    a.wide = static_cast<__half*>(wide);
+    a.early = early;
     a.rows = rows;
     a.D = K;
     return launch_rows<false>(a, type, sms, st);
@@ -475,7 +486,7 @@ cudaError_t launch_dequant_q8(const int8_t* codes, const float* scales, void* ou
 
 cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* gamma, int type, long long ldx, void* h, void* y,
                               int8_t* codes, float* scales, int rows, int D, float eps, int sms, cudaStream_t st) {
-    const RowArgs a = {x, residual, gamma, h, y, codes, scales, ldx, rows, D, eps, 0};
+    const RowArgs a = {x, residual, gamma, h, y, codes, scales, ldx, rows, D, eps};
     return launch_rows<true>(a, type, sms, st);
 }
 

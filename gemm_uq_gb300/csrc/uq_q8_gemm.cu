@@ -1,11 +1,31 @@
 // uq_q8_gemm.cu -- product of 8-bit operands with one scale per row of each:
 //     y[m][n] = sx[m] * sw[n] * sum_k x[m][k] * w[n][k].
 //
-// The integer tensor instruction mma.m16n8k32 (s8 x s8 -> s32) on 16 rows of w and 8 tokens.  Where a lane's k lie in the
+// Few tokens (q8_gemv_kernel): the integer tensor instruction mma.m16n8k32 (s8 x s8 -> s32) on 16 rows of w and 8 tokens.  Where a lane's k lie in the
 // instruction does not matter as long as both operands agree, so a lane takes 16 consecutive k of its rows with one
 // 16-byte load straight from global memory and feeds them to two instructions.
 // A CTA takes 32 rows of w: two warps of 16 rows times four shares of k; a cluster of S CTAs shares k further where the
 // rows alone would leave SMs idle.  The shares' integer sums are added in shared memory, in any order the same.
+//
+// More tokens (q8_tc_kernel): this part multiplies integers at a tenth of its 16-bit floating-point rate, and an int8 is
+// exact in fp16, so the product runs on tcgen05 kind::f16 with fp32 accumulators.  Products are below 2^14 and the sums of
+// 1024 k at most 2^24: exact.  After each 1024 k the accumulator is added to fp32 sums in registers.
+//   A: 128 rows of w per CTA.  Their int8 comes by TMA; eight warps widen it and write it straight to tensor memory, so that
+//      of the two operands only the tokens cross shared memory a second time.
+//   B: the tokens as fp16, widened once before (launch_q8_widen, or the quantizer writes fp16 at once), by TMA.
+//   D: 128 lanes (rows of w) x TN columns (tokens).
+// Stages of 128 k.  Warp 0 loads, warp 1 issues the MMAs, warps 4..11 widen, and read the accumulator when a chunk of 1024 k
+// or a tile is complete: by then they have widened all but one of the stages ahead, so the MMAs wait for the reads alone.
+// PAIR: two CTAs work on 256 rows of w x 256 tokens (cta_group::2), each holding its 128 rows and half of the tokens: with
+// one CTA per tile a 128 x 256 tile needs 80 KB of shared memory traffic in the 512 cycles that 64 k compute, which is more
+// than it delivers; the pair 48.
+// Few tiles: a cluster of S CTAs shares a tile's k, and adds its fp32 sums through distributed shared memory in rank order.
+// Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is freed,
+// and the fault word tells.
+#include <cuda.h>
+#include <algorithm>
+#include <atomic>
+
 #include "uq_mx.cuh"
 
 namespace uq {
@@ -33,6 +53,12 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
     int v;
     asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.s32 %0, [r];\n\t}"
                  : "=r"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
 __device__ __forceinline__ void store_one(const Q8GemmArgs& a, long long at, float v) {
@@ -98,7 +124,645 @@ __global__ void __launch_bounds__(THREADS, 3) q8_gemv_kernel(const Q8GemmArgs a,
     }
 }
 
+
+// ------------------------------------------------------------------------------------------------
+// tcgen05
+
+constexpr unsigned int FAULT_Q8_WAIT = 32u;
+constexpr int TC_THREADS = 384;               // three warpgroups: producer and issuer, and two that widen
+constexpr int STAGE_K = 128, W_BYTES = 128 * STAGE_K;
+constexpr int CHUNK = 1024 / STAGE_K;           // stages whose sums are exact
+constexpr int HEAD = 1024;                      // barriers and flags before the stages
+constexpr int WIDE_WARPS = 8;
+
+struct TcArgs8 {
+    Q8GemmArgs g;
+    int steps;                                  // stages along K
+    int NT, MT;                                 // tiles along N and M
+    int S, group, ctas;
+    int wait;                                   // the kernel before on the stream may still run
+};
+
+#define UQ_ELECT "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e "
+#define UQ_OPERAND_HI "0x40004040"              // K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+// the same, counted on a barrier of the pair's even CTA
+__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile(UQ_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+template <bool PAIR> __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t on) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, " UQ_OPERAND_HI "};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(on) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, " UQ_OPERAND_HI "};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+                     :: "r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(on) : "memory");
+}
+// arrive on the barrier (PAIR: at this offset in both CTAs) when the MMAs issued so far are complete
+template <bool PAIR> __device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+                     :: "r"(bar) : "memory");
+    else
+        asm volatile(UQ_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+// An arrival, perhaps on the other CTA's barrier, that orders tensor memory alone (between the tcgen05 fences).  Relaxed: a
+// release at cluster scope waits for all of the thread's stores, the outputs of the tile before among them.
+__device__ __forceinline__ void arrive_relaxed(uint32_t mapped) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(mapped) : "memory");
+}
+// A whole warp's wait: false for all lanes once WAIT_LIMIT_NS have passed (the fault word then tells) or the CTA was told to
+// stop.  LOCAL: only this CTA arrives; CLUSTER: arrivals of the pair's other CTA count; TENSOR: the wait orders tensor memory
+// alone.
+enum { LOCAL, CLUSTER, TENSOR };
+template <int KIND> __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned int* fault, volatile int* stop_flag) {
+    unsigned long long t0 = 0;
+    for (unsigned int i = 0;; ++i) {
+        uint32_t ok;
+        if constexpr (KIND == TENSOR)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        else if constexpr (KIND == CLUSTER)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (i % 64 == 63) {
+            bool stop = *stop_flag != 0;
+            if (!t0) t0 = global_ns();
+            else if (global_ns() - t0 > WAIT_LIMIT_NS) {
+                atomicOr(fault, FAULT_Q8_WAIT);
+                stop = true;
+            }
+            if (__any_sync(0xffffffffu, stop)) return false;
+        }
+    }
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+                    "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+                    "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr) : "memory");
+}
+// four int8 -> two f16x2, exact: a byte with its sign bit turned over is the low byte of 1024 + 128 + v in fp16
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+__device__ __forceinline__ void after_prior_work(const TcArgs8& a) {
+    if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+// Writes 16 columns (tokens m0 .. m0 + count) of this lane's output nn; the warp's lanes hold 32 consecutive outputs.  16-bit
+// types with an even N: neighbouring lanes exchange every other value and store pairs of outputs.
+template <class T> __device__ __forceinline__ void put16(const Q8GemmArgs& a, int m0, int count, int nn, const float (&v)[16]) {
+    T* y = static_cast<T*>(a.y);
+    if constexpr (sizeof(T) == 2) {
+        if (!(a.N & 1)) {
+            const int odd = threadIdx.x & 1;
+            T* p = y + (long long)(m0 + odd) * a.N + (nn & ~1);
+            const long long step = 2ll * a.N;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2, p += step) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const uint32_t w = pack2(T(), odd ? got : v[j], odd ? v[j + 1] : got);
+                if (nn < a.N && j + odd < count) *reinterpret_cast<uint32_t*>(p) = w;
+            }
+            return;
+        }
+    }
+    T* p = y + (long long)m0 * a.N + nn;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, p += a.N)
+        if (nn < a.N && j < count) *p = from_f32<T>(v[j]);
+}
+
+struct Tile8 { int nt, m0, rows; };
+// Tiles are numbered in groups of a.group weight tiles, token tiles within a group, weight tiles fastest, so that CTAs
+// running at the same time share both operands in L2.
+template <int TN> __device__ __forceinline__ Tile8 find_tile(const TcArgs8& a, int tile) {
+    const unsigned per = a.group * a.MT, g = (unsigned)tile / per, in = tile - g * per;
+    const unsigned width = min(a.group, a.NT - (int)g * a.group);
+    const int tt = in / width;
+    return {(int)(g * a.group + in - tt * width), tt * TN, min(TN, a.g.M - tt * TN)};
+}
+
+// Rings and tensor memory of a tile shape.
+template <int TN, bool PAIR> struct Plan8 {
+    static constexpr int XR = PAIR ? TN / 2 : TN;                  // token rows of a CTA
+    static constexpr int X_BYTES = XR * STAGE_K * 2;
+    static constexpr int XS = TN >= 256 ? 5 : (TN == 128 ? 4 : 5); // stages of tokens, of weights, and widened ones
+    static constexpr int WS = TN >= 256 ? 3 : (TN == 128 ? 5 : (TN == 64 ? 8 : 10));
+    static constexpr int AS = (512 - TN) / 64 < 8 ? (512 - TN) / 64 : 8;
+    static constexpr int RING = WS * W_BYTES + XS * X_BYTES;
+    // The accumulator in two halves of columns whose chunks end half a chunk apart: while one is read the MMAs go on with
+    // the other, which in the two stages around the end of the chunk come in such an order that twice half a stage lies
+    // between (a 256 x 256 tile's 1024 k: 8200 cycles of MMAs, and about 1000 from their end to the next one's start).
+    static constexpr int HALVES = TN >= 128 ? 2 : 1;
+    static_assert(1024 + HEAD + RING <= 227 * 1024 && TN + 64 * AS <= 512, "memory");
+};
+enum { W_FULL = 0, W_EMPTY = 10, X_FULL = 20, X_EMPTY = 28, A_FULL = 36, A_EMPTY = 44, ACC_FULL = 52, ACC_EMPTY = 54, DRAINED = 56 };
+
+template <int TN, bool PAIR>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const TcArgs8 a) {
+    using P = Plan8<TN, PAIR>;
+    constexpr int XR = P::XR, XS = P::XS, WS = P::WS, AS = P::AS, HALVES = P::HALVES;
+    constexpr int COLS = TN / 2;                                   // accumulator columns of a reading warp
+    constexpr int BOX = PAIR ? XR / 2 : XR;                        // token rows of a TMA box
+    constexpr int ACROSS = PAIR ? CLUSTER : LOCAL;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* head = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(head);
+    const uint32_t bar0 = smem_u32(bars);
+    auto bar = [&](int which) { return bar0 + 8 * which; };
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + DRAINED + 1);
+    volatile int* stop = reinterpret_cast<volatile int*>(tmem_ptr + 1);
+    const uint32_t ring = smem_u32(head + HEAD), xring = ring + WS * W_BYTES;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR || a.S > 1 ? cluster_rank() : 0;
+    const bool lead = !PAIR || rank == 0;
+    unsigned int* fault = a.g.fault;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" :: "l"(&wmap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" :: "l"(&xmap) : "memory");
+            for (int i = 0; i < WS; ++i) {
+                mbar_init(bars + W_FULL + i, 1);
+                mbar_init(bars + W_EMPTY + i, WIDE_WARPS / 2);
+            }
+            for (int i = 0; i < XS; ++i) {
+                mbar_init(bars + X_FULL + i, 1);
+                mbar_init(bars + X_EMPTY + i, 1);
+            }
+            for (int i = 0; i < AS; ++i) {
+                mbar_init(bars + A_FULL + i, WIDE_WARPS / 2 * (PAIR ? 2 : 1));
+                mbar_init(bars + A_EMPTY + i, 1);
+            }
+            for (int i = 0; i < HALVES; ++i) {
+                mbar_init(bars + ACC_FULL + i, 1);
+                mbar_init(bars + ACC_EMPTY + i, WIDE_WARPS / HALVES * (PAIR ? 2 : 1));
+            }
+            mbar_init(bars + DRAINED, 1);
+            *stop = 0;
+            fence_barrier_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_ptr)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_ptr)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();                            // the other CTA's barriers are ready
+    fence_after();
+    const uint32_t tmem = (uint32_t)__shfl_sync(0xffffffffu, (int)*tmem_ptr, 0);
+    const uint32_t acol = tmem + TN;                               // widened stages, 64 columns each
+
+    // this CTA's tiles, and its k steps of them
+    const int tiles = a.NT * a.MT, width = PAIR ? 2 : a.S;         // CTAs of a tile
+    int k0 = 0, k1 = a.steps;
+    if (!PAIR && a.S > 1) {
+        k0 = (int)((long long)a.steps * rank / a.S);
+        k1 = (int)((long long)a.steps * (rank + 1) / a.S);
+    }
+    const int first = blockIdx.x / width, stride = gridDim.x / width;
+    // token columns of half h that the MMAs compute
+    auto columns = [&](const Tile8& t, int h) { return (min(max(t.rows - h * (TN / HALVES), 0), TN / HALVES) + 15) / 16 * 16; };
+    // whether a chunk of half h begins, or ends, with stage j of the tile
+    auto begins = [&](int j, int h) { return j == 0 || j % CHUNK == h * (CHUNK / 2); };
+    auto ends = [&](int j, int h) { return j == k1 - k0 - 1 || (j + 1) % CHUNK == h * (CHUNK / 2); };
+
+    // 128 sums a thread and the stage being widened take more than a third of the registers: 168 a thread at launch become
+    // 56 + 224 + 224 of the three warpgroups.
+    if (warp < 4) {
+        if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            // -------------------------------------------------------- weights
+            // They do not depend on the kernel before, so they are requested while it may still run.
+            int issued = 0, s = 0;
+            uint32_t ph = 1;                                       // the first round's stages count as free
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += stride) {
+                const int row = find_tile<TN>(a, tile).nt * (PAIR ? 256 : 128) + (PAIR ? (int)rank * 128 : 0);
+                for (int kt = k0; kt < k1; ++kt, ++issued) {
+                    if (issued >= WS && !warp_wait<LOCAL>(bar(W_EMPTY + s), ph, fault, stop)) { ok = false; break; }
+                    expect_bytes(bar(W_FULL + s), W_BYTES);
+                    tma_2d(ring + s * W_BYTES, &wmap, kt * STAGE_K, row, bar(W_FULL + s));
+                    if (++s == WS) { s = 0; ph ^= 1; }
+                }
+            }
+            if (!ok) *stop = 1;
+            // let the last copies land before the CTA can leave
+            for (int j = issued - 1; j >= 0 && j >= issued - WS; --j)
+                mbar_wait_bounded(bars + W_FULL + j % WS, (uint32_t)((j / WS) & 1), fault, FAULT_Q8_WAIT);
+        } else if (warp == 2) {
+            // -------------------------------------------------------- tokens, which do
+            after_prior_work(a);
+            int issued = 0, s = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            const uint32_t lead_full = PAIR ? cluster_addr(bar(X_FULL), 0) : bar(X_FULL);
+            for (int tile = first; ok && tile < tiles; tile += stride) {
+                const Tile8 t = find_tile<TN>(a, tile);
+                for (int kt = k0; kt < k1; ++kt, ++issued) {
+                    if (issued >= XS && !warp_wait<ACROSS>(bar(X_EMPTY + s), ph, fault, stop)) { ok = false; break; }
+                    if (lead) expect_bytes(bar(X_FULL + s), P::X_BYTES * (PAIR ? 2 : 1));
+                    const uint32_t dst = xring + s * P::X_BYTES;
+                    // [64 k][rows], of a pair the CTA's half of the rows of each half of the columns
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if constexpr (PAIR) {
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h)
+                                pair_tma_2d(dst + (j * 2 + h) * (BOX * 128), &xmap, kt * STAGE_K + j * 64,
+                                            t.m0 + h * (TN / 2) + (int)rank * (columns(t, h) >> 1), lead_full + s * 8);
+                        } else {
+                            tma_2d(dst + j * (XR * 128), &xmap, kt * STAGE_K + j * 64, t.m0, bar(X_FULL + s));
+                        }
+                    }
+                    if (++s == XS) { s = 0; ph ^= 1; }
+                }
+            }
+            if (!ok) *stop = 1;
+            // (both CTAs' tokens are counted on the even one's barriers, and the CTAs leave together)
+            if (lead)
+                for (int j = issued - 1; j >= 0 && j >= issued - XS; --j)
+                    mbar_wait_bounded(bars + X_FULL + j % XS, (uint32_t)((j / XS) & 1), fault, FAULT_Q8_WAIT);
+        } else if (warp == 1 && lead) {
+            // -------------------------------------------------------- MMA issue (PAIR: for both CTAs)
+            int xs = 0, as = 0;
+            uint32_t used = 0, eph = 3;                            // bit h: half h has had a chunk; parity of its next read
+            uint32_t xph = 0, aph = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += stride) {
+                const Tile8 t = find_tile<TN>(a, tile);
+                // D fp32, A and B fp16, both K-major, M = 128 or 256, N = the half's columns
+                const uint32_t base = (1u << 4) | ((PAIR ? 16u : 8u) << 24);
+                uint32_t idesc[HALVES];
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) idesc[h] = base | ((uint32_t)(columns(t, h) >> 3) << 17);
+                for (int j = 0; ok && j < k1 - k0; ++j) {
+                    if (!warp_wait<ACROSS>(bar(X_FULL + xs), xph, fault, stop) || !warp_wait<TENSOR>(bar(A_FULL + as), aph, fault, stop)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t b = desc_lo(xring + xs * P::X_BYTES), ac = acol + as * 64;
+                    // the half whose chunk has just ended comes last, one whose chunk ends now first
+                    const int swap = HALVES == 2 && ((j && begins(j, 0)) || (ends(j, 1) && !ends(j, 0)));
+#pragma unroll
+                    for (int o = 0; o < HALVES; ++o) {
+                        const int h = HALVES == 2 ? o ^ swap : 0;
+                        if (begins(j, h)) {
+                            // the half's chunk before has been read
+                            eph ^= (used >> h & 1u) << h;
+                            if ((used >> h & 1u) && !warp_wait<TENSOR>(bar(ACC_EMPTY + h), eph >> h & 1u, fault, stop)) {
+                                ok = false;
+                                break;
+                            }
+                            used |= 1u << h;
+                            fence_after();
+                        }
+                        const uint32_t id = h ? idesc[HALVES - 1] : idesc[0], d = tmem + h * (TN / 2);
+                        // the half's rows of the first 64 k; the second 64 k follow all rows of the first
+                        const uint32_t bh = b + h * (PAIR ? BOX * 8 : XR * 4);
+                        const uint32_t more = begins(j, h) ? 0u : 1u;
+                        if (id >> 17 & 63u) {
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) mma<PAIR>(d, ac + m * 8, bh + (m >> 2) * (XR * 8) + (m & 3) * 2, id, more | m);
+                        }
+                        if (ends(j, h)) commit<PAIR>(bar(ACC_FULL + h));
+                    }
+                    commit<PAIR>(bar(X_EMPTY + xs));
+                    commit<PAIR>(bar(A_EMPTY + as));
+                    if (++xs == XS) { xs = 0; xph ^= 1; }
+                    if (++as == AS) { as = 0; aph ^= 1; }
+                }
+            }
+            if (!ok) {
+                *stop = 1;
+                __syncwarp();
+                commit<PAIR>(bar(DRAINED));
+                mbar_wait_bounded(bars + DRAINED, 0, fault, FAULT_Q8_WAIT);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ widening, and the accumulator: lane = row of w
+        if constexpr (TN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int q = warp & 3, half = (warp - 4) >> 2, row = q * 32 + lane;
+        const int which = HALVES == 2 ? half : 0;                  // the chunks that this warp's columns belong to
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const uint32_t lead_a_full = PAIR ? cluster_addr(bar(A_FULL), 0) : bar(A_FULL);
+        const uint32_t lead_acc_empty = PAIR ? cluster_addr(bar(ACC_EMPTY + which), 0) : bar(ACC_EMPTY + which);
+        float sums[COLS];
+        int ws = 0, as = 0, i = 0, read = 0, boundary = 0;
+        uint32_t wph = 0, aph = 1;
+        bool pending = false, waited = false, ok = true, fresh = true, last = false;
+        Tile8 pt = {};
+        // reads a complete chunk; behind a tile's last one the outputs are written
+        auto read_chunk = [&] {
+            pending = false;
+            if (!warp_wait<TENSOR>(bar(ACC_FULL + which), (uint32_t)read & 1, fault, stop)) { ok = false; return; }
+            ++read;
+            fence_after();
+#pragma unroll
+            for (int c = 0; c < COLS; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + lanes + half * COLS + c, r);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sums[c + j] = fresh ? __uint_as_float(r[j]) : sums[c + j] + __uint_as_float(r[j]);
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_relaxed(lead_acc_empty);
+            fresh = last;
+            if (!last) return;
+            if (!waited) {
+                after_prior_work(a);                               // the scales may be its output, and y its input
+                waited = true;
+            }
+            if (!PAIR && a.S > 1) return;
+            const int nn = pt.nt * (PAIR ? 256 : 128) + (PAIR ? (int)rank * 128 : 0) + row;
+            const float sw = nn < a.g.N ? __ldg(a.g.sw + nn) : 0.f;
+#pragma unroll
+            for (int c = 0; c < COLS; c += 16) {
+                const int m = half * COLS + c;                     // token of the tile
+                if (m >= pt.rows) break;
+                const float mine = ld_written(a.g.sx + min(pt.m0 + m + (lane & 15), a.g.M - 1));
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = sums[c + j] * __shfl_sync(0xffffffffu, mine, j) * sw;
+                if (a.g.ytype == UQ_BF16) put16<__nv_bfloat16>(a.g, pt.m0 + m, pt.rows - m, nn, v);
+                else if (a.g.ytype == UQ_FP16) put16<__half>(a.g, pt.m0 + m, pt.rows - m, nn, v);
+                else put16<float>(a.g, pt.m0 + m, pt.rows - m, nn, v);
+            }
+        };
+        for (int tile = first; ok && tile < tiles; tile += stride) {
+            const Tile8 t = find_tile<TN>(a, tile);
+            for (int j = 0; ok && j < k1 - k0; ++j, ++i) {
+                if (pending && i - boundary >= AS - 1) read_chunk();
+                if (!ok) break;
+                // the two groups of four warps take the stages in turn, so that one's loads run under the other's stores
+                if ((i & 1) == half) {
+                    if (!warp_wait<LOCAL>(bar(W_FULL + ws), wph, fault, stop)) { ok = false; break; }
+                    // this row's 128 k, in the swizzled tile
+                    const uint32_t base = ring + ws * W_BYTES + row * 128;
+                    uint4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                                     : "r"(base + ((c ^ (row & 7)) << 4)));
+                    // the MMAs that read these columns before are complete
+                    if (i >= AS && !warp_wait<TENSOR>(bar(A_EMPTY + as), aph, fault, stop)) { ok = false; break; }
+                    fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            widen4(v[4 * h + c].x, r[8 * c], r[8 * c + 1]);
+                            widen4(v[4 * h + c].y, r[8 * c + 2], r[8 * c + 3]);
+                            widen4(v[4 * h + c].z, r[8 * c + 4], r[8 * c + 5]);
+                            widen4(v[4 * h + c].w, r[8 * c + 6], r[8 * c + 7]);
+                        }
+                        tmem_st32(acol + lanes + as * 64 + h * 32, r);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(W_EMPTY + ws));
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_relaxed(lead_a_full + as * 8);
+                }
+                if (ends(j, which)) {
+                    if (pending) read_chunk();
+                    pending = true;
+                    boundary = i + 1;
+                    last = j == k1 - k0 - 1;
+                    pt = t;
+                }
+                if (++ws == WS) { ws = 0; wph ^= 1; }
+                if (++as == AS) { as = 0; aph ^= 1; }
+            }
+        }
+        if (ok && pending) read_chunk();
+        if (!ok) *stop = 1;
+        if (!PAIR && a.S > 1) {
+            // when all warps are done with the ring the sums are left there, [token][row]
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            float* left = reinterpret_cast<float*>(head + HEAD);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+                if (half * COLS + c < pt.rows) left[(half * COLS + c) * 128 + row] = sums[c];
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();                            // both CTAs are done with each other's memory
+    fence_after();
+    if (warp == 1) {
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    }
+    if (!PAIR && a.S > 1) {
+        cluster_sync();
+        if (first < tiles) {
+            after_prior_work(a);
+            const Tile8 t = find_tile<TN>(a, first);
+            // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
+            for (int it = (int)rank * TC_THREADS + threadIdx.x; it < t.rows * 32; it += a.S * TC_THREADS) {
+                const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
+                if (nn >= a.g.N) continue;
+                float4 p[MAX_SPLIT];
+#pragma unroll
+                for (int k = 0; k < MAX_SPLIT; ++k)
+                    p[k] = k < a.S ? ld_cluster4(ring + (c * 128 + r) * 4, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float v[4] = {};
+#pragma unroll
+                for (int k = 0; k < MAX_SPLIT; ++k) {
+                    v[0] += p[k].x; v[1] += p[k].y; v[2] += p[k].z; v[3] += p[k].w;
+                }
+                const float sx = ld_written(a.g.sx + t.m0 + c);
+                const long long at = (long long)(t.m0 + c) * a.g.N + nn;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (nn + j < a.g.N) store_one(a.g, at + j, v[j] * sx * __ldg(a.g.sw + nn + j));
+            }
+        }
+        cluster_sync();
+    }
+}
+
+// int8 codes -> fp16, 16 a thread; the product that follows may start meanwhile
+__global__ void __launch_bounds__(256) q8_widen_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, long long n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+        const uint4 v = x[i];
+        uint4 lo, hi;
+        widen4(v.x, lo.x, lo.y);
+        widen4(v.y, lo.z, lo.w);
+        widen4(v.z, hi.x, hi.y);
+        widen4(v.w, hi.z, hi.w);
+        out[2 * i] = lo;
+        out[2 * i + 1] = hi;
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static std::atomic<EncodeTiledFn> known{nullptr};
+    EncodeTiledFn fn = known.load(std::memory_order_relaxed);
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess && q == cudaDriverEntryPointSuccess)
+            known.store(fn = reinterpret_cast<EncodeTiledFn>(p), std::memory_order_relaxed);
+    }
+    return fn;
+}
+// rows of `cols` elements of `size` bytes, boxes of 128 bytes x `box` rows, 128-byte swizzle, zeros beyond the ends
+bool rows_map(CUtensorMap* m, const void* p, long long rows, int cols, int size, int box) {
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * size};
+    cuuint32_t b[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box};
+    cuuint32_t es[2] = {1, 1};
+    return encode_fn()(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dims,
+                       strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
+using Done = std::atomic<bool>[64];
+template <class K> cudaError_t configure(K kernel, Done& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+template <int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, int sms, cudaStream_t st) {
+    static Done ready = {};
+    cudaError_t e = configure(q8_tc_kernel<TN, PAIR>, ready);
+    if (e != cudaSuccess) return e;
+    using P = Plan8<TN, PAIR>;
+    const int wide = PAIR ? 256 : 128;
+    a.steps = (a.g.K + STAGE_K - 1) / STAGE_K;
+    a.NT = (a.g.N + wide - 1) / wide;
+    a.MT = (a.g.M + TN - 1) / TN;
+    a.group = 8;
+    const long long tiles = (long long)a.NT * a.MT;
+    a.S = 1;
+    if (!PAIR)
+        while (a.S < MAX_SPLIT && tiles * a.S * 2 <= sms && a.steps >= a.S * 4) a.S *= 2;
+    const int width = PAIR ? 2 : a.S;
+    a.ctas = (int)std::min(tiles * width, (long long)(sms / width * width));
+    if (a.S > 1) a.ctas = (int)tiles * a.S;
+    CUtensorMap wmap, xmap;
+    if (!rows_map(&wmap, a.g.w, a.g.N, a.g.K, 1, 128) || !rows_map(&xmap, x16, a.g.M, a.g.K, 2, PAIR ? P::XR / 2 : P::XR)) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.ctas);
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = 1024 + HEAD + P::RING;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (width > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = width;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (a.wait) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, q8_tc_kernel<TN, PAIR>, wmap, xmap, a);
+}
+
 }  // namespace
+
+bool q8_gemm_wide(int M) { return M > TOKENS; }
+
+cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st) {
+    const long long n = (long long)M * K / 16, ctas = (n + 255) / 256;
+    q8_widen_kernel<<<(unsigned)std::min(ctas, 16LL * sms), 256, 0, st>>>(reinterpret_cast<const uint4*>(x), static_cast<uint4*>(x16), n);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& g, const void* x16, int sms, cudaStream_t st) {
+    if (!encode_fn()) return cudaErrorNotSupported;
+    TcArgs8 a = {};
+    a.g = g;
+    a.wait = 1;
+    if (g.M <= 32) return launch_tc<32, false>(a, x16, sms, st);
+    if (g.M <= 64) return launch_tc<64, false>(a, x16, sms, st);
+    if (g.M <= 128) return launch_tc<128, false>(a, x16, sms, st);
+    if ((long long)((g.N + 255) / 256) * ((g.M + 255) / 256) * 2 < sms) return launch_tc<128, false>(a, x16, sms, st);
+    return launch_tc<256, true>(a, x16, sms, st);
+}
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, int sms, cudaStream_t st) {
     const long long tiles = (long long)((a.N + ROWS - 1) / ROWS) * ((a.M + TOKENS - 1) / TOKENS);

@@ -351,7 +351,7 @@ uq_status uq_gemm_kernel_count(int M, int N, int K, int group, uq_fmt fmt, int* 
  * tensor-core kernel's bounded wait ran out and the kernel returned early instead of hanging;
  * its output is then unspecified; bit 2: a GEMV launch was given a work split larger than the
  * kernel holds and computed nothing; bit 3: uq_rmsnorm_rope met a position outside its table; bit 4: a
- * microscaled product's bounded wait ran out).  Synchronizes the device; allocates nothing.
+ * microscaled product's, bit 5: an 8-bit product's bounded wait ran out).  Synchronizes the device; allocates nothing.
  * *flag = 0 when no fault.
  */
 uq_status uq_device_fault(unsigned int* flag);

@@ -145,3 +145,19 @@ def test_streams_and_graphs():
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert uq.device_fault() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(2560, 2048, 128), (2500, 2100, 1184), (2305, 2304, 2048), (2560, 2304, 4112), (4100, 1300, 640)])
+def test_pairs_of_ctas(M, N, K):
+    """Enough tiles of 256 x 256 for a pair of CTAs on every two SMs, ragged ends, chunks of all lengths; against integer sums
+    in 64 bits on the device."""
+    for kind in ("random", "largest"):
+        x, w = _operand(1, M, K, kind), _operand(2, N, K)
+        y = uq.gemm_w8a8(x, w, dtype=torch.float32)
+        a, b = x[0].double() * x[1].double()[:, None], w[0].double() * w[1].double()[:, None]
+        mag = sum((a[:, k:k + 1024] @ b[:, k:k + 1024].t()).abs() for k in range(0, K, 1024))
+        bad = (y.double() - a @ b.t()).abs() > (K / 1024 + 4) * U * mag + 2.0 ** -149 + (a.abs() @ b.abs().t()) * 2.0 ** -50
+        assert not bool(bad.any()), f"{int(bad.sum())} outputs off, first at {bad.nonzero()[0].tolist()}"
+        y16 = uq.gemm_w8a8(x, w)
+        assert torch.equal(y16, y.bfloat16())
+    assert uq.device_fault() == 0
