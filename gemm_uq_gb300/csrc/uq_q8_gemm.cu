@@ -61,6 +61,20 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
+// up to four neighbouring outputs (count of them) at element `at`
+template <class T> __device__ __forceinline__ void store4(const Q8GemmArgs& a, long long at, int count, const float (&v)[4]) {
+    T* y = static_cast<T*>(a.y) + at;
+    if (count >= 4 && a.N % 4 == 0) {
+        Vec<T, 4> o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.v[i] = from_f32<T>(v[i]);
+        *reinterpret_cast<Vec<T, 4>*>(y) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) y[i] = from_f32<T>(v[i]);
+    }
+}
 __device__ __forceinline__ void store_one(const Q8GemmArgs& a, long long at, float v) {
     if (a.ytype == UQ_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
     else if (a.ytype == UQ_FP16) static_cast<__half*>(a.y)[at] = __float2half_rn(v);
@@ -223,13 +237,11 @@ template <int KIND> __device__ __forceinline__ bool warp_wait(uint32_t bar, uint
         }
     }
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16};"
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-                    "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-                    "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -258,27 +270,31 @@ __device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
     return d;
 }
 // Writes 16 columns (tokens m0 .. m0 + count) of this lane's output nn; the warp's lanes hold 32 consecutive outputs.  16-bit
-// types with an even N: neighbouring lanes exchange every other value and store pairs of outputs.
+// types: neighbouring lanes exchange every other value and hold pairs of outputs, stored together where N is even.
 template <class T> __device__ __forceinline__ void put16(const Q8GemmArgs& a, int m0, int count, int nn, const float (&v)[16]) {
-    T* y = static_cast<T*>(a.y);
     if constexpr (sizeof(T) == 2) {
-        if (!(a.N & 1)) {
-            const int odd = threadIdx.x & 1;
-            T* p = y + (long long)(m0 + odd) * a.N + (nn & ~1);
-            const long long step = 2ll * a.N;
+        const int odd = threadIdx.x & 1, n = nn & ~1;
+        T* p = static_cast<T*>(a.y) + (long long)(m0 + odd) * a.N + n;
+        const long long step = 2ll * a.N;
+        const bool even = !(a.N & 1);
 #pragma unroll
-            for (int j = 0; j < 16; j += 2, p += step) {
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-                const uint32_t w = pack2(T(), odd ? got : v[j], odd ? v[j + 1] : got);
-                if (nn < a.N && j + odd < count) *reinterpret_cast<uint32_t*>(p) = w;
+        for (int j = 0; j < 16; j += 2, p += step) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = pack2(T(), odd ? got : v[j], odd ? v[j + 1] : got);
+            if (j + odd >= count) continue;
+            if (even) {
+                if (n < a.N) *reinterpret_cast<uint32_t*>(p) = w;
+            } else {
+                if (n < a.N) reinterpret_cast<uint16_t*>(p)[0] = (uint16_t)w;
+                if (n + 1 < a.N) reinterpret_cast<uint16_t*>(p)[1] = (uint16_t)(w >> 16);
             }
-            return;
         }
-    }
-    T* p = y + (long long)m0 * a.N + nn;
+    } else {
+        T* p = static_cast<T*>(a.y) + (long long)m0 * a.N + nn;
 #pragma unroll
-    for (int j = 0; j < 16; ++j, p += a.N)
-        if (nn < a.N && j < count) *p = from_f32<T>(v[j]);
+        for (int j = 0; j < 16; ++j, p += a.N)
+            if (nn < a.N && j < count) *p = v[j];
+    }
 }
 
 struct Tile8 { int nt, m0, rows; };
@@ -299,15 +315,16 @@ template <int TN, bool PAIR> struct Plan8 {
     static constexpr int WS = TN >= 256 ? 3 : (TN == 128 ? 5 : (TN == 64 ? 8 : 10));
     static constexpr int AS = (512 - TN) / 64 < 8 ? (512 - TN) / 64 : 8;
     static constexpr int RING = WS * W_BYTES + XS * X_BYTES;
-    // The accumulator in two halves of columns whose chunks end half a chunk apart: while one is read the MMAs go on with
-    // the other, which in the two stages around the end of the chunk come in such an order that twice half a stage lies
-    // between (a 256 x 256 tile's 1024 k: 8200 cycles of MMAs, and about 1000 from their end to the next one's start).
-    static constexpr int HALVES = TN >= 128 ? 2 : 1;
+    // Pairs have the accumulator in two halves of columns whose chunks end half a chunk apart: while one is read the MMAs go
+    // on with the other, which in the two stages around the end of the chunk come in such an order that twice half a stage
+    // lies between (a 256 x 256 tile's 1024 k: 8200 cycles of MMAs, and about 1000 from their end to the next one's start).
+    // Not so a CTA alone: an MMA with A in tensor memory takes 60 cycles however few columns it has.
+    static constexpr int HALVES = PAIR ? 2 : 1;
     static_assert(1024 + HEAD + RING <= 227 * 1024 && TN + 64 * AS <= 512, "memory");
 };
 enum { W_FULL = 0, W_EMPTY = 10, X_FULL = 20, X_EMPTY = 28, A_FULL = 36, A_EMPTY = 44, ACC_FULL = 52, ACC_EMPTY = 54, DRAINED = 56 };
 
-template <int TN, bool PAIR>
+template <class T, int TN, bool PAIR>
 __global__ void __launch_bounds__(TC_THREADS, 1)
 q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const TcArgs8 a) {
     using P = Plan8<TN, PAIR>;
@@ -325,7 +342,9 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     const uint32_t ring = smem_u32(head + HEAD), xring = ring + WS * W_BYTES;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR || a.S > 1 ? cluster_rank() : 0;
-    const bool lead = !PAIR || rank == 0;
+    const uint32_t side = PAIR ? rank : 0;                         // which CTA of the pair
+    const int share = PAIR ? 0 : (int)rank;                        // which of the S shares of k
+    const bool lead = side == 0;
     unsigned int* fault = a.g.fault;
 
     if (warp == 0) {
@@ -372,11 +391,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 
     // this CTA's tiles, and its k steps of them
     const int tiles = a.NT * a.MT, width = PAIR ? 2 : a.S;         // CTAs of a tile
-    int k0 = 0, k1 = a.steps;
-    if (!PAIR && a.S > 1) {
-        k0 = (int)((long long)a.steps * rank / a.S);
-        k1 = (int)((long long)a.steps * (rank + 1) / a.S);
-    }
+    const int k0 = (int)((long long)a.steps * share / a.S), k1 = (int)((long long)a.steps * (share + 1) / a.S);
     const int first = blockIdx.x / width, stride = gridDim.x / width;
     // token columns of half h that the MMAs compute
     auto columns = [&](const Tile8& t, int h) { return (min(max(t.rows - h * (TN / HALVES), 0), TN / HALVES) + 15) / 16 * 16; };
@@ -395,7 +410,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             uint32_t ph = 1;                                       // the first round's stages count as free
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += stride) {
-                const int row = find_tile<TN>(a, tile).nt * (PAIR ? 256 : 128) + (PAIR ? (int)rank * 128 : 0);
+                const int row = find_tile<TN>(a, tile).nt * (PAIR ? 256 : 128) + (int)side * 128;
                 for (int kt = k0; kt < k1; ++kt, ++issued) {
                     if (issued >= WS && !warp_wait<LOCAL>(bar(W_EMPTY + s), ph, fault, stop)) { ok = false; break; }
                     expect_bytes(bar(W_FULL + s), W_BYTES);
@@ -427,7 +442,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
                                 pair_tma_2d(dst + (j * 2 + h) * (BOX * 128), &xmap, kt * STAGE_K + j * 64,
-                                            t.m0 + h * (TN / 2) + (int)rank * (columns(t, h) >> 1), lead_full + s * 8);
+                                            t.m0 + h * (TN / 2) + (int)side * (columns(t, h) >> 1), lead_full + s * 8);
                         } else {
                             tma_2d(dst + j * (XR * 128), &xmap, kt * STAGE_K + j * 64, t.m0, bar(X_FULL + s));
                         }
@@ -506,99 +521,122 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const uint32_t lead_a_full = PAIR ? cluster_addr(bar(A_FULL), 0) : bar(A_FULL);
         const uint32_t lead_acc_empty = PAIR ? cluster_addr(bar(ACC_EMPTY + which), 0) : bar(ACC_EMPTY + which);
-        float sums[COLS];
+        float sums[COLS] = {};
         int ws = 0, as = 0, i = 0, read = 0, boundary = 0;
         uint32_t wph = 0, aph = 1;
-        bool pending = false, waited = false, ok = true, fresh = true, last = false;
-        Tile8 pt = {};
-        // reads a complete chunk; behind a tile's last one the outputs are written
-        auto read_chunk = [&] {
-            pending = false;
-            if (!warp_wait<TENSOR>(bar(ACC_FULL + which), (uint32_t)read & 1, fault, stop)) { ok = false; return; }
-            ++read;
-            fence_after();
+        bool pending = false, ok = true, fresh = true, last = false, widened = false;
+        Tile8 t = find_tile<TN>(a, first), pt = t, ot = t;         // tile of the stage, of the chunk to be read, of the outputs
+        // A finished tile's outputs are written behind the next tile's stages, 32 columns at a time: all at once they would hold
+        // up the widening for longer than there are stages ahead.  This code is in the loop once, and for one type: it is
+        // executed once a tile, so what it takes is its fetching (a 256 x 256 tile's epilogue, for three types in four places:
+        // 18000 cycles).
+        constexpr int GROUPS = COLS / 16;
+        int written = GROUPS;
+        float sx[(COLS + 31) / 32], sw = 0.f;                      // scales of tokens 32 i + lane, and of this lane's output
+        auto write_groups = [&](int to) {
+            const int nn = ot.nt * (PAIR ? 256 : 128) + (int)side * 128 + row;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + lanes + half * COLS + c, r);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sums[c + j] = fresh ? __uint_as_float(r[j]) : sums[c + j] + __uint_as_float(r[j]);
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_relaxed(lead_acc_empty);
-            fresh = last;
-            if (!last) return;
-            if (!waited) {
-                after_prior_work(a);                               // the scales may be its output, and y its input
-                waited = true;
-            }
-            if (!PAIR && a.S > 1) return;
-            const int nn = pt.nt * (PAIR ? 256 : 128) + (PAIR ? (int)rank * 128 : 0) + row;
-            const float sw = nn < a.g.N ? __ldg(a.g.sw + nn) : 0.f;
-#pragma unroll
-            for (int c = 0; c < COLS; c += 16) {
-                const int m = half * COLS + c;                     // token of the tile
-                if (m >= pt.rows) break;
-                const float mine = ld_written(a.g.sx + min(pt.m0 + m + (lane & 15), a.g.M - 1));
+            for (int g = 0; g < GROUPS; ++g) {
+                const int m = half * COLS + 16 * g;                // token of the tile
+                if (g < written || g >= to || m >= ot.rows) continue;
                 float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = sums[c + j] * __shfl_sync(0xffffffffu, mine, j) * sw;
-                if (a.g.ytype == UQ_BF16) put16<__nv_bfloat16>(a.g, pt.m0 + m, pt.rows - m, nn, v);
-                else if (a.g.ytype == UQ_FP16) put16<__half>(a.g, pt.m0 + m, pt.rows - m, nn, v);
-                else put16<float>(a.g, pt.m0 + m, pt.rows - m, nn, v);
+                for (int c = 0; c < 16; ++c) v[c] = sums[16 * g + c] * __shfl_sync(0xffffffffu, sx[g / 2], (16 * g + c) & 31) * sw;
+                put16<T>(a.g, ot.m0 + m, ot.rows - m, nn, v);
             }
+            written = min(to, GROUPS);
         };
-        for (int tile = first; ok && tile < tiles; tile += stride) {
-            const Tile8 t = find_tile<TN>(a, tile);
-            for (int j = 0; ok && j < k1 - k0; ++j, ++i) {
-                if (pending && i - boundary >= AS - 1) read_chunk();
-                if (!ok) break;
-                // the two groups of four warps take the stages in turn, so that one's loads run under the other's stores
-                if ((i & 1) == half) {
-                    if (!warp_wait<LOCAL>(bar(W_FULL + ws), wph, fault, stop)) { ok = false; break; }
-                    // this row's 128 k, in the swizzled tile
-                    const uint32_t base = ring + ws * W_BYTES + row * 128;
-                    uint4 v[8];
+        for (int tile = first, j = 0; ok;) {
+            const bool over = tile >= tiles;
+            // a complete chunk is read when the stages ahead are widened, or another one ends
+            const bool reads = pending && (over || i - boundary >= AS - 1 || ends(j, which));
+            if (written < GROUPS && (reads || over || widened)) write_groups(reads || over ? GROUPS : written + 2);
+            widened = false;
+            if (reads) {
+                pending = false;
+                if (!warp_wait<TENSOR>(bar(ACC_FULL + which), (uint32_t)read & 1, fault, stop)) { ok = false; break; }
+                ++read;
+                fence_after();
+                // sums = (a tile's first chunk ? 0 : sums) + chunk, in place: as an expression the sums took twice the registers
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                                     : "r"(base + ((c ^ (row & 7)) << 4)));
-                    // the MMAs that read these columns before are complete
-                    if (i >= AS && !warp_wait<TENSOR>(bar(A_EMPTY + as), aph, fault, stop)) { ok = false; break; }
-                    fence_after();
+                for (int c = 0; c < COLS; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lanes + half * COLS + c, r);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
+                    for (int e = 0; e < 16; ++e) asm volatile("{\n\t.reg .pred p;\n\t.reg .f32 t;\n\tsetp.ne.b32 p, %2, 0;\n\tselp.f32 t, 0f00000000, %0, p;\n\tadd.f32 %0, t, %1;\n\t}"
+                                     : "+f"(sums[c + e]) : "f"(__uint_as_float(r[e])), "r"((int)fresh));
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_relaxed(lead_acc_empty);
+                fresh = last;
+                if (last && (PAIR || a.S == 1)) {
+                    after_prior_work(a);                           // the scales may be its output, and y its input
+                    ot = pt;
+                    written = 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            widen4(v[4 * h + c].x, r[8 * c], r[8 * c + 1]);
-                            widen4(v[4 * h + c].y, r[8 * c + 2], r[8 * c + 3]);
-                            widen4(v[4 * h + c].z, r[8 * c + 4], r[8 * c + 5]);
-                            widen4(v[4 * h + c].w, r[8 * c + 6], r[8 * c + 7]);
-                        }
-                        tmem_st32(acol + lanes + as * 64 + h * 32, r);
+                    for (int c = 0; c < COLS; c += 32) sx[c / 32] = ld_written(a.g.sx + min(ot.m0 + half * COLS + c + lane, a.g.M - 1));
+                    sw = __ldg(a.g.sw + min(ot.nt * (PAIR ? 256 : 128) + (int)side * 128 + row, a.g.N - 1));
+                }
+            }
+            if (over) {
+                if (written == GROUPS) break;
+                continue;
+            }
+            // the two groups of four warps take the stages in turn, so that one's loads run under the other's stores
+            if ((i & 1) == half) {
+                if (!warp_wait<LOCAL>(bar(W_FULL + ws), wph, fault, stop)) { ok = false; break; }
+                // this row's 128 k, in the swizzled tile: 32 at a time, the next 32 on their way
+                const uint32_t base = ring + ws * W_BYTES + row * 128;
+                uint4 v[2][2];
+                auto load = [&](uint4 (&to)[2], int from) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(to[c].x), "=r"(to[c].y), "=r"(to[c].z), "=r"(to[c].w)
+                                     : "r"(base + (((from + c) ^ (row & 7)) << 4)));
+                };
+                load(v[0], 0);
+                // the MMAs that read these columns before are complete
+                if (i >= AS && !warp_wait<TENSOR>(bar(A_EMPTY + as), aph, fault, stop)) { ok = false; break; }
+                fence_after();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t r[16];
+                    if (h < 3) load(v[(h + 1) & 1], 2 * h + 2);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint4 u = v[h & 1][c];
+                        widen4(u.x, r[8 * c], r[8 * c + 1]);
+                        widen4(u.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4(u.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4(u.w, r[8 * c + 6], r[8 * c + 7]);
                     }
-                    __syncwarp();
-                    if (lane == 0) arrive(bar(W_EMPTY + ws));
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_relaxed(lead_a_full + as * 8);
+                    tmem_st16(acol + lanes + as * 64 + h * 16, r);
                 }
-                if (ends(j, which)) {
-                    if (pending) read_chunk();
-                    pending = true;
-                    boundary = i + 1;
-                    last = j == k1 - k0 - 1;
-                    pt = t;
-                }
-                if (++ws == WS) { ws = 0; wph ^= 1; }
-                if (++as == AS) { as = 0; aph ^= 1; }
+                __syncwarp();
+                if (lane == 0) arrive(bar(W_EMPTY + ws));
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_relaxed(lead_a_full + as * 8);
+                widened = true;
+            }
+            if (ends(j, which)) {
+                pending = true;
+                boundary = i + 1;
+                last = j == k1 - k0 - 1;
+                pt = t;
+            }
+            if (++ws == WS) { ws = 0; wph ^= 1; }
+            if (++as == AS) { as = 0; aph ^= 1; }
+            ++i;
+            if (++j == k1 - k0) {
+                j = 0;
+                tile += stride;
+                if (tile < tiles) t = find_tile<TN>(a, tile);
             }
         }
-        if (ok && pending) read_chunk();
         if (!ok) *stop = 1;
         if (!PAIR && a.S > 1) {
             // when all warps are done with the ring the sums are left there, [token][row]
@@ -611,39 +649,51 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     }
     __syncwarp();
     fence_before();
+    // (split tiles) this thread's four neighbouring outputs, and their scales
+    const Tile8 t = find_tile<TN>(a, first);
+    const int r = (threadIdx.x & 31) * 4, nn = t.nt * 128 + r;
+    float sw4[4] = {};
+    if (!PAIR && a.S > 1) {
+        after_prior_work(a);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sw4[j] = __ldg(a.g.sw + min(nn + j, a.g.N - 1));
+    }
     __syncthreads();
-    if constexpr (PAIR) cluster_sync();                            // both CTAs are done with each other's memory
+    if (PAIR || a.S > 1) cluster_sync();                           // the pair is done with each other's memory; the sums are there
     fence_after();
     if (warp == 1) {
         if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
         else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
     }
     if (!PAIR && a.S > 1) {
-        cluster_sync();
-        if (first < tiles) {
-            after_prior_work(a);
-            const Tile8 t = find_tile<TN>(a, first);
-            // a thread takes four neighbouring outputs of a token; the CTAs' sums are all requested before they are added
-            for (int it = (int)rank * TC_THREADS + threadIdx.x; it < t.rows * 32; it += a.S * TC_THREADS) {
-                const int c = it >> 5, r = (it & 31) * 4, nn = t.nt * 128 + r;
-                if (nn >= a.g.N) continue;
-                float4 p[MAX_SPLIT];
+        // A thread takes four neighbouring outputs of two tokens at a time; the CTAs' sums of both are requested before they are
+        // added.
+        for (int it = share * TC_THREADS + threadIdx.x; it < t.rows * 32; it += 2 * a.S * TC_THREADS) {
+            float4 p[2][MAX_SPLIT];
+            float sx[2];
+            int c[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                c[i] = min((it >> 5) + i * a.S * (TC_THREADS / 32), t.rows - 1);
 #pragma unroll
                 for (int k = 0; k < MAX_SPLIT; ++k)
-                    p[k] = k < a.S ? ld_cluster4(ring + (c * 128 + r) * 4, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    p[i][k] = k < a.S ? ld_cluster4(ring + (c[i] * 128 + r) * 4, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                sx[i] = ld_written(a.g.sx + t.m0 + c[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (nn >= a.g.N || (i && (it >> 5) + a.S * (TC_THREADS / 32) >= t.rows)) break;
                 float v[4] = {};
 #pragma unroll
                 for (int k = 0; k < MAX_SPLIT; ++k) {
-                    v[0] += p[k].x; v[1] += p[k].y; v[2] += p[k].z; v[3] += p[k].w;
+                    v[0] += p[i][k].x; v[1] += p[i][k].y; v[2] += p[i][k].z; v[3] += p[i][k].w;
                 }
-                const float sx = ld_written(a.g.sx + t.m0 + c);
-                const long long at = (long long)(t.m0 + c) * a.g.N + nn;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (nn + j < a.g.N) store_one(a.g, at + j, v[j] * sx * __ldg(a.g.sw + nn + j));
+                for (int j = 0; j < 4; ++j) v[j] *= sx[i] * sw4[j];
+                store4<T>(a.g, (long long)(t.m0 + c[i]) * a.g.N + nn, a.g.N - nn, v);
             }
         }
-        cluster_sync();
+        cluster_sync();                                            // nobody leaves while its sums may be read
     }
 }
 
@@ -701,9 +751,9 @@ template <class K> cudaError_t configure(K kernel, Done& done) {
     return e;
 }
 
-template <int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, int sms, cudaStream_t st) {
+template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, int sms, cudaStream_t st) {
     static Done ready = {};
-    cudaError_t e = configure(q8_tc_kernel<TN, PAIR>, ready);
+    cudaError_t e = configure(q8_tc_kernel<T, TN, PAIR>, ready);
     if (e != cudaSuccess) return e;
     using P = Plan8<TN, PAIR>;
     const int wide = PAIR ? 256 : 128;
@@ -713,11 +763,9 @@ template <int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, i
     a.group = 8;
     const long long tiles = (long long)a.NT * a.MT;
     a.S = 1;
-    if (!PAIR)
-        while (a.S < MAX_SPLIT && tiles * a.S * 2 <= sms && a.steps >= a.S * 4) a.S *= 2;
+    while (!PAIR && a.S < MAX_SPLIT && tiles * a.S * 2 <= sms && a.steps >= a.S * 4) a.S *= 2;
     const int width = PAIR ? 2 : a.S;
-    a.ctas = (int)std::min(tiles * width, (long long)(sms / width * width));
-    if (a.S > 1) a.ctas = (int)tiles * a.S;
+    a.ctas = a.S > 1 ? (int)tiles * width : (int)std::min(tiles * width, (long long)(sms / width * width));
     CUtensorMap wmap, xmap;
     if (!rows_map(&wmap, a.g.w, a.g.N, a.g.K, 1, 128) || !rows_map(&xmap, x16, a.g.M, a.g.K, 2, PAIR ? P::XR / 2 : P::XR)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -739,7 +787,16 @@ template <int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, i
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, q8_tc_kernel<TN, PAIR>, wmap, xmap, a);
+    return cudaLaunchKernelEx(&cfg, q8_tc_kernel<T, TN, PAIR>, wmap, xmap, a);
+}
+
+// Whether pairs of CTAs are the faster kernel, by waves: a stage of 256 x 256 tiles takes about 15/8 of the time of one of 128 x
+// 128 tiles (0.80 us to 0.43 at K = 4096, 0.69 to 0.39 at 8192^3; the MMAs of both are less, what is left is the way of a stage
+// through its ring).  Measured, us single / pairs: 4096 x 4096, M = 1024 33.1 / 31.0, 2048 60.4 / 59.7; 14336 x 4096, M = 256 33.2 /
+// 31.2, 512 47.0 / 57.4; 8192 x 8192, M = 256 32.2 / 43 (31.0 with k shared by two pairs), 8192 718 / 660.
+bool pays_in_pairs(const Q8GemmArgs& g, int sms) {
+    const long long one = (long long)((g.N + 127) / 128) * ((g.M + 127) / 128), two = 2LL * ((g.N + 255) / 256) * ((g.M + 255) / 256);
+    return (two + sms - 1) / sms * 15 < (one + sms - 1) / sms * 8;
 }
 
 }  // namespace
@@ -757,11 +814,13 @@ cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& g, const void* x16, int sms, c
     TcArgs8 a = {};
     a.g = g;
     a.wait = 1;
-    if (g.M <= 32) return launch_tc<32, false>(a, x16, sms, st);
-    if (g.M <= 64) return launch_tc<64, false>(a, x16, sms, st);
-    if (g.M <= 128) return launch_tc<128, false>(a, x16, sms, st);
-    if ((long long)((g.N + 255) / 256) * ((g.M + 255) / 256) * 2 < sms) return launch_tc<128, false>(a, x16, sms, st);
-    return launch_tc<256, true>(a, x16, sms, st);
+    return with_dtype(g.ytype, [&](auto t) {
+        using T = decltype(t);
+        if (g.M <= 32) return launch_tc<T, 32, false>(a, x16, sms, st);
+        if (g.M <= 64) return launch_tc<T, 64, false>(a, x16, sms, st);
+        if (!pays_in_pairs(g, sms)) return launch_tc<T, 128, false>(a, x16, sms, st);
+        return launch_tc<T, 256, true>(a, x16, sms, st);
+    });
 }
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, int sms, cudaStream_t st) {

@@ -147,7 +147,9 @@ def test_streams_and_graphs():
     assert uq.device_fault() == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(2560, 2048, 128), (2500, 2100, 1184), (2305, 2304, 2048), (2560, 2304, 4112), (4100, 1300, 640)])
+@pytest.mark.parametrize("M,N,K", [(2560, 2048, 128), (2500, 2100, 1184), (2305, 2304, 2048), (2560, 2304, 4112), (4100, 1300, 640),
+                                   (1024, 4096, 128), (1000, 4100, 1184), (2305, 1792, 2048), (2000, 2304, 4112), (4100, 1000, 640),
+                                   (2300, 3900, 1296), (2100, 4097, 3088)])
 def test_pairs_of_ctas(M, N, K):
     """Enough tiles of 256 x 256 for a pair of CTAs on every two SMs, ragged ends, chunks of all lengths; against integer sums
     in 64 bits on the device."""
