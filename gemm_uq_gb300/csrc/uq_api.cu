@@ -1316,7 +1316,10 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
     a.K = K;
     const bool wide = uq::q8_gemm_wide(M);
     void* x16 = nullptr;
-    if (wide || !xscales) {
+    if (!xscales && uq::q8_gemm_quantizes(x, xtype, M, K)) {
+        a.raw = x;
+        a.xtype = xtype;
+    } else if (wide || !xscales) {
         // codes for the product (as fp16 for many tokens) | scales, in the workspace
         const size_t code_bytes = ((size_t)M * K * (wide ? 2 : 1) + 255) / 256 * 256;
         Workspace* ws = nullptr;

@@ -237,7 +237,11 @@ struct Q8GemmArgs {
     void* y;                  // [M][N]
     unsigned int* fault;
     int ytype, M, N, K;
+    const void* raw;          // a token that the kernel quantizes itself (x and sx unused), or NULL
+    int xtype;
 };
+// whether launch_q8_gemm quantizes the token itself
+bool q8_gemm_quantizes(const void* x, int type, int M, int K);
 bool q8_gemm_wide(int M);           // whether a product of so many tokens takes their codes as fp16 (launch_q8_gemm_wide)
 cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st);
 cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& a, const void* x16, int sms, cudaStream_t st);

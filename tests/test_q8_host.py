@@ -154,9 +154,10 @@ def test_no_memory_is_an_error_and_nothing_is_launched(tmp_path):
     f.launches(lambda: f.lib.uq_quantize_q8(a, 0, 64, a, a, 4, 64, None))          # the device's words
     f.lib.fake_set_no_memory(1)
     f.lib.fake_clear()
-    assert f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 4, 64, 64, None) == 5
+    assert f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 7, 64, 64, None) == 5
+    assert f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 40, 64, 64, None) == 5
     assert f.lib.uq_rmsnorm_grad(a, a, a, None, 0, a + 256, a, 4, 64, 1e-5, None) == 5
     assert f.lib.fake_launch_count() == 0
     f.lib.fake_set_no_memory(0)
-    assert len(f.launches(lambda: f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 4, 64, 64, None))) == 2
+    assert len(f.launches(lambda: f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 7, 64, 64, None))) == 2
     assert len(f.launches(lambda: f.lib.uq_rmsnorm_grad(a, a, a, None, 0, a + 256, a, 4, 64, 1e-5, None))) == 2
