@@ -40,46 +40,46 @@ struct RowArgs {
     int early;                                  // the next kernel may start before this one is done
 };
 
+// the larger magnitude, NaN if one is
+__device__ __forceinline__ float larger(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+    return d;
+}
+
 // NORM: the norm; else the plain quantizer (h, y, residual and gamma unused).
 // V elements per access, NV accesses of a thread kept in registers; what a longer row has beyond is read again.
+// A row is a chain of loads, a reduction, and stores, with about 15 instructions an element, nearly half of what the SM can
+// issue in the time that memory takes; so rows are spread over small groups of threads, many of them on an SM, whose chains
+// overlap (8192 rows of 8192 bf16, all outputs: 256 threads a row XX us, 512 threads 152, 1024 with the next row's loads
+// issued ahead 172).
 template <class T, int V, int NV, bool NORM>
-__global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
     using W = Vec<T, V>;
     __shared__ float sums[2][MAX_THREADS / 32];
-    __shared__ uint32_t maxima[2][MAX_THREADS / 32];
+    __shared__ float maxima[2][MAX_THREADS / 32];
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
     const int nvec = a.D / V;
     if constexpr (!NORM)
         if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const W* gamma = static_cast<const W*>(a.gamma);
-    W gam[NV];
-    if constexpr (NORM) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (tid + i * a.group < nvec) gam[i] = gamma[tid + i * a.group];
-    }
     int buf = 0;
     for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += (long long)gridDim.x * per_cta, buf ^= 1) {
         const long long row = base + mine;
         const bool on = row < a.rows;
         const W* x = reinterpret_cast<const W*>(static_cast<const T*>(a.x) + (on ? row : 0) * a.ldx);
-        const W* res = reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + (on ? row : 0) * a.D);
-        auto load = [&](int v) {
-            W w = x[v];
-            if constexpr (NORM)
-                if (a.residual) {
-                    float f[V], r[V];
-                    unpack(w, f);
-                    unpack(res[v], r);
+        const W* res = NORM && a.residual ? reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + (on ? row : 0) * a.D) : nullptr;
+        auto add = [&](const W& w, const W& r) {                   // h
+            float f[V], g[V];
+            unpack(w, f);
+            unpack(r, g);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) f[j] += r[j];
-                    w = pack<T, V>(f);
-                }
-            return w;
+            for (int j = 0; j < V; ++j) f[j] += g[j];
+            return pack<T, V>(f);
         };
-        float sum = 0.f;
-        uint32_t most = 0;
+        auto load = [&](int v) { return res ? add(x[v], res[v]) : x[v]; };
+        float sum = 0.f, most = 0.f;
         auto look = [&](const W& w, const W& g) {
             float f[V], c[V];
             unpack(w, f);
@@ -87,21 +87,34 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if constexpr (NORM) sum = fmaf(f[j], f[j], sum);
-                most = max(most, magnitude(NORM ? f[j] * c[j] : f[j]));
+                most = larger(most, NORM ? f[j] * c[j] : f[j]);
             }
         };
         W kept[NV];
         if (on) {
+            if (res) {
+                W r[NV];
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * a.group < nvec) {
+                        kept[i] = x[tid + i * a.group];
+                        r[i] = res[tid + i * a.group];
+                    }
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * a.group < nvec) kept[i] = add(kept[i], r[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * a.group < nvec) kept[i] = x[tid + i * a.group];
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) kept[i] = load(tid + i * a.group);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) look(kept[i], gam[i]);
+                if (tid + i * a.group < nvec) look(kept[i], NORM ? gamma[tid + i * a.group] : W());
             for (int v = tid + NV * a.group; v < nvec; v += a.group) look(load(v), NORM ? gamma[v] : W());
         }
         if constexpr (NORM) sum = warp_sum(sum);
-        most = warp_max(most);
+        most = __uint_as_float(warp_max(__float_as_uint(most)));   // (NaN and infinity are the largest patterns)
         if (warps > 1) {
             // two sets of slots: those of this row are written again only after the barrier of the next one
             if (lane == 0) {
@@ -111,17 +124,17 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
             __syncthreads();
             const int w = first_warp + lane;
             if constexpr (NORM) sum = warp_sum(lane < warps ? sums[buf][w] : 0.f);
-            most = warp_max(lane < warps ? maxima[buf][w] : 0u);
+            most = __uint_as_float(warp_max(__float_as_uint(lane < warps ? maxima[buf][w] : 0.f)));
         }
         if (!on) continue;
-        const bool bad = most >= INF_BITS;
-        const float m = __uint_as_float(most);
+        const bool bad = !(most < __uint_as_float(INF_BITS));
+        const float nan = __uint_as_float(0x7FC00000u);
         if constexpr (NORM) {
             const float r = __frsqrt_rn(sum / (float)a.D + a.eps);
-            // 127 / m stays finite for the smallest m
-            const float up = m < 0x1p-64f ? 0x1p80f : 1.f;
-            const float inv = most == 0 || bad ? 0.f : 127.f / (m * up);
-            if (tid == 0 && a.scales) a.scales[row] = bad ? __uint_as_float(0x7FC00000u) : r * m / 127.f;
+            if (tid == 0 && a.scales) a.scales[row] = bad ? nan : r * most / 127.f;
+            // 127 / most stays finite for the smallest; a bad row's codes are zero
+            const float up = most < 0x1p-64f ? 0x1p80f : 1.f;
+            const float inv = most > 0.f && !bad ? 127.f / (most * up) : 0.f;
             W* h = a.h ? reinterpret_cast<W*>(static_cast<T*>(a.h) + row * a.D) : nullptr;
             W* y = a.y ? reinterpret_cast<W*>(static_cast<T*>(a.y) + row * a.D) : nullptr;
             int8_t* codes = a.codes ? a.codes + row * a.D : nullptr;
@@ -130,16 +143,26 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
                 if (h) h[v] = w;
                 unpack(w, f);
                 unpack(g, c);
+#pragma unroll
+                for (int j = 0; j < V; ++j) c[j] *= f[j];
                 if (y) {
                     float o[V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] = f[j] * r * c[j];
+                    for (int j = 0; j < V; ++j) o[j] = c[j] * r;
                     y[v] = pack<T, V>(o);
                 }
                 if (codes) {
                     uint32_t q[V];
+                    if (up != 1.f) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) q[j] = bad ? 0u : code_bits(f[j] * c[j] * up, inv);
+                        for (int j = 0; j < V; ++j) c[j] *= up;
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) c[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; ++j) q[j] = code_bits(c[j], inv);
                     store_codes<V>(codes + (long long)v * V, q);
                 }
             };
@@ -147,17 +170,16 @@ __global__ void __launch_bounds__(MAX_THREADS) row_kernel(const RowArgs a) {
             for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), gamma[v]);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gam[i]);
+                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gamma[tid + i * a.group]);
         } else {
-            const float s = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(m, 127.f);
+            const float s = bad ? nan : __fdiv_rn(most, 127.f);
             if (tid == 0) a.scales[row] = s;
             const Divisor d(s);
             auto write = [&](int v, const W& w) {
                 float f[V];
                 uint32_t c[V];
                 unpack(w, f);
-#pragma unroll
-                for (int j = 0; j < V; ++j) c[j] = d.code(f[j]);
+                d.codes(f, c);
                 if (a.wide) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) f[j] = (float)(int8_t)c[j];
@@ -201,30 +223,27 @@ struct GradArgs {
     int group;
 };
 
-// A group of threads takes every P-th row; its share of dgamma stays in registers (of a longer row, in its own row of
-// `partials`) until its rows are done.
+// A group of threads takes every so many-th row; its share of dgamma stays in registers (of a longer row, in its CTA's row of
+// `partials`, where a CTA has one group) until its rows are done; then a CTA's groups are added in order.  As above many small
+// groups, and named barriers, so that a CTA's groups do not wait for one another.
 template <class T, int V, int NV>
-__global__ void __launch_bounds__(GRAD_THREADS) norm_grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {
     using W = Vec<T, V>;
+    extern __shared__ float together[];         // several groups: [D]
     __shared__ float2 sums[2][GRAD_THREADS / 32];
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
     const int nvec = a.D / V;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                // the kernel that adds the partials
     const W* gamma = static_cast<const W*>(a.gamma);
-    float* part = a.partials + ((long long)blockIdx.x * per_cta + mine) * a.D;
-    W gam[NV];
+    float* part = a.partials + (long long)blockIdx.x * a.D;
     float dg[NV][V] = {};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (tid + i * a.group < nvec) gam[i] = gamma[tid + i * a.group];
     for (int v = tid + NV * a.group; v < nvec; v += a.group)
 #pragma unroll
         for (int j = 0; j < V; ++j) part[(long long)v * V + j] = 0.f;
     int buf = 0;
-    for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += (long long)gridDim.x * per_cta, buf ^= 1) {
-        const long long row = base + mine;
-        const bool on = row < a.rows;
-        const long long at = (on ? row : 0) * (long long)nvec;
+    for (long long row = (long long)blockIdx.x * per_cta + mine; row < a.rows; row += (long long)gridDim.x * per_cta, buf ^= 1) {
+        const long long at = row * nvec;
         const W *dy = static_cast<const W*>(a.dy) + at, *h = static_cast<const W*>(a.h) + at;
         const W* dh = a.dh ? static_cast<const W*>(a.dh) + at : nullptr;
         W* dx = static_cast<W*>(a.dx) + at;
@@ -241,29 +260,26 @@ __global__ void __launch_bounds__(GRAD_THREADS) norm_grad_kernel(const GradArgs 
             }
         };
         W ku[NV], kw[NV], kd[NV];
-        if (on) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) {
-                    ku[i] = dy[tid + i * a.group];
-                    kw[i] = h[tid + i * a.group];
-                    if (dh) kd[i] = dh[tid + i * a.group];
-                }
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * a.group < nvec) {
+                ku[i] = dy[tid + i * a.group];
+                kw[i] = h[tid + i * a.group];
+                if (dh) kd[i] = dh[tid + i * a.group];
+            }
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) look(ku[i], kw[i], gam[i]);
-            for (int v = tid + NV * a.group; v < nvec; v += a.group) look(dy[v], h[v], gamma[v]);
-        }
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * a.group < nvec) look(ku[i], kw[i], gamma[tid + i * a.group]);
+        for (int v = tid + NV * a.group; v < nvec; v += a.group) look(dy[v], h[v], gamma[v]);
         s1 = warp_sum(s1);
         s2 = warp_sum(s2);
         if (warps > 1) {
             if (lane == 0) sums[buf][threadIdx.x >> 5] = make_float2(s1, s2);
-            __syncthreads();
+            asm volatile("bar.sync %0, %1;" :: "r"(1 + mine), "r"(a.group) : "memory");
             const float2 p = lane < warps ? sums[buf][first_warp + lane] : make_float2(0.f, 0.f);
             s1 = warp_sum(p.x);
             s2 = warp_sum(p.y);
         }
-        if (!on) continue;
         const float r = __frsqrt_rn(s1 / (float)a.D + a.eps);
         const float c = r * r * (s2 / (float)a.D);                 // n mean(g n) = h r (r s2 / D)
         auto write = [&](int v, const W& u, const W& w, const W& g, const W& d, float (&out)[V]) {
@@ -293,24 +309,34 @@ __global__ void __launch_bounds__(GRAD_THREADS) norm_grad_kernel(const GradArgs 
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (tid + i * a.group < nvec) write(tid + i * a.group, ku[i], kw[i], gam[i], kd[i], dg[i]);
+            if (tid + i * a.group < nvec) write(tid + i * a.group, ku[i], kw[i], gamma[tid + i * a.group], kd[i], dg[i]);
     }
+    for (int g = 0; g < per_cta; ++g) {
+        if (g == mine)
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (tid + i * a.group < nvec)
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec)
 #pragma unroll
-            for (int j = 0; j < V; ++j) part[(long long)(tid + i * a.group) * V + j] = dg[i][j];
+                    for (int j = 0; j < V; ++j) {
+                        const int col = (tid + i * a.group) * V + j;
+                        const float v = g ? together[col] + dg[i][j] : dg[i][j];
+                        if (g == per_cta - 1) part[col] = v;
+                        else together[col] = v;
+                    }
+        if (g < per_cta - 1) __syncthreads();
+    }
 }
 
 // dgamma = the sum of the P partial rows, in order: a CTA of 32 x 8 threads takes 32 columns, its warps every 8th row, and
 // adds the warps' sums in order.
 __global__ void __launch_bounds__(256) partials_sum_kernel(const float* __restrict__ partials, float* __restrict__ out, int P, int D) {
     __shared__ float part[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     float s = 0.f;
     if (col < D) {
 #pragma unroll 8
-        for (int p = w; p < P; p += 8) s += partials[(long long)p * D + col];
+        for (int p = w; p < P; p += 8) s += ld_written(partials + (long long)p * D + col);
     }
     part[w][threadIdx.x & 31] = s;
     __syncthreads();
@@ -329,13 +355,13 @@ template <class T> int access(int D, long long ld) {
     return both % (4 / (int)sizeof(T)) == 0 ? 4 / sizeof(T) : 1;
 }
 
-// Threads per row and accesses per thread for rows of nvec accesses.
-struct Shape { int group, nv, block; };
-Shape shape_of(int nvec, int most_threads) {
-    Shape s = {32, 1, 0};
-    while (s.group < most_threads && s.group * 2 < nvec) s.group *= 2;
+// Threads per row and accesses per thread (1, 2 or 4) for rows of nvec accesses: four where there are rows enough, else as
+// many threads as the row has accesses.
+struct Shape { int group, nv; };
+Shape shape_of(int nvec, int most_threads, bool few) {
+    Shape s = {32, 1};
+    while (s.group < most_threads && s.group * (few ? 1 : 4) < nvec) s.group *= 2;
     while (s.nv < 4 && s.group * s.nv < nvec) s.nv *= 2;
-    s.block = s.group < 128 ? 128 : s.group;
     return s;
 }
 
@@ -357,11 +383,12 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
         using T = decltype(t);
         RowArgs a = a0;
         const int v = access<T>(a.D, a.ldx);
-        const Shape s = shape_of(a.D / v, MAX_THREADS);
+        const Shape s = shape_of(a.D / v, MAX_THREADS, a.rows <= 2 * sms);
         a.group = s.group;
-        const long long tiles = ((long long)a.rows + s.block / s.group - 1) / (s.block / s.group), most = (long long)sms * (2048 / s.block);
+        const int block = s.group < 128 ? 128 : s.group, per = block / s.group;
+        const long long tiles = ((long long)a.rows + per - 1) / per, most = (long long)sms * (2048 / block);
         return with_shape<T>(v, s.nv, [&](auto V, auto NV) {
-            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM><<<(unsigned)(tiles < most ? tiles : most), s.block, 0, st>>>(a);
+            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM><<<(unsigned)(tiles < most ? tiles : most), block, 0, st>>>(a);
             return cudaGetLastError();
         });
     });
@@ -404,33 +431,40 @@ cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* g
     return launch_rows<true>(a, type, sms, st);
 }
 
-// Row groups of the gradient's grid, each with a partial row of dgamma.
-static Shape grad_shape(int type, int D) {
+// CTAs of the gradient, each with a partial row of dgamma.
+static Shape grad_shape(int type, int rows, int D, int sms) {
     const int v = type == UQ_FP32 ? access<float>(D, D) : access<__half>(D, D);
-    return shape_of(D / v, GRAD_THREADS);
+    return shape_of(D / v, GRAD_THREADS, rows <= 2 * sms);
 }
 int norm_grad_partials(int type, int rows, int D, int sms) {
-    const Shape s = grad_shape(type, D);
-    const int per = s.block / s.group;
-    const long long tiles = ((long long)rows + per - 1) / per, most = (long long)sms * (1024 / s.block);
-    return (int)(tiles < most ? tiles : most) * per;
+    const int per = GRAD_THREADS / grad_shape(type, rows, D, sms).group, tiles = (int)(((long long)rows + per - 1) / per);
+    return tiles < sms ? tiles : sms;
 }
 
 cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, int type, void* dx, float* dgamma,
                                 float* partials, int rows, int D, float eps, int sms, cudaStream_t st) {
-    const Shape s = grad_shape(type, D);
+    const Shape s = grad_shape(type, rows, D, sms);
     const int P = norm_grad_partials(type, rows, D, sms);
     const GradArgs a = {dy, h, gamma, dh, dx, partials, rows, D, eps, s.group};
     cudaError_t e = with_dtype(type, [&](auto t) {
         using T = decltype(t);
         return with_shape<T>(access<T>(D, D), s.nv, [&](auto V, auto NV) {
-            norm_grad_kernel<T, decltype(V)::value, decltype(NV)::value><<<P / (s.block / s.group), s.block, 0, st>>>(a);
+            norm_grad_kernel<T, decltype(V)::value, decltype(NV)::value>
+                <<<P, GRAD_THREADS, GRAD_THREADS > s.group ? (size_t)D * sizeof(float) : 0, st>>>(a);
             return cudaGetLastError();
         });
     });
     if (e != cudaSuccess) return e;
-    partials_sum_kernel<<<(D + 31) / 32, 256, 0, st>>>(partials, dgamma, P, D);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((D + 31) / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, partials_sum_kernel, (const float*)partials, dgamma, P, D);
 }
 
 }  // namespace uq

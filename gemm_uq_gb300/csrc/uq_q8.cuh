@@ -27,12 +27,17 @@ struct Divisor {
         fast = scale >= 0x1p-90f && scale <= 0x1p90f;
         zero = !(scale > 0.f) || scale > 3.0e38f;
     }
-    __device__ __forceinline__ uint32_t code(float x) const {
+    template <int V> __device__ __forceinline__ void codes(const float (&x)[V], uint32_t (&c)[V]) const {
         if (fast) {
-            const float q = x * r;
-            return code_bits(fmaf(fmaf(-q, s, x), r, q));
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float q = x[j] * r;
+                c[j] = code_bits(fmaf(fmaf(-q, s, x[j]), r, q));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] = zero ? 0u : code_bits(fminf(fmaxf(__fdiv_rn(x[j], s), -127.f), 127.f));
         }
-        return zero ? 0u : code_bits(fminf(fmaxf(__fdiv_rn(x, s), -127.f), 127.f));
     }
 };
 

@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(THREADS, 3) q8_gemv_kernel(const Q8GemmArgs a,
                     float f[V];
                     uint32_t c[V];
                     unpack(held[i], f);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) c[j] = d.code(f[j]);
+                    d.codes(f, c);
                     store_codes<V>(reinterpret_cast<int8_t*>(xs) + (v - own0) * V, c);
                 }
                 __syncthreads();

@@ -73,6 +73,27 @@ __device__ __forceinline__ void best_of(double& c, int& e, int E) {
     if (c == (double)low_value()) e = E;
 }
 
+// Scores in approximate instructions, with a bound on their error as a part of the largest score, one:
+//   sigmoid  e^-x loses 2^-22 and |x| 2^-23.4 by its argument's rounding, of which s (1 - s) reaches s: below 2^-24 together; the
+//            reciprocal 2^-23 s;
+//   softmax  as much of each score, and E / 32 + 5 roundings of the sum, which all scores share.
+// The addition of the bias loses 2^-24 of its result besides.
+__device__ __forceinline__ float exp_about(float x) {
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+    return e;
+}
+__device__ __forceinline__ float reciprocal_about(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float score_error(const RouteArgs& a) { return a.sigmoid ? 0x1p-22f : (float)(a.E / 32 + 16) * 0x1p-24f; }
+// whether fp32 values of this error (`terms` of them in each of the two) are in their order
+__device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, float terms) {
+    return hi - lo > 2.f * terms * (fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-24f + score_error(a));
+}
+
 // Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it).  Lane j returns choice j, -1 for
 // none.  `exact`: c is the logits themselves; `sure`: every decision had more distance than the error of the values.
 template <class S, class T>
@@ -80,12 +101,6 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
     const int lane = threadIdx.x & 31, E = a.E;
     const S none = (S)low_value();
     sure = true;
-    // Error of a choice value: the score's, some roundings of it (softmax: and of its exponent, |x - max| 2^-24 relative,
-    // at most e^-1 2^-24 of the largest score), and the addition's.
-    auto apart = [&](S hi, S lo, S terms) {
-        const S m = fmax(fabs(hi), fabs(lo));
-        return hi - lo > (S)2 * terms * (m * (S)0x1p-24f + (S)0x1p-21f);
-    };
     if (a.groups > 1) {
         // 2^k lanes per group, each every 2^k-th member; the group's best two by shuffles
         int per = 32;
@@ -116,7 +131,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
             if (!exact) {
                 // distance between the groups that stay and the others (one with the same members' values may tie)
                 const S worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
-                if (next > none && !apart(worst, next, (S)(2 * a.group_top))) sure = false;
+                if (next > none && !apart(a, worst, next, 2.f * a.group_top)) sure = false;
             }
         }
         const uint32_t open_ = __ballot_sync(ALL, stays && lane % per == 0);
@@ -148,7 +163,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         best_of(v, e, E);
         if (e == E) break;
         if constexpr (sizeof(S) == 4) {
-            if (!exact && j && !apart(before, v, (S)1)) {
+            if (!exact && j && !apart(a, before, v, 1.f)) {
                 // the same logit and bias give the same value: the lower index is right
                 if (!(before == v && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) sure = false;
             }
@@ -175,7 +190,7 @@ __device__ __forceinline__ void values(const RouteArgs& a, S* c, const T* x, boo
         m = warp_max_f(m);
         for (int e = lane; e < a.E; e += 32) {
             const float v = to_f32(x[e]);
-            if (v > low_value()) sum += sizeof(S) == 8 ? (S)exp((double)v - (double)m) : (S)expf(v - m);
+            if (v > low_value()) sum += sizeof(S) == 8 ? (S)exp((double)v - (double)m) : (S)exp_about(v - m);
         }
         sum = warp_add(sum);
     }
@@ -184,11 +199,195 @@ __device__ __forceinline__ void values(const RouteArgs& a, S* c, const T* x, boo
         S s;
         if (by_logit) s = (S)v;
         else if (sizeof(S) == 8) s = (S)(a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / (double)sum);
-        else s = (S)(a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - m) / (float)sum);
+        else s = (S)(a.sigmoid ? reciprocal_about(1.f + exp_about(-v)) : exp_about(v - m) * reciprocal_about((float)sum));
         if (v != v) s = (S)v;
         c[e] = ranked<S>(s + (S)b, v != low_value() && b != low_value());
     }
     __syncwarp();
+}
+
+// Weight (without the factor) of lane j's choice; `nan`: this lane has seen a NaN among the logits.
+template <class T> __device__ __forceinline__ float weight_of(const RouteArgs& a, const T* x, int id, bool nan) {
+    const int lane = threadIdx.x & 31;
+    const float v = id >= 0 ? to_f32(x[id]) : low_value();
+    if (a.renorm) {
+        // among the chosen alone, from the largest logit of them: their ratios survive where the scores underflow
+        bool bad = id >= 0 && v != v;
+        const float m = warp_max_f(v);
+        float w = 0.f;
+        if (a.sigmoid) {
+            if (id >= 0) w = sigmoid_over(v, fminf(m, 0.f));
+        } else {
+            bad |= nan;                         // makes all of softmax NaN
+            if (id >= 0) w = expf(v - m);
+        }
+        const float all = warp_add(w);
+        return __any_sync(ALL, bad) ? __uint_as_float(0x7FC00000u) : (all > 0.f || all != all ? w / all : 0.f);
+    }
+    if (a.sigmoid) return 1.f / (1.f + expf(-v));
+    float m = low_value(), sum = 0.f;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+    m = warp_max_f(m);
+    for (int e = lane; e < a.E; e += 32) {
+        const float u = to_f32(x[e]);
+        if (u != low_value()) sum += expf(u - m);
+    }
+    return expf(v - m) / warp_add(sum);
+}
+
+// The same choice with the values in registers: lane l holds experts l NL .. l NL + NL - 1 (of E <= 32 NL), so that the lowest
+// of the lanes with the largest value has the lower index.  Groups have to be whole lanes, a power of two of them.
+// Scores that need 64 bits: sigmoids of the choices that are too near to tell are done again, a lane each; anything else
+// that fp32 leaves open (softmax with a bias, groups, more than 32 near ones) is done by choose() in 64 bits.
+template <class T, int NL>
+__global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * NL;
+    const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+    constexpr int V = NL * (int)sizeof(T) < 16 ? NL : 16 / (int)sizeof(T);
+    const bool whole = a.E % V == 0;            // rows of whole accesses
+    double* mine = reinterpret_cast<double*>(smem + (size_t)warp * a.E * 8);
+    float bias[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+    for (long long t = (long long)blockIdx.x * WARPS + warp; t < a.T; t += (long long)gridDim.x * WARPS) {
+        const T* x = static_cast<const T*>(a.logits) + t * a.E;
+        float v[NL], c[NL];
+#pragma unroll
+        for (int i = 0; i < NL; i += V) {
+            Vec<T, V> w;
+            if (whole) {
+                if (e0 + i < a.E) w = *reinterpret_cast<const Vec<T, V>*>(x + e0 + i);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (e0 + i + j < a.E) w.v[j] = x[e0 + i + j];
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i + j] = e0 + i + j < a.E ? to_f32(w.v[j]) : low_value();
+        }
+        if (by_logit) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) c[i] = ranked<float>(v[i] + 0.f, v[i] != low_value());
+        } else {
+            float m = 0.f, over = 1.f;
+            if (!a.sigmoid) {
+                m = v[0];
+#pragma unroll
+                for (int i = 1; i < NL; ++i) m = fmaxf(m, v[i]);
+                m = warp_max_f(m);
+                over = 0.f;
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    if (v[i] > low_value()) over += exp_about(v[i] - m);
+                over = reciprocal_about(warp_add(over));
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                float s = a.sigmoid ? reciprocal_about(1.f + exp_about(-v[i])) : exp_about(v[i] - m) * over;
+                if (v[i] != v[i]) s = v[i];
+                c[i] = ranked<float>(s + bias[i], v[i] != low_value() && bias[i] != low_value());
+            }
+        }
+        const float none = low_value();
+        bool sure = true, exact = by_logit, groups_sure = true;
+        if (a.groups > 1) {
+            const int per = a.E / a.groups / NL, g = lane / per;   // lanes of a group
+            float b1 = none, b2 = none;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                b2 = fmaxf(b2, fminf(b1, c[i]));
+                b1 = fmaxf(b1, c[i]);
+            }
+            for (int o = 1; o < per; o <<= 1) {
+                const float o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                b1 = fmaxf(b1, o1);
+            }
+            float total = b1;
+            if (a.group_top == 2 && b2 > none) total += b2;
+            if (g >= a.groups) total = none;
+            int ahead = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const float other = __shfl_sync(ALL, total, o * per);
+                ahead += other > total || (other == total && o < g);
+            }
+            const bool stays = total > none && ahead < a.top_groups;
+            if (!exact) {
+                const float worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
+                groups_sure = next == none || apart(a, worst, next, 2.f * a.group_top);
+            }
+            if (!a.bias) exact = true;          // the order within the groups is that of x
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                c[i] = !stays ? none : (a.bias ? c[i] : ranked<float>(v[i] + 0.f, v[i] != none));
+        }
+        // lane j: choice j; behind the last one, those that are too near to it
+        int id = -1, last = -1, found = 0;
+        float before = none;
+        for (int j = 0; j < 32; ++j) {
+            if (exact && j == a.topk) break;
+            float best = c[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < NL; ++i)
+                if (c[i] > best) best = c[i], at = i;
+            uint32_t k = __float_as_uint(best);
+            k = k & 0x80000000u ? ~k : k | 0x80000000u;            // the order of the values
+            const uint32_t top = __reduce_max_sync(ALL, k);
+            const int who = __ffs(__ballot_sync(ALL, k == top)) - 1;
+            best = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+            if (best == none) break;
+            const int e = __shfl_sync(ALL, e0 + at, who);
+            if (!exact && j) {
+                if (apart(a, before, best, 1.f)) {
+                    if (j >= a.topk) break;
+                } else if (!(before == best && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
+                    sure = false;               // (the same logit and bias give the same value: the lower index is right)
+                }
+            }
+            before = best;
+            last = e;
+            if (lane == j) id = e;
+            found = j + 1;
+            if (lane == who)
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    if (i == at) c[i] = none;
+        }
+        if (!sure || !groups_sure) {
+            const float u = id >= 0 ? to_f32(x[id]) : 0.f;
+            const bool odd = u != u || (id >= 0 && a.bias && a.bias[id] != a.bias[id]);
+            if (groups_sure && a.sigmoid && found < 32 && !__any_sync(ALL, odd)) {
+                double d = id >= 0 ? 1.0 / (1.0 + exp(-(double)u)) + (double)(a.bias ? a.bias[id] : 0.f) : 0.0;
+                int rank = 0, got = -1;
+                for (int o = 0; o < found; ++o) {
+                    const double od = __shfl_sync(ALL, d, o);
+                    const int oe = __shfl_sync(ALL, id, o);
+                    rank += od > d || (od == d && oe < id);
+                }
+                for (int o = 0; o < found; ++o) {
+                    const int r = __shfl_sync(ALL, rank, o), oe = __shfl_sync(ALL, id, o);
+                    if (r == lane) got = oe;
+                }
+                id = got;
+            } else {
+                bool yes;
+                __syncwarp();
+                values<double>(a, mine, x, false);
+                id = choose<double>(a, mine, x, false, yes);
+            }
+        }
+        if (lane >= a.topk) id = -1;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) nan |= v[i] != v[i];
+        const float w = weight_of(a, x, id, nan);
+        if (lane < a.topk) {
+            a.ids[t * a.topk + lane] = id;
+            a.weights[t * a.topk + lane] = id >= 0 ? w * a.scale : 0.f;
+        }
+    }
 }
 
 template <class T>
@@ -208,35 +407,9 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a) {
             values<double>(a, reinterpret_cast<double*>(mine), x, false);
             id = choose<double>(a, reinterpret_cast<double*>(mine), x, false, sure);
         }
-        // weights: lane j's
-        const float v = id >= 0 ? to_f32(x[id]) : low_value();
-        float w;
-        if (a.renorm) {
-            // among the chosen alone, from the largest logit of them: their ratios survive where the scores underflow
-            bool bad = id >= 0 && v != v;
-            const float m = warp_max_f(v);
-            if (a.sigmoid) {
-                w = id >= 0 ? sigmoid_over(v, fminf(m, 0.f)) : 0.f;
-            } else {
-                // a NaN among the logits makes all of softmax NaN
-                for (int e = lane; e < a.E; e += 32) bad |= to_f32(x[e]) != to_f32(x[e]);
-                w = id >= 0 ? expf(v - m) : 0.f;
-            }
-            const float all = warp_add(w);
-            w = __any_sync(ALL, bad) ? __uint_as_float(0x7FC00000u) : (all > 0.f || all != all ? w / all : 0.f);
-        } else if (a.sigmoid) {
-            w = 1.f / (1.f + expf(-v));
-        } else {
-            float m = low_value(), sum = 0.f;
-            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
-            m = warp_max_f(m);
-            for (int e = lane; e < a.E; e += 32) {
-                const float u = to_f32(x[e]);
-                if (u != low_value()) sum += expf(u - m);
-            }
-            sum = warp_add(sum);
-            w = expf(v - m) / sum;
-        }
+        bool nan = false;
+        for (int e = lane; e < a.E; e += 32) nan |= to_f32(x[e]) != to_f32(x[e]);
+        const float w = weight_of(a, x, id, nan);
         if (lane < a.topk) {
             a.ids[t * a.topk + lane] = id;
             a.weights[t * a.topk + lane] = id >= 0 ? w * a.scale : 0.f;
@@ -321,8 +494,17 @@ cudaError_t launch_moe_route(const void* logits, int type, const float* bias, in
     const bool by_logit = !bias && (groups == 1 || group_top == 1);
     const size_t smem = (size_t)WARPS * E * (by_logit ? 4 : 8);    // at most 32 KB
     const long long ctas = ((long long)T + WARPS - 1) / WARPS, most = 16LL * sms;
+    const unsigned grid = (unsigned)(ctas < most ? ctas : most);
+    // values in registers where the groups are whole lanes
+    const int nl = E <= 64 ? 2 : (E <= 256 ? 8 : 32);
+    const int size = E / groups, per = size / nl;
+    const bool lanes = groups == 1 || (size % nl == 0 && (per & (per - 1)) == 0);
     return with_dtype(type, [&](auto t) {
-        route_kernel<decltype(t)><<<(unsigned)(ctas < most ? ctas : most), WARPS * 32, smem, st>>>(a);
+        using T_ = decltype(t);
+        if (!lanes) route_kernel<T_><<<grid, WARPS * 32, smem, st>>>(a);
+        else if (nl == 2) route_lanes_kernel<T_, 2><<<grid, WARPS * 32, by_logit ? 0 : smem, st>>>(a);
+        else if (nl == 8) route_lanes_kernel<T_, 8><<<grid, WARPS * 32, by_logit ? 0 : smem, st>>>(a);
+        else route_lanes_kernel<T_, 32><<<grid, WARPS * 32, by_logit ? 0 : smem, st>>>(a);
         return cudaGetLastError();
     });
 }
