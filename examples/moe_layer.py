@@ -1,6 +1,9 @@
-"""A mixture-of-experts layer whose weights and activations are microscaled 4-bit floating point.
+"""A mixture-of-experts layer whose weights and activations are microscaled 4-bit floating point, and the block around it.
 
     python examples/moe_layer.py [--tokens 4 --experts 8 --topk 2 --hidden 4096 --inner 14336 --fmt MXFP4]
+
+block(): the residual's addition and the norm, in 8 bits too (rmsnorm_q8), the router (moe_route), the layer, and beside it a
+shared expert on 8-bit weights (gemm_w8a8) that takes the norm's codes.
 
 Per call: the router's routes are sorted by expert (moe_sort), the tokens quantized once and gathered by expert
 (quantize_mx with pos), gate and up multiplied and combined by silu(g) * u (gemm_mx_grouped with up), the result
@@ -24,8 +27,7 @@ import gemm_uq_gb300 as uq  # noqa: E402
 
 def route(x: torch.Tensor, router: torch.Tensor, topk: int):
     """Expert ids int32 [T][topk] and weights fp32 [T][topk] (softmax over the chosen experts)."""
-    top, ids = torch.topk(x.float() @ router.t(), topk, dim=1)
-    return ids.to(torch.int32), torch.softmax(top, dim=1)
+    return uq.moe_route(x.float() @ router.t(), topk)
 
 
 def quantize_weights(w: torch.Tensor, fmt: str):
@@ -42,6 +44,19 @@ def moe_layer(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate, u
     hq = uq.quantize_mx(h, fmt, offsets=offsets)
     y = uq.gemm_mx_grouped(hq, down, offsets, fmt)
     return uq.moe_combine(y, pos, weights)
+
+
+def block(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, router: torch.Tensor, bias, topk: int, experts, shared,
+          fmt: str, groups: int = 1, top_groups: int = 1, eps: float = 1e-5) -> dict:
+    """h = x + residual; y = the routed experts' and the shared expert's outputs of the normed rows.
+
+    ``experts``: gate, up, down of moe_layer; ``shared``: gate, up, down as (codes, scales) of quantize_q8."""
+    h, normed, q = uq.rmsnorm_q8(x, gamma, eps, residual=residual, normed=True)
+    ids, weights = uq.moe_route(normed.float() @ router.t(), topk, score="sigmoid", bias=bias, groups=groups, top_groups=top_groups,
+                                group_top=2)
+    y = moe_layer(normed, ids, weights, *experts, fmt)
+    gate, up = (uq.gemm_w8a8(q, w, dtype=torch.float32) for w in shared[:2])
+    return {"h": h, "y": y + uq.gemm_w8a8((torch.nn.functional.silu(gate) * up).to(x.dtype), shared[2])}
 
 
 def main():

@@ -46,15 +46,26 @@ __device__ __forceinline__ float sigmoid_over(float x, float low) {
     return x >= 0.f ? 1.f / (1.f + expf(-x)) : expf(x - low) / (1.f + expf(x));
 }
 
-// A choice value of NaN (a NaN logit or bias) ranks below all numbers and above what cannot be chosen, which is marked by
-// minus infinity; NaN itself must not be compared.
-template <class S> __device__ __forceinline__ S ranked(S c, bool can) {
-    const S least = sizeof(S) == 8 ? (S)-1.7e308 : (S)-3.4e38f;
-    if (!can) return (S)low_value();
-    return c != c ? least : (c < least ? least : c);
+// Choice values as they are compared: fp32, or the bit pattern of fp64 as an integer in the same order (this part compares
+// integers far faster than fp64).  A value of NaN (a NaN logit or bias) ranks below all numbers and above what cannot be chosen,
+// which is none_of().
+__device__ __forceinline__ long long key_of(double v) {
+    const long long k = __double_as_longlong(v);
+    return k < 0 ? k ^ 0x7FFFFFFFFFFFFFFFll : k;
 }
+__device__ __forceinline__ double value_of(long long k) { return __longlong_as_double(k < 0 ? k ^ 0x7FFFFFFFFFFFFFFFll : k); }
+template <class S> __device__ __forceinline__ S none_of();
+template <> __device__ __forceinline__ float none_of<float>() { return low_value(); }
+template <> __device__ __forceinline__ long long none_of<long long>() { return -0x7FFFFFFFFFFFFFFFll; }
+__device__ __forceinline__ float ranked(float c, bool can) { return !can ? low_value() : (c > -3.4e38f ? c : -3.4e38f); }
+__device__ __forceinline__ long long ranked(double c, bool can) {
+    return !can ? none_of<long long>() : key_of(c > -1.7e308 ? c : -1.7e308);
+}
+// the sum of two values, as they are compared
+__device__ __forceinline__ float together(float a, float b) { return a + b; }
+__device__ __forceinline__ long long together(long long a, long long b) { return key_of(value_of(a) + value_of(b)); }
 
-// The largest of the lanes' values and, among equal ones, the smallest index; index E where all are minus infinity.
+// The largest of the lanes' values and, among equal ones, the smallest index; index E where none can be chosen.
 __device__ __forceinline__ void best_of(float& c, int& e, int E) {
     uint32_t k = __float_as_uint(c);
     k = k & 0x80000000u ? ~k : k | 0x80000000u;                    // the order of the values
@@ -63,14 +74,14 @@ __device__ __forceinline__ void best_of(float& c, int& e, int E) {
     c = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
     if (c == low_value()) e = E;
 }
-__device__ __forceinline__ void best_of(double& c, int& e, int E) {
+__device__ __forceinline__ void best_of(long long& c, int& e, int E) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const double oc = __shfl_xor_sync(ALL, c, o);
+        const long long oc = __shfl_xor_sync(ALL, c, o);
         const int oe = __shfl_xor_sync(ALL, e, o);
         if (oc > c || (oc == c && oe < e)) c = oc, e = oe;
     }
-    if (c == (double)low_value()) e = E;
+    if (c == none_of<long long>()) e = E;
 }
 
 // Scores in approximate instructions, with a bound on their error as a part of the largest score, one:
@@ -94,12 +105,13 @@ __device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, fl
     return hi - lo > 2.f * terms * (fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-24f + score_error(a));
 }
 
-// Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it).  Lane j returns choice j, -1 for
+// Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it), in fp32 or 64 bits.  Lane j returns choice j, -1 for
 // none.  `exact`: c is the logits themselves; `sure`: every decision had more distance than the error of the values.
 template <class S, class T>
 __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool exact, bool& sure) {
+    constexpr bool WIDE = sizeof(S) == 8;
     const int lane = threadIdx.x & 31, E = a.E;
-    const S none = (S)low_value();
+    const S none = none_of<S>();
     sure = true;
     if (a.groups > 1) {
         // 2^k lanes per group, each every 2^k-th member; the group's best two by shuffles
@@ -110,16 +122,15 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         if (g < a.groups)
             for (int i = lane % per; i < size; i += per) {
                 const S v = c[g * size + i];
-                if (v > b1) b2 = b1, b1 = v;
-                else if (v > b2) b2 = v;
+                b2 = max(b2, min(b1, v));
+                b1 = max(b1, v);
             }
         for (int o = 1; o < per; o <<= 1) {
             const S o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
-            b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-            b1 = fmax(b1, o1);
+            b2 = max(min(b1, o1), max(b2, o2));
+            b1 = max(b1, o1);
         }
-        S total = b1;
-        if (a.group_top == 2 && b2 > none) total += b2;
+        S total = a.group_top == 2 && b2 > none ? together(b1, b2) : b1;
         if (g >= a.groups) total = none;
         int ahead = 0;                          // groups before this one
         for (int o = 0; o < a.groups; ++o) {
@@ -127,10 +138,9 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
             ahead += t > total || (t == total && o < g);
         }
         const bool stays = total > none && ahead < a.top_groups;
-        if constexpr (sizeof(S) == 4) {
+        if constexpr (!WIDE) {
             if (!exact) {
-                // distance between the groups that stay and the others (one with the same members' values may tie)
-                const S worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
+                const float worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
                 if (next > none && !apart(a, worst, next, 2.f * a.group_top)) sure = false;
             }
         }
@@ -138,8 +148,10 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         // without a bias the order within the groups is that of x
         if (!a.bias) exact = true;
         for (int e = lane; e < E; e += 32) {
+            const float v = a.bias ? 0.f : to_f32(x[e]) + 0.f;
             if (!(open_ >> (e / size * per) & 1u)) c[e] = none;
-            else if (!a.bias) c[e] = ranked<S>((S)to_f32(x[e]) + (S)0, to_f32(x[e]) != low_value());
+            else if constexpr (WIDE) c[e] = a.bias ? c[e] : ranked((double)v, v != low_value());
+            else c[e] = a.bias ? c[e] : ranked(v, v != low_value());
         }
         __syncwarp();
     }
@@ -156,13 +168,13 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
     rescan();
     int id = -1, last = -1;
     S before = none;
-    const int rounds = sizeof(S) == 4 && !exact ? a.topk + 1 : a.topk;     // the first that is not chosen, too
+    const int rounds = !WIDE && !exact ? a.topk + 1 : a.topk;      // the first that is not chosen, too
     for (int j = 0; j < rounds; ++j) {
         S v = mine;
         int e = at;
         best_of(v, e, E);
         if (e == E) break;
-        if constexpr (sizeof(S) == 4) {
+        if constexpr (!WIDE) {
             if (!exact && j && !apart(a, before, v, 1.f)) {
                 // the same logit and bias give the same value: the lower index is right
                 if (!(before == v && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) sure = false;
@@ -179,29 +191,47 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
     return id;
 }
 
-// Choice values of a token in S, into c[] (by_logit: the logits themselves).
-template <class S, class T>
-__device__ __forceinline__ void values(const RouteArgs& a, S* c, const T* x, bool by_logit) {
+// Choice values of a token in fp32, into c[] (by_logit: the logits themselves), and in 64 bits.
+template <class T> __device__ __forceinline__ void values(const RouteArgs& a, float* c, const T* x, bool by_logit) {
     const int lane = threadIdx.x & 31;
-    float m = low_value();
-    S sum = 0;
+    float m = low_value(), over = 0.f;
     if (!a.sigmoid && !by_logit) {
         for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
         m = warp_max_f(m);
         for (int e = lane; e < a.E; e += 32) {
             const float v = to_f32(x[e]);
-            if (v > low_value()) sum += sizeof(S) == 8 ? (S)exp((double)v - (double)m) : (S)exp_about(v - m);
+            if (v > low_value()) over += exp_about(v - m);
         }
-        sum = warp_add(sum);
+        over = reciprocal_about(warp_add(over));
     }
     for (int e = lane; e < a.E; e += 32) {
         const float v = to_f32(x[e]), b = a.bias ? a.bias[e] : 0.f;
-        S s;
-        if (by_logit) s = (S)v;
-        else if (sizeof(S) == 8) s = (S)(a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / (double)sum);
-        else s = (S)(a.sigmoid ? reciprocal_about(1.f + exp_about(-v)) : exp_about(v - m) * reciprocal_about((float)sum));
-        if (v != v) s = (S)v;
-        c[e] = ranked<S>(s + (S)b, v != low_value() && b != low_value());
+        float s = by_logit || v != v ? v : (a.sigmoid ? reciprocal_about(1.f + exp_about(-v)) : exp_about(v - m) * over);
+        c[e] = ranked(s + b, v != low_value() && b != low_value());
+    }
+    __syncwarp();
+}
+template <class T> __device__ __forceinline__ void values(const RouteArgs& a, long long* c, const T* x) {
+    const int lane = threadIdx.x & 31;
+    double m = 0, sum = 1;
+    if (!a.sigmoid) {
+        float top = low_value();
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, to_f32(x[e]));
+        m = (double)warp_max_f(top);
+        sum = 0;
+#pragma unroll 4
+        for (int e = lane; e < a.E; e += 32) {
+            const float v = to_f32(x[e]);
+            if (v > low_value()) sum += exp((double)v - m);
+        }
+        sum = warp_add(sum);
+    }
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) {
+        const float v = to_f32(x[e]), b = a.bias ? a.bias[e] : 0.f;
+        double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - m) / sum;
+        if (v != v) s = (double)v;
+        c[e] = ranked(s + (double)b, v != low_value() && b != low_value());
     }
     __syncwarp();
 }
@@ -246,7 +276,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
     const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
     constexpr int V = NL * (int)sizeof(T) < 16 ? NL : 16 / (int)sizeof(T);
     const bool whole = a.E % V == 0;            // rows of whole accesses
-    double* mine = reinterpret_cast<double*>(smem + (size_t)warp * a.E * 8);
+    long long* mine = reinterpret_cast<long long*>(smem + (size_t)warp * a.E * 8);
     float bias[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
         }
         if (by_logit) {
 #pragma unroll
-            for (int i = 0; i < NL; ++i) c[i] = ranked<float>(v[i] + 0.f, v[i] != low_value());
+            for (int i = 0; i < NL; ++i) c[i] = ranked(v[i] + 0.f, v[i] != low_value());
         } else {
             float m = 0.f, over = 1.f;
             if (!a.sigmoid) {
@@ -286,7 +316,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             for (int i = 0; i < NL; ++i) {
                 float s = a.sigmoid ? reciprocal_about(1.f + exp_about(-v[i])) : exp_about(v[i] - m) * over;
                 if (v[i] != v[i]) s = v[i];
-                c[i] = ranked<float>(s + bias[i], v[i] != low_value() && bias[i] != low_value());
+                c[i] = ranked(s + bias[i], v[i] != low_value() && bias[i] != low_value());
             }
         }
         const float none = low_value();
@@ -320,7 +350,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             if (!a.bias) exact = true;          // the order within the groups is that of x
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                c[i] = !stays ? none : (a.bias ? c[i] : ranked<float>(v[i] + 0.f, v[i] != none));
+                c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != none));
         }
         // lane j: choice j; behind the last one, those that are too near to it
         int id = -1, last = -1, found = 0;
@@ -374,8 +404,8 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             } else {
                 bool yes;
                 __syncwarp();
-                values<double>(a, mine, x, false);
-                id = choose<double>(a, mine, x, false, yes);
+                values(a, mine, x);
+                id = choose(a, mine, x, false, yes);
             }
         }
         if (lane >= a.topk) id = -1;
@@ -400,12 +430,12 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a) {
         const T* x = static_cast<const T*>(a.logits) + t * a.E;
         bool sure;
         __syncwarp();
-        values<float>(a, reinterpret_cast<float*>(mine), x, by_logit);
-        int id = choose<float>(a, reinterpret_cast<float*>(mine), x, by_logit, sure);
+        values(a, reinterpret_cast<float*>(mine), x, by_logit);
+        int id = choose(a, reinterpret_cast<float*>(mine), x, by_logit, sure);
         if (!sure) {
             __syncwarp();
-            values<double>(a, reinterpret_cast<double*>(mine), x, false);
-            id = choose<double>(a, reinterpret_cast<double*>(mine), x, false, sure);
+            values(a, reinterpret_cast<long long*>(mine), x);
+            id = choose(a, reinterpret_cast<long long*>(mine), x, false, sure);
         }
         bool nan = false;
         for (int e = lane; e < a.E; e += 32) nan |= to_f32(x[e]) != to_f32(x[e]);
