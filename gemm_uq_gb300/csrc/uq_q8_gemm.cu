@@ -1,27 +1,33 @@
 // uq_q8_gemm.cu -- product of 8-bit operands with one scale per row of each:
 //     y[m][n] = sx[m] * sw[n] * sum_k x[m][k] * w[n][k].
 //
-// Few tokens (q8_gemv_kernel): the integer tensor instruction mma.m16n8k32 (s8 x s8 -> s32) on 16 rows of w and 8 tokens.  Where a lane's k lie in the
-// instruction does not matter as long as both operands agree, so a lane takes 16 consecutive k of its rows with one
-// 16-byte load straight from global memory and feeds them to two instructions.
+// Few tokens (q8_gemv_kernel): the integer tensor instruction mma.m16n8k32 (s8 x s8 -> s32) on 16 rows of w and 8 tokens.
+// Where a lane's k lie in the instruction does not matter as long as both operands agree, so a lane takes 16 consecutive k
+// of its rows with one 16-byte load straight from global memory and feeds them to two instructions.
 // A CTA takes 32 rows of w: two warps of 16 rows times four shares of k; a cluster of S CTAs shares k further where the
 // rows alone would leave SMs idle.  The shares' integer sums are added in shared memory, in any order the same.
+// 14336 x 4096, one to eight tokens in codes: 12.9 us (4.6 TB/s, of which 3 us are a kernel's start and end).
 //
 // More tokens (q8_tc_kernel): this part multiplies integers at a tenth of its 16-bit floating-point rate, and an int8 is
-// exact in fp16, so the product runs on tcgen05 kind::f16 with fp32 accumulators.  Products are below 2^14 and the sums of
+// exact in fp16, so the product runs on tcgen05 kind::f16 with fp32 accumulators.  Products are at most 2^14 and the sums of
 // 1024 k at most 2^24: exact.  After each 1024 k the accumulator is added to fp32 sums in registers.
 //   A: 128 rows of w per CTA.  Their int8 comes by TMA; eight warps widen it and write it straight to tensor memory, so that
 //      of the two operands only the tokens cross shared memory a second time.
 //   B: the tokens as fp16, widened once before (launch_q8_widen, or the quantizer writes fp16 at once), by TMA.
 //   D: 128 lanes (rows of w) x TN columns (tokens).
-// Stages of 128 k.  Warp 0 loads, warp 1 issues the MMAs, warps 4..11 widen, and read the accumulator when a chunk of 1024 k
-// or a tile is complete: by then they have widened all but one of the stages ahead, so the MMAs wait for the reads alone.
+// Stages of 128 k.  Warp 0 loads the weights, warp 2 the tokens, warp 1 issues the MMAs, warps 4..11 widen in two groups that
+// take the stages in turn, and read the accumulator when a chunk of 1024 k or a tile is complete: by then they have widened
+// all but one of the stages ahead.  A finished tile's outputs are written behind the next tile's stages.
 // PAIR: two CTAs work on 256 rows of w x 256 tokens (cta_group::2), each holding its 128 rows and half of the tokens: with
 // one CTA per tile a 128 x 256 tile needs 80 KB of shared memory traffic in the 512 cycles that 64 k compute, which is more
 // than it delivers; the pair 48.
 // Few tiles: a cluster of S CTAs shares a tile's k, and adds its fp32 sums through distributed shared memory in rank order.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is freed,
 // and the fault word tells.
+// 8192^3 660 us (39 of them widening the tokens; 1.67 PFLOP/s, 0.84 of the measured bf16 burst rate); 1024 x 4096 x 4096 31 us;
+// 64 x 14336 x 4096 19.5 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the way of a stage through its ring (load, widening,
+// MMAs: 430 ns with 128 tokens, of which the MMAs are 270; pairs 690 to 800 of 530), for few tokens the start, the widening
+// kernel before (2 us) and the sums of shared tiles (2 us).
 #include <cuda.h>
 #include <algorithm>
 #include <atomic>
@@ -82,6 +88,13 @@ __device__ __forceinline__ void store_one(const Q8GemmArgs& a, long long at, flo
     else static_cast<float*>(a.y)[at] = v;
 }
 
+// a load that stays where it is written: ahead of the barriers between it and its use
+__device__ __forceinline__ uint4 ldg_now(const int8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // X int8_t: the tokens are codes with scales.  Else there is one token, a row of X, which every CTA quantizes for itself as
 // quantize_q8 does: all of it for the scale, its own share of k for the codes, which go to shared memory.  Its first weights
 // are on their way meanwhile.
@@ -110,8 +123,11 @@ __global__ void __launch_bounds__(THREADS, 3) q8_gemv_kernel(const Q8GemmArgs a,
             for (int i = 0; i < UNROLL; ++i) {
                 const int k = (b + i) * 64;
                 const bool in = b + i < b1 && k + 16 * t < a.K;
-                p[i] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + k)) : make_uint4(0, 0, 0, 0);
-                q[i] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + k)) : make_uint4(0, 0, 0, 0);
+                p[i] = q[i] = make_uint4(0, 0, 0, 0);
+                if (in) {
+                    p[i] = ldg_now(w0 + k);
+                    q[i] = ldg_now(w1 + k);
+                }
             }
         };
         if constexpr (RAW) {
@@ -761,18 +777,25 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     }
 }
 
-// int8 codes -> fp16, 16 a thread; the product that follows may start meanwhile
+// int8 codes -> fp16, 16 at a time, four of a thread under way together; the product that follows may start meanwhile
 __global__ void __launch_bounds__(256) q8_widen_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, long long n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-        const uint4 v = x[i];
-        uint4 lo, hi;
-        widen4(v.x, lo.x, lo.y);
-        widen4(v.y, lo.z, lo.w);
-        widen4(v.z, hi.x, hi.y);
-        widen4(v.w, hi.z, hi.w);
-        out[2 * i] = lo;
-        out[2 * i + 1] = hi;
+    for (long long i = blockIdx.x * 1024LL + threadIdx.x; i < n; i += gridDim.x * 1024LL) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * 256 < n) v[j] = x[i + j * 256];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i + j * 256 >= n) break;
+            uint4 lo, hi;
+            widen4(v[j].x, lo.x, lo.y);
+            widen4(v[j].y, lo.z, lo.w);
+            widen4(v[j].z, hi.x, hi.y);
+            widen4(v[j].w, hi.z, hi.w);
+            out[2 * (i + j * 256)] = lo;
+            out[2 * (i + j * 256) + 1] = hi;
+        }
     }
 }
 
@@ -868,8 +891,8 @@ bool pays_in_pairs(const Q8GemmArgs& g, int sms) {
 bool q8_gemm_wide(int M) { return M > TOKENS; }
 
 cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st) {
-    const long long n = (long long)M * K / 16, ctas = (n + 255) / 256;
-    q8_widen_kernel<<<(unsigned)std::min(ctas, 16LL * sms), 256, 0, st>>>(reinterpret_cast<const uint4*>(x), static_cast<uint4*>(x16), n);
+    const long long n = (long long)M * K / 16, ctas = (n + 1023) / 1024;
+    q8_widen_kernel<<<(unsigned)std::min(ctas, 8LL * sms), 256, 0, st>>>(reinterpret_cast<const uint4*>(x), static_cast<uint4*>(x16), n);
     return cudaGetLastError();
 }
 
