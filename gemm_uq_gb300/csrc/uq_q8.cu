@@ -10,7 +10,9 @@
 // Its gradient, g = dy gamma and n = h r:  dx = r (g - n mean(g n)) + dh,  dgamma = sum over rows of dy n.
 //
 // All of it is bound by memory: a row is read once and written once, in the widest accesses that its address, stride and
-// length allow.
+// length allow.  Small calls are a launch and a chain of latencies: one row of 4096 2.4 us.
+#include <atomic>
+
 #include "uq_q8.cuh"
 
 namespace uq {
@@ -19,6 +21,7 @@ namespace {
 
 constexpr int MAX_THREADS = 1024;               // of a row; of the gradient's, whose threads hold more
 constexpr int GRAD_THREADS = 512;
+constexpr int PIPE_THREADS = 256;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -26,6 +29,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// A thread's own prefetches: it copies 16-byte parts of a coming row to shared memory, each row's as one group, and reads back
+// what it copied itself, so no other thread is waited for.
+__device__ __forceinline__ void copy_ahead(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+constexpr int ROWS_AHEAD = 2;                   // groups under way
+__device__ __forceinline__ void oldest_copies_landed() { asm volatile("cp.async.wait_group %0;" :: "n"(ROWS_AHEAD - 1) : "memory"); }
+template <class W> __device__ __forceinline__ W copied(uint32_t at) {
+    static_assert(sizeof(W) == 16, "parts of 16 bytes");
+    uint4 u;
+    W w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+    memcpy(&w, &u, 16);
+    return w;
+}
 
 struct RowArgs {
     const void *x, *residual, *gamma;
@@ -49,27 +69,55 @@ __device__ __forceinline__ float larger(float a, float b) {
 
 // NORM: the norm; else the plain quantizer (h, y, residual and gamma unused).
 // V elements per access, NV accesses of a thread kept in registers; what a longer row has beyond is read again.
-// A row is a chain of loads, a reduction, and stores, with about 15 instructions an element, half of what the SM can issue in
-// the time that it takes.  Measured, 8192 rows of 8192 bf16 with all outputs: 256 threads a row with four accesses each 134 us
-// (4.5 TB/s; the quantizer alone 44 us, also 4.5 TB/s), 512 with two 152, 128 with eight and gamma in registers 174, 1024 with
-// one and the next row's loads issued ahead 172.
-template <class T, int V, int NV, bool NORM>
-__global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
+// PIPE (16-byte accesses, rows without a rest, many of them): the next rows' loads are under way while a row is reduced and
+// written, and gamma stays in registers.  Without, a row is a chain of loads, a reduction, and stores; measured, 8192 rows of 8192
+// bf16 with all outputs: PIPE 100 us (6.0 TB/s, 0.89 of the measured copy); else 256 threads a row with four accesses each 134
+// us, 512 with two 152; the quantizer 37 (5.4 TB/s) and 44 us.
+template <class T, int V, int NV, bool NORM, bool PIPE>
+__global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 1) row_kernel(const RowArgs a) {
     using W = Vec<T, V>;
     __shared__ float sums[2][MAX_THREADS / 32];
     __shared__ float maxima[2][MAX_THREADS / 32];
+    extern __shared__ __align__(16) uint8_t ahead[];               // PIPE: [row][x, residual][part][thread] of 16 bytes
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
     const int nvec = a.D / V;
+    const long long step = (long long)gridDim.x * per_cta;
     if constexpr (!NORM)
         if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const W* gamma = static_cast<const W*>(a.gamma);
+    auto x_of = [&](long long row) { return reinterpret_cast<const W*>(static_cast<const T*>(a.x) + row * a.ldx); };
+    auto res_of = [&](long long row) { return reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + row * a.D); };
+    const bool has_res = NORM && a.residual;
+    uint32_t slot = smem_u32(ahead) + threadIdx.x * 16, part = blockDim.x * 16, other = 0;
+    auto request = [&](long long row) {
+        if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) {
+                    copy_ahead(slot + other + i * part, x_of(row) + tid + i * a.group);
+                    if (has_res) copy_ahead(slot + other + (NV + i) * part, res_of(row) + tid + i * a.group);
+                }
+        }
+        copies_issued();
+        other ^= (has_res ? 2 : 1) * NV * part;
+    };
+    W held[PIPE && NORM ? NV : 1];
+    if constexpr (PIPE) {
+        for (int i = 0; i < ROWS_AHEAD; ++i) request((long long)blockIdx.x * per_cta + mine + i * step);
+        if constexpr (NORM) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) held[i] = gamma[tid + i * a.group];
+        }
+    }
+    auto gam = [&](int i) { return !NORM ? W() : (PIPE ? held[PIPE && NORM ? i : 0] : gamma[tid + i * a.group]); };
     int buf = 0;
-    for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += (long long)gridDim.x * per_cta, buf ^= 1) {
+    for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += step, buf ^= 1) {
         const long long row = base + mine;
         const bool on = row < a.rows;
-        const W* x = reinterpret_cast<const W*>(static_cast<const T*>(a.x) + (on ? row : 0) * a.ldx);
-        const W* res = NORM && a.residual ? reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + (on ? row : 0) * a.D) : nullptr;
+        const W* x = x_of(on ? row : 0);
+        const W* res = has_res ? res_of(on ? row : 0) : nullptr;
         auto add = [&](const W& w, const W& r) {                   // h
             float f[V], g[V];
             unpack(w, f);
@@ -91,7 +139,19 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
             }
         };
         W kept[NV];
-        if (on) {
+        if constexpr (PIPE) {
+            oldest_copies_landed();
+            if (on) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * a.group < nvec) {
+                        kept[i] = copied<W>(slot + other + i * part);
+                        if (has_res) kept[i] = add(kept[i], copied<W>(slot + other + (NV + i) * part));
+                        look(kept[i], gam(i));
+                    }
+            }
+            request(row + ROWS_AHEAD * step);                      // over what has just been read
+        } else if (on) {
             if (res) {
                 W r[NV];
 #pragma unroll
@@ -110,7 +170,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) look(kept[i], NORM ? gamma[tid + i * a.group] : W());
+                if (tid + i * a.group < nvec) look(kept[i], gam(i));
             for (int v = tid + NV * a.group; v < nvec; v += a.group) look(load(v), NORM ? gamma[v] : W());
         }
         if constexpr (NORM) sum = warp_sum(sum);
@@ -167,10 +227,11 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
                 }
             };
             // before anything is written, which may be over x or the residual
-            for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), gamma[v]);
+            if constexpr (!PIPE)
+                for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), gamma[v]);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gamma[tid + i * a.group]);
+                if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gam(i));
         } else {
             const float s = bad ? nan : __fdiv_rn(most, 127.f);
             if (tid == 0) a.scales[row] = s;
@@ -191,7 +252,8 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) row_kernel(const RowArgs a) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i]);
-            for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v));
+            if constexpr (!PIPE)
+                for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v));
         }
     }
 }
@@ -226,18 +288,39 @@ struct GradArgs {
 // A group of threads takes every so many-th row; its share of dgamma stays in registers (of a longer row, in its CTA's row of
 // `partials`, where a CTA has one group) until its rows are done; then a CTA's groups are added in order.  Named barriers, so
 // that a CTA's groups do not wait for one another.  gamma stays in registers: read again for every row, four accesses a thread,
-// it kept L1 73 % busy (8192 rows of 4096 bf16 with dh 96 us, so 68 us: 3.9 TB/s).
-template <class T, int V, int NV>
+// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 57 us (4.7 TB/s, the addition of the partials in it), without PIPE 68, with gamma read again 96.
+template <class T, int V, int NV, bool PIPE>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {
     using W = Vec<T, V>;
-    extern __shared__ float together[];         // several groups: [D]
+    extern __shared__ __align__(16) uint8_t ahead[];               // PIPE: [row][dy, h, dh][part][thread] of 16 bytes; then
     __shared__ float2 sums[2][GRAD_THREADS / 32];
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
     const int nvec = a.D / V;
+    const long long step = (long long)gridDim.x * per_cta;
+    const uint32_t part16 = blockDim.x * 16, stage = 3 * NV * part16;
+    float* together = reinterpret_cast<float*>(ahead + (PIPE ? ROWS_AHEAD * stage : 0));           // several groups: [D]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                // the kernel that adds the partials
     const W* gamma = static_cast<const W*>(a.gamma);
     float* part = a.partials + (long long)blockIdx.x * a.D;
+    const uint32_t slot = smem_u32(ahead) + threadIdx.x * 16;
+    uint32_t other = 0;
+    auto request = [&](long long row) {
+        if (row < a.rows) {
+            const long long at = row * nvec + tid;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) {
+                    copy_ahead(slot + other + i * part16, static_cast<const W*>(a.dy) + at + i * a.group);
+                    copy_ahead(slot + other + (NV + i) * part16, static_cast<const W*>(a.h) + at + i * a.group);
+                    if (a.dh) copy_ahead(slot + other + (2 * NV + i) * part16, static_cast<const W*>(a.dh) + at + i * a.group);
+                }
+        }
+        copies_issued();
+        other ^= stage;
+    };
+    if constexpr (PIPE)
+        for (int i = 0; i < ROWS_AHEAD; ++i) request((long long)blockIdx.x * per_cta + mine + i * step);
     W gam[NV];
     float dg[NV][V] = {};
 #pragma unroll
@@ -247,7 +330,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
 #pragma unroll
         for (int j = 0; j < V; ++j) part[(long long)v * V + j] = 0.f;
     int buf = 0;
-    for (long long row = (long long)blockIdx.x * per_cta + mine; row < a.rows; row += (long long)gridDim.x * per_cta, buf ^= 1) {
+    for (long long row = (long long)blockIdx.x * per_cta + mine; row < a.rows; row += step, buf ^= 1) {
         const long long at = row * nvec;
         const W *dy = static_cast<const W*>(a.dy) + at, *h = static_cast<const W*>(a.h) + at;
         const W* dh = a.dh ? static_cast<const W*>(a.dh) + at : nullptr;
@@ -265,16 +348,28 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
             }
         };
         W ku[NV], kw[NV], kd[NV];
+        if constexpr (PIPE) {
+            oldest_copies_landed();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (tid + i * a.group < nvec) {
-                ku[i] = dy[tid + i * a.group];
-                kw[i] = h[tid + i * a.group];
-                if (dh) kd[i] = dh[tid + i * a.group];
-            }
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) {
+                    ku[i] = copied<W>(slot + other + i * part16);
+                    kw[i] = copied<W>(slot + other + (NV + i) * part16);
+                    if (dh) kd[i] = copied<W>(slot + other + (2 * NV + i) * part16);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * a.group < nvec) {
+                    ku[i] = dy[tid + i * a.group];
+                    kw[i] = h[tid + i * a.group];
+                    if (dh) kd[i] = dh[tid + i * a.group];
+                }
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (tid + i * a.group < nvec) look(ku[i], kw[i], gam[i]);
+        if constexpr (PIPE) request(row + ROWS_AHEAD * step);      // over what has just been read
         for (int v = tid + NV * a.group; v < nvec; v += a.group) look(dy[v], h[v], gamma[v]);
         s1 = warp_sum(s1);
         s2 = warp_sum(s2);
@@ -383,6 +478,19 @@ template <class T, class F> cudaError_t with_shape(int v, int nv, F&& f) {
     return by_nv(std::integral_constant<int, 1>());
 }
 
+// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
+using Done = std::atomic<bool>[64];
+template <class K> cudaError_t configure(K kernel, Done& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sms, cudaStream_t st) {
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
@@ -391,9 +499,21 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
         const Shape s = shape_of(a.D / v, MAX_THREADS, 4, a.rows <= 2 * sms);
         a.group = s.group;
         const int block = s.group < 128 ? 128 : s.group, per = block / s.group;
-        const long long tiles = ((long long)a.rows + per - 1) / per, most = (long long)sms * (2048 / block);
+        const long long tiles = ((long long)a.rows + per - 1) / per;
+        if (v * sizeof(T) == 16 && s.nv == 4 && block <= PIPE_THREADS && s.group * 4 >= a.D / v && a.rows > 2 * sms) {
+            constexpr int V = 16 / sizeof(T);
+            static Done done = {};
+            const cudaError_t e = configure(row_kernel<T, V, 4, NORM, true>, done);
+            if (e != cudaSuccess) return e;
+            const long long most = (long long)sms * 3 * (PIPE_THREADS / block);
+            row_kernel<T, V, 4, NORM, true><<<(unsigned)(tiles < most ? tiles : most), block,
+                                              ROWS_AHEAD * (a.residual ? 2 : 1) * 4 * 16 * block, st>>>(a);
+            return cudaGetLastError();
+        }
+        const long long most = (long long)sms * (2048 / block);
         return with_shape<T>(v, s.nv, [&](auto V, auto NV) {
-            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM><<<(unsigned)(tiles < most ? tiles : most), block, 0, st>>>(a);
+            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM, false>
+                <<<(unsigned)(tiles < most ? tiles : most), block, 0, st>>>(a);
             return cudaGetLastError();
         });
     });
@@ -455,9 +575,20 @@ cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma
     const GradArgs a = {dy, h, gamma, dh, dx, partials, rows, D, eps, s.group};
     cudaError_t e = with_dtype(type, [&](auto t) {
         using T = decltype(t);
-        return with_shape<T>(access<T>(D, D), s.nv, [&](auto V, auto NV) {
-            norm_grad_kernel<T, decltype(V)::value, decltype(NV)::value>
-                <<<P, grad_block(s), grad_block(s) > s.group ? (size_t)D * sizeof(float) : 0, st>>>(a);
+        const int block = grad_block(s);
+        const size_t add = block > s.group ? (size_t)D * sizeof(float) : 0;
+        return with_shape<T>(access<T>(D, D), s.nv, [&](auto V_, auto NV_) {
+            constexpr int V = decltype(V_)::value, NV = decltype(NV_)::value;
+            if constexpr (V * sizeof(T) == 16 && NV <= 2) {
+                if (rows > 2 * sms) {
+                    static Done done = {};
+                    const cudaError_t f = configure(norm_grad_kernel<T, V, NV, true>, done);
+                    if (f != cudaSuccess) return f;
+                    norm_grad_kernel<T, V, NV, true><<<P, block, ROWS_AHEAD * 3 * NV * 16 * block + add, st>>>(a);
+                    return cudaGetLastError();
+                }
+            }
+            norm_grad_kernel<T, V, NV, false><<<P, block, add, st>>>(a);
             return cudaGetLastError();
         });
     });
