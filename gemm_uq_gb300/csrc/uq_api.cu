@@ -1206,10 +1206,15 @@ uq_status uq_quantize_q8(const void* x, uq_dtype xtype, long long ldx, int8_t* c
                          void* stream) {
     uq_status s = check_rows(rows, K, xtype);
     if (s != UQ_OK) return s;
-    if (rows == 0 || K == 0) return UQ_OK;
-    if ((s = check_x8(x, ldx, K)) != UQ_OK) return s;
-    if (!codes || !scales) return fail(UQ_ERR_INVALID, "codes or scales is NULL");
+    if (rows == 0) return UQ_OK;
+    if (!scales) return fail(UQ_ERR_INVALID, "codes or scales is NULL");
     if (!aligned16(codes) || !aligned16(scales)) return fail(UQ_ERR_ALIGN, "pointers must be 16-byte aligned");
+    if (K == 0) {
+        const cudaError_t e = cudaMemsetAsync(scales, 0, (size_t)rows * sizeof(float), static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? UQ_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!codes) return fail(UQ_ERR_INVALID, "codes or scales is NULL");
+    if ((s = check_x8(x, ldx, K)) != UQ_OK) return s;
     DeviceState* ds = nullptr;
     if ((s = device_state(&ds, nullptr)) != UQ_OK) return s;
     cudaError_t e = uq::launch_quantize_q8(x, xtype, ldx, codes, nullptr, scales, rows, K, false, ds->sms,

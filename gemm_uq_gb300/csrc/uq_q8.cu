@@ -288,7 +288,8 @@ struct GradArgs {
 // A group of threads takes every so many-th row; its share of dgamma stays in registers (of a longer row, in its CTA's row of
 // `partials`, where a CTA has one group) until its rows are done; then a CTA's groups are added in order.  Named barriers, so
 // that a CTA's groups do not wait for one another.  gamma stays in registers: read again for every row, four accesses a thread,
-// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 57 us (4.7 TB/s, the addition of the partials in it), without PIPE 68, with gamma read again 96.
+// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 57 us (4.7 TB/s, the addition of the
+// partials in it), without PIPE 68, with gamma read again 96.
 template <class T, int V, int NV, bool PIPE>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {
     using W = Vec<T, V>;

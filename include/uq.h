@@ -482,7 +482,7 @@ uq_status uq_gemm_mx_grouped(const uint8_t* xcodes, const uint8_t* xscales, cons
  * uq_quantize_q8 -- rows -> codes and scales: s = max|x| / 127, code = RNE(x / s), both fp32 divisions; a row of zeros has
  * s = 0, and a row that holds a NaN or an infinity s = NaN and codes 0, so that all of it reads back as NaN.
  *   x (device) [rows][K] of xtype, rows ldx elements apart (any stride; every row element-aligned); codes (device) int8
- *   [rows][K], scales (device) fp32 [rows], written.  K of any size.  Asynchronous.
+ *   [rows][K], scales (device) fp32 [rows], written.  K of any size (0: the scales are 0).  Asynchronous.
  */
 uq_status uq_quantize_q8(const void* x, uq_dtype xtype, long long ldx, int8_t* codes, float* scales, int rows, int K,
                          void* stream);
@@ -496,7 +496,8 @@ uq_status uq_dequant_q8(const int8_t* codes, const float* scales, void* out, uq_
  *     h = x + residual (fp32, rounded to `type`: the residual stream, of which the norm is taken),
  *     y[j] = h[j] / sqrt(mean(h^2) + eps) * gamma[j]  (fp32),  s = max|y| / 127,  code = y / s to the nearest integer
  *     (ties to even; y and s in fp32 before they are rounded: a quotient within 2^-20 of a tie may go either way).
- *   x (device) [rows][D] of `type`, rows ldx elements apart; residual (device, or NULL: h = x) [rows][D]; gamma (device) [D].
+ *   x (device) [rows][D] of `type`, rows ldx elements apart; residual (device, or NULL: h = x) [rows][D]; gamma
+ *   (device) [D].
  *   h, y (device, or NULL: not wanted) [rows][D] of `type`; codes (device) int8 [rows][D] and scales (device) fp32 [rows],
  *   both or neither; written.  h may be x (with ldx = D) or residual, and so may y.
  * The mean of the squares has to lie within fp32.  A row with a NaN or an infinity gets a NaN scale and codes 0.  The
@@ -522,7 +523,8 @@ uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, cons
  *   x: int8 codes [M][K] with xscales fp32 [M] (both device; xtype and ldx ignored); or, with xscales NULL, rows of xtype,
  *      ldx apart, quantized in the call as uq_quantize_q8 does (into the per-stream workspace)
  *   w (device) int8 [N][K], wscales (device) fp32 [N]; y (device) [M][N], written.
- * K a multiple of 16, at most 131056 (UQ_ERR_UNSUPPORTED beyond).  M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Equal calls give equal bits.
+ * K a multiple of 16, at most 131056 (UQ_ERR_UNSUPPORTED beyond).  M == 0 or N == 0 is a no-op; K == 0 writes zeros.
+ * Equal calls give equal bits.
  * Workspace and stream capture as uq_gemm.
  */
 uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float* xscales, const int8_t* w,

@@ -175,6 +175,8 @@ def test_nothing_to_do():
     dx, dgamma = uq.rmsnorm_grad(e, e, gamma, 1e-5)
     assert dx.shape == (0, 64) and not dgamma.any()
     assert uq.dequant_q8((codes, scales)).shape == (0, 64)
+    codes, scales = uq.quantize_q8(torch.empty(5, 0, device=DEV))
+    assert codes.shape == (5, 0) and not scales.any()
 
 
 def test_on_another_stream_and_in_graphs():
@@ -202,3 +204,41 @@ def test_on_another_stream_and_in_graphs():
     for o, w, rows in ((outs[0], want, T), (outs[1], half, 50)):
         assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
         assert torch.equal(o[2], q[0][:rows]) and torch.equal(o[3], q[1][:rows])
+
+
+def test_offsets_past_32_bits():
+    """Over 2^31 elements: the last rows of the quantizer, the norm, its gradient and the values."""
+    T, D = 70000, 32768
+    x = torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+    x.zero_()
+    x[-3:] = _rows(1, 3, D, "bf16")
+    gamma = _rows(3, 1, D, "bf16")[0].contiguous()
+    tail = x[-3:].clone()
+    q = uq.quantize_q8(x)
+    want = uq.quantize_q8(tail)
+    assert torch.equal(q[0][-3:], want[0]) and torch.equal(q[1][-3:], want[1]) and not q[0][:100].any()
+    assert torch.equal(uq.dequant_q8(q)[-3:], uq.dequant_q8(want))
+    h, y, q = uq.rmsnorm_q8(x, gamma, 1e-5, residual=x, normed=True)
+    _check_norm((tail.float() * 2).bfloat16(), gamma, 1e-5, y[-3:], (q[0][-3:], q[1][-3:]), "bf16")
+    assert torch.equal(h[-3:], (tail.float() * 2).bfloat16()) and not y[:100].any()
+    del h, y, q
+    dx, dgamma = uq.rmsnorm_grad(x, x, gamma, 1e-2)
+    ref, rg = oq.rmsnorm_grad(n(tail), n(tail), n(gamma), 1e-2)
+    assert np.all(np.abs(n(dx[-3:]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2e-3 * np.abs(ref).max())
+    assert np.all(np.abs(n(dgamma) - rg) <= 1e-2 * np.abs(rg).max()) and not dx[:100].any()
+
+
+def test_many_short_rows():
+    """Groups of one warp and of several, more rows than the grid takes at once."""
+    for T, D, dtype in ((40000, 8, "bf16"), (5000, 256, "fp16"), (3000, 1024, "fp32"), (1000, 8192, "bf16"), (700, 8200, "bf16")):
+        x, r, gamma = _rows(1, T, D, dtype), _rows(2, T, D, dtype), _rows(3, 1, D, dtype)[0]
+        h, y, q = uq.rmsnorm_q8(x, gamma, 1e-5, residual=r, normed=True)
+        assert torch.equal(h, (x.float() + r.float()).to(x.dtype))
+        _check_norm(h, gamma, 1e-5, y, q, dtype)
+        rq, rs = oq.quantize(f32(x))
+        codes, scales = uq.quantize_q8(x)
+        assert np.array_equal(codes.cpu().numpy(), rq) and np.array_equal(scales.cpu().numpy(), rs)
+        # in place, with the next rows' copies under way
+        a = x.clone()
+        got = uq.rmsnorm_q8(a, gamma, 1e-5, residual=r, h=a)
+        assert torch.equal(a, h) and torch.equal(got[2][0], q[0])

@@ -163,3 +163,17 @@ def test_pairs_of_ctas(M, N, K):
         y16 = uq.gemm_w8a8(x, w)
         assert torch.equal(y16, y.bfloat16())
     assert uq.device_fault() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(70000, 32768, 64), (3, 70000, 32768), (40, 70000, 32768)])
+def test_offsets_past_32_bits(M, N, K):
+    """Over 2^31 outputs, or weights: the ends against integer sums of those rows and columns."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = torch.randint(-127, 128, (M, K), dtype=torch.int8, device=DEV, generator=g)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV, generator=g)
+    sx, sw = torch.rand(M, device=DEV, generator=g), torch.rand(N, device=DEV, generator=g)
+    y = uq.gemm_w8a8((x, sx), (w, sw))
+    for rows, cols in ((slice(-9, None), slice(-300, None)), (slice(0, 9), slice(0, 300))):
+        _check(y[rows, cols], (x[rows].contiguous(), sx[rows]), (w[cols].contiguous(), sw[cols]), "bf16")
+    assert uq.device_fault() == 0

@@ -33,7 +33,8 @@ def _bad(L, status, got):
 def test_quantize_and_dequant(L, p):
     q, d = L.uq_quantize_q8, L.uq_dequant_q8
     assert q(None, 0, 8, None, None, 0, 8, None) == 0 and d(None, None, None, 0, 0, 8, None) == 0
-    assert q(None, 0, 8, None, None, 3, 0, None) == 0 and d(None, None, None, 0, 3, 0, None) == 0
+    assert d(None, None, None, 0, 3, 0, None) == 0
+    _bad(L, INVALID, q(None, 0, 8, None, None, 3, 0, None))   # rows without elements have scales, too
     _bad(L, INVALID, q(p, 0, 8, p, p, -1, 8, None))
     _bad(L, INVALID, q(p, 3, 8, p, p, 1, 8, None))
     _bad(L, INVALID, q(p, 0, 7, p, p, 1, 8, None))            # rows closer than they are long
