@@ -610,7 +610,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         // up the widening for longer than there are stages ahead.  This code is in the loop once, and for one type: it is
         // executed once a tile, so what it takes is its fetching (a 256 x 256 tile's epilogue, for three types in four places:
         // 18000 cycles).
-        constexpr int GROUPS = COLS / 16;
+        constexpr int GROUPS = COLS / 16, READ = COLS < 32 ? COLS : 32;
         int written = GROUPS;
         float sx[(COLS + 31) / 32], sw = 0.f;                      // scales of tokens 32 i + lane, and of this lane's output
         auto write_groups = [&](int to) {
@@ -628,8 +628,9 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         };
         for (int tile = first, j = 0; ok;) {
             const bool over = tile >= tiles;
-            // a complete chunk is read when the stages ahead are widened, or another one ends
-            const bool reads = pending && (over || i - boundary >= AS - 1 || ends(j, which));
+            // a complete chunk is read when the stages ahead are widened (of pairs, whose group 0 has the first of them, before
+            // its second one), or another one ends
+            const bool reads = pending && (over || i - boundary >= (PAIR && half == 0 ? AS - 2 : AS - 1) || ends(j, which));
             if (written < GROUPS && (reads || over || widened)) write_groups(reads || over ? GROUPS : written + 2);
             widened = false;
             if (reads) {
@@ -639,12 +640,14 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                 fence_after();
                 // sums = (a tile's first chunk ? 0 : sums) + chunk, in place: as an expression the sums took twice the registers
 #pragma unroll
-                for (int c = 0; c < COLS; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lanes + half * COLS + c, r);
+                for (int c = 0; c < COLS; c += READ) {
+                    uint32_t r[READ];
+#pragma unroll
+                    for (int e = 0; e < READ; e += 16)
+                        tmem_ld16(tmem + lanes + half * COLS + c + e, *reinterpret_cast<uint32_t(*)[16]>(r + e));
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) asm volatile("{\n\t.reg .pred p;\n\t.reg .f32 t;\n\tsetp.ne.b32 p, %2, 0;\n\tselp.f32 t, 0f00000000, %0, p;\n\tadd.f32 %0, t, %1;\n\t}"
+                    for (int e = 0; e < READ; ++e) asm volatile("{\n\t.reg .pred p;\n\t.reg .f32 t;\n\tsetp.ne.b32 p, %2, 0;\n\tselp.f32 t, 0f00000000, %0, p;\n\tadd.f32 %0, t, %1;\n\t}"
                                      : "+f"(sums[c + e]) : "f"(__uint_as_float(r[e])), "r"((int)fresh));
                 }
                 fence_before();
