@@ -1319,8 +1319,10 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
     a.M = M;
     a.N = N;
     a.K = K;
-    const bool wide = uq::q8_gemm_wide(M);
+    const uq::Q8Form form = uq::q8_gemm_form(M);
+    const bool wide = form == uq::Q8_WIDE;
     void* x16 = nullptr;
+    bool before = false;                         // a kernel of this call runs before the product
     if (!xscales && uq::q8_gemm_quantizes(x, xtype, M, K)) {
         a.raw = x;
         a.xtype = xtype;
@@ -1335,13 +1337,14 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
         if (xscales) {
             e = uq::launch_q8_widen(a.x, x16, M, K, ds->sms, st);
         } else {
-            e = uq::launch_quantize_q8(x, xtype, ldx, codes, x16, scales, M, K, wide, ds->sms, st);
+            e = uq::launch_quantize_q8(x, xtype, ldx, codes, x16, scales, M, K, form != uq::Q8_GEMV, ds->sms, st);
             a.x = codes;
             a.sx = scales;
         }
         if (e != cudaSuccess) return cuda_fail(e, "8-bit quantization launch");
+        before = true;
     }
-    e = wide ? uq::launch_q8_gemm_wide(a, x16, ds->sms, st) : uq::launch_q8_gemm(a, ds->sms, st);
+    e = form == uq::Q8_GEMV ? uq::launch_q8_gemm(a, ds->sms, st) : uq::launch_q8_gemm_tc(a, x16, before, ds->sms, st);
     return e == cudaSuccess ? UQ_OK : cuda_fail(e, "8-bit product launch");
 }
 

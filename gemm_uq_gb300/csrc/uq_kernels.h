@@ -242,9 +242,12 @@ struct Q8GemmArgs {
 };
 // whether launch_q8_gemm quantizes the token itself
 bool q8_gemm_quantizes(const void* x, int type, int M, int K);
-bool q8_gemm_wide(int M);           // whether a product of so many tokens takes their codes as fp16 (launch_q8_gemm_wide)
+// how a product of so many tokens takes them: codes, launch_q8_gemm; codes, launch_q8_gemm_tc; as fp16, launch_q8_gemm_tc
+enum Q8Form { Q8_GEMV, Q8_CODES, Q8_WIDE };
+Q8Form q8_gemm_form(int M);
 cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st);
-cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& a, const void* x16, int sms, cudaStream_t st);
+// wait: the call's own kernel before it may still run
+cudaError_t launch_q8_gemm_tc(const Q8GemmArgs& a, const void* x16, bool wait, int sms, cudaStream_t st);
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, int sms, cudaStream_t st);
 
 // the router (uq_route.cu)

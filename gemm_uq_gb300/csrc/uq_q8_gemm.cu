@@ -13,7 +13,8 @@
 // 1024 k at most 2^24: exact.  After each 1024 k the accumulator is added to fp32 sums in registers.
 //   A: 128 rows of w per CTA.  Their int8 comes by TMA; eight warps widen it and write it straight to tensor memory, so that
 //      of the two operands only the tokens cross shared memory a second time.
-//   B: the tokens as fp16, widened once before (launch_q8_widen, or the quantizer writes fp16 at once), by TMA.
+//   B: the tokens as fp16, widened once before (launch_q8_widen, or the quantizer writes fp16 at once), by TMA; up to 32 tokens
+//      come as codes and are widened in the kernel.
 //   D: 128 lanes (rows of w) x TN columns (tokens).
 // Stages of 128 k.  Warp 0 loads the weights, warp 2 the tokens, warp 1 issues the MMAs, warps 4..11 widen in two groups that
 // take the stages in turn, and read the accumulator when a chunk of 1024 k or a tile is complete: by then they have widened
@@ -24,10 +25,10 @@
 // Few tiles: a cluster of S CTAs shares a tile's k, and adds its fp32 sums through distributed shared memory in rank order.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is freed,
 // and the fault word tells.
-// 8192^3 660 us (39 of them widening the tokens; 1.67 PFLOP/s, 0.84 of the measured bf16 burst rate); 1024 x 4096 x 4096 31 us;
-// 64 x 14336 x 4096 19.5 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the way of a stage through its ring (load, widening,
-// MMAs: 430 ns with 128 tokens, of which the MMAs are 270; pairs 690 to 800 of 530), for few tokens the start, the widening
-// kernel before (2 us) and the sums of shared tiles (2 us).
+// 8192^3 629 us (36 of them widening the tokens; 1.75 PFLOP/s, 0.88 of the measured bf16 burst rate); 1024 x 4096 x 4096 30 us;
+// 64 x 14336 x 4096 19.5 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the MMAs of pairs (a stage 660 ns where they take 530;
+// a deeper ring changed nothing); with 128 tokens the way of a stage through its ring (load, widening, MMAs: 430 ns, of which
+// the MMAs are 270); for few tokens the start, the widening kernel before (2 us) and the sums of shared tiles (2 us).
 #include <cuda.h>
 #include <algorithm>
 #include <atomic>
@@ -223,11 +224,13 @@ __global__ void __launch_bounds__(THREADS, 3) q8_gemv_kernel(const Q8GemmArgs a,
 // tcgen05
 
 constexpr unsigned int FAULT_Q8_WAIT = 32u;
-constexpr int TC_THREADS = 384;               // three warpgroups: producer and issuer, and two that widen
+constexpr int TC_THREADS = 384;                 // warpgroups: producers and issuer, and two that widen the weights
+constexpr int X_WARPS = 4;                      // of a fourth, which widens few tokens
 constexpr int STAGE_K = 128, W_BYTES = 128 * STAGE_K;
 constexpr int CHUNK = 1024 / STAGE_K;           // stages whose sums are exact
 constexpr int HEAD = 1024;                      // barriers and flags before the stages
 constexpr int WIDE_WARPS = 8;
+constexpr int MOST_CODES = 32;                  // most tokens that the kernel takes as int8 codes
 
 struct TcArgs8 {
     Q8GemmArgs g;
@@ -389,12 +392,18 @@ template <int TN> __device__ __forceinline__ Tile8 find_tile(const TcArgs8& a, i
 
 // Rings and tensor memory of a tile shape.
 template <int TN, bool PAIR> struct Plan8 {
+    // Up to 32 tokens are widened in the kernel, by a warpgroup of their own, in one launch: 10.6 us of host time a call instead
+    // of 15.3, and on the GPU 16 x 14336 x 4096 takes 18.7 us and 18.5.  More tokens add to what shared memory delivers: 64 x
+    // 14336 x 4096 21.3 us in the kernel and 19.5 with their own, under which the first weights are loaded.
+    static constexpr bool CODES = !PAIR && TN <= MOST_CODES;
+    static constexpr int THREADS = TC_THREADS + (CODES ? X_WARPS * 32 : 0);
     static constexpr int XR = PAIR ? TN / 2 : TN;                  // token rows of a CTA
-    static constexpr int X_BYTES = XR * STAGE_K * 2;
-    static constexpr int XS = TN >= 256 ? 5 : (TN == 128 ? 4 : 5); // stages of tokens, of weights, and widened ones
+    static constexpr int X_BYTES = XR * STAGE_K * 2, C_BYTES = CODES ? XR * STAGE_K : 0;
+    static constexpr int XS = TN >= 256 || TN == 64 ? 5 : 4;       // stages of fp16 tokens, of weights, and widened ones
     static constexpr int WS = TN >= 256 ? 3 : (TN == 128 ? 5 : (TN == 64 ? 8 : 10));
     static constexpr int AS = (512 - TN) / 64 < 8 ? (512 - TN) / 64 : 8;
-    static constexpr int RING = WS * W_BYTES + XS * X_BYTES;
+    static constexpr int CS = 4;                                   // of tokens' codes
+    static constexpr int RING = WS * W_BYTES + XS * X_BYTES + CS * C_BYTES;
     // Pairs have the accumulator in two halves of columns whose chunks end half a chunk apart: while one is read the MMAs go
     // on with the other, which in the two stages around the end of the chunk come in such an order that twice half a stage
     // lies between (a 256 x 256 tile's 1024 k: 8200 cycles of MMAs, and about 1000 from their end to the next one's start).
@@ -402,10 +411,11 @@ template <int TN, bool PAIR> struct Plan8 {
     static constexpr int HALVES = PAIR ? 2 : 1;
     static_assert(1024 + HEAD + RING <= 227 * 1024 && TN + 64 * AS <= 512, "memory");
 };
-enum { W_FULL = 0, W_EMPTY = 10, X_FULL = 20, X_EMPTY = 28, A_FULL = 36, A_EMPTY = 44, ACC_FULL = 52, ACC_EMPTY = 54, DRAINED = 56 };
+enum { W_FULL = 0, W_EMPTY = 10, X_FULL = 20, X_EMPTY = 28, A_FULL = 36, A_EMPTY = 44, ACC_FULL = 52, ACC_EMPTY = 54,
+       C_FULL = 56, C_EMPTY = 60, DRAINED = 64 };
 
 template <class T, int TN, bool PAIR>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(Plan8<TN, PAIR>::THREADS, 1)
 q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const TcArgs8 a) {
     using P = Plan8<TN, PAIR>;
     constexpr int XR = P::XR, XS = P::XS, WS = P::WS, AS = P::AS, HALVES = P::HALVES;
@@ -419,7 +429,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     auto bar = [&](int which) { return bar0 + 8 * which; };
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + DRAINED + 1);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_ptr + 1);
-    const uint32_t ring = smem_u32(head + HEAD), xring = ring + WS * W_BYTES;
+    const uint32_t ring = smem_u32(head + HEAD), xring = ring + WS * W_BYTES, cring = xring + XS * P::X_BYTES;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR || a.S > 1 ? cluster_rank() : 0;
     const uint32_t side = PAIR ? rank : 0;                         // which CTA of the pair
@@ -436,8 +446,12 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                 mbar_init(bars + W_EMPTY + i, WIDE_WARPS / 2);
             }
             for (int i = 0; i < XS; ++i) {
-                mbar_init(bars + X_FULL + i, 1);
+                mbar_init(bars + X_FULL + i, P::CODES ? X_WARPS : 1);
                 mbar_init(bars + X_EMPTY + i, 1);
+            }
+            for (int i = 0; i < P::CS; ++i) {
+                mbar_init(bars + C_FULL + i, 1);
+                mbar_init(bars + C_EMPTY + i, X_WARPS);
             }
             for (int i = 0; i < AS; ++i) {
                 mbar_init(bars + A_FULL + i, WIDE_WARPS / 2 * (PAIR ? 2 : 1));
@@ -505,36 +519,41 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         } else if (warp == 2) {
             // -------------------------------------------------------- tokens, which do
             after_prior_work(a);
+            constexpr int SLOTS = P::CODES ? P::CS : XS, FULL = P::CODES ? C_FULL : X_FULL, EMPTY = P::CODES ? C_EMPTY : X_EMPTY;
             int issued = 0, s = 0;
             uint32_t ph = 1;
             bool ok = true;
-            const uint32_t lead_full = PAIR ? cluster_addr(bar(X_FULL), 0) : bar(X_FULL);
+            const uint32_t lead_full = PAIR ? cluster_addr(bar(FULL), 0) : bar(FULL);
             for (int tile = first; ok && tile < tiles; tile += stride) {
                 const Tile8 t = find_tile<TN>(a, tile);
                 for (int kt = k0; kt < k1; ++kt, ++issued) {
-                    if (issued >= XS && !warp_wait<ACROSS>(bar(X_EMPTY + s), ph, fault, stop)) { ok = false; break; }
-                    if (lead) expect_bytes(bar(X_FULL + s), P::X_BYTES * (PAIR ? 2 : 1));
-                    const uint32_t dst = xring + s * P::X_BYTES;
-                    // [64 k][rows], of a pair the CTA's half of the rows of each half of the columns
+                    if (issued >= SLOTS && !warp_wait<ACROSS>(bar(EMPTY + s), ph, fault, stop)) { ok = false; break; }
+                    if (lead) expect_bytes(bar(FULL + s), P::CODES ? P::C_BYTES : P::X_BYTES * (PAIR ? 2 : 1));
+                    if constexpr (P::CODES) {
+                        tma_2d(cring + s * P::C_BYTES, &xmap, kt * STAGE_K, t.m0, bar(FULL + s));
+                    } else {
+                        const uint32_t dst = xring + s * P::X_BYTES;
+                        // [64 k][rows], of a pair the CTA's half of the rows of each half of the columns
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if constexpr (PAIR) {
+                        for (int j = 0; j < 2; ++j) {
+                            if constexpr (PAIR) {
 #pragma unroll
-                            for (int h = 0; h < HALVES; ++h)
-                                pair_tma_2d(dst + (j * 2 + h) * (BOX * 128), &xmap, kt * STAGE_K + j * 64,
-                                            t.m0 + h * (TN / 2) + (int)side * (columns(t, h) >> 1), lead_full + s * 8);
-                        } else {
-                            tma_2d(dst + j * (XR * 128), &xmap, kt * STAGE_K + j * 64, t.m0, bar(X_FULL + s));
+                                for (int h = 0; h < HALVES; ++h)
+                                    pair_tma_2d(dst + (j * 2 + h) * (BOX * 128), &xmap, kt * STAGE_K + j * 64,
+                                                t.m0 + h * (TN / 2) + (int)side * (columns(t, h) >> 1), lead_full + s * 8);
+                            } else {
+                                tma_2d(dst + j * (XR * 128), &xmap, kt * STAGE_K + j * 64, t.m0, bar(FULL + s));
+                            }
                         }
                     }
-                    if (++s == XS) { s = 0; ph ^= 1; }
+                    if (++s == SLOTS) { s = 0; ph ^= 1; }
                 }
             }
             if (!ok) *stop = 1;
             // (both CTAs' tokens are counted on the even one's barriers, and the CTAs leave together)
             if (lead)
-                for (int j = issued - 1; j >= 0 && j >= issued - XS; --j)
-                    mbar_wait_bounded(bars + X_FULL + j % XS, (uint32_t)((j / XS) & 1), fault, FAULT_Q8_WAIT);
+                for (int j = issued - 1; j >= 0 && j >= issued - SLOTS; --j)
+                    mbar_wait_bounded(bars + FULL + j % SLOTS, (uint32_t)((j / SLOTS) & 1), fault, FAULT_Q8_WAIT);
         } else if (warp == 1 && lead) {
             // -------------------------------------------------------- MMA issue (PAIR: for both CTAs)
             int xs = 0, as = 0;
@@ -592,6 +611,47 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                 commit<PAIR>(bar(DRAINED));
                 mbar_wait_bounded(bars + DRAINED, 0, fault, FAULT_Q8_WAIT);
             }
+        }
+    } else if (P::CODES && warp >= TC_THREADS / 32) {
+        // ------------------------------------------------------------ widening of the tokens: 16 codes of a row at a time
+        if constexpr (P::CODES) {
+            const int w = warp - TC_THREADS / 32;
+            int cs = 0, xs = 0, i = 0;
+            uint32_t cph = 0, xph = 1;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += stride)
+                for (int kt = k0; kt < k1; ++kt, ++i) {
+                    if (!warp_wait<LOCAL>(bar(C_FULL + cs), cph, fault, stop) ||
+                        (i >= XS && !warp_wait<LOCAL>(bar(X_EMPTY + xs), xph, fault, stop))) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < TN / 16; ++j) {
+                        const int row = j * 16 + w * 4 + (lane >> 3), c = lane & 7;        // eight lanes to a row's 128 bytes
+                        uint4 v, lo, hi;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(cring + cs * P::C_BYTES + row * 128 + ((c ^ (row & 7)) << 4)) : "memory");
+                        widen4(v.x, lo.x, lo.y);
+                        widen4(v.y, lo.z, lo.w);
+                        widen4(v.z, hi.x, hi.y);
+                        widen4(v.w, hi.z, hi.w);
+                        const uint32_t to = xring + xs * P::X_BYTES + (c >> 2) * (XR * 128) + row * 128, part = (c & 3) * 2;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(to + ((part ^ (row & 7)) << 4)), "r"(lo.x),
+                                     "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(to + (((part + 1) ^ (row & 7)) << 4)), "r"(hi.x),
+                                     "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+                    }
+                    fence_proxy_async_smem();                      // the MMAs read through the async proxy
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive(bar(X_FULL + xs));
+                        arrive(bar(C_EMPTY + cs));
+                    }
+                    if (++cs == P::CS) { cs = 0; cph ^= 1; }
+                    if (++xs == XS) { xs = 0; xph ^= 1; }
+                }
+            if (!ok) *stop = 1;
         }
     } else {
         // ------------------------------------------------------------ widening, and the accumulator: lane = row of w
@@ -751,13 +811,13 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
     if (!PAIR && a.S > 1) {
         // A thread takes four neighbouring outputs of two tokens at a time; the CTAs' sums of both are requested before they are
         // added.
-        for (int it = share * TC_THREADS + threadIdx.x; it < t.rows * 32; it += 2 * a.S * TC_THREADS) {
+        for (int it = share * P::THREADS + threadIdx.x; it < t.rows * 32; it += 2 * a.S * P::THREADS) {
             float4 p[2][MAX_SPLIT];
             float sx[2];
             int c[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                c[i] = min((it >> 5) + i * a.S * (TC_THREADS / 32), t.rows - 1);
+                c[i] = min((it >> 5) + i * a.S * (P::THREADS / 32), t.rows - 1);
 #pragma unroll
                 for (int k = 0; k < MAX_SPLIT; ++k)
                     p[i][k] = k < a.S ? ld_cluster4(ring + (c[i] * 128 + r) * 4, k) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -765,7 +825,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (nn >= a.g.N || (i && (it >> 5) + a.S * (TC_THREADS / 32) >= t.rows)) break;
+                if (nn >= a.g.N || (i && (it >> 5) + a.S * (P::THREADS / 32) >= t.rows)) break;
                 float v[4] = {};
 #pragma unroll
                 for (int k = 0; k < MAX_SPLIT; ++k) {
@@ -842,6 +902,7 @@ template <class K> cudaError_t configure(K kernel, Done& done) {
 }
 
 template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, int sms, cudaStream_t st) {
+    static_assert(Plan8<TN, PAIR>::CODES == (TN <= MOST_CODES), "which form the tokens come in");
     static Done ready = {};
     cudaError_t e = configure(q8_tc_kernel<T, TN, PAIR>, ready);
     if (e != cudaSuccess) return e;
@@ -857,10 +918,10 @@ template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const voi
     const int width = PAIR ? 2 : a.S;
     a.ctas = a.S > 1 ? (int)tiles * width : (int)std::min(tiles * width, (long long)(sms / width * width));
     CUtensorMap wmap, xmap;
-    if (!rows_map(&wmap, a.g.w, a.g.N, a.g.K, 1, 128) || !rows_map(&xmap, x16, a.g.M, a.g.K, 2, PAIR ? P::XR / 2 : P::XR)) return cudaErrorInvalidValue;
+    if (!rows_map(&wmap, a.g.w, a.g.N, a.g.K, 1, 128) || !rows_map(&xmap, P::CODES ? a.g.x : x16, a.g.M, a.g.K, P::CODES ? 1 : 2, PAIR ? P::XR / 2 : P::XR)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.ctas);
-    cfg.blockDim = dim3(TC_THREADS);
+    cfg.blockDim = dim3(P::THREADS);
     cfg.dynamicSmemBytes = 1024 + HEAD + P::RING;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -881,9 +942,9 @@ template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const voi
 }
 
 // Whether pairs of CTAs are the faster kernel, by waves: a stage of 256 x 256 tiles takes about 15/8 of the time of one of 128 x
-// 128 tiles (0.80 us to 0.43 at K = 4096, 0.69 to 0.39 at 8192^3; the MMAs of both are less, what is left is the way of a stage
-// through its ring).  Measured, us single / pairs: 4096 x 4096, M = 1024 33.1 / 31.0, 2048 60.4 / 59.7; 14336 x 4096, M = 256 33.2 /
-// 31.2, 512 47.0 / 57.4; 8192 x 8192, M = 256 32.2 / 43 (31.0 with k shared by two pairs), 8192 718 / 660.
+// 128 tiles (0.75 us to 0.43 at K = 4096, 0.66 to 0.39 at 8192^3).  Measured, us single / pairs: 4096 x 4096, M = 1024 33.1 / 30.1,
+// 2048 60.4 / 56.3; 14336 x 4096, M = 256 33.2 / 31.2, 512 47.0 / 57.4; 8192 x 8192, M = 256 32.2 / 31.0 with k shared by two
+// pairs, which no rule here takes, 8192 718 / 629.
 bool pays_in_pairs(const Q8GemmArgs& g, int sms) {
     const long long one = (long long)((g.N + 127) / 128) * ((g.M + 127) / 128), two = 2LL * ((g.N + 255) / 256) * ((g.M + 255) / 256);
     return (two + sms - 1) / sms * 15 < (one + sms - 1) / sms * 8;
@@ -891,7 +952,7 @@ bool pays_in_pairs(const Q8GemmArgs& g, int sms) {
 
 }  // namespace
 
-bool q8_gemm_wide(int M) { return M > TOKENS; }
+Q8Form q8_gemm_form(int M) { return M <= TOKENS ? Q8_GEMV : (M <= MOST_CODES ? Q8_CODES : Q8_WIDE); }
 
 cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, cudaStream_t st) {
     const long long n = (long long)M * K / 16, ctas = (n + 1023) / 1024;
@@ -899,11 +960,11 @@ cudaError_t launch_q8_widen(const int8_t* x, void* x16, int M, int K, int sms, c
     return cudaGetLastError();
 }
 
-cudaError_t launch_q8_gemm_wide(const Q8GemmArgs& g, const void* x16, int sms, cudaStream_t st) {
+cudaError_t launch_q8_gemm_tc(const Q8GemmArgs& g, const void* x16, bool wait, int sms, cudaStream_t st) {
     if (!encode_fn()) return cudaErrorNotSupported;
     TcArgs8 a = {};
     a.g = g;
-    a.wait = 1;
+    a.wait = wait;
     return with_dtype(g.ytype, [&](auto t) {
         using T = decltype(t);
         if (g.M <= 32) return launch_tc<T, 32, false>(a, x16, sms, st);
