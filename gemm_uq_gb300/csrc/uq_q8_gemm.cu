@@ -25,10 +25,11 @@
 // Few tiles: a cluster of S CTAs shares a tile's k, and adds its fp32 sums through distributed shared memory in rank order.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is freed,
 // and the fault word tells.
-// 8192^3 629 us (36 of them widening the tokens; 1.75 PFLOP/s, 0.88 of the measured bf16 burst rate); 1024 x 4096 x 4096 30 us;
-// 64 x 14336 x 4096 19.5 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the MMAs of pairs (a stage 660 ns where they take 530;
-// a deeper ring changed nothing); with 128 tokens the way of a stage through its ring (load, widening, MMAs: 430 ns, of which
-// the MMAs are 270); for few tokens the start, the widening kernel before (2 us) and the sums of shared tiles (2 us).
+// 8192^3 621 us (36 of them widening the tokens; 1.77 PFLOP/s, 0.89 of the measured bf16 burst rate); 1024 x 4096 x 4096 30 us;
+// 64 x 14336 x 4096 18.8 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the MMAs of pairs (within a tile a stage takes 1020
+// cycles, as long as its MMAs), the widening before and 13.5 rounds of tiles that take 14; for up to 128 tokens HBM while it
+// streams (5.8 to 6 TB/s: 600 cycles a stage on 112 SMs, of which the MMAs are 480), and besides 8 us for the start, the first
+// weights, the outputs and the sums of shared tiles.
 #include <cuda.h>
 #include <algorithm>
 #include <atomic>
@@ -394,7 +395,7 @@ template <int TN> __device__ __forceinline__ Tile8 find_tile(const TcArgs8& a, i
 template <int TN, bool PAIR> struct Plan8 {
     // Up to 32 tokens are widened in the kernel, by a warpgroup of their own, in one launch: 10.6 us of host time a call instead
     // of 15.3, and on the GPU 16 x 14336 x 4096 takes 18.7 us and 18.5.  More tokens add to what shared memory delivers: 64 x
-    // 14336 x 4096 21.3 us in the kernel and 19.5 with their own, under which the first weights are loaded.
+    // 14336 x 4096 21.3 us in the kernel and 18.8 with their own, under which the first weights are loaded.
     static constexpr bool CODES = !PAIR && TN <= MOST_CODES;
     static constexpr int THREADS = TC_THREADS + (CODES ? X_WARPS * 32 : 0);
     static constexpr int XR = PAIR ? TN / 2 : TN;                  // token rows of a CTA
@@ -688,12 +689,14 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
         };
         for (int tile = first, j = 0; ok;) {
             const bool over = tile >= tiles;
-            // a complete chunk is read when the stages ahead are widened (of pairs, whose group 0 has the first of them, before
+            // What does not happen in every stage is marked so: laid out of the loop's way, a stage's instructions are fetched sooner
+            // (8192^3 629 us, then 621).
+            // A complete chunk is read when the stages ahead are widened (of pairs, whose group 0 has the first of them, before
             // its second one), or another one ends
             const bool reads = pending && (over || i - boundary >= (PAIR && half == 0 ? AS - 2 : AS - 1) || ends(j, which));
-            if (written < GROUPS && (reads || over || widened)) write_groups(reads || over ? GROUPS : written + 2);
+            if (__builtin_expect(written < GROUPS && (reads || over || widened), 0)) write_groups(reads || over ? GROUPS : written + 2);
             widened = false;
-            if (reads) {
+            if (__builtin_expect(reads, 0)) {
                 pending = false;
                 if (!warp_wait<TENSOR>(bar(ACC_FULL + which), (uint32_t)read & 1, fault, stop)) { ok = false; break; }
                 ++read;
@@ -723,7 +726,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                     sw = __ldg(a.g.sw + min(ot.nt * (PAIR ? 256 : 128) + (int)side * 128 + row, a.g.N - 1));
                 }
             }
-            if (over) {
+            if (__builtin_expect(over, 0)) {
                 if (written == GROUPS) break;
                 continue;
             }
@@ -765,7 +768,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                 if (lane == 0) arrive_relaxed(lead_a_full + as * 8);
                 widened = true;
             }
-            if (ends(j, which)) {
+            if (__builtin_expect(ends(j, which), 0)) {
                 pending = true;
                 boundary = i + 1;
                 last = j == k1 - k0 - 1;
@@ -774,7 +777,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
             if (++ws == WS) { ws = 0; wph ^= 1; }
             if (++as == AS) { as = 0; aph ^= 1; }
             ++i;
-            if (++j == k1 - k0) {
+            if (__builtin_expect(++j == k1 - k0, 0)) {
                 j = 0;
                 tile += stride;
                 if (tile < tiles) t = find_tile<TN>(a, tile);
