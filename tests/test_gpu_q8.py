@@ -179,6 +179,12 @@ def test_nothing_to_do():
     assert codes.shape == (5, 0) and not scales.any()
 
 
+def test_rows_without_elements_have_scale_zero():
+    e = torch.empty(5, 0, device=DEV)
+    for scales in (uq.rmsnorm_q8(e, e[0], 1e-5)[2][1], uq.rmsnorm_q8(e, e[0], 1e-5, residual=e, normed=True)[2][1]):
+        assert scales.shape == (5,) and not scales.any()
+
+
 def test_on_another_stream_and_in_graphs():
     """Results on a given stream; two graphs captured on one stream share its workspace and are replayed one after the other."""
     T, D = 200, 2048
