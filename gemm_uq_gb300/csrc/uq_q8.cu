@@ -32,9 +32,6 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_s
 
 // A thread's own prefetches: it copies 16-byte parts of a coming row to shared memory, each row's as one group, and reads back
 // what it copied itself, so no other thread is waited for.
-__device__ __forceinline__ void copy_ahead(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 constexpr int ROWS_AHEAD = 2;                   // groups under way
 __device__ __forceinline__ void oldest_copies_landed() { asm volatile("cp.async.wait_group %0;" :: "n"(ROWS_AHEAD - 1) : "memory"); }
@@ -45,6 +42,72 @@ template <class W> __device__ __forceinline__ W copied(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
     memcpy(&w, &u, 16);
     return w;
+}
+
+// The 16-byte parts of a row.  A matrix without gaps begins at a 16-byte boundary, its rows need not (ODD): then parts are cut
+// at the matrix's boundaries, and those at a row's ends hold elements of its neighbours, which are read as zeros and not written.
+// Groups of threads take rows V apart (or a multiple), which all begin at the same place in a part: so a thread's columns stay
+// the same.  Rows of an odd length in accesses of one element, and this way: bf16 norm of 4096 x 4097 with all outputs 84 us and
+// 57, its gradient 127 and 54, quantizer 48 and 22; 8192 x 1001 fp32 37 and 25, 80 and 29, 20 and 11.
+template <class T, int V, bool ODD> struct Parts {
+    using W = Vec<T, V>;
+    int off, D, count;                          // of the row's first element in its first part
+    __device__ __forceinline__ Parts(long long row, int d) : D(d) {
+        off = ODD ? (int)(row * d & (V - 1)) : 0;
+        count = (off + d + (ODD ? V - 1 : 0)) / V;
+    }
+    __device__ __forceinline__ int column(int part, int j) const { return part * V - off + j; }
+    __device__ __forceinline__ bool whole(int part) const { return !ODD || ((part || !off) && (part + 1) * V <= off + D); }
+    __device__ __forceinline__ bool in(int part, int j) const { return !ODD || (unsigned)column(part, j) < (unsigned)D; }
+    __device__ __forceinline__ void clip(W& w, int part) const {
+        if (!whole(part)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (!in(part, j)) w.v[j] = from_f32<T>(0.f);
+        }
+    }
+    // row: the address of its first part
+    __device__ __forceinline__ W load(const T* row, int part) const {
+        if (whole(part)) return reinterpret_cast<const W*>(row)[part];
+        W w;
+#pragma unroll
+        for (int j = 0; j < V; ++j) w.v[j] = in(part, j) ? row[part * V + j] : from_f32<T>(0.f);
+        return w;
+    }
+    template <class Y> __device__ __forceinline__ void store(Y* row, int part, const Vec<Y, V>& w) const {
+        if (whole(part)) reinterpret_cast<Vec<Y, V>*>(row)[part] = w;
+        else
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (in(part, j)) row[part * V + j] = w.v[j];
+    }
+    __device__ __forceinline__ W of_vector(const T* p, int part) const {           // of gamma
+        if constexpr (!ODD) return reinterpret_cast<const W*>(p)[part];
+        else {
+            W w;
+#pragma unroll
+            for (int j = 0; j < V; ++j) w.v[j] = in(part, j) ? p[column(part, j)] : from_f32<T>(0.f);
+            return w;
+        }
+    }
+    // Copies a part ahead; left: elements of the matrix from the row's first part on (beyond them nothing is read).
+    __device__ __forceinline__ void copy(uint32_t dst, const T* row, int part, long long left) const {
+        if constexpr (ODD) {
+            const long long here = left - part * V;
+            const int bytes = (here < V ? (int)here : V) * (int)sizeof(T);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(reinterpret_cast<const W*>(row) + part), "r"(bytes) : "memory");
+        } else {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(reinterpret_cast<const W*>(row) + part) : "memory");
+        }
+    }
+};
+
+template <class P, int V> __device__ __forceinline__ void put_codes(const P& parts, int8_t* row, int part, const uint32_t (&c)[V]) {
+    if (parts.whole(part)) store_codes<V>(row + (long long)part * V, c);
+    else
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (parts.in(part, j)) row[part * V + j] = (int8_t)c[j];
 }
 
 struct RowArgs {
@@ -73,7 +136,7 @@ __device__ __forceinline__ float larger(float a, float b) {
 // written, and gamma stays in registers.  Without, a row is a chain of loads, a reduction, and stores; measured, 8192 rows of 8192
 // bf16 with all outputs: PIPE 100 us (6.0 TB/s, 0.89 of the measured copy); else 256 threads a row with four accesses each 134
 // us, 512 with two 152; the quantizer 37 (5.4 TB/s) and 44 us.
-template <class T, int V, int NV, bool NORM, bool PIPE>
+template <class T, int V, int NV, bool NORM, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 1) row_kernel(const RowArgs a) {
     using W = Vec<T, V>;
     __shared__ float sums[2][MAX_THREADS / 32];
@@ -81,43 +144,49 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
     extern __shared__ __align__(16) uint8_t ahead[];               // PIPE: [row][x, residual][part][thread] of 16 bytes
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
-    const int nvec = a.D / V;
     const long long step = (long long)gridDim.x * per_cta;
+    const Parts<T, V, ODD> parts((long long)blockIdx.x * per_cta + mine, a.D);
+    const int nvec = parts.count;
     if constexpr (!NORM)
         if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const W* gamma = static_cast<const W*>(a.gamma);
-    auto x_of = [&](long long row) { return reinterpret_cast<const W*>(static_cast<const T*>(a.x) + row * a.ldx); };
-    auto res_of = [&](long long row) { return reinterpret_cast<const W*>(static_cast<const T*>(a.residual) + row * a.D); };
+    const T* gamma = static_cast<const T*>(a.gamma);
+    auto x_of = [&](long long row) { return static_cast<const T*>(a.x) + row * a.ldx - parts.off; };
+    auto res_of = [&](long long row) { return static_cast<const T*>(a.residual) + row * a.D - parts.off; };
     const bool has_res = NORM && a.residual;
     uint32_t slot = smem_u32(ahead) + threadIdx.x * 16, part = blockDim.x * 16, other = 0;
     auto request = [&](long long row) {
         if (row < a.rows) {
+            const long long left = (a.rows - row) * a.D + parts.off;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) {
-                    copy_ahead(slot + other + i * part, x_of(row) + tid + i * a.group);
-                    if (has_res) copy_ahead(slot + other + (NV + i) * part, res_of(row) + tid + i * a.group);
+                    parts.copy(slot + other + i * part, x_of(row), tid + i * a.group, left);
+                    if (has_res) parts.copy(slot + other + (NV + i) * part, res_of(row), tid + i * a.group, left);
                 }
         }
         copies_issued();
         other ^= (has_res ? 2 : 1) * NV * part;
     };
-    W held[PIPE && NORM ? NV : 1];
-    if constexpr (PIPE) {
+    constexpr bool HELD = NORM && (PIPE || ODD);
+    W held[HELD ? NV : 1];
+    if constexpr (PIPE)
         for (int i = 0; i < ROWS_AHEAD; ++i) request((long long)blockIdx.x * per_cta + mine + i * step);
-        if constexpr (NORM) {
+    if constexpr (HELD) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) held[i] = gamma[tid + i * a.group];
-        }
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * a.group < nvec) held[i] = parts.of_vector(gamma, tid + i * a.group);
     }
-    auto gam = [&](int i) { return !NORM ? W() : (PIPE ? held[PIPE && NORM ? i : 0] : gamma[tid + i * a.group]); };
+    auto gam = [&](int i) {
+        if constexpr (!NORM) return W();
+        else if constexpr (HELD) return held[i];
+        else return parts.of_vector(gamma, tid + i * a.group);
+    };
     int buf = 0;
     for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += step, buf ^= 1) {
         const long long row = base + mine;
         const bool on = row < a.rows;
-        const W* x = x_of(on ? row : 0);
-        const W* res = has_res ? res_of(on ? row : 0) : nullptr;
+        const T* x = x_of(on ? row : 0);
+        const T* res = has_res ? res_of(on ? row : 0) : nullptr;
         auto add = [&](const W& w, const W& r) {                   // h
             float f[V], g[V];
             unpack(w, f);
@@ -126,7 +195,7 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
             for (int j = 0; j < V; ++j) f[j] += g[j];
             return pack<T, V>(f);
         };
-        auto load = [&](int v) { return res ? add(x[v], res[v]) : x[v]; };
+        auto load = [&](int v) { return res ? add(parts.load(x, v), parts.load(res, v)) : parts.load(x, v); };
         float sum = 0.f, most = 0.f;
         auto look = [&](const W& w, const W& g) {
             float f[V], c[V];
@@ -147,6 +216,7 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
                     if (tid + i * a.group < nvec) {
                         kept[i] = copied<W>(slot + other + i * part);
                         if (has_res) kept[i] = add(kept[i], copied<W>(slot + other + (NV + i) * part));
+                        parts.clip(kept[i], tid + i * a.group);
                         look(kept[i], gam(i));
                     }
             }
@@ -157,8 +227,8 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (tid + i * a.group < nvec) {
-                        kept[i] = x[tid + i * a.group];
-                        r[i] = res[tid + i * a.group];
+                        kept[i] = parts.load(x, tid + i * a.group);
+                        r[i] = parts.load(res, tid + i * a.group);
                     }
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
@@ -166,12 +236,14 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
             } else {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    if (tid + i * a.group < nvec) kept[i] = x[tid + i * a.group];
+                    if (tid + i * a.group < nvec) kept[i] = parts.load(x, tid + i * a.group);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) look(kept[i], gam(i));
-            for (int v = tid + NV * a.group; v < nvec; v += a.group) look(load(v), NORM ? gamma[v] : W());
+            if constexpr (!ODD) {
+                for (int v = tid + NV * a.group; v < nvec; v += a.group) look(load(v), NORM ? parts.of_vector(gamma, v) : W());
+            }
         }
         if constexpr (NORM) sum = warp_sum(sum);
         most = __uint_as_float(warp_max(__float_as_uint(most)));   // (NaN and infinity are the largest patterns)
@@ -195,12 +267,13 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
             // 127 / most stays finite for the smallest; a bad row's codes are zero
             const float up = most < 0x1p-64f ? 0x1p80f : 1.f;
             const float inv = most > 0.f && !bad ? 127.f / (most * up) : 0.f;
-            W* h = a.h ? reinterpret_cast<W*>(static_cast<T*>(a.h) + row * a.D) : nullptr;
-            W* y = a.y ? reinterpret_cast<W*>(static_cast<T*>(a.y) + row * a.D) : nullptr;
-            int8_t* codes = a.codes ? a.codes + row * a.D : nullptr;
+            const long long start = row * a.D - parts.off;
+            T* h = a.h ? static_cast<T*>(a.h) + start : nullptr;
+            T* y = a.y ? static_cast<T*>(a.y) + start : nullptr;
+            int8_t* codes = a.codes ? a.codes + start : nullptr;
             auto write = [&](int v, const W& w, const W& g) {
                 float f[V], c[V];
-                if (h) h[v] = w;
+                if (h) parts.store(h, v, w);
                 unpack(w, f);
                 unpack(g, c);
 #pragma unroll
@@ -209,7 +282,7 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
                     float o[V];
 #pragma unroll
                     for (int j = 0; j < V; ++j) o[j] = c[j] * r;
-                    y[v] = pack<T, V>(o);
+                    parts.store(y, v, pack<T, V>(o));
                 }
                 if (codes) {
                     uint32_t q[V];
@@ -223,12 +296,13 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
                     }
 #pragma unroll
                     for (int j = 0; j < V; ++j) q[j] = code_bits(c[j], inv);
-                    store_codes<V>(codes + (long long)v * V, q);
+                    put_codes(parts, codes, v, q);
                 }
             };
             // before anything is written, which may be over x or the residual
-            if constexpr (!PIPE)
-                for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), gamma[v]);
+            if constexpr (!PIPE && !ODD) {
+                for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v), parts.of_vector(gamma, v));
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i], gam(i));
@@ -236,6 +310,7 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
             const float s = bad ? nan : __fdiv_rn(most, 127.f);
             if (tid == 0) a.scales[row] = s;
             const Divisor d(s);
+            const long long start = row * a.D - parts.off;
             auto write = [&](int v, const W& w) {
                 float f[V];
                 uint32_t c[V];
@@ -244,34 +319,48 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
                 if (a.wide) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) f[j] = (float)(int8_t)c[j];
-                    reinterpret_cast<Vec<__half, V>*>(a.wide + row * a.D)[v] = pack<__half, V>(f);
+                    parts.store(a.wide + start, v, pack<__half, V>(f));
                 } else {
-                    store_codes<V>(a.codes + row * a.D + (long long)v * V, c);
+                    put_codes(parts, a.codes + start, v, c);
                 }
             };
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) write(tid + i * a.group, kept[i]);
-            if constexpr (!PIPE)
+            if constexpr (!PIPE && !ODD) {
                 for (int v = tid + NV * a.group; v < nvec; v += a.group) write(v, load(v));
+            }
         }
     }
 }
 
-// out = code * scale, rounded once; 16 codes a thread where the rows allow it
-template <class T, int V>
+// out = code * scale, rounded once; V codes a thread.  ODD: rows of more than V codes that are not whole V, so that a
+// thread's codes may belong to two rows (fp32: 4 codes a thread, whose 16 bytes lie beside its neighbours'; 4096 x 4096 11 us,
+// with 16 codes a thread 18).  4096 x 4097 bf16 8.8 us, 27 with a code a thread.
+template <class T, int V, bool ODD>
 __global__ void __launch_bounds__(256) dequant_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales,
-                                                      T* __restrict__ out, long long vecs, int per_row) {
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < vecs; i += gridDim.x * 256LL) {
-        const Vec<int8_t, V> c = reinterpret_cast<const Vec<int8_t, V>*>(codes)[i];
-        const float s = scales[i / per_row];
+                                                      T* __restrict__ out, long long n, int K) {
+    for (long long i = (blockIdx.x * 256LL + threadIdx.x) * V; i < n; i += gridDim.x * (256LL * V)) {
+        const long long row = n <= 0xFFFFFFFFll ? (long long)((uint32_t)i / (uint32_t)K) : i / K;
+        const float s = scales[row];
+        int own = V;                            // codes of that row
+        float next = s;
+        if constexpr (ODD) {
+            const long long end = (row + 1) * K;
+            if (end - i < V && end < n) own = (int)(end - i), next = scales[row + 1];
+            if (n - i < V) {
+                for (int j = 0; j < (int)(n - i); ++j) out[i + j] = from_f32<T>((float)codes[i + j] * (j < own ? s : next));
+                continue;
+            }
+        }
+        const Vec<int8_t, V> c = *reinterpret_cast<const Vec<int8_t, V>*>(codes + i);
         constexpr int O = V * sizeof(T) <= 16 ? V : 16 / sizeof(T);
 #pragma unroll
         for (int b = 0; b < V; b += O) {
             Vec<T, O> o;
 #pragma unroll
-            for (int j = 0; j < O; ++j) o.v[j] = from_f32<T>((float)c.v[b + j] * s);
-            *reinterpret_cast<Vec<T, O>*>(out + i * V + b) = o;
+            for (int j = 0; j < O; ++j) o.v[j] = from_f32<T>((float)c.v[b + j] * (b + j < own ? s : next));
+            *reinterpret_cast<Vec<T, O>*>(out + i + b) = o;
         }
     }
 }
@@ -290,32 +379,35 @@ struct GradArgs {
 // that a CTA's groups do not wait for one another.  gamma stays in registers: read again for every row, four accesses a thread,
 // it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 57 us (4.7 TB/s, the addition of the
 // partials in it), without PIPE 68, with gamma read again 96.
-template <class T, int V, int NV, bool PIPE>
+template <class T, int V, int NV, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {
     using W = Vec<T, V>;
     extern __shared__ __align__(16) uint8_t ahead[];               // PIPE: [row][dy, h, dh][part][thread] of 16 bytes; then
     __shared__ float2 sums[2][GRAD_THREADS / 32];
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
-    const int nvec = a.D / V;
     const long long step = (long long)gridDim.x * per_cta;
+    const Parts<T, V, ODD> parts((long long)blockIdx.x * per_cta + mine, a.D);
+    const int nvec = parts.count;
     const uint32_t part16 = blockDim.x * 16, stage = 3 * NV * part16;
     float* together = reinterpret_cast<float*>(ahead + (PIPE ? ROWS_AHEAD * stage : 0));           // several groups: [D]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                // the kernel that adds the partials
-    const W* gamma = static_cast<const W*>(a.gamma);
+    const T* gamma = static_cast<const T*>(a.gamma);
     float* part = a.partials + (long long)blockIdx.x * a.D;
     const uint32_t slot = smem_u32(ahead) + threadIdx.x * 16;
     uint32_t other = 0;
     auto request = [&](long long row) {
         if (row < a.rows) {
-            const long long at = row * nvec + tid;
+            const long long at = row * a.D - parts.off;
+            const long long left = (a.rows - row) * a.D + parts.off;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * a.group < nvec) {
-                    copy_ahead(slot + other + i * part16, static_cast<const W*>(a.dy) + at + i * a.group);
-                    copy_ahead(slot + other + (NV + i) * part16, static_cast<const W*>(a.h) + at + i * a.group);
-                    if (a.dh) copy_ahead(slot + other + (2 * NV + i) * part16, static_cast<const W*>(a.dh) + at + i * a.group);
-                }
+            for (int i = 0; i < NV; ++i) {
+                const int v = tid + i * a.group;
+                if (v >= nvec) continue;
+                parts.copy(slot + other + i * part16, static_cast<const T*>(a.dy) + at, v, left);
+                parts.copy(slot + other + (NV + i) * part16, static_cast<const T*>(a.h) + at, v, left);
+                if (a.dh) parts.copy(slot + other + (2 * NV + i) * part16, static_cast<const T*>(a.dh) + at, v, left);
+            }
         }
         copies_issued();
         other ^= stage;
@@ -326,16 +418,18 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
     float dg[NV][V] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (tid + i * a.group < nvec) gam[i] = gamma[tid + i * a.group];
-    for (int v = tid + NV * a.group; v < nvec; v += a.group)
+        if (tid + i * a.group < nvec) gam[i] = parts.of_vector(gamma, tid + i * a.group);
+    if constexpr (!ODD) {
+        for (int v = tid + NV * a.group; v < nvec; v += a.group)
 #pragma unroll
-        for (int j = 0; j < V; ++j) part[(long long)v * V + j] = 0.f;
+            for (int j = 0; j < V; ++j) part[(long long)v * V + j] = 0.f;
+    }
     int buf = 0;
     for (long long row = (long long)blockIdx.x * per_cta + mine; row < a.rows; row += step, buf ^= 1) {
-        const long long at = row * nvec;
-        const W *dy = static_cast<const W*>(a.dy) + at, *h = static_cast<const W*>(a.h) + at;
-        const W* dh = a.dh ? static_cast<const W*>(a.dh) + at : nullptr;
-        W* dx = static_cast<W*>(a.dx) + at;
+        const long long at = row * a.D - parts.off;
+        const T *dy = static_cast<const T*>(a.dy) + at, *h = static_cast<const T*>(a.h) + at;
+        const T* dh = a.dh ? static_cast<const T*>(a.dh) + at : nullptr;
+        T* dx = static_cast<T*>(a.dx) + at;
         float s1 = 0.f, s2 = 0.f;
         auto look = [&](const W& u, const W& w, const W& g) {
             float t[V], f[V], c[V];
@@ -357,21 +451,25 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
                     ku[i] = copied<W>(slot + other + i * part16);
                     kw[i] = copied<W>(slot + other + (NV + i) * part16);
                     if (dh) kd[i] = copied<W>(slot + other + (2 * NV + i) * part16);
+                    parts.clip(ku[i], tid + i * a.group);
+                    parts.clip(kw[i], tid + i * a.group);
                 }
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) {
-                    ku[i] = dy[tid + i * a.group];
-                    kw[i] = h[tid + i * a.group];
-                    if (dh) kd[i] = dh[tid + i * a.group];
+                    ku[i] = parts.load(dy, tid + i * a.group);
+                    kw[i] = parts.load(h, tid + i * a.group);
+                    if (dh) kd[i] = parts.load(dh, tid + i * a.group);
                 }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (tid + i * a.group < nvec) look(ku[i], kw[i], gam[i]);
         if constexpr (PIPE) request(row + ROWS_AHEAD * step);      // over what has just been read
-        for (int v = tid + NV * a.group; v < nvec; v += a.group) look(dy[v], h[v], gamma[v]);
+        if constexpr (!ODD) {
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) look(parts.load(dy, v), parts.load(h, v), parts.of_vector(gamma, v));
+        }
         s1 = warp_sum(s1);
         s2 = warp_sum(s2);
         if (warps > 1) {
@@ -398,15 +496,17 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
 #pragma unroll
                 for (int j = 0; j < V; ++j) e[j] += t[j];
             }
-            dx[v] = pack<T, V>(e);
+            parts.store(dx, v, pack<T, V>(e));
         };
-        for (int v = tid + NV * a.group; v < nvec; v += a.group) {
-            float out[V];
+        if constexpr (!ODD) {
+            for (int v = tid + NV * a.group; v < nvec; v += a.group) {
+                float out[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) out[j] = part[(long long)v * V + j];
-            write(v, dy[v], h[v], gamma[v], dh ? dh[v] : W(), out);
+                for (int j = 0; j < V; ++j) out[j] = part[(long long)v * V + j];
+                write(v, parts.load(dy, v), parts.load(h, v), parts.of_vector(gamma, v), dh ? parts.load(dh, v) : W(), out);
 #pragma unroll
-            for (int j = 0; j < V; ++j) part[(long long)v * V + j] = out[j];
+                for (int j = 0; j < V; ++j) part[(long long)v * V + j] = out[j];
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -419,7 +519,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
                 if (tid + i * a.group < nvec)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const int col = (tid + i * a.group) * V + j;
+                        if (!parts.in(tid + i * a.group, j)) continue;
+                        const int col = parts.column(tid + i * a.group, j);
                         const float v = g ? together[col] + dg[i][j] : dg[i][j];
                         if (g == per_cta - 1) part[col] = v;
                         else together[col] = v;
@@ -466,17 +567,37 @@ Shape shape_of(int nvec, int most_threads, int most_nv, bool few) {
     return s;
 }
 
-// f(integral constants V, NV)
-template <class T, class F> cudaError_t with_shape(int v, int nv, F&& f) {
-    auto by_nv = [&](auto V) {
-        if (nv == 1) return f(V, std::integral_constant<int, 1>());
-        if (nv == 2) return f(V, std::integral_constant<int, 2>());
-        return f(V, std::integral_constant<int, 4>());
+// How rows are taken: elements per access; whether in 16-byte parts that rows do not begin or end with.
+struct Plan { int v; bool odd; Shape s; };
+template <class T> Plan plan_of(int D, long long ld, int rows, int most_threads, int most_nv, int sms) {
+    constexpr int WIDE = 16 / sizeof(T);
+    const bool few = rows <= 2 * sms;
+    const int v = access<T>(D, ld);
+    if (v < WIDE && (ld == D || rows == 1)) {
+        const int most = (int)(((long long)D + 2 * WIDE - 2) / WIDE);              // parts of a row, begun anywhere
+        const Shape s = shape_of(most, most_threads, most_nv, few);
+        if (s.group * s.nv >= most) return {WIDE, true, s};
+    }
+    return {v, false, shape_of(D / v, most_threads, most_nv, few)};
+}
+
+// CTAs for rows in groups of `per`, at most `most`; a group's rows V apart or a multiple
+int grid_of(long long tiles, long long most, const Plan& p) {
+    return (int)(tiles <= most ? tiles : (p.odd && most >= p.v ? most / p.v * p.v : most));
+}
+
+// f(integral constants V, NV, ODD)
+template <class T, class F> cudaError_t with_plan(const Plan& p, F&& f) {
+    auto by_nv = [&](auto V, auto ODD) {
+        if (p.s.nv == 1) return f(V, std::integral_constant<int, 1>(), ODD);
+        if (p.s.nv == 2) return f(V, std::integral_constant<int, 2>(), ODD);
+        return f(V, std::integral_constant<int, 4>(), ODD);
     };
     constexpr int WIDE = 16 / sizeof(T), FOUR = 4 / sizeof(T);
-    if (v == WIDE) return by_nv(std::integral_constant<int, WIDE>());
-    if (FOUR > 1 && v == FOUR) return by_nv(std::integral_constant<int, FOUR>());
-    return by_nv(std::integral_constant<int, 1>());
+    if (p.odd) return by_nv(std::integral_constant<int, WIDE>(), std::true_type());
+    if (p.v == WIDE) return by_nv(std::integral_constant<int, WIDE>(), std::false_type());
+    if (FOUR > 1 && p.v == FOUR) return by_nv(std::integral_constant<int, FOUR>(), std::false_type());
+    return by_nv(std::integral_constant<int, 1>(), std::false_type());
 }
 
 // Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
@@ -496,25 +617,24 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
         RowArgs a = a0;
-        const int v = access<T>(a.D, a.ldx);
-        const Shape s = shape_of(a.D / v, MAX_THREADS, 4, a.rows <= 2 * sms);
-        a.group = s.group;
-        const int block = s.group < 128 ? 128 : s.group, per = block / s.group;
+        const Plan p = plan_of<T>(a.D, a.ldx, a.rows, MAX_THREADS, 4, sms);
+        a.group = p.s.group;
+        const int block = a.group < 128 ? 128 : a.group, per = block / a.group;
         const long long tiles = ((long long)a.rows + per - 1) / per;
-        if (v * sizeof(T) == 16 && s.nv == 4 && block <= PIPE_THREADS && s.group * 4 >= a.D / v && a.rows > 2 * sms) {
-            constexpr int V = 16 / sizeof(T);
-            static Done done = {};
-            const cudaError_t e = configure(row_kernel<T, V, 4, NORM, true>, done);
-            if (e != cudaSuccess) return e;
-            const long long most = (long long)sms * 3 * (PIPE_THREADS / block);
-            row_kernel<T, V, 4, NORM, true><<<(unsigned)(tiles < most ? tiles : most), block,
-                                              ROWS_AHEAD * (a.residual ? 2 : 1) * 4 * 16 * block, st>>>(a);
-            return cudaGetLastError();
-        }
-        const long long most = (long long)sms * (2048 / block);
-        return with_shape<T>(v, s.nv, [&](auto V, auto NV) {
-            row_kernel<T, decltype(V)::value, decltype(NV)::value, NORM, false>
-                <<<(unsigned)(tiles < most ? tiles : most), block, 0, st>>>(a);
+        return with_plan<T>(p, [&](auto V_, auto NV_, auto ODD_) {
+            constexpr int V = decltype(V_)::value, NV = decltype(NV_)::value;
+            constexpr bool ODD = decltype(ODD_)::value;
+            if constexpr (V * sizeof(T) == 16 && NV == 4) {
+                if (block <= PIPE_THREADS && (ODD || a.group * NV >= a.D / V) && a.rows > 2 * sms) {
+                    static Done done = {};
+                    const cudaError_t e = configure(row_kernel<T, V, NV, NORM, true, ODD>, done);
+                    if (e != cudaSuccess) return e;
+                    row_kernel<T, V, NV, NORM, true, ODD><<<grid_of(tiles, (long long)sms * 3 * (PIPE_THREADS / block), p), block,
+                                                           ROWS_AHEAD * (a.residual ? 2 : 1) * NV * 16 * block, st>>>(a);
+                    return cudaGetLastError();
+                }
+            }
+            row_kernel<T, V, NV, NORM, false, ODD><<<grid_of(tiles, (long long)sms * (2048 / block), p), block, 0, st>>>(a);
             return cudaGetLastError();
         });
     });
@@ -539,15 +659,16 @@ cudaError_t launch_quantize_q8(const void* x, int type, long long ldx, int8_t* c
 cudaError_t launch_dequant_q8(const int8_t* codes, const float* scales, void* out, int type, int rows, int K, int sms, cudaStream_t st) {
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
-        auto go = [&](auto V) {
+        auto go = [&](auto V, auto ODD) {
             constexpr int N = decltype(V)::value;
-            const long long vecs = (long long)rows * (K / N), ctas = (vecs + 255) / 256;
-            dequant_kernel<T, N><<<(unsigned)(ctas < 16LL * sms ? ctas : 16LL * sms), 256, 0, st>>>(codes, scales, static_cast<T*>(out), vecs, K / N);
+            const long long n = (long long)rows * K, ctas = (n + 256 * N - 1) / (256 * N);
+            dequant_kernel<T, N, decltype(ODD)::value><<<(unsigned)(ctas < 16LL * sms ? ctas : 16LL * sms), 256, 0, st>>>(codes, scales, static_cast<T*>(out), n, K);
             return cudaGetLastError();
         };
-        if (K % 16 == 0) return go(std::integral_constant<int, 16>());
-        if (K % 4 == 0) return go(std::integral_constant<int, 4>());
-        return go(std::integral_constant<int, 1>());
+        constexpr int V = sizeof(T) == 4 ? 4 : 16;
+        if (K % V == 0) return go(std::integral_constant<int, V>(), std::false_type());
+        if (K > V) return go(std::integral_constant<int, V>(), std::true_type());
+        return go(std::integral_constant<int, 1>(), std::false_type());
     });
 }
 
@@ -558,38 +679,38 @@ cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* g
 }
 
 // CTAs of the gradient, each with a partial row of dgamma.
-static Shape grad_shape(int type, int rows, int D, int sms) {
-    const int v = type == UQ_FP32 ? access<float>(D, D) : access<__half>(D, D);
-    return shape_of(D / v, GRAD_THREADS, 2, rows <= 2 * sms);
+static Plan grad_plan(int type, int rows, int D, int sms) {
+    return type == UQ_FP32 ? plan_of<float>(D, D, rows, GRAD_THREADS, 2, sms) : plan_of<__half>(D, D, rows, GRAD_THREADS, 2, sms);
 }
 static int grad_block(const Shape& s) { return s.group < 256 ? 256 : s.group; }
 int norm_grad_partials(int type, int rows, int D, int sms) {
-    const Shape s = grad_shape(type, rows, D, sms);
-    const int per = grad_block(s) / s.group, tiles = (int)(((long long)rows + per - 1) / per), most = sms * (GRAD_THREADS / grad_block(s));
-    return tiles < most ? tiles : most;
+    const Plan p = grad_plan(type, rows, D, sms);
+    const int block = grad_block(p.s), per = block / p.s.group;
+    return grid_of(((long long)rows + per - 1) / per, (long long)sms * (GRAD_THREADS / block), p);
 }
 
 cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, int type, void* dx, float* dgamma,
                                 float* partials, int rows, int D, float eps, int sms, cudaStream_t st) {
-    const Shape s = grad_shape(type, rows, D, sms);
-    const int P = norm_grad_partials(type, rows, D, sms);
-    const GradArgs a = {dy, h, gamma, dh, dx, partials, rows, D, eps, s.group};
+    const Plan p = grad_plan(type, rows, D, sms);
+    const int P = norm_grad_partials(type, rows, D, sms), group = p.s.group;
+    const GradArgs a = {dy, h, gamma, dh, dx, partials, rows, D, eps, group};
     cudaError_t e = with_dtype(type, [&](auto t) {
         using T = decltype(t);
-        const int block = grad_block(s);
-        const size_t add = block > s.group ? (size_t)D * sizeof(float) : 0;
-        return with_shape<T>(access<T>(D, D), s.nv, [&](auto V_, auto NV_) {
+        const int block = grad_block(p.s);
+        const size_t add = block > group ? (size_t)D * sizeof(float) : 0;
+        return with_plan<T>(p, [&](auto V_, auto NV_, auto ODD_) {
             constexpr int V = decltype(V_)::value, NV = decltype(NV_)::value;
+            constexpr bool ODD = decltype(ODD_)::value;
             if constexpr (V * sizeof(T) == 16 && NV <= 2) {
                 if (rows > 2 * sms) {
                     static Done done = {};
-                    const cudaError_t f = configure(norm_grad_kernel<T, V, NV, true>, done);
+                    const cudaError_t f = configure(norm_grad_kernel<T, V, NV, true, ODD>, done);
                     if (f != cudaSuccess) return f;
-                    norm_grad_kernel<T, V, NV, true><<<P, block, ROWS_AHEAD * 3 * NV * 16 * block + add, st>>>(a);
+                    norm_grad_kernel<T, V, NV, true, ODD><<<P, block, ROWS_AHEAD * 3 * NV * 16 * block + add, st>>>(a);
                     return cudaGetLastError();
                 }
             }
-            norm_grad_kernel<T, V, NV, false><<<P, block, add, st>>>(a);
+            norm_grad_kernel<T, V, NV, false, ODD><<<P, block, add, st>>>(a);
             return cudaGetLastError();
         });
     });

@@ -179,6 +179,59 @@ def test_nothing_to_do():
     assert codes.shape == (5, 0) and not scales.any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,D", [(1, 5), (306, 3), (1000, 9), (400, 127), (2500, 1001), (3, 4099), (700, 4097), (320, 9001), (2, 16379)])
+def test_rows_that_begin_anywhere(T, D, dtype):
+    """Rows that are not whole 16-byte parts, many of them too: in place, beside a row of NaN, and nothing behind the last one."""
+    n_, pad, code = T * D, 64, uq.DTYPES[DTYPE[dtype]]
+    x, r, gamma = _rows(1, T, D, dtype), _rows(2, T, D, dtype), _rows(3, 1, D, dtype)[0].contiguous()
+    if T > 5:
+        x[4] = float("nan")
+    h = (x.float() + r.float()).to(x.dtype)
+    keep = [i for i in range(T) if i != 4 or T <= 5]
+    buf = lambda t: torch.full((n_ + pad,), 77, dtype=t, device=DEV)                # noqa: E731
+    hx, y, codes, scales = buf(x.dtype), buf(x.dtype), buf(torch.int8), torch.full((T + pad,), 77.0, device=DEV)
+    hx[:n_] = x.reshape(-1)
+    assert uq.lib().uq_rmsnorm_q8(hx.data_ptr(), r.data_ptr(), gamma.data_ptr(), code, D, hx.data_ptr(), y.data_ptr(),
+                                  codes.data_ptr(), scales.data_ptr(), T, D, 1e-5, None) == 0
+    got = hx[:n_].view(T, D)
+    assert torch.equal(got[keep], h[keep])
+    _check_norm(h[keep], gamma, 1e-5, y[:n_].view(T, D)[keep], (codes[:n_].view(T, D)[keep], scales[:T][keep]), dtype)
+    if T > 5:
+        assert torch.isnan(got[4]).all() and torch.isnan(y[:n_].view(T, D)[4]).all()
+        assert torch.isnan(scales[4]) and not codes[:n_].view(T, D)[4].any()
+    for t, m in ((hx, n_), (y, n_), (codes, n_), (scales, T)):
+        assert (t[m:] == 77).all()
+    q = buf(torch.int8)
+    s2, back = torch.full((T + pad,), 77.0, device=DEV), buf(torch.bfloat16)
+    assert uq.lib().uq_quantize_q8(h.data_ptr(), code, D, q.data_ptr(), s2.data_ptr(), T, D, None) == 0
+    assert uq.lib().uq_dequant_q8(q.data_ptr(), s2.data_ptr(), back.data_ptr(), uq.DTYPES[torch.bfloat16], T, D, None) == 0
+    rq, rs = oq.quantize(f32(h))
+    assert np.array_equal(q[:n_].view(T, D).cpu().numpy(), rq) and np.array_equal(s2[:T].cpu().numpy(), rs, equal_nan=True)
+    want = (q[:n_].view(T, D).float() * s2[:T, None]).to(torch.bfloat16)
+    assert torch.equal(back[:n_].view(T, D).isnan(), want.isnan()) and torch.equal(back[:n_].view(T, D).nan_to_num(), want.nan_to_num())
+    for t, m in ((q, n_), (back, n_), (s2, T)):
+        assert (t[m:] == 77).all()
+    # the gradient, over dy; a row of NaN reaches its own dx alone
+    dy, hh = buf(x.dtype), h.clone()
+    dy[:n_] = r.reshape(-1)
+    dgamma = torch.full((D + pad,), 77.0, device=DEV)
+    assert uq.lib().uq_rmsnorm_grad(dy.data_ptr(), hh.data_ptr(), gamma.data_ptr(), None, code, dy.data_ptr(), dgamma.data_ptr(),
+                                    T, D, 1e-2, None) == 0
+    rx, rg = oq.rmsnorm_grad(n(r[keep]), n(h[keep]), n(gamma), 1e-2, None)
+    H, G = n(h[keep]), n(r[keep]) * n(gamma)
+    rr = 1 / np.sqrt((H * H).mean(axis=1, keepdims=True) + 1e-2)
+    mag = rr * (np.abs(G) + np.abs(H) * rr * rr * np.abs(G * H).mean(axis=1, keepdims=True))
+    steps = 3 * (D / 32 + 16) + 16
+    dx = dy[:n_].view(T, D)
+    assert np.all(np.abs(n(dx[keep]) - rx) <= ROUND[dtype] * np.abs(rx) * 1.0001 + steps * U * mag + TINY[dtype])
+    if T > 5:
+        assert torch.isnan(dx[4]).all() and torch.isnan(dgamma[:D]).all()
+    else:
+        assert np.all(np.abs(n(dgamma[:D]) - rg) <= (T + steps) * U * np.abs(n(r) * H * rr).sum(axis=0) + 2.0 ** -140)
+    assert (dy[n_:] == 77).all() and (dgamma[D:] == 77).all()
+
+
 def test_rows_without_elements_have_scale_zero():
     e = torch.empty(5, 0, device=DEV)
     for scales in (uq.rmsnorm_q8(e, e[0], 1e-5)[2][1], uq.rmsnorm_q8(e, e[0], 1e-5, residual=e, normed=True)[2][1]):
