@@ -563,8 +563,11 @@ def rmsnorm_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: torch
         assert h.dtype == x.dtype and h.shape == x.shape
         hp = _at(h, dev)
     y = _empty((T, D), x.dtype, x.device, stream) if normed else None
-    codes = _empty((T, D), torch.int8, x.device, stream) if quantized else None
-    scales = _empty(T, torch.float32, x.device, stream) if quantized else None
+    if D == 0 and quantized:
+        codes, scales = quantize_q8(x, stream)                     # scales of 0, which the norm of no elements does not write
+    else:
+        codes = _empty((T, D), torch.int8, x.device, stream) if quantized else None
+        scales = _empty(T, torch.float32, x.device, stream) if quantized else None
     _check(lib().uq_rmsnorm_q8(x.data_ptr(), rp, _at(gamma, dev), DTYPES[x.dtype], _row_stride(x, T, D), hp, _at_opt(y, dev),
                                _at_opt(codes, dev), _at_opt(scales, dev), T, D, eps, _handle(stream, dev)), "uq_rmsnorm_q8")
     return x if h is None else h, y, (codes, scales) if quantized else None

@@ -1240,11 +1240,7 @@ uq_status uq_rmsnorm_q8(const void* x, const void* residual, const void* gamma, 
     if (s != UQ_OK) return s;
     if (!(eps >= 0.f) || eps > 3.0e38f) return fail(UQ_ERR_INVALID, "eps must be finite and not negative");
     if (D && (codes != nullptr) != (scales != nullptr)) return fail(UQ_ERR_INVALID, "codes and scales must be given together");
-    if (rows == 0) return UQ_OK;
-    if (D == 0) {
-        const cudaError_t z = scales ? cudaMemsetAsync(scales, 0, (size_t)rows * sizeof(float), static_cast<cudaStream_t>(stream)) : cudaSuccess;
-        return z == cudaSuccess ? UQ_OK : cuda_fail(z, "cudaMemsetAsync");
-    }
+    if (rows == 0 || D == 0) return UQ_OK;
     if ((s = check_x8(x, ldx, D)) != UQ_OK) return s;
     if (!gamma) return fail(UQ_ERR_INVALID, "gamma is NULL");
     if (!h && !y && !codes) return fail(UQ_ERR_INVALID, "no output is wanted");

@@ -135,7 +135,7 @@ __device__ __forceinline__ float larger(float a, float b) {
 // PIPE (16-byte accesses, rows without a rest, many of them): the next rows' loads are under way while a row is reduced and
 // written, and gamma stays in registers.  Without, a row is a chain of loads, a reduction, and stores; measured, 8192 rows of 8192
 // bf16 with all outputs: PIPE 100 us (6.0 TB/s, 0.89 of the measured copy); else 256 threads a row with four accesses each 134
-// us, 512 with two 152; the quantizer 37 (5.4 TB/s) and 44 us.
+// us, 512 with two 152; the quantizer 39 (5.1 TB/s) and 44 us.
 template <class T, int V, int NV, bool NORM, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 1) row_kernel(const RowArgs a) {
     using W = Vec<T, V>;
@@ -377,7 +377,7 @@ struct GradArgs {
 // A group of threads takes every so many-th row; its share of dgamma stays in registers (of a longer row, in its CTA's row of
 // `partials`, where a CTA has one group) until its rows are done; then a CTA's groups are added in order.  Named barriers, so
 // that a CTA's groups do not wait for one another.  gamma stays in registers: read again for every row, four accesses a thread,
-// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 57 us (4.7 TB/s, the addition of the
+// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 58 us (4.6 TB/s, the addition of the
 // partials in it), without PIPE 68, with gamma read again 96.
 template <class T, int V, int NV, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {
