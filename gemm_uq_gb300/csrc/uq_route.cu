@@ -46,33 +46,36 @@ __device__ __forceinline__ float sigmoid_over(float x, float low) {
     return x >= 0.f ? 1.f / (1.f + expf(-x)) : expf(x - low) / (1.f + expf(x));
 }
 
-// Choice values as they are compared: fp32, or the bit pattern of fp64 as an integer in the same order (this part compares
+// Choice values are compared as integers in the order of the numbers, fp32 in 32 bits and fp64 in 64 (this part compares
 // integers far faster than fp64).  A value of NaN (a NaN logit or bias) ranks below all numbers and above what cannot be chosen,
-// which is none_of().
+// which is none_of(): in 32 bits it has minus infinity's place, which no value that can be chosen takes, and in 64 bits that of
+// a number far below fp32's, so that even a group's sum of two of them stays above none_of().
+__device__ __forceinline__ int key_of(float v) {
+    const int k = __float_as_int(v);
+    return k < 0 ? k ^ 0x7FFFFFFF : k;
+}
+__device__ __forceinline__ float value_of(int k) { return __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k); }
 __device__ __forceinline__ long long key_of(double v) {
     const long long k = __double_as_longlong(v);
     return k < 0 ? k ^ 0x7FFFFFFFFFFFFFFFll : k;
 }
 __device__ __forceinline__ double value_of(long long k) { return __longlong_as_double(k < 0 ? k ^ 0x7FFFFFFFFFFFFFFFll : k); }
 template <class S> __device__ __forceinline__ S none_of();
-template <> __device__ __forceinline__ float none_of<float>() { return low_value(); }
+template <> __device__ __forceinline__ int none_of<int>() { return -0x7FFFFFFF - 1; }
 template <> __device__ __forceinline__ long long none_of<long long>() { return -0x7FFFFFFFFFFFFFFFll; }
-__device__ __forceinline__ float ranked(float c, bool can) { return !can ? low_value() : (c > -3.4e38f ? c : -3.4e38f); }
+__device__ __forceinline__ int ranked(float c, bool can) { return can ? key_of(fmaxf(c, low_value())) : none_of<int>(); }
 __device__ __forceinline__ long long ranked(double c, bool can) {
     return !can ? none_of<long long>() : key_of(c > -1.7e308 ? c : -1.7e308);
 }
 // the sum of two values, as they are compared
-__device__ __forceinline__ float together(float a, float b) { return a + b; }
-__device__ __forceinline__ long long together(long long a, long long b) { return key_of(value_of(a) + value_of(b)); }
+template <class S> __device__ __forceinline__ S together(S a, S b) { return key_of(value_of(a) + value_of(b)); }
 
 // The largest of the lanes' values and, among equal ones, the smallest index; index E where none can be chosen.
-__device__ __forceinline__ void best_of(float& c, int& e, int E) {
-    uint32_t k = __float_as_uint(c);
-    k = k & 0x80000000u ? ~k : k | 0x80000000u;                    // the order of the values
-    const uint32_t top = __reduce_max_sync(ALL, k);
-    e = (int)__reduce_min_sync(ALL, k == top ? (unsigned)e : (unsigned)E);
-    c = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
-    if (c == low_value()) e = E;
+__device__ __forceinline__ void best_of(int& c, int& e, int E) {
+    const int top = __reduce_max_sync(ALL, c);
+    e = __reduce_min_sync(ALL, c == top ? e : E);
+    c = top;
+    if (c == none_of<int>()) e = E;
 }
 __device__ __forceinline__ void best_of(long long& c, int& e, int E) {
 #pragma unroll
@@ -100,7 +103,7 @@ __device__ __forceinline__ float reciprocal_about(float x) {
     return r;
 }
 __device__ __forceinline__ float score_error(const RouteArgs& a) { return a.sigmoid ? 0x1p-22f : (float)(a.E / 32 + 16) * 0x1p-24f; }
-// whether fp32 values of this error (`terms` of them in each of the two) are in their order
+// whether fp32 values of this error (`terms` of them in each of the two) are in their order; never where one is infinite or NaN
 __device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, float terms) {
     return hi - lo > 2.f * terms * (fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-24f + score_error(a));
 }
@@ -140,8 +143,8 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         const bool stays = total > none && ahead < a.top_groups;
         if constexpr (!WIDE) {
             if (!exact) {
-                const float worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
-                if (next > none && !apart(a, worst, next, 2.f * a.group_top)) sure = false;
+                const int worst = __reduce_min_sync(ALL, stays ? total : 0x7FFFFFFF), next = __reduce_max_sync(ALL, stays ? none : total);
+                if (next > none && !apart(a, value_of(worst), value_of(next), 2.f * a.group_top)) sure = false;
             }
         }
         const uint32_t open_ = __ballot_sync(ALL, stays && lane % per == 0);
@@ -167,7 +170,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
     };
     rescan();
     int id = -1, last = -1;
-    S before = none;
+    float before = 0.f;
     const int rounds = !WIDE && !exact ? a.topk + 1 : a.topk;      // the first that is not chosen, too
     for (int j = 0; j < rounds; ++j) {
         S v = mine;
@@ -175,11 +178,12 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         best_of(v, e, E);
         if (e == E) break;
         if constexpr (!WIDE) {
-            if (!exact && j && !apart(a, before, v, 1.f)) {
+            const float value = value_of(v);
+            if (!exact && j && !apart(a, before, value, 1.f)) {
                 // the same logit and bias give the same value: the lower index is right
-                if (!(before == v && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) sure = false;
+                if (!(before == value && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) sure = false;
             }
-            before = v;
+            before = value;
             last = e;
         }
         if (j < a.topk && lane == j) id = e;
@@ -192,7 +196,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
 }
 
 // Choice values of a token in fp32, into c[] (by_logit: the logits themselves), and in 64 bits.
-template <class T> __device__ __forceinline__ void values(const RouteArgs& a, float* c, const T* x, bool by_logit) {
+template <class T> __device__ __forceinline__ void values(const RouteArgs& a, int* c, const T* x, bool by_logit) {
     const int lane = threadIdx.x & 31;
     float m = low_value(), over = 0.f;
     if (!a.sigmoid && !by_logit) {
@@ -282,7 +286,8 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
     for (int i = 0; i < NL; ++i) bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
     for (long long t = (long long)blockIdx.x * WARPS + warp; t < a.T; t += (long long)gridDim.x * WARPS) {
         const T* x = static_cast<const T*>(a.logits) + t * a.E;
-        float v[NL], c[NL];
+        float v[NL];
+        int c[NL];
 #pragma unroll
         for (int i = 0; i < NL; i += V) {
             Vec<T, V> w;
@@ -319,64 +324,59 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
                 c[i] = ranked(s + bias[i], v[i] != low_value() && bias[i] != low_value());
             }
         }
-        const float none = low_value();
+        const int none = none_of<int>();
         bool sure = true, exact = by_logit, groups_sure = true;
         if (a.groups > 1) {
             const int per = a.E / a.groups / NL, g = lane / per;   // lanes of a group
-            float b1 = none, b2 = none;
+            int b1 = none, b2 = none;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                b2 = fmaxf(b2, fminf(b1, c[i]));
-                b1 = fmaxf(b1, c[i]);
+                b2 = max(b2, min(b1, c[i]));
+                b1 = max(b1, c[i]);
             }
             for (int o = 1; o < per; o <<= 1) {
-                const float o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
-                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-                b1 = fmaxf(b1, o1);
+                const int o1 = __shfl_xor_sync(ALL, b1, o), o2 = __shfl_xor_sync(ALL, b2, o);
+                b2 = max(min(b1, o1), max(b2, o2));
+                b1 = max(b1, o1);
             }
-            float total = b1;
-            if (a.group_top == 2 && b2 > none) total += b2;
+            int total = a.group_top == 2 && b2 > none ? together(b1, b2) : b1;
             if (g >= a.groups) total = none;
             int ahead = 0;
             for (int o = 0; o < a.groups; ++o) {
-                const float other = __shfl_sync(ALL, total, o * per);
+                const int other = __shfl_sync(ALL, total, o * per);
                 ahead += other > total || (other == total && o < g);
             }
             const bool stays = total > none && ahead < a.top_groups;
             if (!exact) {
-                const float worst = -warp_max_f(stays ? -total : none), next = warp_max_f(stays ? none : total);
-                groups_sure = next == none || apart(a, worst, next, 2.f * a.group_top);
+                const int worst = __reduce_min_sync(ALL, stays ? total : 0x7FFFFFFF), next = __reduce_max_sync(ALL, stays ? none : total);
+                groups_sure = next == none || apart(a, value_of(worst), value_of(next), 2.f * a.group_top);
             }
             if (!a.bias) exact = true;          // the order within the groups is that of x
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != none));
+                c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != low_value()));
         }
         // lane j: choice j; behind the last one, those that are too near to it
         int id = -1, last = -1, found = 0;
-        float before = none;
+        float before = 0.f;
         for (int j = 0; j < 32; ++j) {
             if (exact && j == a.topk) break;
-            float best = c[0];
-            int at = 0;
+            int best = c[0], at = 0;
 #pragma unroll
             for (int i = 1; i < NL; ++i)
                 if (c[i] > best) best = c[i], at = i;
-            uint32_t k = __float_as_uint(best);
-            k = k & 0x80000000u ? ~k : k | 0x80000000u;            // the order of the values
-            const uint32_t top = __reduce_max_sync(ALL, k);
-            const int who = __ffs(__ballot_sync(ALL, k == top)) - 1;
-            best = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
-            if (best == none) break;
+            const int top = __reduce_max_sync(ALL, best), who = __ffs(__ballot_sync(ALL, best == top)) - 1;
+            if (top == none) break;
+            const float value = value_of(top);
             const int e = __shfl_sync(ALL, e0 + at, who);
             if (!exact && j) {
-                if (apart(a, before, best, 1.f)) {
+                if (apart(a, before, value, 1.f)) {
                     if (j >= a.topk) break;
-                } else if (!(before == best && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
+                } else if (!(before == value && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
                     sure = false;               // (the same logit and bias give the same value: the lower index is right)
                 }
             }
-            before = best;
+            before = value;
             last = e;
             if (lane == j) id = e;
             found = j + 1;
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(WARPS * 32) route_kernel(const RouteArgs a) {
         const T* x = static_cast<const T*>(a.logits) + t * a.E;
         bool sure;
         __syncwarp();
-        values(a, reinterpret_cast<float*>(mine), x, by_logit);
-        int id = choose(a, reinterpret_cast<float*>(mine), x, by_logit, sure);
+        values(a, reinterpret_cast<int*>(mine), x, by_logit);
+        int id = choose(a, reinterpret_cast<int*>(mine), x, by_logit, sure);
         if (!sure) {
             __syncwarp();
             values(a, reinterpret_cast<long long*>(mine), x);

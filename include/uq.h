@@ -535,8 +535,9 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
  *   scores   s = softmax of the token's logits (over all experts), or 1 / (1 + e^-logit)
  *   choice   c = s + bias; the topk experts of the highest c, in that order, equal c by lower index.  Decided as in 64-bit
  *            arithmetic, without a bias by the logits themselves.  An expert whose logit (or bias) is minus infinity is
- *            never chosen; one whose logit is NaN is chosen last.  Where fewer than topk can be chosen, the remaining ids are -1
- *            and their weights 0.
+ *            never chosen; one whose logit is NaN is chosen last, behind all numbers (the softmax of the others is then
+ *            taken among themselves for the choice; as weights they are NaN).  Where fewer than topk can be chosen, the
+ *            remaining ids are -1 and their weights 0.
  *   groups   > 1: the experts form `groups` equal groups of neighbours; only experts of the top_groups best ones may be
  *            chosen.  A group counts the sum of its group_top (1 or 2) highest c of experts that may be chosen; equal groups by
  *            lower index.

@@ -1,0 +1,107 @@
+"""Choices of the router that 64 bits decide, at the edges of its forms: groups whose best members are NaN or lie at the end of
+fp32, the first expert behind the last choice, and neighbours nearer than fp32 scores can tell in each kernel's own way of
+deciding them again.
+
+E = 96 and 100 in 8 (4) groups take the kernel with the values in shared memory, E = 64, 256 and 1024 the one that holds them in
+registers (2, 8 and 32 a lane).  The choice has to be the oracle's exactly."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import gemm_uq_gb300 as uq  # noqa: E402
+from oracle import router as orr  # noqa: E402
+
+DEV = torch.device("cuda:0")
+NAN, LOW = float("nan"), float("-inf")
+
+
+def n(t):
+    return t.double().cpu().numpy()
+
+
+def _choose(x, k, score, bias=None, G=1, tg=1, gt=1):
+    """The oracle's choice; the scores of a token with NaN logits are those over its other logits."""
+    scores = orr.scores
+
+    def among_numbers(v, how):
+        v = np.asarray(v, np.float64)
+        with np.errstate(invalid="ignore"):
+            s = scores(np.where(np.isnan(v), -np.inf, v), how)
+        return np.where(np.isnan(v), np.nan, s)
+    orr.scores = among_numbers
+    try:
+        return orr.choose(n(x), k, score, None if bias is None else n(bias), G, tg, gt)
+    finally:
+        orr.scores = scores
+
+
+def _check(x, k, score, bias=None, G=1, tg=1, gt=1, renorm=True):
+    ids, w = uq.moe_route(x, k, score=score, bias=bias, groups=G, top_groups=tg, group_top=gt, renormalize=renorm)
+    want = _choose(x, k, score, bias, G, tg, gt)
+    bad = np.argwhere((ids.cpu().numpy() != want).any(axis=1)).reshape(-1)
+    assert len(bad) == 0, f"{len(bad)} tokens, first {bad[0]}: {ids[bad[0]].tolist()}, in 64 bits {want[bad[0]].tolist()}"
+    return ids, w
+
+
+def _scores64(x, score):
+    return orr.scores(np.asarray(x, np.float64), score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (96, 8), (100, 4), (256, 8), (1024, 32)])
+def test_groups_of_nan(E, G, score):
+    """A group whose members are all NaN can be chosen, last: a token of NaN alone keeps its experts, and its weights are NaN."""
+    size, g = E // G, np.random.default_rng(E)
+    x = torch.from_numpy(g.normal(size=(7, E)).astype(np.float32)).to(DEV)
+    x[0] = NAN
+    x[1, :(G - 1) * size] = NAN                                          # numbers in the last group alone
+    x[2, :G // 2 * size] = NAN
+    x[3] = LOW
+    x[3, size:3 * size] = NAN                                            # NaN is all that may be chosen
+    x[4, ::2] = NAN
+    x[5, size:2 * size] = NAN
+    x[5, size + 1] = 0.3                                                 # one number beside NaN
+    x[6, 1::size] = LOW
+    bias = torch.from_numpy(g.normal(size=E).astype(np.float32) * 0.1).to(DEV)
+    k = min(4, size)
+    for b in (None, bias):
+        for gt in (1, 2):
+            for tg in (1, 2, G - 1):
+                for renorm in (True, False):
+                    ids, w = _check(x, k, score, b, G, tg, gt, renorm)
+                    assert ids[0].tolist() == list(range(k)) and torch.isnan(w[0]).all()
+                    assert ids[3].tolist() == list(range(size, size + k)) and torch.isnan(w[3]).all()
+
+
+@pytest.mark.parametrize("E,G", [(64, 8), (96, 8), (256, 8)])
+def test_groups_at_the_end_of_fp32(E, G):
+    """Sums of two biases that leave fp32: the group counts, and in the order of the sums."""
+    size = E // G
+    x = torch.zeros(3, E, device=DEV)
+    x[1, :size], x[2] = LOW, LOW
+    x[2, 2 * size:3 * size] = 0.5
+    for sign in (1.0, -1.0):
+        bias = sign * torch.linspace(3.3e38, 2.9e38, G, device=DEV).repeat_interleave(size)
+        for tg in (1, 2, 3):
+            _check(x, 2, "sigmoid", bias, G, tg, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(8, 1), (64, 8), (96, 8), (256, 1), (256, 8), (1000, 1)])
+def test_nan_behind_the_lowest_numbers(E, G, score):
+    """Masks of fp32's lowest value, and logits next to it, are numbers: they come in their order, and before NaN."""
+    size = E // G
+    low = torch.finfo(torch.float32).min
+    x = torch.full((4, E), low, device=DEV)
+    x[:, 0] = NAN
+    x[1, 2::2] = -3.4012e38
+    x[1, 3::4] = -3.4025e38
+    x[2, 1:] = NAN
+    x[2, size - 1] = low                                                 # one number, behind NaN
+    x[3, 1:size] = LOW                                                   # the first group: NaN alone
+    k = min(6, size)
+    for tg in {1, max(G - 1, 1)}:
+        for gt in (1, 2) if G > 1 else (1,):
+            _check(x, k, score, None, G, tg, gt)
