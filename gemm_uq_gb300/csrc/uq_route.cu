@@ -356,10 +356,11 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             for (int i = 0; i < NL; ++i)
                 c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != low_value()));
         }
-        // lane j: choice j; behind the last one, those that are too near to it
+        // lane j: choice j; behind the last one, those that are too near to it.  What is behind the 32nd is looked at, too: near to
+        // it, it makes the choice unsure.
         int id = -1, last = -1, found = 0;
         float before = 0.f;
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j <= 32; ++j) {
             if (exact && j == a.topk) break;
             int best = c[0], at = 0;
 #pragma unroll

@@ -105,3 +105,17 @@ def test_nan_behind_the_lowest_numbers(E, G, score):
     for tg in {1, max(G - 1, 1)}:
         for gt in (1, 2) if G > 1 else (1,):
             _check(x, k, score, None, G, tg, gt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [40, 64, 200, 256, 1024])
+def test_the_first_expert_behind_32_choices(E, score):
+    """32 choices, the last of which and those behind it are nearer than fp32 can tell, all others far apart."""
+    T, g = 64, np.random.default_rng(E)
+    x = torch.from_numpy(g.normal(size=E).astype(np.float32) + g.integers(-40, 41, (T, E)).astype(np.float32) * np.float32(2.0 ** -22))
+    s = _scores64(x.numpy()[:1], score)[0]
+    bias = (2.0 - s).astype(np.float32)                                  # all choice values near two
+    bias[g.permutation(E)[:31]] += np.arange(1, 32, dtype=np.float32)    # but for those of 31 experts
+    x, bias = x.to(DEV), torch.from_numpy(bias).to(DEV)
+    for k in (31, 32):
+        _check(x, k, score, bias)
