@@ -104,8 +104,13 @@ __device__ __forceinline__ float reciprocal_about(float x) {
 }
 __device__ __forceinline__ float score_error(const RouteArgs& a) { return a.sigmoid ? 0x1p-22f : (float)(a.E / 32 + 16) * 0x1p-24f; }
 // whether fp32 values of this error (`terms` of them in each of the two) are in their order; never where one is infinite or NaN
-__device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, float terms) {
-    return hi - lo > 2.f * terms * (fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-24f + score_error(a));
+__device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, float terms, float best = 0.f) {
+    return hi - lo > 2.f * terms * ((fmaxf(fabsf(hi), fabsf(lo)) + best) * 0x1p-24f + score_error(a));
+}
+// The same for the sums of two groups, given the best value of each lane's group.  A bias may give a sum's terms opposite signs, so
+// that each is larger than the sum; but the first is at most the best of all, and the second at most that and the sum together.
+__device__ __forceinline__ bool groups_apart(const RouteArgs& a, int hi, int lo, int b1) {
+    return apart(a, value_of(hi), value_of(lo), 2.f * a.group_top, fmaxf(value_of(__reduce_max_sync(ALL, b1)), 0.f));
 }
 
 // Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it), in fp32 or 64 bits.  Lane j returns choice j, -1 for
@@ -144,7 +149,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
         if constexpr (!WIDE) {
             if (!exact) {
                 const int worst = __reduce_min_sync(ALL, stays ? total : 0x7FFFFFFF), next = __reduce_max_sync(ALL, stays ? none : total);
-                if (next > none && !apart(a, value_of(worst), value_of(next), 2.f * a.group_top)) sure = false;
+                if (next > none && !groups_apart(a, worst, next, b1)) sure = false;
             }
         }
         const uint32_t open_ = __ballot_sync(ALL, stays && lane % per == 0);
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             const bool stays = total > none && ahead < a.top_groups;
             if (!exact) {
                 const int worst = __reduce_min_sync(ALL, stays ? total : 0x7FFFFFFF), next = __reduce_max_sync(ALL, stays ? none : total);
-                groups_sure = next == none || apart(a, value_of(worst), value_of(next), 2.f * a.group_top);
+                groups_sure = next == none || groups_apart(a, worst, next, b1);
             }
             if (!a.bias) exact = true;          // the order within the groups is that of x
 #pragma unroll

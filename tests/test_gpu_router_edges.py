@@ -119,3 +119,16 @@ def test_the_first_expert_behind_32_choices(E, score):
     x, bias = x.to(DEV), torch.from_numpy(bias).to(DEV)
     for k in (31, 32):
         _check(x, k, score, bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (96, 8), (256, 8), (1024, 32)])
+def test_groups_whose_best_two_cancel(E, G, score):
+    """A group's best two far from one and of opposite signs: its sum has the error of the two, not one of its own size."""
+    T, size, tg = 64, E // G, G // 2
+    g = np.random.default_rng(E)
+    x = torch.from_numpy(g.normal(size=(T, E)).astype(np.float32)).to(DEV)
+    lead = 2.0 ** 20 * (1 + np.arange(G) / 64)                           # leaders far apart, so that their own order is plain
+    bias = (-lead[:, None] + np.zeros((G, size))).astype(np.float32)     # the others undo the leader
+    bias[:, 3] = lead
+    _check(x, tg, score, torch.from_numpy(bias.reshape(-1)).to(DEV), G, tg, 2)
