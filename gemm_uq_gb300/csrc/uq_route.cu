@@ -479,9 +479,10 @@ __global__ void __launch_bounds__(WARPS * 32) route_grad_kernel(const RouteGradA
         float q = dw;                           // what route j adds to its expert
         float m = low_value(), sum = 0.f, dot = 0.f;
         if (a.renorm) {
+            // (from the largest of them; where all are minus infinity the weights are 0 and there is no gradient)
             const float top = warp_max_f(v);
             float w = 0.f;
-            if (id >= 0) w = a.sigmoid ? sigmoid_over(v, fminf(top, 0.f)) : expf(v - top);
+            if (id >= 0 && top != low_value()) w = a.sigmoid ? sigmoid_over(v, fminf(top, 0.f)) : expf(v - top);
             const float all = warp_add(w);
             w = all > 0.f || all != all ? w / all : 0.f;
             q = w * (dw - warp_add(w * dw));

@@ -554,7 +554,8 @@ uq_status uq_moe_route(const void* logits, uq_dtype type, const float* bias, uq_
  * uq_moe_route_grad -- the gradient of uq_moe_route's weights with respect to the logits (the ids, and with them the bias
  * and the groups, have none):  dlogits (device) [T][experts] of `type`, written whole.
  *   logits as given to uq_moe_route, ids (device) int32 [T][topk] its ids (or any: an entry outside [0, experts) is no route,
- *   and an expert named twice gets both routes' gradients), dweights (device) fp32 [T][topk].
+ *   and an expert named twice gets both routes' gradients; routes to experts whose logits are minus infinity have weights of
+ *   0, renormalised or not, and no gradient), dweights (device) fp32 [T][topk].
  * Limits as uq_moe_route.  Asynchronous.
  */
 uq_status uq_moe_route_grad(const void* logits, uq_dtype type, const int32_t* ids, const float* dweights, uq_score score,

@@ -166,3 +166,23 @@ def test_many_tokens_and_a_graph():
     s.synchronize()
     assert torch.equal(got[0], ids) and torch.equal(got[1], w)
     assert torch.equal(dx, uq.moe_route_grad(x, ids, w))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_gradient_of_routes_to_masked_experts(dtype, score, renorm):
+    """Routes whose experts' logits are all minus infinity have weights of 0, and the logits no gradient from them."""
+    x = _logits(7, 6, 20, dtype)
+    x[1, 3:6] = float("-inf")
+    x[2] = float("-inf")
+    x[3, 4] = float("-inf")
+    ids = torch.tensor([[0, 1, 2], [3, 4, 5], [0, 1, 2], [4, 5, 6], [-1, -1, -1], [7, 7, 20]], dtype=torch.int32)
+    dw = torch.from_numpy(np.random.default_rng(3).normal(size=(6, 3)).astype(np.float32)).to(DEV)
+    dx = uq.moe_route_grad(x, ids.to(DEV), dw, score=score, renormalize=renorm, scale=1.5)
+    ref, mag = orr.grad(n(x), ids.numpy(), n(dw), score, renorm, 1.5)
+    tol = ROUND[dtype] * np.abs(ref) * 1.0001 + 4 * (20 / 32 + 40) * U * mag + TINY[dtype]
+    assert np.all(np.abs(n(dx) - ref) <= tol)
+    assert not dx[2].any() and not dx[4].any()
+    if renorm:
+        assert not dx[1].any()
