@@ -831,7 +831,7 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ C
                     v[0] += p[i][k].x; v[1] += p[i][k].y; v[2] += p[i][k].z; v[3] += p[i][k].w;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] *= sx[i] * sw4[j];
+                for (int j = 0; j < 4; ++j) v[j] = v[j] * sx[i] * sw4[j];
                 store4<T>(a.g, (long long)(t.m0 + c[i]) * a.g.N + nn, a.g.N - nn, v);
             }
         }

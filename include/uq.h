@@ -519,7 +519,8 @@ uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, cons
 
 /*
  * uq_gemm_w8a8 -- y[m][n] = xscales[m] * wscales[n] * sum_k x[m][k] * w[n][k] of 8-bit operands, rounded once to ytype.
- * The integer sums are exact over every 1024 k, and are added up in fp32 or exactly.
+ * The integer sums are exact over every 1024 k, and are added up in fp32 or exactly; a sum is multiplied by xscales[m] and then
+ * by wscales[n], in fp32 (both products have to lie within it).
  *   x: int8 codes [M][K] with xscales fp32 [M] (both device; xtype and ldx ignored); or, with xscales NULL, rows of xtype,
  *      ldx apart, quantized in the call as uq_quantize_q8 does (into the per-stream workspace)
  *   w (device) int8 [N][K], wscales (device) fp32 [N]; y (device) [M][N], written.

@@ -177,3 +177,21 @@ def test_offsets_past_32_bits(M, N, K):
     for rows, cols in ((slice(-9, None), slice(-300, None)), (slice(0, 9), slice(0, 300))):
         _check(y[rows, cols], (x[rows].contiguous(), sx[rows]), (w[cols].contiguous(), sw[cols]), "bf16")
     assert uq.device_fault() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(1, 96, 4096), (8, 512, 4096), (20, 128, 4096), (20, 20000, 1024), (50, 200, 4096), (50, 20000, 1024),
+                                   (100, 257, 4096), (100, 20000, 1024), (2500, 2100, 1184)])
+def test_scales_whose_product_leaves_fp32(M, N, K, dtype):
+    """Scales that together are below fp32's smallest number while the outputs are not, in each form of the product: single
+    tokens, tiles that share k, whole tiles, pairs.  Rounded as ever: each factor once."""
+    x, w = _operand(1, M, K, "largest"), _operand(2, N, K, "largest")
+    x, w = ((q, (1 + torch.rand(len(q), device=DEV)) * 2.0 ** -73) for q, _ in (x, w))
+    y = uq.gemm_w8a8(x, w, dtype=DTYPE[dtype])
+    a, b = x[0].double() * x[1].double()[:, None], w[0].double() * w[1].double()[:, None]
+    want = a @ b.t()
+    assert float(want.abs().min()) > 2.0 ** -126
+    mag = sum((a[:, k:k + 1024] @ b[:, k:k + 1024].t()).abs() for k in range(0, K, 1024))
+    tol = ROUND[dtype] * want.abs() * 1.0001 + (K / 1024 + 4) * U * mag + (a.abs() @ b.abs().t()) * 2.0 ** -50
+    bad = (y.double() - want).abs() > tol
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outputs off, first at {bad.nonzero()[0].tolist()}"
