@@ -132,3 +132,59 @@ def test_groups_whose_best_two_cancel(E, G, score):
     bias = (-lead[:, None] + np.zeros((G, size))).astype(np.float32)     # the others undo the leader
     bias[:, 3] = lead
     _check(x, tg, score, torch.from_numpy(bias.reshape(-1)).to(DEV), G, tg, 2)
+
+
+def _near_pairs(E, score, ranks, g):
+    """Logits [64][E] and a bias whose choice values lie 2^-6 apart, but for the experts of ranks r and r + 1 (r in `ranks`), which
+    are so near that fp32 does not tell, and whose order differs from token to token."""
+    T = 64
+    base = g.normal(size=E).astype(np.float32)
+    level = (np.arange(E)[::-1] * 2.0 ** -6).astype(np.float64)
+    order = g.permutation(E)                                             # order[r]: the expert of rank r
+    for r in ranks:
+        level[r + 1] = level[r]
+    x = np.tile(base, (T, 1))
+    for r in ranks:
+        for e in order[r:r + 2]:
+            x[:, e] += g.integers(-3, 4, T).astype(np.float32) * np.float32(2.0 ** -23)
+    want = np.empty(E)
+    want[order] = level
+    bias = (want - _scores64(base[None], score)[0]).astype(np.float32)
+    return torch.from_numpy(x).to(DEV), torch.from_numpy(bias).to(DEV)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(60, 1), (64, 8), (96, 8), (256, 1), (256, 8), (1000, 1), (1024, 8)])
+def test_a_few_near_pairs(E, G, score):
+    """Pairs among choices that are far apart otherwise: within the choice, at its end, and behind it."""
+    g = np.random.default_rng([E, G])
+    k = 8
+    for ranks in ((k - 1,), (1,), (0, 3, 6), (2, k - 1), (k,)):
+        x, bias = _near_pairs(E, score, ranks, g)
+        for gt in (1, 2) if G > 1 else (1,):
+            _check(x, k, score, bias, G, G if G == 1 else 5, gt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (96, 8), (256, 8), (1024, 32)])
+def test_near_groups(E, G, score):
+    """Groups far apart but for two, the last that stays and the first that does not, whose order differs from token to token."""
+    T, size, tg = 64, E // G, 3
+    for gt in (1, 2):
+        g = np.random.default_rng([E, gt])
+        base = g.normal(size=E).astype(np.float32)
+        s = _scores64(base[None], score)[0]
+        total = np.arange(G)[::-1] * 0.125                               # of the groups by rank
+        total[tg] = total[tg - 1]
+        ranks = g.permutation(G)
+        want = np.full(E, -8.0) + np.arange(E) * 2.0 ** -9               # members that do not count
+        for r in range(G):
+            lead = ranks[r] * size + g.permutation(size)[:2]
+            want[lead[0]] = total[r] + (1.0 if gt == 2 else 0.0)
+            if gt == 2:
+                want[lead[1]] = -1.0
+        bias = (want - s).astype(np.float32)
+        x = np.tile(base, (T, 1))
+        for r in (tg - 1, tg):
+            x[:, ranks[r] * size:(ranks[r] + 1) * size] += g.integers(-3, 4, (T, size)).astype(np.float32) * np.float32(2.0 ** -23)
+        _check(torch.from_numpy(x).to(DEV), 2, score, torch.from_numpy(bias).to(DEV), G, tg, gt)
