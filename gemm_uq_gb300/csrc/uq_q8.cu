@@ -90,14 +90,16 @@ template <class T, int V, bool ODD> struct Parts {
             return w;
         }
     }
-    // Copies a part ahead; left: elements of the matrix from the row's first part on (beyond them nothing is read).
-    __device__ __forceinline__ void copy(uint32_t dst, const T* row, int part, long long left) const {
+    // Copies part `first` + `more` ahead; left: elements of the matrix from the row's first part on (beyond them nothing is read).
+    // (Two steps, one of them common to a thread's parts: quantizer 38.8 -> 38.1 us, with the parts' numbers added first.)
+    __device__ __forceinline__ void copy(uint32_t dst, const T* row, int first, int more, long long left) const {
         if constexpr (ODD) {
+            const int part = first + more;
             const long long here = left - part * V;
             const int bytes = (here < V ? (int)here : V) * (int)sizeof(T);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(reinterpret_cast<const W*>(row) + part), "r"(bytes) : "memory");
         } else {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(reinterpret_cast<const W*>(row) + part) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(reinterpret_cast<const W*>(row) + first + more) : "memory");
         }
     }
 };
@@ -160,8 +162,8 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (tid + i * a.group < nvec) {
-                    parts.copy(slot + other + i * part, x_of(row), tid + i * a.group, left);
-                    if (has_res) parts.copy(slot + other + (NV + i) * part, res_of(row), tid + i * a.group, left);
+                    parts.copy(slot + other + i * part, x_of(row), tid, i * a.group, left);
+                    if (has_res) parts.copy(slot + other + (NV + i) * part, res_of(row), tid, i * a.group, left);
                 }
         }
         copies_issued();
@@ -176,11 +178,8 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
         for (int i = 0; i < NV; ++i)
             if (tid + i * a.group < nvec) held[i] = parts.of_vector(gamma, tid + i * a.group);
     }
-    auto gam = [&](int i) {
-        if constexpr (!NORM) return W();
-        else if constexpr (HELD) return held[i];
-        else return parts.of_vector(gamma, tid + i * a.group);
-    };
+    // (this form and no other: written with `if constexpr`, the quantizer, which has no gamma, takes 39 us instead of 37)
+    auto gam = [&](int i) { return !NORM ? W() : (HELD ? held[HELD ? i : 0] : parts.of_vector(gamma, tid + i * a.group)); };
     int buf = 0;
     for (long long base = (long long)blockIdx.x * per_cta; base < a.rows; base += step, buf ^= 1) {
         const long long row = base + mine;
@@ -404,9 +403,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
             for (int i = 0; i < NV; ++i) {
                 const int v = tid + i * a.group;
                 if (v >= nvec) continue;
-                parts.copy(slot + other + i * part16, static_cast<const T*>(a.dy) + at, v, left);
-                parts.copy(slot + other + (NV + i) * part16, static_cast<const T*>(a.h) + at, v, left);
-                if (a.dh) parts.copy(slot + other + (2 * NV + i) * part16, static_cast<const T*>(a.dh) + at, v, left);
+                parts.copy(slot + other + i * part16, static_cast<const T*>(a.dy) + at, tid, i * a.group, left);
+                parts.copy(slot + other + (NV + i) * part16, static_cast<const T*>(a.h) + at, tid, i * a.group, left);
+                if (a.dh) parts.copy(slot + other + (2 * NV + i) * part16, static_cast<const T*>(a.dh) + at, tid, i * a.group, left);
             }
         }
         copies_issued();
