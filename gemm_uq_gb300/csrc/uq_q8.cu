@@ -567,15 +567,25 @@ Shape shape_of(int nvec, int most_threads, int most_nv, bool few) {
 }
 
 // How rows are taken: elements per access; whether in 16-byte parts that rows do not begin or end with.
+// The parts' ends cost each access a test, and gamma, which does not begin where a row's part does, is read by elements.  So the
+// norm and its gradient (`plain`: the quantizer) take rows by elements where that is more than the wider accesses save: rows of
+// few parts, and 16-bit rows that the forms which copy ahead do not hold, of which gamma and the rows fill the registers.
+// Measured, us, by elements / in parts: gradient of 400 x 101 bf16 5.2 / 8.4, 301 8.6 / 7.0; norm of 4000 x 101 3.8 / 4.4; 4000
+// x 8191 bf16 139 / 150 and 154 / 211, 16001 226 / 238 and 370 / 357; 4000 x 8003 fp32 153 / 99 and 192 / 84; quantizer 4000 x
+// 8191 bf16 85 / 44, 8003 fp32 91 / 36.
+// Few elements in all are spread over more threads, as few rows are, and so are norms that do not copy ahead: 400 x 601 bf16 3.4 us
+// and 5.5 with four parts a thread, gradient of 400 x 301 7.0 and 12.5, norm of 4000 x 301 7.1 and 10.1.
 struct Plan { int v; bool odd; Shape s; };
-template <class T> Plan plan_of(int D, long long ld, int rows, int most_threads, int most_nv, int sms) {
+template <class T> Plan plan_of(bool plain, int D, long long ld, int rows, int most_threads, int most_nv, int sms) {
     constexpr int WIDE = 16 / sizeof(T);
     const bool few = rows <= 2 * sms;
     const int v = access<T>(D, ld);
     if (v < WIDE && (ld == D || rows == 1)) {
         const int most = (int)(((long long)D + 2 * WIDE - 2) / WIDE);              // parts of a row, begun anywhere
-        const Shape s = shape_of(most, most_threads, most_nv, few);
-        if (s.group * s.nv >= most) return {WIDE, true, s};
+        Shape s = shape_of(most, most_threads, most_nv, few || (long long)rows * most <= (long long)sms * (most_threads * 5 / 8));
+        if (!plain && s.nv < most_nv) s = shape_of(most, most_threads, most_nv, true);
+        const bool pays = plain || (most > 32 && (sizeof(T) == 4 || most <= 1024));
+        if (pays && s.group * s.nv >= most) return {WIDE, true, s};
     }
     return {v, false, shape_of(D / v, most_threads, most_nv, few)};
 }
@@ -616,7 +626,7 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
         RowArgs a = a0;
-        const Plan p = plan_of<T>(a.D, a.ldx, a.rows, MAX_THREADS, 4, sms);
+        const Plan p = plan_of<T>(!NORM, a.D, a.ldx, a.rows, MAX_THREADS, 4, sms);
         a.group = p.s.group;
         const int block = a.group < 128 ? 128 : a.group, per = block / a.group;
         const long long tiles = ((long long)a.rows + per - 1) / per;
@@ -633,8 +643,12 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
                     return cudaGetLastError();
                 }
             }
-            row_kernel<T, V, NV, NORM, false, ODD><<<grid_of(tiles, (long long)sms * (2048 / block), p), block, 0, st>>>(a);
-            return cudaGetLastError();
+            if constexpr (NORM && ODD && sizeof(T) == 2 && NV > 1) {
+                return cudaErrorInvalidConfiguration;              // (not among plan_of's)
+            } else {
+                row_kernel<T, V, NV, NORM, false, ODD><<<grid_of(tiles, (long long)sms * (2048 / block), p), block, 0, st>>>(a);
+                return cudaGetLastError();
+            }
         });
     });
 }
@@ -679,7 +693,7 @@ cudaError_t launch_rmsnorm_q8(const void* x, const void* residual, const void* g
 
 // CTAs of the gradient, each with a partial row of dgamma.
 static Plan grad_plan(int type, int rows, int D, int sms) {
-    return type == UQ_FP32 ? plan_of<float>(D, D, rows, GRAD_THREADS, 2, sms) : plan_of<__half>(D, D, rows, GRAD_THREADS, 2, sms);
+    return type == UQ_FP32 ? plan_of<float>(false, D, D, rows, GRAD_THREADS, 2, sms) : plan_of<__half>(false, D, D, rows, GRAD_THREADS, 2, sms);
 }
 static int grad_block(const Shape& s) { return s.group < 256 ? 256 : s.group; }
 int norm_grad_partials(int type, int rows, int D, int sms) {
@@ -709,8 +723,12 @@ cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma
                     return cudaGetLastError();
                 }
             }
-            norm_grad_kernel<T, V, NV, false, ODD><<<P, block, add, st>>>(a);
-            return cudaGetLastError();
+            if constexpr (ODD && sizeof(T) == 2 && NV > 2) {
+                return cudaErrorInvalidConfiguration;              // (not among plan_of's)
+            } else {
+                norm_grad_kernel<T, V, NV, false, ODD><<<P, block, add, st>>>(a);
+                return cudaGetLastError();
+            }
         });
     });
     if (e != cudaSuccess) return e;
