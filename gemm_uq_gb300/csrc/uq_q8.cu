@@ -30,6 +30,20 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
+// What a row is multiplied with whose squares, or their sum, have left fp32: 2^31 squares of fp32's largest value then stay within
+// it, and a sum that had left it is above 2^-32.
+constexpr float FAR = 0x1p-80f;
+// A barrier of one of a CTA's four groups of threads.  (Constant barriers: with a number in a register a CTA claims all 16, and
+// fewer CTAs fit an SM, 16384 x 512 18.7 us instead of 13.7.)
+__device__ __forceinline__ void group_sync(int group, int threads) {
+    switch (group) {
+        case 0: asm volatile("bar.sync 1, %0;" :: "r"(threads) : "memory"); break;
+        case 1: asm volatile("bar.sync 2, %0;" :: "r"(threads) : "memory"); break;
+        case 2: asm volatile("bar.sync 3, %0;" :: "r"(threads) : "memory"); break;
+        default: asm volatile("bar.sync 4, %0;" :: "r"(threads) : "memory");
+    }
+}
+
 // A thread's own prefetches: it copies 16-byte parts of a coming row to shared memory, each row's as one group, and reads back
 // what it copied itself, so no other thread is waited for.
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -143,6 +157,7 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
     using W = Vec<T, V>;
     __shared__ float sums[2][MAX_THREADS / 32];
     __shared__ float maxima[2][MAX_THREADS / 32];
+    constexpr bool WIDE_RANGE = !std::is_same<T, __half>::value;   // squares of fp16 values stay within fp32
     extern __shared__ __align__(16) uint8_t ahead[];               // PIPE: [row][x, residual][part][thread] of 16 bytes
     const int per_cta = blockDim.x / a.group, tid = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const int warps = a.group >> 5, first_warp = mine * warps, lane = threadIdx.x & 31;
@@ -261,7 +276,33 @@ __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 
         const bool bad = !(most < __uint_as_float(INF_BITS));
         const float nan = __uint_as_float(0x7FC00000u);
         if constexpr (NORM) {
-            const float r = __frsqrt_rn(sum / (float)a.D + a.eps);
+            float r = __frsqrt_rn(sum / (float)a.D + a.eps);
+            if constexpr (WIDE_RANGE) {
+                if (__builtin_expect(!(sum < __uint_as_float(INF_BITS)), 0)) {
+                    // The squares, or their sum, have left fp32, which their mean need not: again, from FAR h.
+                    sum = 0.f;
+                    auto add_far = [&](const W& w) {
+                        float f[V];
+                        unpack(w, f);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) sum = fmaf(f[j] * FAR, f[j] * FAR, sum);
+                    };
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        if (tid + i * a.group < nvec) add_far(kept[i]);
+                    if constexpr (!PIPE && !ODD) {
+                        for (int v = tid + NV * a.group; v < nvec; v += a.group) add_far(load(v));
+                    }
+                    sum = warp_sum(sum);
+                    if (warps > 1) {
+                        group_sync(mine, a.group);                 // the first sums have been read
+                        if (lane == 0) sums[buf][threadIdx.x >> 5] = sum;
+                        group_sync(mine, a.group);
+                        sum = warp_sum(lane < warps ? sums[buf][first_warp + lane] : 0.f);
+                    }
+                    r = FAR * __frsqrt_rn(sum / (float)a.D + FAR * (FAR * a.eps));
+                }
+            }
             if (tid == 0 && a.scales) a.scales[row] = bad ? nan : r * most / 127.f;
             // 127 / most stays finite for the smallest; a bad row's codes are zero
             const float up = most < 0x1p-64f ? 0x1p80f : 1.f;

@@ -500,7 +500,7 @@ uq_status uq_dequant_q8(const int8_t* codes, const float* scales, void* out, uq_
  *   (device) [D].
  *   h, y (device, or NULL: not wanted) [rows][D] of `type`; codes (device) int8 [rows][D] and scales (device) fp32 [rows],
  *   both or neither; written.  h may be x (with ldx = D) or residual, and so may y.
- * The mean of the squares has to lie within fp32.  A row with a NaN or an infinity gets a NaN scale and codes 0.  D == 0 is
+ * The mean of the squares and the products h[j] * gamma[j] have to lie within fp32.  A row with a NaN or an infinity gets a NaN scale and codes 0.  D == 0 is
  * a no-op.  The gradient, with the codes taken for the values they stand for, is uq_rmsnorm_grad.  Asynchronous.
  */
 uq_status uq_rmsnorm_q8(const void* x, const void* residual, const void* gamma, uq_dtype type, long long ldx, void* h, void* y,

@@ -301,3 +301,28 @@ def test_many_short_rows():
         a = x.clone()
         got = uq.rmsnorm_q8(a, gamma, 1e-5, residual=r, h=a)
         assert torch.equal(a, h) and torch.equal(got[2][0], q[0])
+
+
+def _loud(seed, T, D, dtype, kind):
+    """Rows whose squares, or whose squares' sum, leave fp32 while their mean does not; every third row is ordinary."""
+    x = _rows(seed, T, D, "fp32")
+    x[x == 0] = 0.5
+    if kind == "all":
+        x[::3] *= 2.0 ** 65 / x[::3].abs().amax(dim=1, keepdim=True)
+    else:
+        x[::3, D // 2] = 2.0 ** 65
+    return x.to(DTYPE[dtype])
+
+
+@pytest.mark.parametrize("kind", ["all", "one"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,D", [(4, 8192), (5, 8191), (700, 8192), (340, 9001), (900, 4000), (2000, 4001), (3, 33001), (400, 16384)])
+def test_squares_whose_sum_leaves_fp32(T, D, dtype, kind):
+    h, gamma = _loud(1, T, D, dtype, kind), _rows(3, 1, D, dtype)[0].contiguous()
+    for eps in (1e-5, 0.0):
+        got, y, q = uq.rmsnorm_q8(h, gamma, eps, normed=True)
+        assert got is h
+        _check_norm(h, gamma, eps, y, q, dtype)
+    half = (h.float() * 0.5).to(h.dtype)
+    again = uq.rmsnorm_q8(half, gamma, 0.0, residual=half, normed=True)
+    assert torch.equal(again[0], h) and torch.equal(again[1], y) and torch.equal(again[2][0], q[0]) and torch.equal(again[2][1], q[1])
