@@ -519,8 +519,44 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
             s1 = warp_sum(p.x);
             s2 = warp_sum(p.y);
         }
-        const float r = __frsqrt_rn(s1 / (float)a.D + a.eps);
-        const float c = r * r * (s2 / (float)a.D);                 // n mean(g n) = h r (r s2 / D)
+        float r = __frsqrt_rn(s1 / (float)a.D + a.eps);
+        float c = r * r * (s2 / (float)a.D);                       // n mean(g n) = h r (r s2 / D)
+        if constexpr (!std::is_same<T, __half>::value) {
+            if (__builtin_expect(!(s1 < __uint_as_float(INF_BITS)), 0)) {
+                // The squares, or their sum, have left fp32, which their mean need not: both sums again, from FAR h.
+                s1 = s2 = 0.f;
+                auto look_far = [&](const W& u, const W& w, const W& g) {
+                    float t[V], f[V], e[V];
+                    unpack(u, t);
+                    unpack(w, f);
+                    unpack(g, e);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        s1 = fmaf(f[j] * FAR, f[j] * FAR, s1);
+                        s2 = fmaf(t[j] * e[j], f[j] * FAR, s2);
+                    }
+                };
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * a.group < nvec) look_far(ku[i], kw[i], gam[i]);
+                if constexpr (!ODD) {
+                    for (int v = tid + NV * a.group; v < nvec; v += a.group) look_far(parts.load(dy, v), parts.load(h, v), parts.of_vector(gamma, v));
+                }
+                s1 = warp_sum(s1);
+                s2 = warp_sum(s2);
+                if (warps > 1) {
+                    asm volatile("bar.sync %0, %1;" :: "r"(1 + mine), "r"(a.group) : "memory");    // the first sums have been read
+                    if (lane == 0) sums[buf][threadIdx.x >> 5] = make_float2(s1, s2);
+                    asm volatile("bar.sync %0, %1;" :: "r"(1 + mine), "r"(a.group) : "memory");
+                    const float2 p = lane < warps ? sums[buf][first_warp + lane] : make_float2(0.f, 0.f);
+                    s1 = warp_sum(p.x);
+                    s2 = warp_sum(p.y);
+                }
+                const float far = __frsqrt_rn(s1 / (float)a.D + FAR * (FAR * a.eps));              // r / FAR
+                r = FAR * far;
+                c = r * (far * (s2 / (float)a.D));
+            }
+        }
         auto write = [&](int v, const W& u, const W& w, const W& g, const W& d, float (&out)[V]) {
             float t[V], f[V], e[V];
             unpack(u, t);

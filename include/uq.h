@@ -512,6 +512,7 @@ uq_status uq_rmsnorm_q8(const void* x, const void* residual, const void* gamma, 
  *   dy, h (device) [rows][D] of `type`; gamma (device) [D]; dh (device, or NULL) [rows][D], the gradient that reaches h
  *   besides; dx (device) [rows][D] of `type`: the gradient of h, and so of x and of the residual; it may be dy or dh.
  *   dgamma (device) fp32 [D], written.  Sums in fp32 in a fixed order: equal calls give equal bits.
+ * The mean of the squares has to lie within fp32, and so do the sums of dy * gamma * h over a row and of dy * n over the rows.
  * Workspace and stream capture as uq_gemm.
  */
 uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, uq_dtype type, void* dx,

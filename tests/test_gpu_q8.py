@@ -326,3 +326,19 @@ def test_squares_whose_sum_leaves_fp32(T, D, dtype, kind):
     half = (h.float() * 0.5).to(h.dtype)
     again = uq.rmsnorm_q8(half, gamma, 0.0, residual=half, normed=True)
     assert torch.equal(again[0], h) and torch.equal(again[1], y) and torch.equal(again[2][0], q[0]) and torch.equal(again[2][1], q[1])
+
+
+@pytest.mark.parametrize("kind", ["all", "one"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,D", [(4, 8192), (5, 8191), (700, 8192), (340, 9001), (900, 4000), (2000, 4001), (3, 33001), (400, 16384)])
+def test_gradient_where_the_squares_sum_leaves_fp32(T, D, dtype, kind):
+    h, gamma, eps = _loud(1, T, D, dtype, kind), _rows(3, 1, D, dtype)[0].contiguous(), 1e-2
+    dy = _rows(2, T, D, dtype)
+    dx, dgamma = uq.rmsnorm_grad(dy, h, gamma, eps)
+    rx, rg = oq.rmsnorm_grad(n(dy), n(h), n(gamma), eps, None)
+    H, G = n(h), n(dy) * n(gamma)
+    r = 1 / np.sqrt((H * H).mean(axis=1, keepdims=True) + eps)
+    mag = r * (np.abs(G) + np.abs(H) * r * r * np.abs(G * H).mean(axis=1, keepdims=True))
+    steps = 3 * (D / 32 + 16) + 16
+    assert np.all(np.abs(n(dx) - rx) <= ROUND[dtype] * np.abs(rx) * 1.0001 + steps * U * mag + TINY[dtype])
+    assert np.all(np.abs(n(dgamma) - rg) <= (T + steps) * U * np.abs(n(dy) * H * r).sum(axis=0) + 2.0 ** -140)
