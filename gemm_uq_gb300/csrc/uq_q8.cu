@@ -438,15 +438,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
     uint32_t other = 0;
     auto request = [&](long long row) {
         if (row < a.rows) {
-            const long long at = row * a.D - parts.off;
+            const long long at = ODD ? row * a.D - parts.off : (row * nvec + tid) * V;     // of the row, or of this thread's first part
             const long long left = (a.rows - row) * a.D + parts.off;
+            constexpr int OWN = ODD ? 1 : 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = tid + i * a.group;
-                if (v >= nvec) continue;
-                parts.copy(slot + other + i * part16, static_cast<const T*>(a.dy) + at, tid, i * a.group, left);
-                parts.copy(slot + other + (NV + i) * part16, static_cast<const T*>(a.h) + at, tid, i * a.group, left);
-                if (a.dh) parts.copy(slot + other + (2 * NV + i) * part16, static_cast<const T*>(a.dh) + at, tid, i * a.group, left);
+                if (tid + i * a.group >= nvec) continue;
+                parts.copy(slot + other + i * part16, static_cast<const T*>(a.dy) + at, OWN * tid, i * a.group, left);
+                parts.copy(slot + other + (NV + i) * part16, static_cast<const T*>(a.h) + at, OWN * tid, i * a.group, left);
+                if (a.dh) parts.copy(slot + other + (2 * NV + i) * part16, static_cast<const T*>(a.dh) + at, OWN * tid, i * a.group, left);
             }
         }
         copies_issued();
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradAr
                 for (int i = 0; i < NV; ++i)
                     if (tid + i * a.group < nvec) look_far(ku[i], kw[i], gam[i]);
                 if constexpr (!ODD) {
+#pragma unroll 1
                     for (int v = tid + NV * a.group; v < nvec; v += a.group) look_far(parts.load(dy, v), parts.load(h, v), parts.of_vector(gamma, v));
                 }
                 s1 = warp_sum(s1);
