@@ -166,6 +166,20 @@ uq_status workspace(int dev, cudaStream_t st, size_t partial_bytes, size_t ticke
     return UQ_OK;
 }
 
+// A call whose launches hand each other the stream's workspace takes its turn on the stream: launches of another thread's call
+// come before or after all of them.
+std::map<std::pair<int, void*>, std::mutex> g_turns;
+class Turn {
+public:
+    Turn(int dev, cudaStream_t st) : held_(of(dev, st)) {}
+private:
+    static std::mutex& of(int dev, cudaStream_t st) {
+        std::lock_guard<std::mutex> lk(g_mu);
+        return g_turns[{dev, (void*)st}];
+    }
+    std::lock_guard<std::mutex> held_;
+};
+
 // Launch overlap of the microscaled calls.  A product requests its weights before it waits for the work before it, so one
 // that follows a call that writes operands (they may be its weights) starts without overlap.
 void operands_written(int dev, cudaStream_t st) {
@@ -478,6 +492,7 @@ uq_status uq_gemm(const uint16_t* x, const void* wq, const void* scales, const v
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     const Route rt = route(fmt, M, N, K);
     if (rt == ROUTE_MMA_GEMM) {
         // blocks of at most 64 rows on the mma.sync GEMM; a last block of at most 8 rows on the GEMV
@@ -533,6 +548,7 @@ uq_status uq_gemm_gated(const uint16_t* x, const void* wq_gate, const void* scal
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     const Route rt = route(fmt, M, N, K);
     const bool tc = rt == ROUTE_TC;
     const int block = rt == ROUTE_GEMV ? 8 : 64;
@@ -687,6 +703,7 @@ uq_status uq_gemm_w4a8(const uint16_t* x, const void* wq, const void* scales, co
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     const uq::Layout L(N, K, fmt);
     const int Kp = L.Kp, G = (Kp + group - 1) / group;
     // scratch: x codes [M][Kp] | s_x [M] | per (row, group) code sums [M][G]; partial sums
@@ -1000,6 +1017,7 @@ uq_status uq_gemm_mx(const void* x, uq_dtype xtype, long long ldx, const uint8_t
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     uq::MxGemmArgs a = {};
     const uint8_t* xcodes = static_cast<const uint8_t*>(x);
     a.xscales = xscales;
@@ -1276,6 +1294,7 @@ uq_status uq_rmsnorm_grad(const void* dy, const void* h, const void* gamma, cons
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     Workspace* ws = nullptr;
     if ((s = workspace(dev, st, 0, 0, &ws, (size_t)uq::norm_grad_partials(type, rows, D, ds->sms) * D * sizeof(float))) != UQ_OK)
         return s;
@@ -1308,6 +1327,7 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
     DeviceState* ds = nullptr;
     int dev = 0;
     if ((s = device_state(&ds, &dev)) != UQ_OK) return s;
+    const Turn turn(dev, st);
     uq::Q8GemmArgs a = {};
     a.x = static_cast<const int8_t*>(x);
     a.w = w;

@@ -180,7 +180,8 @@ uq_status uq_pack_kmeta(const uint16_t* d, const uint16_t* dmin, const uint8_t* 
  * captured, so make one call of the largest size before capturing.  A buffer replaced
  * by growth is kept allocated until the process exits, so a CUDA graph captured before
  * the growth stays valid and may be replayed afterwards.  Calls on the same stream are
- * serialised by the stream; concurrent streams use separate workspaces.  A captured
+ * serialised by the stream, several threads' calls too (the launches of one call follow
+ * one another); concurrent streams use separate workspaces.  A captured
  * graph uses the workspace of the stream it was captured on: do not run it concurrently
  * with other calls on that stream (or with another replay of itself).
  */

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from tests.fake_cuda import load
+from tests.fake_cuda import Launch, load
 
 INVALID, UNSUPPORTED, ALIGN = 1, 2, 3
 BIG = 0x7FFFF000                                 # past 2^31 - 4097
@@ -162,3 +162,43 @@ def test_no_memory_is_an_error_and_nothing_is_launched(tmp_path):
     f.lib.fake_set_no_memory(0)
     assert len(f.launches(lambda: f.lib.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 7, 64, 64, None))) == 2
     assert len(f.launches(lambda: f.lib.uq_rmsnorm_grad(a, a, a, None, 0, a + 256, a, 4, 64, 1e-5, None))) == 2
+
+
+def test_calls_of_several_threads_on_one_stream_do_not_mix(tmp_path):
+    """The launches of a call that hand each other the stream's workspace follow one another, whichever threads call."""
+    import threading
+    f = load(tmp_path)
+    a, L = f.at, f.lib
+    calls = [lambda: L.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 7, 64, 64, None),
+             lambda: L.uq_gemm_w8a8(a, 0, 64, None, a, a, a, 0, 40, 64, 64, None),
+             lambda: L.uq_gemm_w8a8(a, 0, 64, a, a, a, a, 0, 50, 64, 64, None),
+             lambda: L.uq_rmsnorm_grad(a, a, a, None, 0, a + 256, a, 4, 64, 1e-5, None),
+             lambda: L.uq_gemm_mx(a, 0, 64, None, 1.0, a, a, a, 0, 40, 64, 64, 0, 1.0, None),
+             lambda: L.uq_gemm_w4a8(a, a, a, None, a, 11, 64, 256, 64, 0, None),
+             lambda: L.uq_gemm(a, a, a, None, a, 20, 64, 256, 256, 5, None),
+             lambda: L.uq_gemm_gated(a, a, a, None, a, a, None, a, 20, 64, 256, 64, 0, None)]
+    alone = [tuple(f.launches(c)) for c in calls]
+    assert all(len(s) > 1 for s in alone)
+    f.lib.fake_clear()
+    bad = []
+
+    def many(i):
+        for _ in range(400):
+            if calls[i]() != 0:
+                bad.append(i)
+    threads = [threading.Thread(target=many, args=(i % len(calls),)) for i in range(2 * len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    n = f.lib.fake_launch_count()
+    assert n == 800 * sum(len(s) for s in alone)
+    seen, at = [], 0
+    for i in range(n):
+        v = [ctypes.c_uint() for _ in range(3)] + [ctypes.c_int()]
+        seen.append(Launch(f.lib.fake_launch(i, *(ctypes.byref(x) for x in v)).decode(), *(x.value for x in v)))
+    while at < n:
+        whole = [s for s in alone if tuple(seen[at:at + len(s)]) == s]
+        assert whole, f"launches of different calls follow one another: {[x.kernel[:80] for x in seen[at:at + 4]]}"
+        at += len(whole[0])
