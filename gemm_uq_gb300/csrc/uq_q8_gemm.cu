@@ -940,13 +940,16 @@ template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const voi
     return cudaLaunchKernelEx(&cfg, q8_tc_kernel<T, TN, PAIR>, wmap, xmap, a);
 }
 
-// Whether pairs of CTAs are the faster kernel, by waves: a stage of 256 x 256 tiles takes about 15/8 of the time of one of 128 x
-// 128 tiles (0.75 us to 0.43 at K = 4096, 0.66 to 0.39 at 8192^3).  Measured, us single / pairs: 4096 x 4096, M = 1024 33.1 / 30.1,
-// 2048 60.4 / 56.3; 14336 x 4096, M = 256 33.2 / 31.2, 512 47.0 / 57.4; 8192 x 8192, M = 256 32.2 / 31.0 with k shared by two
-// pairs, which no rule here takes, 8192 718 / 629.
+// Whether pairs of CTAs are the faster kernel, by rounds of tiles: a round of 128 x 128 tiles takes about 1.9 us and 0.39 a stage,
+// one of 256 x 256 tiles, whose outputs are four times as many, 8.0 us and 0.58 a stage (fitted to K = 2048 to 8192).  Measured, us
+// single / pairs: 8192 x 8192 (27 / 14 rounds) K = 512 82 / 126, 1024 122 / 165, 2048 211 / 234, 8192 729 / 633; 2048 x 8192 (7 / 4)
+// K = 4096 101 / 107, 8192 189 / 181; 2560 x 8192 (9 / 5) 127 / 133 and 241 / 227; 2500 x 4096 (5 / 3) K = 14336 238 / 224;
+// 4096 x 4096 (7 / 4) K = 2048 60 / 71; 1024 x 4096 (2 / 1) K = 1408 17.2 / 18.3, 2048 20.9 / 20.7, 4096 34.0 / 30.5; 512 x 14336
+// (3 / 2) K = 4096 47 / 55; 256 x 14336 (2 / 1) 33.2 / 30.3.
 bool pays_in_pairs(const Q8GemmArgs& g, int sms) {
     const long long one = (long long)((g.N + 127) / 128) * ((g.M + 127) / 128), two = 2LL * ((g.N + 255) / 256) * ((g.M + 255) / 256);
-    return (two + sms - 1) / sms * 15 < (one + sms - 1) / sms * 8;
+    const int steps = (g.K + STAGE_K - 1) / STAGE_K;
+    return (two + sms - 1) / sms * (206 + 15 * steps) < (one + sms - 1) / sms * (49 + 10 * steps);
 }
 
 }  // namespace

@@ -195,3 +195,19 @@ def test_scales_whose_product_leaves_fp32(M, N, K, dtype):
     tol = ROUND[dtype] * want.abs() * 1.0001 + (K / 1024 + 4) * U * mag + (a.abs() @ b.abs().t()) * 2.0 ** -50
     bad = (y.double() - want).abs() > tol
     assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outputs off, first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 4100, 2832), (2040, 4090, 2944), (2305, 1792, 3088), (2000, 2304, 3216), (2300, 3900, 3344),
+                                   (4600, 4090, 2832), (1024, 4096, 1024), (8192, 2304, 512)])
+def test_pairs_of_ctas_and_the_sizes_that_leave_them(M, N, K):
+    """Tiles that pairs take, with ragged ends and chunks of several lengths, and some that they leave for their few k."""
+    for kind in ("random", "largest"):
+        x, w = _operand(3, M, K, kind), _operand(4, N, K)
+        y = uq.gemm_w8a8(x, w, dtype=torch.float32)
+        a, b = x[0].double() * x[1].double()[:, None], w[0].double() * w[1].double()[:, None]
+        mag = sum((a[:, k:k + 512] @ b[:, k:k + 512].t()).abs() for k in range(0, K, 512))
+        bad = (y.double() - a @ b.t()).abs() > (K / 512 + 4) * U * mag + 2.0 ** -149 + (a.abs() @ b.abs().t()) * 2.0 ** -50
+        assert not bool(bad.any()), f"{int(bad.sum())} outputs off, first at {bad.nonzero()[0].tolist()}"
+        for dtype in ("bf16", "fp16"):
+            assert torch.equal(uq.gemm_w8a8(x, w, dtype=DTYPE[dtype]), y.to(DTYPE[dtype]))
+    assert uq.device_fault() == 0
