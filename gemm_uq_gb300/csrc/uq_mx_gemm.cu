@@ -21,11 +21,10 @@
 // end of a kernel (3 us) and then memory; many the tensor cores (their pipe is active in 81 % of an 8192^3's cycles).
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is
 // freed, and the fault word tells.
-#include <cuda.h>
 #include <algorithm>
-#include <atomic>
 
 #include "uq_mx_quant.cuh"
+#include "uq_tcgen05.cuh"
 
 namespace uq {
 
@@ -48,25 +47,12 @@ constexpr int HEAD = 1024;                      // barriers and flags before the
 // ---- PTX wrappers ------------------------------------------------------------------------------
 // The producer and the MMA warp run their loops as whole warps, so that every operand is a warp-uniform value, and the
 // elected lane issues (one lane in a divergent branch issued a tcgen05 instruction every ~120 cycles).
-#define UQ_ELECT "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e "
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
-                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(UQ_ELECT "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
                  :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
-    asm volatile(UQ_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes) : "memory");
-}
-// Low words of the shared-memory descriptors (address in 16-byte units, bit 16 set); the high words are constants:
-// an operand is K-major with the 128-byte swizzle, 8-row groups 1024 bytes apart; a scale tile is 32 rows of 16 bytes,
-// unswizzled, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
-#define UQ_OPERAND_HI "0x40004040"
+// (high word of a scale tile's descriptor: 32 rows of 16 bytes, unswizzled, 8-row groups 128 bytes apart)
 #define UQ_SCALES_HI "0x00004008"
 
 // The instructions that share a scale tile, issued by the elected lane of the converged warp: tcgen05.cp of the tile
@@ -131,30 +117,7 @@ __device__ __forceinline__ void issue_more(uint32_t d, uint32_t a, uint32_t b, u
 template <int FMT> __device__ __forceinline__ uint32_t block_idesc(int n) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (FMT == UQ_MXFP4 ? 1u << 23 : 0u) | (1u << 27);
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile(UQ_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-                 :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr) : "memory");
-}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
-    return v;
-}
-
 // A whole warp's wait: false for all lanes once WAIT_LIMIT_NS have passed (the fault word then tells) or the CTA was
 // told to stop.  Polls without a suspend hint: a warp put to sleep for up to a microsecond woke too late for a ring
 // whose steps take a quarter of that.
@@ -293,12 +256,6 @@ __device__ __forceinline__ void launch_dependents(const MxGemmArgs& a) {
 }
 
 // The tiles of a CTA and its k steps of them.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
 struct Schedule {
     int tile, tiles, stride, k0, k1;
     __device__ __forceinline__ Schedule(const MxGemmArgs& a, int tt_all) {
@@ -340,17 +297,6 @@ __device__ __forceinline__ void store4(const MxGemmArgs& a, long long at, int co
     else if (a.ytype == UQ_FP16) go(__half());
     else go(float());
 }
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
 // Writes 16 columns (tokens m0 .. m0 + count) of this lane's output nn; the warp's lanes hold 32 consecutive outputs.
 // 16-bit types with an even N: neighbouring lanes exchange every other value and store pairs of outputs, so a store
 // covers 64 bytes of each of two tokens, and conversions and stores are halved.
@@ -767,16 +713,6 @@ template <int FMT, int NA> struct Pair {
     static_assert(STAGE % 1024 == 0 && STAGES <= MAX_STAGES, "stage layout");
 };
 
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
-                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
 __device__ __forceinline__ void pair_tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(UQ_ELECT "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
@@ -825,12 +761,6 @@ __device__ __forceinline__ void pair_tile(uint32_t d, uint32_t a, uint32_t b, ui
                      UQ_PAIR_ARGS);
 #undef UQ_PAIR_HEAD
 #undef UQ_PAIR_ARGS
-}
-// arrive on the barrier at this offset in both CTAs when the MMAs issued so far are complete
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
-    asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
-                 :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
@@ -1047,22 +977,6 @@ mx_gemm_pair_kernel(const __grid_constant__ MxGemmMaps maps, const MxGemmArgs a)
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-    static std::atomic<EncodeTiledFn> known{nullptr};
-    EncodeTiledFn fn = known.load(std::memory_order_relaxed);
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess && q == cudaDriverEntryPointSuccess)
-            known.store(fn = reinterpret_cast<EncodeTiledFn>(p), std::memory_order_relaxed);
-    }
-    return fn;
-}
-
 // codes [rows][K/2] as bytes, 128-byte columns x `box` rows, 128-byte swizzle; folded (K a multiple of 256): the columns
 // are the third dimension and a box takes two of them
 bool codes_map(CUtensorMap* m, const uint8_t* codes, long long rows, int K, int box, bool folded) {
@@ -1083,19 +997,6 @@ bool scales_map(CUtensorMap* m, const uint8_t* scales, long long row_tiles, int 
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 3, const_cast<uint8_t*>(scales), dims, strides, b, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
-using Done = std::atomic<bool>[64];
-template <class K> cudaError_t configure(K kernel, Done& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
-    return e;
 }
 
 template <int FMT, int NA>

@@ -11,9 +11,9 @@
 //
 // All of it is bound by memory: a row is read once and written once, in the widest accesses that its address, stride and
 // length allow.  Small calls are a launch and a chain of latencies: one row of 4096 2.4 us.
-#include <atomic>
 
 #include "uq_q8.cuh"
+#include "uq_tcgen05.cuh"
 
 namespace uq {
 
@@ -687,19 +687,6 @@ template <class T, class F> cudaError_t with_plan(const Plan& p, F&& f) {
     return by_nv(std::integral_constant<int, 1>(), std::false_type());
 }
 
-// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
-using Done = std::atomic<bool>[64];
-template <class K> cudaError_t configure(K kernel, Done& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sms, cudaStream_t st) {
     return with_dtype(type, [&](auto t) {
         using T = decltype(t);
@@ -714,7 +701,7 @@ template <bool NORM> cudaError_t launch_rows(const RowArgs& a0, int type, int sm
             if constexpr (V * sizeof(T) == 16 && NV == 4) {
                 if (block <= PIPE_THREADS && (ODD || a.group * NV >= a.D / V) && a.rows > 2 * sms) {
                     static Done done = {};
-                    const cudaError_t e = configure(row_kernel<T, V, NV, NORM, true, ODD>, done);
+                    const cudaError_t e = configure(row_kernel<T, V, NV, NORM, true, ODD>, done, 200 * 1024);
                     if (e != cudaSuccess) return e;
                     row_kernel<T, V, NV, NORM, true, ODD><<<grid_of(tiles, (long long)sms * 3 * (PIPE_THREADS / block), p), block,
                                                            ROWS_AHEAD * (a.residual ? 2 : 1) * NV * 16 * block, st>>>(a);
@@ -795,7 +782,7 @@ cudaError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma
             if constexpr (V * sizeof(T) == 16 && NV <= 2) {
                 if (rows > 2 * sms) {
                     static Done done = {};
-                    const cudaError_t f = configure(norm_grad_kernel<T, V, NV, true, ODD>, done);
+                    const cudaError_t f = configure(norm_grad_kernel<T, V, NV, true, ODD>, done, 200 * 1024);
                     if (f != cudaSuccess) return f;
                     norm_grad_kernel<T, V, NV, true, ODD><<<P, block, ROWS_AHEAD * 3 * NV * 16 * block + add, st>>>(a);
                     return cudaGetLastError();

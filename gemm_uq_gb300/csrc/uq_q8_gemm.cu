@@ -30,11 +30,10 @@
 // cycles, as long as its MMAs), the widening before and 13.5 rounds of tiles that take 14; for up to 128 tokens HBM while it
 // streams (5.8 to 6 TB/s: 600 cycles a stage on 112 SMs, of which the MMAs are 480), and besides 8 us for the start, the first
 // weights, the outputs and the sums of shared tiles.
-#include <cuda.h>
 #include <algorithm>
-#include <atomic>
 
 #include "uq_q8.cuh"
+#include "uq_tcgen05.cuh"
 
 namespace uq {
 
@@ -50,24 +49,10 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
     asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
     int v;
     asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.s32 %0, [r];\n\t}"
                  : "=r"(v) : "r"(addr), "r"(rank) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
 // up to four neighbouring outputs (count of them) at element `at`
@@ -241,23 +226,6 @@ struct TcArgs8 {
     int wait;                                   // the kernel before on the stream may still run
 };
 
-#define UQ_ELECT "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e "
-#define UQ_OPERAND_HI "0x40004040"              // K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
-                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-// the same, counted on a barrier of the pair's even CTA
-__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(UQ_ELECT "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
-                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
-    asm volatile(UQ_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" :: "r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 template <bool PAIR> __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t on) {
     if constexpr (PAIR)
         asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, " UQ_OPERAND_HI "};\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -268,21 +236,9 @@ template <bool PAIR> __device__ __forceinline__ void mma(uint32_t d, uint32_t a,
                      "elect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
                      :: "r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(on) : "memory");
 }
-// arrive on the barrier (PAIR: at this offset in both CTAs) when the MMAs issued so far are complete
 template <bool PAIR> __device__ __forceinline__ void commit(uint32_t bar) {
-    if constexpr (PAIR)
-        asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
-                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
-                     :: "r"(bar) : "memory");
-    else
-        asm volatile(UQ_ELECT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    return a;
+    if constexpr (PAIR) pair_commit(bar);
+    else uq::commit(bar);
 }
 __device__ __forceinline__ void arrive(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(addr) : "memory");
@@ -327,13 +283,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
                     "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr) : "memory");
-}
 // four int8 -> two f16x2, exact: a byte with its sign bit turned over is the low byte of 1024 + 128 + v in fp16
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = w ^ 0x80808080u;
@@ -342,16 +291,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 __device__ __forceinline__ void after_prior_work(const TcArgs8& a) {
     if (a.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack2(__half, float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
 }
 // Writes 16 columns (tokens m0 .. m0 + count) of this lane's output nn; the warp's lanes hold 32 consecutive outputs.  16-bit
 // types where N is even: neighbouring lanes exchange every other value and hold pairs of outputs, stored together.  N odd: each
@@ -861,21 +800,6 @@ __global__ void __launch_bounds__(256) q8_widen_kernel(const uint4* __restrict__
     }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-    static std::atomic<EncodeTiledFn> known{nullptr};
-    EncodeTiledFn fn = known.load(std::memory_order_relaxed);
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess && q == cudaDriverEntryPointSuccess)
-            known.store(fn = reinterpret_cast<EncodeTiledFn>(p), std::memory_order_relaxed);
-    }
-    return fn;
-}
 // rows of `cols` elements of `size` bytes, boxes of 128 bytes x `box` rows, 128-byte swizzle, zeros beyond the ends
 bool rows_map(CUtensorMap* m, const void* p, long long rows, int cols, int size, int box) {
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -885,19 +809,6 @@ bool rows_map(CUtensorMap* m, const void* p, long long rows, int cols, int size,
     return encode_fn()(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dims,
                        strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Opts a kernel into its shared memory, once per device (two threads at once: twice, to the same value).
-using Done = std::atomic<bool>[64];
-template <class K> cudaError_t configure(K kernel, Done& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
-    return e;
 }
 
 template <class T, int TN, bool PAIR> cudaError_t launch_tc(TcArgs8 a, const void* x16, int sms, cudaStream_t st) {
