@@ -88,9 +88,11 @@ __device__ __forceinline__ void best_of(long long& c, int& e, int E) {
 }
 
 // Scores in approximate instructions, with a bound on their error as a part of the largest score, one:
-//   sigmoid  e^-x loses 2^-22 and |x| 2^-23.4 by its argument's rounding, of which s (1 - s) reaches s: below 2^-24 together; the
-//            reciprocal 2^-23 s;
-//   softmax  as much of each score, and E / 32 + 5 roundings of the sum, which all scores share.
+//   sigmoid  e^-x loses 2^-22 and, by its argument's rounding, |x| 2^-23.7, of which s (1 - s) reaches s; the sum 1 + e^-x loses
+//            2^-24 s and the reciprocal 2^-23 s: together at most 0.84 of 2^-22, near x = 1.7;
+//   softmax  of each score s the same of e^(x - m) (2^-22 and |x - m| 2^-23), and of the sum, which all scores share, its terms'
+//            mean loss and E / 32 + 5 roundings.  With u = 2^-24: a part p of the sum at the largest logit and the rest at a distance
+//            d lose p (1 - p) d < 2 of 2 u by the distances, the rest at most (4 + 3 + 5 + E / 32) u.
 // The addition of the bias loses 2^-24 of its result besides.
 __device__ __forceinline__ float exp_about(float x) {
     float e;
