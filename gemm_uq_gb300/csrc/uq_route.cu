@@ -109,10 +109,12 @@ __device__ __forceinline__ float score_error(const RouteArgs& a) { return a.sigm
 __device__ __forceinline__ bool apart(const RouteArgs& a, float hi, float lo, float terms, float best = 0.f) {
     return hi - lo > 2.f * terms * ((fmaxf(fabsf(hi), fabsf(lo)) + best) * 0x1p-24f + score_error(a));
 }
-// The same for the sums of two groups, given the best value of each lane's group.  A bias may give a sum's terms opposite signs, so
-// that each is larger than the sum; but the first is at most the best of all, and the second at most that and the sum together.
+// The same for the sums of two groups, given the best value of each lane's group.  A sum loses its terms' errors, 2^-24 of each term
+// and 2^-24 of itself.  A bias may give the terms opposite signs, so that each is larger than the sum; but the first is at most
+// the best of all, and the second at most that and the sum together: group_top times the error of one value, with the sum and the
+// best in the place of the value.
 __device__ __forceinline__ bool groups_apart(const RouteArgs& a, int hi, int lo, int b1) {
-    return apart(a, value_of(hi), value_of(lo), 2.f * a.group_top, fmaxf(value_of(__reduce_max_sync(ALL, b1)), 0.f));
+    return apart(a, value_of(hi), value_of(lo), (float)a.group_top, fmaxf(value_of(__reduce_max_sync(ALL, b1)), 0.f));
 }
 
 // Chooses from c[0 .. E) (the warp's shared memory; chosen experts are taken out of it), in fp32 or 64 bits.  Lane j returns choice j, -1 for
