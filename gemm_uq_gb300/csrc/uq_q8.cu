@@ -32,6 +32,8 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_s
 
 // What a row is multiplied with whose squares, or their sum, have left fp32: 2^31 squares of fp32's largest value then stay within
 // it, and a sum that had left it is above 2^-32.
+// (What rows in range pay for this path, us without / with it: 8192 x 8192 bf16 99.4 / 99.1, 16384 x 512 13.5 / 13.9, 4096 x 4001
+// 43.7 / 45.1, 1 x 4096 2.6 / 2.7; gradient of 8192 x 4096 58.3 / 58.9.  fp16 rows cannot leave fp32 and have none of it.)
 constexpr float FAR = 0x1p-80f;
 // A barrier of one of a CTA's four groups of threads.  (Constant barriers: with a number in a register a CTA claims all 16, and
 // fewer CTAs fit an SM, 16384 x 512 18.7 us instead of 13.7.)
@@ -62,7 +64,7 @@ template <class W> __device__ __forceinline__ W copied(uint32_t at) {
 // at the matrix's boundaries, and those at a row's ends hold elements of its neighbours, which are read as zeros and not written.
 // Groups of threads take rows V apart (or a multiple), which all begin at the same place in a part: so a thread's columns stay
 // the same.  Rows of an odd length in accesses of one element, and this way: bf16 norm of 4096 x 4097 with all outputs 84 us and
-// 57, its gradient 127 and 54, quantizer 48 and 22; 8192 x 1001 fp32 37 and 25, 80 and 29, 20 and 11.
+// 60, its gradient 127 and 55, quantizer 48 and 22; 8192 x 1001 fp32 37 and 26, 80 and 29, 20 and 11.  Where it does not pay: plan_of.
 template <class T, int V, bool ODD> struct Parts {
     using W = Vec<T, V>;
     int off, D, count;                          // of the row's first element in its first part
@@ -151,7 +153,7 @@ __device__ __forceinline__ float larger(float a, float b) {
 // PIPE (16-byte accesses, rows without a rest, many of them): the next rows' loads are under way while a row is reduced and
 // written, and gamma stays in registers.  Without, a row is a chain of loads, a reduction, and stores; measured, 8192 rows of 8192
 // bf16 with all outputs: PIPE 100 us (6.0 TB/s, 0.89 of the measured copy); else 256 threads a row with four accesses each 134
-// us, 512 with two 152; the quantizer 39 (5.1 TB/s) and 44 us.
+// us, 512 with two 152; the quantizer 37 (5.4 TB/s) and 44 us.
 template <class T, int V, int NV, bool NORM, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(PIPE ? PIPE_THREADS : MAX_THREADS, PIPE ? 3 : 1) row_kernel(const RowArgs a) {
     using W = Vec<T, V>;
@@ -417,7 +419,7 @@ struct GradArgs {
 // A group of threads takes every so many-th row; its share of dgamma stays in registers (of a longer row, in its CTA's row of
 // `partials`, where a CTA has one group) until its rows are done; then a CTA's groups are added in order.  Named barriers, so
 // that a CTA's groups do not wait for one another.  gamma stays in registers: read again for every row, four accesses a thread,
-// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 58 us (4.6 TB/s, the addition of the
+// it kept L1 73 % busy.  PIPE as above.  Measured, 8192 rows of 4096 bf16 with dh: 59 us (4.6 TB/s, the addition of the
 // partials in it), without PIPE 68, with gamma read again 96.
 template <class T, int V, int NV, bool PIPE, bool ODD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const GradArgs a) {

@@ -25,9 +25,10 @@
 // Few tiles: a cluster of S CTAs shares a tile's k, and adds its fp32 sums through distributed shared memory in rank order.
 // Every wait is bounded; on a timeout the roles stop, copies in flight are waited for (bounded), the tensor memory is freed,
 // and the fault word tells.
-// 8192^3 621 us (36 of them widening the tokens; 1.77 PFLOP/s, 0.89 of the measured bf16 burst rate); 1024 x 4096 x 4096 30 us;
-// 64 x 14336 x 4096 18.8 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the MMAs of pairs (within a tile a stage takes 1020
-// cycles, as long as its MMAs), the widening before and 13.5 rounds of tiles that take 14; for up to 128 tokens HBM while it
+// 8192^3 621 to 635 us on different boxes (36 of them widening the tokens; 1.75 PFLOP/s, 0.88 of the measured bf16 burst rate);
+// 1024 x 4096 x 4096 30 us; 64 x 14336 x 4096 18.8 to 19.8 us; 37 x 4096 x 14336 19.5 us.  What bounds it: the MMAs of pairs (within a tile
+// a stage takes 1020 cycles, as long as its MMAs; of 8192^3 the tensor pipe is active in 81 % of the cycles, the rest is between
+// tiles), the widening before and 13.5 rounds of tiles that take 14; for up to 128 tokens HBM while it
 // streams (5.8 to 6 TB/s: 600 cycles a stage on 112 SMs, of which the MMAs are 480), and besides 8 us for the start, the first
 // weights, the outputs and the sums of shared tiles.
 #include <algorithm>
