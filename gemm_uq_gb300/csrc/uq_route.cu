@@ -180,8 +180,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
     rescan();
     int id = -1, last = -1;
     float before = 0.f;
-    const int rounds = !WIDE && !exact ? a.topk + 1 : a.topk;      // the first that is not chosen, too
-    for (int j = 0; j < rounds; ++j) {
+    for (int j = 0; j < a.topk; ++j) {
         S v = mine;
         int e = at;
         best_of(v, e, E);
@@ -195,10 +194,21 @@ __device__ __forceinline__ int choose(const RouteArgs& a, S* c, const T* x, bool
             before = value;
             last = e;
         }
-        if (j < a.topk && lane == j) id = e;
+        if (lane == j) id = e;
         if (at == e && mine > none) {
             c[e] = none;
             rescan();
+        }
+    }
+    if constexpr (!WIDE) {
+        // What is not chosen: near the last choice only where the logit and the bias are its own.  (All of it, since between two
+        // of the same there may be a third that fp32 does not tell from them.)
+        if (!exact && last >= 0) {
+            const float xl = to_f32(x[last]), bl = a.bias ? a.bias[last] : 0.f;
+            bool near = false;
+            for (int e = lane; e < E; e += 32)
+                if (c[e] > none && !apart(a, before, value_of(c[e]), 1.f)) near |= to_f32(x[e]) != xl || (a.bias && a.bias[e] != bl);
+            if (__any_sync(ALL, near)) sure = false;
         }
     }
     return id;
@@ -365,8 +375,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             for (int i = 0; i < NL; ++i)
                 c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != low_value()));
         }
-        // lane j: choice j; behind the last one, those that are too near to it.  What is behind the 32nd is looked at, too: near to
-        // it, it makes the choice unsure.
+        // lane j: choice j; behind the last one, those that are too near to it.  Behind the 32nd nothing may be near.
         int id = -1, last = -1, found = 0;
         float before = 0.f;
         for (int j = 0; j <= 32; ++j) {
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             if (!exact && j) {
                 if (apart(a, before, value, 1.f)) {
                     if (j >= a.topk) break;
-                } else if (!(before == value && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
+                } else if (j == 32 || !(before == value && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
                     sure = false;               // (the same logit and bias give the same value: the lower index is right)
                 }
             }

@@ -544,7 +544,8 @@ uq_status uq_gemm_w8a8(const void* x, uq_dtype xtype, long long ldx, const float
  *   groups   > 1: the experts form `groups` equal groups of neighbours; only experts of the top_groups best ones may be
  *            chosen.  A group counts the sum of its group_top (1 or 2) highest c of experts that may be chosen; equal groups by
  *            lower index.
- *   weights  s of the chosen; renormalize: divided by their sum (0 / 0 = 0); times scale.  fp32.
+ *   weights  s of the chosen; renormalize: divided by their sum (of no choice: 0), with their ratios kept where the scores
+ *            themselves would underflow; times scale.  fp32.
  * logits (device) [T][experts] of `type`; bias (device or NULL) fp32 [experts]; ids (device) int32 [T][topk], weights
  * (device) fp32 [T][topk], written.  1 <= experts <= 1024, 1 <= groups <= 32, topk <= 32 and at most the experts of
  * top_groups groups.  Asynchronous.

@@ -188,3 +188,24 @@ def test_near_groups(E, G, score):
         for r in (tg - 1, tg):
             x[:, ranks[r] * size:(ranks[r] + 1) * size] += g.integers(-3, 4, (T, size)).astype(np.float32) * np.float32(2.0 ** -23)
         _check(torch.from_numpy(x).to(DEV), 2, score, torch.from_numpy(bias).to(DEV), G, tg, gt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(40, 1), (64, 8), (96, 8), (256, 1), (256, 8), (480, 16), (1000, 1), (1024, 8)])
+def test_equal_logits_beside_near_ones(E, G, score):
+    """Few different logits, so near that fp32's scores are equal, each of many experts: an equal neighbour behind the last choice does
+    not hide a higher one behind it."""
+    T, g = 48, np.random.default_rng([E, G])
+    if score == "sigmoid":
+        steps = np.array([17.0, 18.25, 19.5, 25.5])
+    else:
+        steps = np.array([0.0, 1.0, 2.0, 3.0]) * 2.0 ** -23
+    often = np.array([0.4, 0.4, 0.15, 0.05])
+    x = torch.from_numpy(steps[g.choice(4, size=(T, E), p=often)].astype(np.float32)).to(DEV)
+    x[0] = 18.25 if score == "sigmoid" else 0.0                          # all equal, as padding is
+    x[1], x[1, E - 1] = x[0], x[1].max()
+    bias = torch.zeros(E, device=DEV)
+    for k in (1, 2, 5, 31, 32):
+        for tg in {max(G // 2, -(-k // (E // G))), G}:
+            for gt in (1, 2) if G > 1 else (1,):
+                _check(x, min(k, E // G * tg), score, bias, G, tg, gt)
