@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             }
         }
         const int none = none_of<int>();
-        bool sure = true, exact = by_logit, groups_sure = true;
+        bool exact = by_logit, groups_sure = true;
+        int doubt = 0;                          // 1: near neighbours; 2: something near behind the 32nd
         if (a.groups > 1) {
             const int per = a.E / a.groups / NL, g = lane / per;   // lanes of a group
             int b1 = none, b2 = none;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
             for (int i = 0; i < NL; ++i)
                 c[i] = !stays ? none : (a.bias ? c[i] : ranked(v[i] + 0.f, v[i] != low_value()));
         }
-        // lane j: choice j; behind the last one, those that are too near to it.  Behind the 32nd nothing may be near.
+        // lane j: choice j; behind the last one, those that are too near to it.  What is near behind the 32nd is looked at below.
         int id = -1, last = -1, found = 0;
         float before = 0.f;
         for (int j = 0; j <= 32; ++j) {
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
                 if (apart(a, before, value, 1.f)) {
                     if (j >= a.topk) break;
                 } else if (j == 32 || !(before == value && to_f32(x[e]) == to_f32(x[last]) && (!a.bias || a.bias[e] == a.bias[last]))) {
-                    sure = false;               // (the same logit and bias give the same value: the lower index is right)
+                    doubt |= j == 32 ? 2 : 1;   // (the same logit and bias give the same value: the lower index is right)
                 }
             }
             before = value;
@@ -404,7 +405,16 @@ __global__ void __launch_bounds__(WARPS * 32) route_lanes_kernel(const RouteArgs
                 for (int i = 0; i < NL; ++i)
                     if (i == at) c[i] = none;
         }
-        if (!sure || !groups_sure) {
+        if (doubt == 2 && groups_sure) {        // all equal, as padding may be?  Then the lower indices are right, too
+            const int e31 = __shfl_sync(ALL, id, 31);
+            const float xl = to_f32(x[e31]), bl = a.bias ? a.bias[e31] : 0.f;
+            bool near = to_f32(x[last]) != xl || (a.bias && a.bias[last] != bl);
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (c[i] > none && !apart(a, before, value_of(c[i]), 1.f)) near |= v[i] != xl || bias[i] != bl;
+            if (!__any_sync(ALL, near)) doubt = 0;
+        }
+        if (doubt || !groups_sure) {
             const float u = id >= 0 ? to_f32(x[id]) : 0.f;
             const bool odd = u != u || (id >= 0 && a.bias && a.bias[id] != a.bias[id]);
             if (groups_sure && a.sigmoid && found < 32 && !__any_sync(ALL, odd)) {
